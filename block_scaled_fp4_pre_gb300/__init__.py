@@ -45,6 +45,20 @@ def make_dims(hidden: int, inter: int, num_experts: int, topk: int, max_tokens: 
     return MoeDims(hidden, inter, num_experts, topk, max_tokens, mma_type)
 
 
+class LinearDims(ctypes.Structure):
+    _fields_ = [("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("mma_type", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"LinearDims(out_features={self.out_features}, in_features={self.in_features}, "
+                f"max_rows={self.max_rows}, mma_type={self.mma_type})")
+
+
+def make_linear_dims(out_features: int, in_features: int, max_rows: int,
+                     mma_type: int = MOE_MMA_MXF4xMXF4) -> LinearDims:
+    return LinearDims(out_features, in_features, max_rows, mma_type)
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{status_string(status)}: {message}")
@@ -62,7 +76,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         l = ctypes.CDLL(LIB_PATH)
-        D = ctypes.POINTER(MoeDims)
+        D, LD = ctypes.POINTER(MoeDims), ctypes.POINTER(LinearDims)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sigs = {
             "moe_last_error": ([], ctypes.c_char_p),
@@ -93,6 +107,15 @@ def lib() -> ctypes.CDLL:
             "moe_workspace_set_dispatch": ([vp, i32], i32),
             "moe_workspace_set_tiles": ([vp, i32], i32),
             "moe_mxfp8_quantize": ([vp, i64, i64, vp, vp, i32, i64, vp], i32),
+            "moe_rmsnorm_mxfp8": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i64, vp, i64, vp,
+                                   i64, vp, vp, i32, i64, vp], i32),
+            "moe_linear_weights_size": ([LD], sz),
+            "moe_linear_workspace_size": ([LD], sz),
+            "moe_linear_prepare": ([LD, vp, vp, vp, sz, vp], i32),
+            "moe_linear_workspace_init": ([LD, vp, sz, vp], i32),
+            "moe_linear_forward": ([LD, vp, vp, i64, i64, vp, i64, i32, vp, sz, vp], i32),
+            "moe_linear_forward_pair": ([LD, vp, vp, vp, i64, vp, i64, i32, vp, sz, vp], i32),
+            "moe_linear_check": ([vp, vp], i32),
         }
         for name, (args, res) in sigs.items():
             f = getattr(l, name)
@@ -277,6 +300,82 @@ def moe_mxfp8_quantize(x, rows: int, K: int, q, sf, layout: int, rows_cap: int |
     """bf16 rows -> E4M3 values and UE8M0 scales (packed int32 or the 4-D 128x4 layout)."""
     _check(lib().moe_mxfp8_quantize(_ptr(x), int(rows), int(K), _ptr(q), _ptr(sf), int(layout),
                                     int(rows if rows_cap is None else rows_cap), _stream(stream)))
+
+
+def _matrix(t, rows: int, cols: int, dtypes, name: str) -> int:
+    """Row stride of a [rows, cols] tensor of one of the dtypes with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype not in dtypes:
+        raise ValueError(f"{name}: need [{rows}, {cols}] of {dtypes}, got {tuple(t.shape)} "
+                         f"of {t.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+
+
+_BF16 = (torch.bfloat16,)
+_OUT = (torch.bfloat16, torch.float32)
+
+
+def moe_rmsnorm_mxfp8(x, gamma, eps: float, q=None, sf=None, layout: int = MOE_SF_128X4, *,
+                      residual=None, residual_out=None, y=None, rows_cap: int | None = None,
+                      stream=None) -> None:
+    """RMSNorm of x + residual: bf16 sum and norm, and the norm's MXFP8 pair (q, sf).
+
+    x, residual, residual_out and y are bf16 [rows, K] tensors with contiguous rows; q and sf
+    as moe_mxfp8_quantize writes them.  Any output may be left out."""
+    rows, K = x.shape
+    ldx = _matrix(x, rows, K, _BF16, "x")
+    ldr = 0 if residual is None else _matrix(residual, rows, K, _BF16, "residual")
+    ldro = 0 if residual_out is None else _matrix(residual_out, rows, K, _BF16, "residual_out")
+    ldy = 0 if y is None else _matrix(y, rows, K, _BF16, "y")
+    if gamma.dtype != torch.bfloat16 or gamma.shape != (K,) or not gamma.is_contiguous():
+        raise ValueError(f"gamma: need contiguous bf16 [{K}]")
+    _check(lib().moe_rmsnorm_mxfp8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(gamma), eps, rows, K,
+                                   _ptr(residual_out), ldro, _ptr(y), ldy, _ptr(q), _ptr(sf),
+                                   layout, rows if rows_cap is None else rows_cap,
+                                   _stream(stream)))
+
+
+def moe_linear_weights_size(dims: LinearDims) -> int:
+    return int(lib().moe_linear_weights_size(ctypes.byref(dims)))
+
+
+def moe_linear_workspace_size(dims: LinearDims) -> int:
+    return int(lib().moe_linear_workspace_size(ctypes.byref(dims)))
+
+
+def moe_linear_prepare(dims: LinearDims, codes, scales, prepared, stream=None) -> None:
+    """Canonical MXFP4 codes [N, K/2] and scales [N, K/32] into the product's layout."""
+    _check(lib().moe_linear_prepare(ctypes.byref(dims), _ptr(codes), _ptr(scales), _ptr(prepared),
+                                    _nbytes(prepared), _stream(stream)))
+
+
+def moe_linear_workspace_init(dims: LinearDims, ws, stream=None) -> None:
+    _check(lib().moe_linear_workspace_init(ctypes.byref(dims), _ptr(ws), _nbytes(ws),
+                                           _stream(stream)))
+
+
+def moe_linear_forward(dims: LinearDims, prepared, x, out, ws, stream=None) -> None:
+    """out = Q(x) W^T: x bf16 [rows, K], out bf16 or fp32 [rows, N], contiguous rows each."""
+    rows = x.shape[0]
+    ldx = _matrix(x, rows, dims.in_features, _BF16, "x")
+    ldo = _matrix(out, rows, dims.out_features, _OUT, "out")
+    _check(lib().moe_linear_forward(ctypes.byref(dims), _ptr(prepared), _ptr(x), ldx, rows,
+                                    _ptr(out), ldo, int(out.dtype == torch.float32), _ptr(ws),
+                                    _nbytes(ws), _stream(stream)))
+
+
+def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, ws,
+                            stream=None) -> None:
+    """The product on an MXFP8 pair (q [rows, K], sf in MOE_SF_128X4 layout)."""
+    ldo = _matrix(out, rows, dims.out_features, _OUT, "out")
+    _check(lib().moe_linear_forward_pair(ctypes.byref(dims), _ptr(prepared), _ptr(q), _ptr(sf),
+                                         rows, _ptr(out), ldo, int(out.dtype == torch.float32),
+                                         _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_linear_check(ws, stream=None) -> None:
+    _check(lib().moe_linear_check(_ptr(ws), _stream(stream)))
 
 
 def moe_fp4_mma_probe(ws, n: int, blocks_per_sm: int, blocks: int, mma_count: int,

@@ -261,4 +261,66 @@ cudaError_t launch_layer(const LayerLaunch& g, cudaStream_t st);
 bool pair_shape_ok(const Shape& s);
 cudaError_t launch_layer_pair(const LayerLaunch& g, cudaStream_t st);
 
+// ---------------------------------------------------------------------------
+// RMSNorm with the residual's addition and an MXFP8 output (norm.cu).  Strides in
+// elements.  residual, residual_out and y may be null; so may q and sf, together.
+struct RmsnormArgs {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const uint16_t* gamma;
+  uint16_t* residual_out;
+  uint16_t* y;
+  uint8_t* q;
+  uint8_t* sf;
+  int64_t ldx, ldr, ldro, ldy;
+  int64_t rows, sf_rows;     // sf_rows: rows whose scales the kernel writes (zero past rows)
+  int K, layout;
+  float eps;
+};
+cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& a, int64_t rows_cap, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// The MXFP4 linear product (linear.cu).
+struct LinearShape {
+  int N, K;   // output and input features
+  int f8;     // 1: fp8xfp4 (E4M3 activations); 0: mxf4xmxf4
+};
+// K and N as the weights are stored: whole scale blocks, whole 128-row slabs.
+__host__ __device__ __forceinline__ int linear_padded_k(const LinearShape& s) {
+  return (s.K + 127) / 128 * 128;
+}
+__host__ __device__ __forceinline__ int linear_slabs(const LinearShape& s) {
+  return (s.N + 127) / 128;
+}
+__host__ __device__ __forceinline__ int linear_num_kb(const LinearShape& s) {
+  const int kb = s.f8 ? 128 : kBK;
+  return (linear_padded_k(s) + kb - 1) / kb;
+}
+inline int64_t linear_code_bytes(const LinearShape& s) {
+  return (int64_t)linear_slabs(s) * linear_num_kb(s) * kBM * (s.f8 ? 64 : 128);
+}
+inline int64_t linear_scale_bytes(const LinearShape& s) {
+  return (int64_t)linear_slabs(s) * (linear_padded_k(s) / 128) * kSFAtomBytes;
+}
+constexpr int kLinMaxParts = 304;   // slabs x parts when K is split
+struct LinearLaunch {
+  LinearShape shape;
+  const uint8_t* w_codes;    // prepared: codes, then scale blocks
+  const uint8_t* q;          // activation codes [rows, K bytes or K/2]
+  const uint8_t* sf;         // their 128x4 scale blocks
+  int64_t rows;
+  void* out;
+  int64_t ldo;
+  int out_f32;
+  float* partial;
+  int32_t* counters;
+  int32_t* flags;
+  int num_sms;
+};
+cudaError_t launch_linear_prepare(const LinearShape& s, const uint8_t* codes,
+                                  const uint8_t* scales, uint8_t* prep, cudaStream_t st);
+cudaError_t launch_linear_quantize(const LinearShape& s, const void* x, int64_t ldx, int64_t rows,
+                                   uint8_t* q, uint8_t* sf, cudaStream_t st);
+cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st);
+
 }  // namespace mxmoe

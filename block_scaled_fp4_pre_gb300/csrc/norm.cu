@@ -1,0 +1,180 @@
+// Root-mean-square norm with the residual's addition and an MXFP8 output, for sm_103a.
+//
+//   r = x + residual                      (fp32; also stored as bf16)
+//   y = r * gamma / sqrt(mean(r^2) + eps) (fp32; optionally stored as bf16)
+//   q, sf = MXFP8 of y                    (E4M3, one UE8M0 scale per 32 elements)
+//
+// One pass: a row's values stay in registers between the sum of squares and the
+// quantisation, so each input element is read once and each output written once.  y is
+// quantised from its fp32 value, not from the bf16 one, so q carries one rounding.  The
+// sum is fp32 in a fixed order (per thread, then a shuffle tree, then the warps in
+// order): the same input gives the same bits, whatever else runs.
+//
+// Layout: a thread holds V vectors of 8 consecutive elements (16 bytes of bf16), so four
+// lanes hold a scale's 32 elements and reduce its amax with two shuffles, and sixteen
+// lanes a whole scale word (four scales), which is stored as one 32-bit word in either
+// layout.  Bound by HBM at large row counts and by launch and load latency at few.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace mxmoe {
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kWarpRowThreads = 256;   // warp-per-row form: eight rows a block
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  v[0] = lo_bf16(w.x); v[1] = hi_bf16(w.x);
+  v[2] = lo_bf16(w.y); v[3] = hi_bf16(w.y);
+  v[4] = lo_bf16(w.z); v[5] = hi_bf16(w.z);
+  v[6] = lo_bf16(w.w); v[7] = hi_bf16(w.w);
+}
+
+// Two fp32 to packed bf16, round to nearest even, `lo` in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                    bf16x2(v[6], v[7]));
+}
+
+// Byte offset of the scale word (groups 4w..4w+3) of a row.
+__device__ __forceinline__ size_t sf_word(int64_t row, int w, int words, int layout) {
+  return layout == MOE_SF_128X4 ? sf_atom_offset((size_t)row, 4 * w, words)
+                                : ((size_t)row * words + w) * 4;
+}
+
+// WARP_ROW: one warp a row (kWarpRowThreads / 32 rows a block); otherwise one block a row.
+template <int V, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
+    rmsnorm_mxfp8_kernel(const RmsnormArgs a) {
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nt = WARP_ROW ? 32 : (int)blockDim.x;       // threads of a row
+  const int t = WARP_ROW ? lane : (int)threadIdx.x;
+  const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * (kWarpRowThreads / 32) + warp
+                               : (int64_t)blockIdx.x;
+  const int vecs = a.K >> 3, words = a.K >> 7;
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait();
+  if (row >= a.rows) {
+    // rows that pad the last 128-row scale block: zero scales
+    if (row < a.sf_rows)
+      for (int w = t; w < words; w += nt)
+        *reinterpret_cast<uint32_t*>(a.sf + sf_word(row, w, words, a.layout)) = 0u;
+    return;
+  }
+  uint4 xw[V], rw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * nt + t;
+    xw[i] = rw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < vecs) {
+      xw[i] = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + c * 8);
+      if (a.residual)
+        rw[i] = *reinterpret_cast<const uint4*>(a.residual + row * a.ldr + c * 8);
+    }
+  }
+  float r[V][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * nt + t;
+    unpack8(xw[i], r[i]);
+    if (a.residual) {
+      float b[8];
+      unpack8(rw[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[i][j] += b[j];
+    }
+    if (a.residual_out && c < vecs)
+      *reinterpret_cast<uint4*>(a.residual_out + row * a.ldro + c * 8) = pack8(r[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+  if (!WARP_ROW) {
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int w = 0; w < (nt >> 5); ++w) ss += part[w];
+  }
+  const float inv = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * nt + t;
+    const bool live = c < vecs;
+    float y[8], g[8];
+    uint4 gw = make_uint4(0u, 0u, 0u, 0u);
+    if (live) gw = *reinterpret_cast<const uint4*>(a.gamma + c * 8);
+    unpack8(gw, g);
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[j] = r[i][j] * inv * g[j];
+      amax = fmaxf(amax, fabsf(y[j]));
+    }
+    if (a.y && live) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c * 8) = pack8(y);
+    if (a.q) {
+      amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
+      const int e = ptx::mxfp8_exponent(amax);
+      const float m = ptx::pow2_neg(e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= m;
+      if (live) *reinterpret_cast<uint2*>(a.q + row * a.K + c * 8) = ptx::e4m3x8(y);
+      uint32_t w = (uint32_t)(e + 127) << (((lane >> 2) & 3) * 8);
+      w |= __shfl_xor_sync(kAll, w, 4);
+      w |= __shfl_xor_sync(kAll, w, 8);
+      if (live && (lane & 15) == 0)
+        *reinterpret_cast<uint32_t*>(a.sf + sf_word(row, c >> 4, words, a.layout)) = w;
+    }
+  }
+}
+
+template <int V, bool WARP_ROW>
+cudaError_t launch(const RmsnormArgs& a, int threads, cudaStream_t st) {
+  const int64_t rows = a.sf_rows > a.rows ? a.sf_rows : a.rows;
+  const int64_t per = WARP_ROW ? kWarpRowThreads / 32 : 1;
+  return launch_pdl(rmsnorm_mxfp8_kernel<V, WARP_ROW>, dim3((unsigned)((rows + per - 1) / per)),
+                    dim3(WARP_ROW ? kWarpRowThreads : threads), 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& args, int64_t rows_cap, cudaStream_t st) {
+  RmsnormArgs a = args;
+  a.sf_rows = 0;
+  if (a.q) {
+    // Scales past the live rows' last block (4-D layout) or row (packed): one tail.
+    const size_t live = mxfp8_scale_bytes(a.rows, a.K, a.layout);
+    const size_t total = mxfp8_scale_bytes(rows_cap, a.K, a.layout);
+    if (total > live) {
+      cudaError_t e = cudaMemsetAsync(a.sf + live, 0, total - live, st);
+      if (e != cudaSuccess) return e;
+    }
+    if (a.layout == MOE_SF_128X4) a.sf_rows = (a.rows + 127) / 128 * 128;
+  }
+  if (a.rows == 0) return cudaSuccess;
+  const int vecs = a.K / 8;
+  if (vecs <= 32) return launch<1, true>(a, 0, st);
+  if (vecs <= 64) return launch<2, true>(a, 0, st);
+  if (vecs <= 128) return launch<4, true>(a, 0, st);
+  auto threads = [&](int v) { return (vecs + v * 32 - 1) / (v * 32) * 32; };
+  if (vecs <= 512) return launch<1, false>(a, threads(1), st);
+  if (vecs <= 1024) return launch<2, false>(a, threads(2), st);
+  if (vecs <= 2048) return launch<4, false>(a, threads(4), st);
+  return launch<8, false>(a, threads(8), st);
+}
+
+}  // namespace mxmoe

@@ -308,6 +308,84 @@ MXMOE_API moe_status moe_mxfp8_quantize(const void *x, int64_t rows, int64_t K, 
                                         void *sf, int32_t sf_layout, int64_t rows_cap,
                                         void *stream);
 
+/* ---- RMSNorm with the residual's addition and an MXFP8 output ----
+ * What stands between two layers: with r = x + residual (fp32),
+ *   residual_out = bf16(r)
+ *   y            = r * gamma / sqrt(mean(r^2) + eps), fp32; also stored as bf16(y)
+ *   (q, sf)      = the MXFP8 pair of the fp32 y: codes, scales and scale layouts as
+ *                  moe_mxfp8_quantize writes them
+ * in one pass over the row; sums are fp32 in a fixed order.  x, residual, residual_out and
+ * y are bf16 [rows, K] with row strides ldx, ldr, ldro, ldy (elements, multiples of 8, at
+ * least K); gamma is bf16 [K]; q is contiguous.  All device pointers, 16-byte aligned.
+ * residual and residual_out may be NULL (either alone: r = x, or r is not stored), so may
+ * y, and so may q with sf (then sf_layout and rows_cap are not read); at least one output
+ * must be given.  residual_out and y may be x or residual themselves (same stride).
+ * 0 <= rows <= rows_cap <= 2^23, K a multiple of 128 in [128, 65536], eps >= 0.  rows =
+ * 0 only clears the scales.  A row that holds an infinity or a NaN, or whose squares
+ * overflow fp32, spoils its own outputs and no other row's.  MOE_ERR_INVALID_ARG
+ * otherwise.  Stream-ordered, no allocation, no synchronisation. */
+MXMOE_API moe_status moe_rmsnorm_mxfp8(const void *x, int64_t ldx, const void *residual,
+                                       int64_t ldr, const void *gamma, float eps, int64_t rows,
+                                       int64_t K, void *residual_out, int64_t ldro, void *y,
+                                       int64_t ldy, void *q, void *sf, int32_t sf_layout,
+                                       int64_t rows_cap, void *stream);
+
+/* ---- MXFP4 linear product ----
+ * out[m, n] = sum over k of Q(x)[m, k] * W[n, k] with MXFP4 weights W and activations
+ * Q(x) in MXFP4 (MOE_MMA_MXF4xMXF4) or MXFP8 (MOE_MMA_FP8xFP4), each with one UE8M0 scale
+ * per 32 elements of K and rounded as the header's conventions say; products summed in
+ * fp32 on the tensor cores, rounded once.  For the projections and shared experts
+ * around the expert layer.
+ *   out_features N in [1, 2^20], in_features K a multiple of 32 in [32, 65536],
+ *   max_rows in [1, 2^20], mma_type one of the two (NVFP4: MOE_ERR_UNSUPPORTED). */
+typedef struct moe_linear_dims {
+    int32_t out_features;
+    int32_t in_features;
+    int32_t max_rows;
+    int32_t mma_type;
+} moe_linear_dims;
+
+/* Bytes of the prepared weights and of the workspace; 0 for bad dims.  Host only. */
+MXMOE_API size_t moe_linear_weights_size(const moe_linear_dims *dims);
+MXMOE_API size_t moe_linear_workspace_size(const moe_linear_dims *dims);
+
+/* Weight transform: canonical MXFP4 codes_dev [N, K/2] and scales_dev [N, K/32] (as
+ * moe_quantize_mxfp4 writes them) into prepared_dev, 256-byte aligned, of at least
+ * moe_linear_weights_size bytes.  The inputs may be freed once the stream has passed. */
+MXMOE_API moe_status moe_linear_prepare(const moe_linear_dims *dims, const uint8_t *codes_dev,
+                                        const uint8_t *scales_dev, void *prepared_dev,
+                                        size_t prepared_bytes, void *stream);
+
+/* Clears and registers a workspace (256-byte aligned) for these dims, as
+ * moe_workspace_init does for the layer's.  One call at a time may use a workspace: calls
+ * that overlap on the GPU need one each. */
+MXMOE_API moe_status moe_linear_workspace_init(const moe_linear_dims *dims, void *ws_dev,
+                                               size_t ws_bytes, void *stream);
+
+/* The product on bf16 rows x_dev [rows, K] (row stride ldx elements, a multiple of 8 and at
+ * least K; 16-byte aligned; finite), quantised into the workspace first.  out_dev is
+ * [rows, N] with row stride ldo >= N elements, bf16 (MOE_OUT_BF16) or fp32 (MOE_OUT_F32),
+ * aligned to its element.  0 <= rows <= max_rows; 0 rows is a no-op.  prepared_dev must
+ * not be written by a kernel still running when the call's kernels start.  Results do not
+ * depend on timing. */
+enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
+MXMOE_API moe_status moe_linear_forward(const moe_linear_dims *dims, const void *prepared_dev,
+                                        const void *x_dev, int64_t ldx, int64_t rows,
+                                        void *out_dev, int64_t ldo, int32_t out_type, void *ws_dev,
+                                        size_t ws_bytes, void *stream);
+
+/* The product on an MXFP8 pair (MOE_MMA_FP8xFP4 dims with K a multiple of 128): q_dev E4M3
+ * [rows, K] contiguous and sf_dev in MOE_SF_128X4 layout, as moe_rmsnorm_mxfp8 and
+ * moe_mxfp8_quantize write them; both 16-byte aligned. */
+MXMOE_API moe_status moe_linear_forward_pair(const moe_linear_dims *dims, const void *prepared_dev,
+                                             const void *q_dev, const void *sf_dev, int64_t rows,
+                                             void *out_dev, int64_t ldo, int32_t out_type,
+                                             void *ws_dev, size_t ws_bytes, void *stream);
+
+/* Synchronises `stream`, then reads and clears the workspace's error flag:
+ * MOE_ERR_TIMEOUT or MOE_OK. */
+MXMOE_API moe_status moe_linear_check(void *ws_dev, void *stream);
+
 /* FP4 tensor-core throughput probe (measurement only; the denominator of the
  * layer's compute roofline).  Launches `blocks` blocks of 128 threads on `stream`,
  * blocks_per_sm (1 or 2) of them resident per SM, each of which issues mma_count
