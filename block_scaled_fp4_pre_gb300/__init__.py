@@ -91,6 +91,7 @@ def lib() -> ctypes.CDLL:
             "moe_pre_dispatch": ([D, vp, vp, vp, i32, vp, sz, vp], i32),
             "moe_forward": ([D, vp, vp, sz, vp, i32, vp], i32),
             "moe_run_host": ([D, vp, vp, sz, vp, vp, vp, vp, i32, vp], i32),
+            "moe_few_forward": ([D, vp, vp, vp, vp, vp, i32, vp, sz, vp, vp], i32),
             "moe_check": ([vp, vp], i32),
             "moe_read_dispatch": ([D, vp, i32, vp, vp, vp, vp, vp], i32),
             "moe_read_intermediate": ([D, vp, i32, vp, vp], i32),
@@ -225,6 +226,15 @@ def moe_run_host(dims: MoeDims, prepared, ws, x_host, topk_ids_host, topk_weight
     _check(lib().moe_run_host(ctypes.byref(dims), _ptr(prepared), _ptr(ws), _nbytes(ws),
                               _ptr(x_host), _ptr(topk_ids_host), _ptr(topk_weights_host),
                               _ptr(out_host), int(num_tokens), _stream(stream)))
+
+
+def moe_few_forward(dims: MoeDims, prepared, router, x, topk_ids, topk_weights, num_tokens: int,
+                    ws, out, stream=None) -> None:
+    """The whole layer for up to 16 tokens: router (or, with router None, given ids and
+    weights), experts and their weighted sum."""
+    _check(lib().moe_few_forward(ctypes.byref(dims), _ptr(prepared), _ptr(router), _ptr(x),
+                                 _ptr(topk_ids), _ptr(topk_weights), num_tokens, _ptr(ws),
+                                 _nbytes(ws), _ptr(out), _stream(stream)))
 
 
 def moe_check(ws, stream=None) -> None:

@@ -96,6 +96,19 @@ WsLayout ws_layout(const moe_dims& d) {
   L.off_stage_ids = take((size_t)L.A_cap * 4);
   L.off_stage_w = take((size_t)L.A_cap * 4);
   L.off_stage_out = take((size_t)L.T_cap * H * 2);
+  // The few-token form's own regions (moe_few_forward).
+  const int64_t few_t = L.T_cap < kFewTokens ? L.T_cap : kFewTokens;
+  L.few_slots = few_t * k < E ? few_t * k : E;
+  L.off_few_ctrl = take(256);
+  L.off_few_list = take((size_t)L.few_slots * 8);
+  L.off_few_wtab = take((size_t)L.few_slots * kFewTokens * 4);
+  L.off_few_counters = take((size_t)(L.few_slots * (2 * I / kBM) + H / kBM) * 4);
+  L.off_few_logits = take((size_t)kFewTokens * E * 4);
+  L.off_few_xq = take((size_t)kFewTokens * act_row_bytes(d, H));
+  L.off_few_xsf = take((size_t)sf_row_bytes(d, H) * 128);
+  L.off_few_hq = take((size_t)L.few_slots * kFewTokens * act_row_bytes(d, I));
+  L.off_few_hsf = take((size_t)L.few_slots * sf_row_bytes(d, I) * 128);
+  L.off_few_parts = take((size_t)kFewRanges * 4 * kFewTokens * kBM * 4);
   L.total = o;
   return L;
 }
@@ -615,6 +628,71 @@ moe_status moe_run_host(const moe_dims* dims, const void* prepared, void* ws, si
       (e = cudaMemcpyAsync(out_host, b + L.off_stage_out, xbytes, cudaMemcpyDeviceToHost, st)))
     return cuda_fail(e, "output copy");
   if ((e = cudaStreamSynchronize(st))) return cuda_fail(e, "stream synchronize");
+  return MOE_OK;
+}
+
+moe_status moe_few_forward(const moe_dims* dims, const void* prepared, const void* router,
+                           const void* x, int32_t* topk_ids, float* topk_weights, int32_t T,
+                           void* ws, size_t ws_bytes, void* out, void* stream) {
+  moe_status s = check_dims(dims);
+  if (s) return s;
+  if ((s = check_ws(dims, ws, ws_bytes))) return s;
+  if ((s = check_tokens(dims, T))) return s;
+  if (T > kFewTokens)
+    return fail(MOE_ERR_UNSUPPORTED, "num_tokens %d above %d: use moe_pre_dispatch and moe_forward",
+                T, kFewTokens);
+  if (T == 0) return MOE_OK;
+  if (!prepared || !x || !topk_ids || !topk_weights || !out)
+    return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(prepared, 256)) return fail(MOE_ERR_INVALID_ARG, "prepared not 256-byte aligned");
+  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(out, 16) || !aligned(topk_ids, 4) ||
+      !aligned(topk_weights, 4))
+    return fail(MOE_ERR_INVALID_ARG,
+                "x, router and out must be 16-byte, ids and weights 4-byte aligned");
+  const WsLayout L = ws_layout(*dims);
+  const PrepLayout P = prep_layout(*dims);
+  const uint8_t* prep = static_cast<const uint8_t*>(prepared);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  FewLaunch g;
+  g.shape = shape_of(*dims);
+  g.w1_codes = prep + P.off_w1c;
+  g.w2_codes = prep + P.off_w2c;
+  g.slots_cap = L.few_slots;
+  g.num_sms = sm_count();
+  if (g.num_sms <= 0) return fail(MOE_ERR_CUDA, "no CUDA device");
+  FewArgs& a = g.args;
+  a.x = static_cast<const uint16_t*>(x);
+  a.router = static_cast<const uint16_t*>(router);
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.out = static_cast<uint16_t*>(out);
+  a.w1_sf = prep + P.off_w1s;
+  a.w2_sf = prep + P.off_w2s;
+  a.logits = reinterpret_cast<float*>(b + L.off_few_logits);
+  a.xq = b + L.off_few_xq;
+  a.xsf = b + L.off_few_xsf;
+  a.list = reinterpret_cast<int2*>(b + L.off_few_list);
+  a.wtab = reinterpret_cast<float*>(b + L.off_few_wtab);
+  a.hq = b + L.off_few_hq;
+  a.hsf = b + L.off_few_hsf;
+  a.parts0 = reinterpret_cast<float*>(b + L.off_few_parts);
+  a.parts1 = a.parts0 + (size_t)kFewRanges * 2 * kFewTokens * kBM;
+  a.counters = reinterpret_cast<int32_t*>(b + L.off_few_counters);
+  a.counters1 = a.counters + L.few_slots * (2 * dims->inter / kBM);
+  a.ctrl = reinterpret_cast<int32_t*>(b + L.off_few_ctrl);
+  a.flags = ws_ptrs(ws, L).flags;
+  a.T = T;
+  a.H = dims->hidden;
+  a.I = dims->inter;
+  a.E = dims->num_experts;
+  a.k = dims->topk;
+  a.t_rows = 0;   // set at the launch
+  cudaError_t e;
+  {
+    ProfScope ps("few", static_cast<cudaStream_t>(stream));
+    e = launch_few(g, static_cast<cudaStream_t>(stream));
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "few-token layer");
   return MOE_OK;
 }
 

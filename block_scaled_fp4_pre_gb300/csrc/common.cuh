@@ -116,7 +116,10 @@ struct WsLayout {
   size_t off_header, off_flags, off_counts, off_seg, off_tiles, off_tile_done, off_assign,
       off_local_rank, off_blk_base, off_tile_start,
       off_slot_token, off_slot_assign, off_slot_weight, off_xb, off_xsf, off_xq, off_xs, off_hb,
-      off_hsf, off_acc, off_stage_x, off_stage_ids, off_stage_w, off_stage_out, total;
+      off_hsf, off_acc, off_stage_x, off_stage_ids, off_stage_w, off_stage_out, off_few_ctrl,
+      off_few_list, off_few_wtab, off_few_counters, off_few_logits, off_few_xq, off_few_xsf,
+      off_few_hq, off_few_hsf, off_few_parts, total;
+  int64_t few_slots;      // experts the few-token form can touch
 };
 
 struct WsPtrs {
@@ -322,5 +325,43 @@ cudaError_t launch_linear_prepare(const LinearShape& s, const uint8_t* codes,
 cudaError_t launch_linear_quantize(const LinearShape& s, const void* x, int64_t ldx, int64_t rows,
                                    uint8_t* q, uint8_t* sf, cudaStream_t st);
 cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// The whole layer for a few tokens (few.cu).
+constexpr int kFewTokens = 16;     // tokens a call takes: the columns of one MMA
+constexpr int kFewRanges = 304;    // most ranges (blocks) of the expert kernel
+struct FewArgs {
+  const uint16_t* x;         // bf16 [T, H]
+  const uint16_t* router;    // bf16 [E, H], or null: ids and weights are given
+  int32_t* ids;              // [T, k]
+  float* weights;            // [T, k]
+  uint16_t* out;             // bf16 [T, H]
+  const uint8_t* w1_sf;
+  const uint8_t* w2_sf;
+  float* logits;             // [T, E]
+  uint8_t* xq;               // [kFewTokens, H or H/2] and its scale blocks
+  uint8_t* xsf;
+  int2* list;                // [slots] (expert, its tokens as bits), experts ascending
+  float* wtab;               // [slots][kFewTokens] routing weights
+  uint8_t* hq;               // [slots * kFewTokens, I or I/2] and, a slot, its scale blocks
+  uint8_t* hsf;
+  float* parts0;             // [kFewRanges][2][kFewTokens][128] fp32 sums of cut lines
+  float* parts1;
+  int32_t* counters;         // [slots * 2I/128], zero between calls
+  int32_t* counters1;        // [H/128], zero between calls
+  int32_t* ctrl;
+  int32_t* flags;
+  int T, H, I, E, k;
+  int t_rows;                // token rows a TMA box holds: 8 or kFewTokens
+};
+struct FewLaunch {
+  FewArgs args;
+  Shape shape;
+  const uint8_t* w1_codes;
+  const uint8_t* w2_codes;
+  int64_t slots_cap;
+  int num_sms;
+};
+cudaError_t launch_few(const FewLaunch& g, cudaStream_t st);
 
 }  // namespace mxmoe

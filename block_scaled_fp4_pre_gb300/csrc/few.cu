@@ -1,0 +1,856 @@
+// The whole expert layer for a few tokens (up to kFewTokens), router included, in two
+// kernels for sm_103a:
+//
+//   few_route_kernel    logits = x Wr^T (fp32), top-k (ties to the lowest expert), softmax
+//                       over the chosen k; x quantised; the list of touched experts with
+//                       their tokens and weights
+//   few_expert_kernel   gate/up products, SwiGLU, requantisation; down products; the
+//                       weighted sum over the experts; bf16
+//
+// The same arithmetic and rounding points as the layer kernel (gemm.cu), on the same
+// prepared weights.  With few tokens an expert has one or two of them, so the time is the
+// touched experts' weight bytes, and what has to be right is that every SM streams the
+// same number of them without a pause:
+//
+// - Every token is a column of every MMA (N = 16): no bucketing, no gather; an expert's
+//   columns of tokens that did not choose it are not used.  The tensor core takes the
+//   same time for 16 columns as for one.
+// - Work is cut into equal ranges of k-block tiles (one 16 KiB weight box each), one range
+//   a block and phase, whatever the number of experts: a range starts and ends inside a
+//   weight slab.  A slab that spans ranges leaves fp32 sums of each part in the workspace,
+//   and the part that finishes last adds them in the order of the ranges, so the result
+//   does not depend on timing.
+// - Phase 1 (down) runs slab by slab over the experts, so a block adds the experts'
+//   weighted products in registers and leaves one sum per slab it touches.
+// - Blocks claim ranges from a counter, all of phase 0 before any of phase 1, so the wait
+//   for the intermediate rows ends however many blocks are resident; the first stages of
+//   a phase 1 range hold its weights before that wait.
+//
+// Roles (192 threads, two blocks an SM): warp 0 claims and issues the TMA copies, warp 1
+// issues the MMAs, warps 2-5 read the accumulators (four of 16 columns each in flight).
+// Every wait is bounded (kWaitLimitNs); a timeout sets the workspace's error flag.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "tmap.cuh"
+
+namespace mxmoe {
+namespace {
+
+constexpr unsigned kFullW = 0xFFFFFFFFu;
+constexpr int kRouteThreads = 256;
+constexpr int kRouteExperts = 2;          // experts a block: four warps share a row of Wr
+constexpr int kFewThreads = 192;
+constexpr int kFewBlocksPerSM = 2;
+constexpr int kFewN = kFewTokens;         // MMA columns
+constexpr int kFewAccs = 4;
+constexpr int kFewTmemCols = 256;
+constexpr int kFewSfCol = kFewAccs * kFewN;   // two buffers of scale registers
+constexpr int kFewRing = 4;
+
+// ws.ctrl words, all zero between calls but the last
+constexpr int kCtlTicket = 0;    // blocks of the routing kernel done
+constexpr int kCtlClaim = 1;     // next range
+constexpr int kCtlDone = 2;      // intermediate slabs written
+constexpr int kCtlExit = 3;      // blocks of the expert kernel done
+constexpr int kCtlSlots = 4;     // touched experts of the last routing
+
+enum Fmt { kMx4 = 0, kMx8 = 1, kNv4 = 2 };
+
+// ---------------------------------------------------------------------------
+// Routing
+
+__device__ __forceinline__ void bf16x8(const uint4& w, float (&v)[8]) {
+  v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+  v[4] = __uint_as_float(w.z << 16); v[5] = __uint_as_float(w.z & 0xFFFF0000u);
+  v[6] = __uint_as_float(w.w << 16); v[7] = __uint_as_float(w.w & 0xFFFF0000u);
+}
+
+// fp32 as an unsigned key of the same order, at least 1 (0 marks a taken value); -0 as +0.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t b = __float_as_uint(f + 0.0f);
+  const uint32_t k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return k == 0 ? 1u : k;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// One token's top-k by one warp: lane j ends with the j-th expert and its weight.
+// R: logits a lane holds (lane l: experts l, l + 32, ...).
+template <int R>
+__device__ __forceinline__ void top_k(const float* logits, int E, int k, int lane, int& id,
+                                      float& weight) {
+  uint32_t key[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < E ? order_key(__ldcg(logits + e)) : 0u;
+  }
+  uint32_t my_key = 0;
+  id = -1;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(kFullW, best);
+    uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = R - 1; i >= 0; --i)
+      if (key[i] == top) at = i * 32 + lane;
+    const uint32_t win = __reduce_min_sync(kFullW, at);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i * 32 + lane == (int)win) key[i] = 0u;
+    if (lane == j) {
+      id = (int)win;
+      my_key = top;
+    }
+  }
+  const float top = key_value(__shfl_sync(kFullW, my_key, 0));
+  float w = lane < k ? expf(key_value(my_key) - top) : 0.f;
+  float sum = w;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullW, sum, o);
+  weight = w / sum;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const FewArgs a) {
+  __shared__ float part[8][kFewTokens];
+  __shared__ int last;
+  __shared__ uint32_t mask[1024];
+  __shared__ int16_t slot_of[1024];
+  __shared__ int warp_sum[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.T, H = a.H, E = a.E, k = a.k;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();   // after the wait: the expert kernel claims before its own
+  // x quantised: a thread takes 8 elements, four lanes a scale (two for NVFP4)
+  {
+    const int vecs = H / 8, total = T * vecs;
+    for (int i = (int)(blockIdx.x * kRouteThreads) + tid; i - lane < total;
+         i += (int)gridDim.x * kRouteThreads) {
+      const bool live = i < total;
+      const int t = live ? i / vecs : 0, c = live ? i - t * vecs : 0;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (live) w = *reinterpret_cast<const uint4*>(a.x + (size_t)t * H + c * 8);
+      float v[8];
+      bf16x8(w, v);
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+      amax = fmaxf(amax, __shfl_xor_sync(kFullW, amax, 1));
+      if (FMT != kNv4) amax = fmaxf(amax, __shfl_xor_sync(kFullW, amax, 2));
+      uint32_t sb;
+      if (FMT == kNv4) {
+        sb = ptx::nvfp4_scale_byte(amax);
+        const float s = ptx::ue4m3_value(sb);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = s > 0.f ? __fdiv_rn(v[j], s) : copysignf(0.f, v[j]);
+      } else {
+        const int e = FMT == kMx8 ? ptx::mxfp8_exponent(amax) : ptx::mx_scale_exponent(amax);
+        sb = (uint32_t)(e + 127);
+        const float m = ptx::pow2_neg(e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= m;
+      }
+      if (live) {
+        if (FMT == kMx8)
+          *reinterpret_cast<uint2*>(a.xq + (size_t)t * H + c * 8) = ptx::e4m3x8(v);
+        else
+          *reinterpret_cast<uint32_t*>(a.xq + (size_t)t * (H / 2) + c * 4) = ptx::e2m1x8(v);
+        // token t is row t of its scale blocks
+        const int s = FMT == kNv4 ? c >> 1 : c >> 2;
+        if ((c & (FMT == kNv4 ? 1 : 3)) == 0)
+          a.xsf[((size_t)(s >> 2) << 9) + t * 16 + (s & 3)] = (uint8_t)sb;
+      }
+    }
+  }
+  if (a.router) {
+    const int e = (int)blockIdx.x * kRouteExperts + (warp >> 2);
+    float acc[kFewTokens];
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t) acc[t] = 0.f;
+    if (e < E) {
+      const uint16_t* wr = a.router + (size_t)e * H;
+      for (int c = (warp & 3) * 32 + lane; c < H / 8; c += 128) {
+        float w[8];
+        bf16x8(*reinterpret_cast<const uint4*>(wr + c * 8), w);
+#pragma unroll
+        for (int t = 0; t < kFewTokens; ++t) {
+          if (t < T) {
+            float v[8];
+            bf16x8(*reinterpret_cast<const uint4*>(a.x + (size_t)t * H + c * 8), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[t] = fmaf(w[j], v[j], acc[t]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t) {
+      if (t < T) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(kFullW, acc[t], o);
+        if (lane == 0) part[warp][t] = acc[t];
+      }
+    }
+    __syncthreads();
+    if (tid < kRouteExperts * kFewTokens) {
+      const int g = tid / kFewTokens, t = tid % kFewTokens;
+      const int ee = (int)blockIdx.x * kRouteExperts + g;
+      if (t < T && ee < E)
+        a.logits[(size_t)t * E + ee] = (part[4 * g][t] + part[4 * g + 1][t]) +
+                                       (part[4 * g + 2][t] + part[4 * g + 3][t]);
+    }
+  }
+  // The last block to get here routes.
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    last = atomicAdd(&a.ctrl[kCtlTicket], 1) == (int)gridDim.x - 1;
+    if (last) a.ctrl[kCtlTicket] = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int e = tid; e < E; e += kRouteThreads) mask[e] = 0u;
+  __syncthreads();
+  for (int t = warp; t < T; t += 8) {
+    int id = -1;
+    if (a.router) {
+      float w;
+      if (E <= 256)
+        top_k<8>(a.logits + (size_t)t * E, E, k, lane, id, w);
+      else
+        top_k<32>(a.logits + (size_t)t * E, E, k, lane, id, w);
+      if (lane < k) {
+        a.ids[t * k + lane] = id;
+        a.weights[t * k + lane] = w;
+      }
+    } else if (lane < k) {
+      id = a.ids[t * k + lane];
+      if (id < 0 || id >= E) {
+        atomicOr(&a.flags[0], kErrRouting);
+        id = -1;
+      }
+    }
+    if (lane < k && id >= 0) atomicOr(&mask[id], 1u << t);
+  }
+  __syncthreads();
+  // Touched experts in ascending order: four experts a thread.
+  {
+    int mine = 0;
+    for (int j = 0; j < 4; ++j) {
+      const int e = tid * 4 + j;
+      if (e < E && mask[e]) ++mine;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFullW, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int at = incl - mine;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    for (int j = 0; j < 4; ++j) {
+      const int e = tid * 4 + j;
+      if (e < E && mask[e]) {
+        a.list[at] = make_int2(e, (int)mask[e]);
+        slot_of[e] = (int16_t)at;
+#pragma unroll
+        for (int t = 0; t < kFewTokens; t += 4)
+          *reinterpret_cast<float4*>(a.wtab + (size_t)at * kFewTokens + t) =
+              make_float4(0.f, 0.f, 0.f, 0.f);
+        ++at;
+      }
+    }
+    if (tid == kRouteThreads - 1) a.ctrl[kCtlSlots] = at;
+  }
+  __syncthreads();
+  // A token's weights by one thread, in order: an expert named twice gets their sum.
+  if (tid < T) {
+    for (int j = 0; j < k; ++j) {
+      const int id = a.ids[tid * k + j];
+      if (id >= 0 && id < E)
+        a.wtab[(size_t)slot_of[id] * kFewTokens + tid] += a.weights[tid * k + j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Experts
+
+template <int FMT>
+struct FewSmem {
+  static constexpr int kSt = FMT == kNv4 ? 4 : 5;
+  static constexpr size_t kBSlot = (size_t)kFewN * kBKBytes;
+  static constexpr size_t kSF = (size_t)(FMT == kNv4 ? 4 : FMT == kMx8 ? 1 : 2) * kSFAtomBytes;
+  static constexpr size_t kB = (size_t)kSt * kATileBytes;
+  static constexpr size_t kSFA = kB + kSt * kBSlot;
+  static constexpr size_t kSFB = kSFA + kSt * kSF;
+  static constexpr size_t kTail = kSFB + kSt * kSF;
+};
+
+struct __align__(16) FewTail {
+  uint64_t full[5], empty[5];
+  uint64_t acc_full[kFewAccs], acc_empty[kFewAccs];
+  uint64_t ring_full[kFewRing], ring_empty[kFewRing];
+  uint64_t mma_done;
+  int ring[kFewRing];
+  uint32_t tmem_base;
+  int abort;
+  int last;
+  float h[kFewN][68];        // one slab's SwiGLU outputs (64 features, padded rows)
+};
+
+template <int FMT>
+constexpr size_t few_smem_bytes() {
+  return FewSmem<FMT>::kTail + sizeof(FewTail) + 1024;
+}
+static_assert(2 * (few_smem_bytes<kMx4>() + 1024) <= 228 * 1024, "two blocks per SM");
+static_assert(2 * (few_smem_bytes<kMx8>() + 1024) <= 228 * 1024, "two blocks per SM");
+static_assert(2 * (few_smem_bytes<kNv4>() + 1024) <= 228 * 1024, "two blocks per SM");
+
+// Tiles of a phase: `kb` of them a line (an expert's weight slab).  Phase 0 lines are
+// slot * m0 + slab, phase 1 lines slab * slots + slot.  No range is empty but those from
+// `ranges` on, which a phase of fewer tiles than blocks has.
+struct Plan {
+  int64_t n;       // tiles
+  int kb, ranges;
+  __device__ __forceinline__ Plan(int64_t tiles, int kb_line, int blocks)
+      : n(tiles), kb(kb_line), ranges((int)min(tiles, (int64_t)blocks)) {}
+  __device__ __forceinline__ int64_t start(int r) const {
+    return r >= ranges ? n : r * n / ranges;
+  }
+  // the range that holds tile t
+  __device__ __forceinline__ int range_of(int64_t t) const {
+    return (int)(((t + 1) * ranges - 1) / n);
+  }
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
+    few_expert_kernel(const __grid_constant__ CUtensorMap tmap_w1,
+                      const __grid_constant__ CUtensorMap tmap_x,
+                      const __grid_constant__ CUtensorMap tmap_w2,
+                      const __grid_constant__ CUtensorMap tmap_h, const FewArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  using SM = FewSmem<FMT>;
+  constexpr int kSt = SM::kSt;
+  constexpr int kKb = FMT == kMx8 ? 128 : kBK;      // elements a k-block
+  constexpr int kAtomK = FMT == kNv4 ? 64 : 128;    // elements a scale block
+  FewTail* tail = reinterpret_cast<FewTail*>(smem + SM::kTail);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = a.T;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      ptx::mbar_init(&tail->full[s], 1);
+      ptx::mbar_init(&tail->empty[s], 1);
+    }
+    for (int s = 0; s < kFewAccs; ++s) {
+      ptx::mbar_init(&tail->acc_full[s], 1);
+      ptx::mbar_init(&tail->acc_empty[s], 128);
+    }
+    for (int s = 0; s < kFewRing; ++s) {
+      ptx::mbar_init(&tail->ring_full[s], 1);
+      ptx::mbar_init(&tail->ring_empty[s], 5);   // the MMA thread + 4 epilogue warps
+    }
+    ptx::mbar_init(&tail->mma_done, 1);
+    tail->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmap_w1);
+    ptx::prefetch_tmap(&tmap_x);
+    ptx::prefetch_tmap(&tmap_w2);
+    ptx::prefetch_tmap(&tmap_h);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&tail->tmem_base, kFewTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = tail->tmem_base;
+  volatile int* abort_flag = &tail->abort;
+  const int ranges = (int)gridDim.x;
+  // The first claim overlaps the routing kernel: that one started after the call before
+  // this one had reset the counter.
+  int claim = 0;
+  if (threadIdx.x == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait();
+
+  const int slots = a.ctrl[kCtlSlots];
+  const int m0 = 2 * a.I / kBM, m1 = a.H / kBM;
+  const int kb0 = (a.H + kKb - 1) / kKb, kb1 = (a.I + kKb - 1) / kKb;
+  const Plan P0((int64_t)slots * m0 * kb0, kb0, ranges);
+  const Plan P1((int64_t)slots * m1 * kb1, kb1, ranges);
+
+  if (slots == 0) {
+    // no valid assignment: zeros
+    for (int64_t i = (int64_t)blockIdx.x * kFewThreads + threadIdx.x; i < (int64_t)T * a.H;
+         i += (int64_t)gridDim.x * kFewThreads)
+      a.out[i] = 0;
+  } else if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_w = ptx::policy_evict_first();
+      const uint64_t pol_t = ptx::policy_evict_last();
+      int stage = 0, r = 0;
+      uint32_t phase = 0, rph = 0;
+      int64_t issued = 0;
+      bool ok = true, waited = false;
+      while (true) {
+        const int idx = claim < 2 * ranges ? claim : -1;
+        ok = ptx::mbar_wait(&tail->ring_empty[r], rph ^ 1u, abort_flag, kWaitLimitNs);
+        if (!ok) break;
+        tail->ring[r] = idx;
+        ptx::mbar_arrive(&tail->ring_full[r]);
+        if (++r == kFewRing) {
+          r = 0;
+          rph ^= 1u;
+        }
+        if (idx < 0) break;
+        claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
+        const bool down = idx >= ranges;
+        const Plan& P = down ? P1 : P0;
+        const int rg = down ? idx - ranges : idx;
+        const int64_t t0 = P.start(rg), t1 = P.start(rg + 1);
+        const CUtensorMap* tw = down ? &tmap_w2 : &tmap_w1;
+        const CUtensorMap* tt = down ? &tmap_h : &tmap_x;
+        const uint8_t* wsf0 = down ? a.w2_sf : a.w1_sf;
+        const uint8_t* tsf0 = down ? a.hsf : a.xsf;
+        const int K = down ? a.I : a.H, kc = K / kAtomK;
+        // The token side of tile t, into stage s: x's rows, or the expert's rows of h.
+        auto tokens = [&](int64_t t, int s) {
+          const int64_t line = t / P.kb;
+          const int kb = (int)(t - line * P.kb);
+          const int slot = down ? (int)(line % slots) : 0;
+          const int atoms = min(kKb, K - kb * kKb) / kAtomK;
+          ptx::tma_load_2d(smem + SM::kB + (size_t)s * SM::kBSlot, tt, kb * kBKBytes,
+                           slot * kFewN, &tail->full[s], pol_t);
+          ptx::bulk_load(smem + SM::kSFB + (size_t)s * SM::kSF,
+                         tsf0 + ((size_t)slot * kc + (size_t)kb * (kKb / kAtomK)) * kSFAtomBytes,
+                         atoms * kSFAtomBytes, &tail->full[s], pol_t);
+        };
+        int64_t held = t0;          // tiles [held, t) have their weights only
+        int held_stage = stage;
+        int64_t cur_line = -1;
+        int wslab = 0;
+        for (int64_t t = t0; t < t1; ++t) {
+          const int64_t line = t / P.kb;
+          const int kb = (int)(t - line * P.kb);
+          if (line != cur_line) {
+            cur_line = line;
+            const int slot = (int)(down ? line % slots : line / m0);
+            const int slab = (int)(down ? line / slots : line % m0);
+            wslab = a.list[slot].x * (down ? m1 : m0) + slab;
+          }
+          if (down && !waited && t - t0 == kSt) {
+            // every stage holds weights of this range: its intermediate rows next
+            ok = ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag, kWaitLimitNs);
+            if (!ok) break;
+            ptx::fence_proxy_async_global();
+            waited = true;
+            for (; held < t; ++held) {
+              tokens(held, held_stage);
+              if (++held_stage == kSt) held_stage = 0;
+            }
+          }
+          ok = ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
+          if (!ok) break;
+          const int atoms = min(kKb, K - kb * kKb) / kAtomK;
+          uint64_t* bar = &tail->full[stage];
+          // a widened E2M1 box counts its packed bytes only
+          ptx::mbar_arrive_expect_tx(
+              bar, (uint32_t)((FMT == kMx8 ? kATileBytes / 2 : kATileBytes) +
+                              a.t_rows * kBKBytes + 2 * atoms * kSFAtomBytes));
+          ptx::tma_load_2d(smem + (size_t)stage * kATileBytes, tw, 0, (wslab * P.kb + kb) * kBM,
+                           bar, pol_w);
+          ptx::bulk_load(smem + SM::kSFA + (size_t)stage * SM::kSF,
+                         wsf0 + ((size_t)wslab * kc + (size_t)kb * (kKb / kAtomK)) * kSFAtomBytes,
+                         atoms * kSFAtomBytes, bar, pol_w);
+          if (!down || waited) tokens(t, stage);
+          ++issued;
+          if (++stage == kSt) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok && down && !waited && t1 > t0) {   // a range shorter than the stages
+          ok = ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag, kWaitLimitNs);
+          if (ok) {
+            ptx::fence_proxy_async_global();
+            waited = true;
+          }
+          for (; ok && held < t1; ++held) {
+            tokens(held, held_stage);
+            if (++held_stage == kSt) held_stage = 0;
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) atomicOr(&a.flags[0], kErrTimeout);
+      // Every copy issued here must have landed before the block exits.  (After a timeout
+      // some stages may lack their token side: their waits run out.)
+      const int64_t first = issued > kSt ? issued - kSt : 0;
+      for (int64_t i = first; i < issued; ++i) {
+        int never = 0;
+        ptx::mbar_wait(&tail->full[i % kSt], (uint32_t)((i / kSt) & 1), &never,
+                       ok ? kWaitLimitNs : kWaitLimitNs / 16);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
+      const uint64_t db0 = ptx::desc_sw128(ptx::smem_addr(smem + SM::kB));
+      const uint64_t dsa0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFA));
+      const uint64_t dsb0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFB));
+      const uint32_t id0 = ptx::idesc_mxf4(kFewN, 0), id2 = ptx::idesc_mxf4(kFewN, 2);
+      const uint32_t idn = ptx::idesc_nvf4(kFewN);
+      constexpr uint32_t kSfCols = FMT == kNv4 ? 16 : 8;
+      int stage = 0, r = 0, acc = 0;
+      uint32_t phase = 0, rph = 0, acc_phase = 0, sfbuf = 0;
+      bool ok = true;
+      while (ok) {
+        ok = ptx::mbar_wait(&tail->ring_full[r], rph, abort_flag, kWaitLimitNs);
+        if (!ok) break;
+        const int idx = tail->ring[r];
+        ptx::mbar_arrive(&tail->ring_empty[r]);
+        if (++r == kFewRing) {
+          r = 0;
+          rph ^= 1u;
+        }
+        if (idx < 0) break;
+        const bool down = idx >= ranges;
+        const Plan& P = down ? P1 : P0;
+        const int rg = down ? idx - ranges : idx;
+        const int64_t t1 = P.start(rg + 1);
+        const int K = down ? a.I : a.H;
+        for (int64_t t = P.start(rg); t < t1 && ok;) {
+          const int kbs = (int)(t % P.kb);
+          const int kbe = (int)min((int64_t)P.kb, kbs + (t1 - t));
+          t += kbe - kbs;
+          ok = ptx::mbar_wait(&tail->acc_empty[acc], acc_phase ^ 1u, abort_flag, kWaitLimitNs);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t d = tmem_base + (uint32_t)(acc * kFewN);
+          for (int kb = kbs; kb < kbe; ++kb) {
+            ok = ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t sfa = tmem_base + (uint32_t)kFewSfCol + (sfbuf ? 2 * kSfCols : 0u);
+            const uint32_t sfb = sfa + kSfCols;
+            const uint64_t dsa = dsa0 + (uint64_t)(stage * (int)(SM::kSF >> 4));
+            const uint64_t dsb = dsb0 + (uint64_t)(stage * (int)(SM::kSF >> 4));
+            const uint64_t da = da0 + (uint64_t)(stage * (kATileBytes >> 4));
+            const uint64_t db = db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4));
+            const uint32_t on = kb != kbs ? 1u : 0u;
+            const bool whole = K - kb * kKb >= kKb;   // a last k-block may be half wide
+            if constexpr (FMT == kMx8) {
+              ptx::tc_cp_sf(sfa, dsa);
+              ptx::tc_cp_sf(sfb, dsb);
+              ptx::tc_mma_f8f4(d, da, db, ptx::idesc_f8f4(kFewN, 0), sfa, sfb, on);
+              ptx::tc_mma_f8f4(d, da + 2, db + 2, ptx::idesc_f8f4(kFewN, 1), sfa, sfb, 1u);
+              ptx::tc_mma_f8f4(d, da + 4, db + 4, ptx::idesc_f8f4(kFewN, 2), sfa, sfb, 1u);
+              ptx::tc_mma_f8f4(d, da + 6, db + 6, ptx::idesc_f8f4(kFewN, 3), sfa, sfb, 1u);
+            } else if constexpr (FMT == kNv4) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                if (s < 2 || whole) {
+                  ptx::tc_cp_sf(sfa + s * 4, dsa + 32 * s);
+                  ptx::tc_cp_sf(sfb + s * 4, dsb + 32 * s);
+                }
+              }
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                if (s < 2 || whole)
+                  ptx::tc_mma_nvf4(d, da + 2 * s, db + 2 * s, idn, sfa + s * 4, sfb + s * 4,
+                                   s == 0 ? on : 1u);
+            } else {
+              ptx::tc_cp_sf(sfa, dsa);
+              ptx::tc_cp_sf(sfb, dsb);
+              if (whole) {
+                ptx::tc_cp_sf(sfa + 4, dsa + 32);
+                ptx::tc_cp_sf(sfb + 4, dsb + 32);
+              }
+              ptx::tc_mma_mxf4(d, da, db, id0, sfa, sfb, on);
+              ptx::tc_mma_mxf4(d, da + 2, db + 2, id2, sfa, sfb, 1u);
+              if (whole) {
+                ptx::tc_mma_mxf4(d, da + 4, db + 4, id0, sfa + 4, sfb + 4, 1u);
+                ptx::tc_mma_mxf4(d, da + 6, db + 6, id2, sfa + 4, sfb + 4, 1u);
+              }
+            }
+            ptx::tc_commit(&tail->empty[stage]);
+            sfbuf ^= 1u;
+            if (++stage == kSt) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          ptx::tc_commit(&tail->acc_full[acc]);
+          if (++acc == kFewAccs) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) atomicOr(&a.flags[0], kErrTimeout);
+      // every MMA issued here has finished before the block frees its tensor memory
+      ptx::tc_commit(&tail->mma_done);
+      int never = 0;
+      ptx::mbar_wait(&tail->mma_done, 0, &never, kWaitLimitNs);
+    }
+  } else {
+    const int q = warp & 3, ep = (int)threadIdx.x - 64, row = q * 32 + lane;
+    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
+    int r = 0, acc = 0;
+    uint32_t rph = 0, acc_phase = 0;
+    bool ok = true;
+    // Waits for the next accumulator and reads it.  Should the wait run out, all four
+    // warps agree on it: they meet at named barriers further on.
+    auto take = [&](float (&v)[kFewN]) {
+      const bool got =
+          ptx::mbar_wait(&tail->acc_full[acc], acc_phase, abort_flag, kWaitLimitNs);
+      if (!ptx::named_bar_and(2, 128, got)) return false;
+      ptx::tc_fence_after();
+      ptx::tmem_ld16(taddr + (uint32_t)(acc * kFewN), v);
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&tail->acc_empty[acc]);
+      if (++acc == kFewAccs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+      return true;
+    };
+    // Adds the parts of tiles [lo, hi), which span ranges first..last, of which this block
+    // has range rg's in v.  Returns false in every part but the last one to finish.
+    auto join = [&](float (&v)[kFewN], const Plan& P, float* parts, int32_t* counter, int rg,
+                    int64_t lo, int64_t hi) {
+      const int first = P.range_of(lo), last = P.range_of(hi - 1);
+      if (first == last) return true;
+      // a range's first line is its piece 0, a later one (its last) piece 1
+      auto piece = [&](int rr) {
+        return parts + ((size_t)rr * 2 + (P.start(rr) >= lo ? 0 : 1)) * (kFewN * kBM) + row;
+      };
+      float* mine = piece(rg);
+#pragma unroll
+      for (int t = 0; t < kFewN; ++t)
+        if (t < T) __stcg(mine + t * kBM, v[t]);
+      ptx::named_bar_sync(1, 128);
+      if (ep == 0) {
+        __threadfence();
+        tail->last = atomicAdd(counter, 1) == last - first;
+        if (tail->last) *counter = 0;
+        __threadfence();
+      }
+      ptx::named_bar_sync(1, 128);
+      const bool mine_last = tail->last != 0;
+      if (!mine_last) return false;
+#pragma unroll
+      for (int t = 0; t < kFewN; ++t) v[t] = 0.f;
+      for (int rr = first; rr <= last; ++rr) {
+        const float* p = piece(rr);
+#pragma unroll
+        for (int t = 0; t < kFewN; ++t)
+          if (t < T) v[t] += __ldcg(p + t * kBM);
+      }
+      return true;
+    };
+    while (ok) {
+      ok = ptx::named_bar_and(
+          2, 128, ptx::mbar_wait(&tail->ring_full[r], rph, abort_flag, kWaitLimitNs));
+      if (!ok) break;
+      const int idx = tail->ring[r];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&tail->ring_empty[r]);
+      if (++r == kFewRing) {
+        r = 0;
+        rph ^= 1u;
+      }
+      if (idx < 0) break;
+      float v[kFewN];
+      if (idx < ranges) {
+        // ---- gate/up: sums, SwiGLU, requantisation
+        const int rg = idx;
+        const int64_t t1 = P0.start(rg + 1);
+        for (int64_t t = P0.start(rg); t < t1;) {
+          const int64_t line = t / kb0, lo = line * kb0, hi = lo + kb0;
+          t = min(hi, t1);
+          const int slot = (int)(line / m0), slab = (int)(line % m0);
+          const uint32_t chosen = (uint32_t)a.list[slot].y;
+          if (!(ok = take(v))) break;
+          if (!join(v, P0, a.parts0, a.counters + line, rg, lo, hi)) continue;
+          // Rows of this warp: [gate 8 | up 8 | gate 8 | up 8], so lane l and l ^ 8 hold
+          // one feature's gate and up: gate lanes take the even columns, up lanes the odd.
+          const bool up = (lane & 8) != 0;
+          const int f = q * 16 + (FMT == kMx8 ? (lane & 7) + ((lane >> 4) << 3)
+                                              : (lane & 7) * 2 + (lane >> 4));
+#pragma unroll
+          for (int p = 0; p < kFewN / 2; ++p) {
+            const float x = __shfl_xor_sync(kFullW, up ? v[2 * p] : v[2 * p + 1], 8);
+            const float g = up ? x : v[2 * p], u = up ? v[2 * p + 1] : x;
+            tail->h[2 * p + (up ? 1 : 0)][f] = __fdividef(g, 1.0f + __expf(-g)) * u;
+          }
+          ptx::named_bar_sync(1, 128);
+          // 16 columns x 64 features: eight threads a column, eight features each
+          const int c = ep >> 3, piece = ep & 7;
+          float hv[8], amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            hv[j] = tail->h[c][piece * 8 + j];
+            amax = fmaxf(amax, fabsf(hv[j]));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(kFullW, amax, 1));
+          if (FMT != kNv4) amax = fmaxf(amax, __shfl_xor_sync(kFullW, amax, 2));
+          uint32_t sb;
+          if (FMT == kNv4) {
+            sb = ptx::nvfp4_scale_byte(amax);
+            const float s = ptx::ue4m3_value(sb);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              hv[j] = s > 0.f ? __fdiv_rn(hv[j], s) : copysignf(0.f, hv[j]);
+          } else {
+            const int e = FMT == kMx8 ? ptx::mxfp8_exponent(amax) : ptx::mx_scale_exponent(amax);
+            sb = (uint32_t)(e + 127);
+            const float m = ptx::pow2_neg(e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) hv[j] *= m;
+          }
+          if ((chosen >> c) & 1u) {
+            const size_t hrow = (size_t)slot * kFewN + c;
+            if (FMT == kMx8)
+              *reinterpret_cast<uint2*>(a.hq + hrow * a.I + (size_t)slab * 64 + piece * 8) =
+                  ptx::e4m3x8(hv);
+            else
+              *reinterpret_cast<uint32_t*>(a.hq + hrow * (a.I / 2) + (size_t)slab * 32 +
+                                           piece * 4) = ptx::e2m1x8(hv);
+            const int s = FMT == kNv4 ? slab * 4 + (piece >> 1) : slab * 2 + (piece >> 2);
+            if ((piece & (FMT == kNv4 ? 1 : 3)) == 0)
+              a.hsf[(((size_t)slot * (a.I / kAtomK) + (s >> 2)) << 9) + c * 16 + (s & 3)] =
+                  (uint8_t)sb;
+          }
+          ptx::named_bar_sync(1, 128);   // all stored; the buffer is free again
+          if (ep == 0) {
+            __threadfence();
+            ptx::fence_proxy_async_global();
+            atomicAdd(&a.ctrl[kCtlDone], 1);
+          }
+        }
+      } else {
+        // ---- down: the experts' products, weighted, summed slab by slab
+        const int rg = idx - ranges;
+        const int64_t t1 = P1.start(rg + 1);
+        float sum[kFewN];
+#pragma unroll
+        for (int t = 0; t < kFewN; ++t) sum[t] = 0.f;
+        const int64_t span = (int64_t)slots * kb1;   // tiles of one output slab
+        for (int64_t t = P1.start(rg); t < t1;) {
+          const int64_t line = t / kb1;
+          t = min((line + 1) * kb1, t1);
+          const int slot = (int)(line % slots), slab = (int)(line / slots);
+          const uint32_t chosen = (uint32_t)a.list[slot].y;
+          float w[kFewN];
+#pragma unroll
+          for (int c = 0; c < kFewN; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(a.wtab + (size_t)slot * kFewN + c);
+            w[c] = f.x; w[c + 1] = f.y; w[c + 2] = f.z; w[c + 3] = f.w;
+          }
+          if (!(ok = take(v))) break;
+          // columns of other tokens hold anything, NaN too: skipped, not multiplied by 0
+#pragma unroll
+          for (int c = 0; c < kFewN; ++c)
+            if ((chosen >> c) & 1u) sum[c] = fmaf(w[c], v[c], sum[c]);
+          if (t == t1 || t == (slab + 1) * span) {
+            if (join(sum, P1, a.parts1, a.counters1 + slab, rg, slab * span, (slab + 1) * span)) {
+              const int n = slab * kBM + row;
+#pragma unroll
+              for (int c = 0; c < kFewN; ++c)
+                if (c < T)
+                  a.out[(size_t)c * a.H + n] = __bfloat16_as_ushort(__float2bfloat16(sum[c]));
+            }
+#pragma unroll
+            for (int c = 0; c < kFewN; ++c) sum[c] = 0.f;
+          }
+        }
+      }
+    }
+    if (!ok && ep == 0) atomicOr(&a.flags[0], kErrTimeout);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, kFewTmemCols);
+  }
+  if (threadIdx.x == 0) {
+    // the last block out resets the counters for the next call
+    __threadfence();
+    if (atomicAdd(&a.ctrl[kCtlExit], 1) == (int)gridDim.x - 1) {
+      a.ctrl[kCtlClaim] = 0;
+      a.ctrl[kCtlDone] = 0;
+      a.ctrl[kCtlExit] = 0;
+      __threadfence();
+    }
+  }
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
+  constexpr size_t kBytes = few_smem_bytes<FMT>();
+  static bool set = false;
+  if (!set) {
+    cudaError_t e = cudaFuncSetAttribute(few_expert_kernel<FMT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
+  FewArgs a = g.args;
+  const Shape& s = g.shape;
+  constexpr bool f8 = FMT == kMx8;
+  const uint64_t w1_rows = (uint64_t)s.E * 2 * s.I * weight_num_kb(s, s.H);
+  const uint64_t w2_rows = (uint64_t)s.E * s.H * weight_num_kb(s, s.I);
+  if (w1_rows > 0x7FFFFFFFull || w2_rows > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  a.t_rows = a.T <= 8 ? 8 : kFewN;
+  CUtensorMap m1, mx, m2, mh;
+  cudaError_t e;
+  if (f8) {
+    if ((e = make_tmap_e2m1_wide(&m1, g.w1_codes, 128, w1_rows)) ||
+        (e = make_tmap_e2m1_wide(&m2, g.w2_codes, 128, w2_rows)))
+      return e;
+  } else if ((e = make_tmap(&m1, g.w1_codes, kBKBytes, w1_rows, kBM)) ||
+             (e = make_tmap(&m2, g.w2_codes, kBKBytes, w2_rows, kBM))) {
+    return e;
+  }
+  if ((e = make_tmap(&mx, a.xq, f8 ? s.H : s.H / 2, kFewN, a.t_rows)) ||
+      (e = make_tmap(&mh, a.hq, f8 ? s.I : s.I / 2, (uint64_t)g.slots_cap * kFewN, a.t_rows)))
+    return e;
+  int blocks = a.router ? (s.E + kRouteExperts - 1) / kRouteExperts
+                        : (a.T * (s.H / 8) + kRouteThreads - 1) / kRouteThreads;
+  e = launch_pdl(few_route_kernel<FMT>, dim3(blocks), dim3(kRouteThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  int grid = kFewBlocksPerSM * g.num_sms;
+  if (grid > kFewRanges) grid = kFewRanges;
+  return launch_pdl(few_expert_kernel<FMT>, dim3(grid), dim3(kFewThreads), kBytes, st, m1, mx, m2,
+                    mh, a);
+}
+
+}  // namespace
+
+cudaError_t launch_few(const FewLaunch& g, cudaStream_t st) {
+  if (g.shape.f8) return launch_fmt<kMx8>(g, st);
+  if (g.shape.nv) return launch_fmt<kNv4>(g, st);
+  return launch_fmt<kMx4>(g, st);
+}
+
+}  // namespace mxmoe

@@ -325,7 +325,10 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
     uint32_t acc_phase = 0;
     for (int g = blockIdx.x; g < total; g += gridDim.x) {
       const LinItem it = lin_item(a, g);
-      if (!ptx::mbar_wait(&tail->acc_full, acc_phase, abort_flag, kWaitLimitNs)) {
+      bool ok = ptx::mbar_wait(&tail->acc_full, acc_phase, abort_flag, kWaitLimitNs);
+      // the warps of a split item meet at named barriers further on: all stop or none
+      if (a.split > 1) ok = ptx::named_bar_and(2, 128, ok);
+      if (!ok) {
         if (ep_tid == 0) atomicOr(&a.flags[0], kErrTimeout);
         break;
       }

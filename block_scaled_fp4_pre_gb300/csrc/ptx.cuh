@@ -364,6 +364,20 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same barrier, returning whether `pred` holds in every one of its threads.
+__device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
 // ---- CTA pairs (2-CTA clusters, tcgen05 cta_group::2) -------------------------
 // A pair's leader (rank 0) issues the MMAs; each MMA spans both CTAs' shared memory
 // (A: 128 rows each, B: N/2 rows each, at the same offsets) and writes each CTA's

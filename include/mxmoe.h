@@ -238,6 +238,32 @@ MXMOE_API moe_status moe_run_host(const moe_dims *dims, const void *prepared_dev
                                   const int32_t *topk_ids_host, const float *topk_weights_host,
                                   void *out_host, int32_t num_tokens, void *stream);
 
+/* The whole layer for a few tokens, router included, in two kernels: the decode step of
+ * one user or of a few, or of drafted tokens.
+ *   router_dev       bf16 [E, H], or NULL
+ *   x_dev            bf16 [num_tokens, H], finite values
+ *   topk_ids_dev     int32 [num_tokens, k]   written with a router, read without
+ *   topk_weights_dev fp32 [num_tokens, k]    the same
+ *   out_dev          bf16 [num_tokens, H]
+ *   num_tokens       0 .. min(16, dims->max_tokens); above 16: MOE_ERR_UNSUPPORTED (use
+ *                    moe_pre_dispatch and moe_forward); 0 is a no-op
+ * With a router: logits = x router^T in fp32, each token's k largest in descending order
+ * (equal logits: the lower expert first), and the softmax over those k as weights.
+ * Without: ids and weights are used as moe_pre_dispatch uses them (ids outside [0, E) are
+ * skipped and raise MOE_ERR_ROUTING at the next moe_check).  Then the layer as moe_forward
+ * computes it, on the same prepared weights and with the same rounding of x and of the
+ * intermediate, every mma_type; sums are fp32 in an order that does not depend on timing,
+ * so the same call gives the same bits.  A token without a valid id gives zeros.
+ * Uses regions of the workspace of its own: a moe_pre_dispatch made before it can still be
+ * followed by its moe_forward.  One call at a time may use a workspace.  After
+ * MOE_ERR_TIMEOUT initialise the workspace again.  x_dev, router_dev and out_dev 16-byte
+ * aligned; prepared_dev must not be written by a kernel still running. */
+MXMOE_API moe_status moe_few_forward(const moe_dims *dims, const void *prepared_dev,
+                                     const void *router_dev, const void *x_dev,
+                                     int32_t *topk_ids_dev, float *topk_weights_dev,
+                                     int32_t num_tokens, void *ws_dev, size_t ws_bytes,
+                                     void *out_dev, void *stream);
+
 /* Synchronises `stream`, then reads and clears the workspace's device error
  * flags: MOE_ERR_ROUTING, MOE_ERR_TIMEOUT, or MOE_OK. */
 MXMOE_API moe_status moe_check(void *ws_dev, void *stream);
