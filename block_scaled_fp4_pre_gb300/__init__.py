@@ -163,7 +163,8 @@ def _nbytes(t) -> int:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -312,14 +313,14 @@ def moe_mxfp8_quantize(x, rows: int, K: int, q, sf, layout: int, rows_cap: int |
                                     int(rows if rows_cap is None else rows_cap), _stream(stream)))
 
 
-def _matrix(t, rows: int, cols: int, dtypes, name: str) -> int:
-    """Row stride of a [rows, cols] tensor of one of the dtypes with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype not in dtypes:
-        raise ValueError(f"{name}: need [{rows}, {cols}] of {dtypes}, got {tuple(t.shape)} "
-                         f"of {t.dtype}")
-    if cols > 1 and t.stride(1) != 1:
+def _matrix(t, shape, dtypes, name: str) -> int:
+    """Row stride of a 2-D tensor of this shape and one of the dtypes, its rows contiguous."""
+    if t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{name}: need {list(shape)} of {dtypes}, got {list(t.shape)} of {t.dtype}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+    return ld if shape[0] > 1 else max(ld, shape[1])
 
 
 _BF16 = (torch.bfloat16,)
@@ -333,11 +334,12 @@ def moe_rmsnorm_mxfp8(x, gamma, eps: float, q=None, sf=None, layout: int = MOE_S
 
     x, residual, residual_out and y are bf16 [rows, K] tensors with contiguous rows; q and sf
     as moe_mxfp8_quantize writes them.  Any output may be left out."""
-    rows, K = x.shape
-    ldx = _matrix(x, rows, K, _BF16, "x")
-    ldr = 0 if residual is None else _matrix(residual, rows, K, _BF16, "residual")
-    ldro = 0 if residual_out is None else _matrix(residual_out, rows, K, _BF16, "residual_out")
-    ldy = 0 if y is None else _matrix(y, rows, K, _BF16, "y")
+    shape = x.shape
+    rows, K = shape
+    ldx = _matrix(x, shape, _BF16, "x")
+    ldr = 0 if residual is None else _matrix(residual, shape, _BF16, "residual")
+    ldro = 0 if residual_out is None else _matrix(residual_out, shape, _BF16, "residual_out")
+    ldy = 0 if y is None else _matrix(y, shape, _BF16, "y")
     if gamma.dtype != torch.bfloat16 or gamma.shape != (K,) or not gamma.is_contiguous():
         raise ValueError(f"gamma: need contiguous bf16 [{K}]")
     _check(lib().moe_rmsnorm_mxfp8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(gamma), eps, rows, K,
@@ -368,8 +370,8 @@ def moe_linear_workspace_init(dims: LinearDims, ws, stream=None) -> None:
 def moe_linear_forward(dims: LinearDims, prepared, x, out, ws, stream=None) -> None:
     """out = Q(x) W^T: x bf16 [rows, K], out bf16 or fp32 [rows, N], contiguous rows each."""
     rows = x.shape[0]
-    ldx = _matrix(x, rows, dims.in_features, _BF16, "x")
-    ldo = _matrix(out, rows, dims.out_features, _OUT, "out")
+    ldx = _matrix(x, (rows, dims.in_features), _BF16, "x")
+    ldo = _matrix(out, (rows, dims.out_features), _OUT, "out")
     _check(lib().moe_linear_forward(ctypes.byref(dims), _ptr(prepared), _ptr(x), ldx, rows,
                                     _ptr(out), ldo, int(out.dtype == torch.float32), _ptr(ws),
                                     _nbytes(ws), _stream(stream)))
@@ -378,7 +380,7 @@ def moe_linear_forward(dims: LinearDims, prepared, x, out, ws, stream=None) -> N
 def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, ws,
                             stream=None) -> None:
     """The product on an MXFP8 pair (q [rows, K], sf in MOE_SF_128X4 layout)."""
-    ldo = _matrix(out, rows, dims.out_features, _OUT, "out")
+    ldo = _matrix(out, (rows, dims.out_features), _OUT, "out")
     _check(lib().moe_linear_forward_pair(ctypes.byref(dims), _ptr(prepared), _ptr(q), _ptr(sf),
                                          rows, _ptr(out), ldo, int(out.dtype == torch.float32),
                                          _ptr(ws), _nbytes(ws), _stream(stream)))

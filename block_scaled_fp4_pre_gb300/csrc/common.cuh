@@ -279,6 +279,7 @@ struct RmsnormArgs {
   int64_t rows, sf_rows;     // sf_rows: rows whose scales the kernel writes (zero past rows)
   int K, layout;
   float eps;
+  float inv_k, inv_k_lo;     // 1 / K as two floats (set at the launch)
 };
 cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& a, int64_t rows_cap, cudaStream_t st);
 
@@ -305,18 +306,18 @@ inline int64_t linear_code_bytes(const LinearShape& s) {
 inline int64_t linear_scale_bytes(const LinearShape& s) {
   return (int64_t)linear_slabs(s) * (linear_padded_k(s) / 128) * kSFAtomBytes;
 }
-constexpr int kLinMaxParts = 304;   // slabs x parts when K is split
+constexpr int kLinFusedRows = 32;   // bf16 rows up to which the product quantises itself
 struct LinearLaunch {
   LinearShape shape;
   const uint8_t* w_codes;    // prepared: codes, then scale blocks
-  const uint8_t* q;          // activation codes [rows, K bytes or K/2]
+  const uint8_t* q;          // activation codes [rows, K bytes or K/2], or null: from x
   const uint8_t* sf;         // their 128x4 scale blocks
+  const void* x;             // bf16 rows, at most kLinFusedRows (q null)
+  int64_t ldx;
   int64_t rows;
   void* out;
   int64_t ldo;
   int out_f32;
-  float* partial;
-  int32_t* counters;
   int32_t* flags;
   int num_sms;
 };

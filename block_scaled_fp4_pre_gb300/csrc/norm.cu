@@ -8,7 +8,10 @@
 // quantisation, so each input element is read once and each output written once.  y is
 // quantised from its fp32 value, not from the bf16 one, so q carries one rounding.  The
 // sum is fp32 in a fixed order (per thread, then a shuffle tree, then the warps in
-// order): the same input gives the same bits, whatever else runs.
+// order): the same input gives the same bits, whatever else runs.  An element that lies
+// next to a rounding boundary of E4M3 flips with the last bit of y, so what follows the
+// sum keeps the rounding errors: the warps' sums, the mean and the reciprocal root are
+// pairs of floats, and y is rounded to fp32 once.
 //
 // Layout: a thread holds V vectors of 8 consecutive elements (16 bytes of bf16), so four
 // lanes hold a scale's 32 elements and reduce its amax with two shuffles, and sixteen
@@ -51,6 +54,31 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 __device__ __forceinline__ size_t sf_word(int64_t row, int w, int words, int layout) {
   return layout == MOE_SF_128X4 ? sf_atom_offset((size_t)row, 4 * w, words)
                                 : ((size_t)row * words + w) * 4;
+}
+
+// A value as the sum of two floats, |lo| at most half a unit of hi's last place.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+// 1 / sqrt(s / K + eps): the hardware's approximate root improved by one Newton step in
+// two-float form (inv_k is 1 / K so).  Every thread of a row does this, so it has no
+// division: with IEEE divisions and root here the large rows took 120 us instead of 96.
+// Where the step is not a small correction (a sum of 0 with eps 0, one not finite) the
+// approximate root stands.
+__device__ __forceinline__ Two inverse_root(Two s, Two inv_k, float eps) {
+  const float q = s.hi * inv_k.hi;
+  const float ql = fmaf(s.hi, inv_k.hi, -q) + fmaf(s.hi, inv_k.lo, s.lo * inv_k.hi);
+  Two m = two_sum(q, eps);
+  m.lo += ql;
+  const float r = rsqrtf(m.hi);
+  const float t = r * r, tl = fmaf(r, r, -t);
+  const float e = fmaf(-m.hi, t, 1.0f) - fmaf(m.hi, tl, m.lo * t);   // 1 - m r^2
+  const float lo = 0.5f * r * e;
+  return {r, fabsf(lo) < r ? lo : 0.0f};
 }
 
 // WARP_ROW: one warp a row (kWarpRowThreads / 32 rows a block); otherwise one block a row.
@@ -103,13 +131,22 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+  Two sum = {ss, 0.f};
   if (!WARP_ROW) {
     if (lane == 0) part[warp] = ss;
     __syncthreads();
-    ss = 0.f;
-    for (int w = 0; w < (nt >> 5); ++w) ss += part[w];
+    // every warp adds the warps' sums, a lane each, as a tree of pairs
+    sum.hi = lane < (nt >> 5) ? part[lane] : 0.f;
+    const int top = 31 - __clz((nt >> 5) * 2 - 1);   // levels: 2^top lanes cover the warps
+#pragma unroll 1
+    for (int o = (1 << top) >> 1; o > 0; o >>= 1) {
+      const Two s = two_sum(sum.hi, __shfl_xor_sync(kAll, sum.hi, o));
+      sum = {s.hi, s.lo + (sum.lo + __shfl_xor_sync(kAll, sum.lo, o))};
+    }
+    sum.hi = __shfl_sync(kAll, sum.hi, 0);   // lanes past the 2^top hold other sums
+    sum.lo = __shfl_sync(kAll, sum.lo, 0);
   }
-  const float inv = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  const Two inv = inverse_root(sum, Two{a.inv_k, a.inv_k_lo}, a.eps);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * nt + t;
@@ -121,7 +158,9 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = r[i][j] * inv * g[j];
+      // r * gamma exactly, as two floats, times the root, rounded once
+      const float p = r[i][j] * g[j], pl = fmaf(r[i][j], g[j], -p);
+      y[j] = fmaf(p, inv.hi, fmaf(p, inv.lo, pl * inv.hi));
       amax = fmaxf(amax, fabsf(y[j]));
     }
     if (a.y && live) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c * 8) = pack8(y);
@@ -155,6 +194,8 @@ cudaError_t launch(const RmsnormArgs& a, int threads, cudaStream_t st) {
 cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& args, int64_t rows_cap, cudaStream_t st) {
   RmsnormArgs a = args;
   a.sf_rows = 0;
+  a.inv_k = (float)(1.0 / a.K);
+  a.inv_k_lo = (float)(1.0 / a.K - (double)a.inv_k);
   if (a.q) {
     // Scales past the live rows' last block (4-D layout) or row (packed): one tail.
     const size_t live = mxfp8_scale_bytes(a.rows, a.K, a.layout);
@@ -171,7 +212,11 @@ cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& args, int64_t rows_cap, cuda
   if (vecs <= 64) return launch<2, true>(a, 0, st);
   if (vecs <= 128) return launch<4, true>(a, 0, st);
   auto threads = [&](int v) { return (vecs + v * 32 - 1) / (v * 32) * 32; };
-  if (vecs <= 512) return launch<1, false>(a, threads(1), st);
+  // With at most one block an SM the latency of a row counts: as many threads as the row
+  // feeds.  With more, a row's fixed work (the sums' trees) is shared by more elements a
+  // thread.  K = 4096, one vector a thread against two: 1 row 2.06 / 2.49 us, 16384 rows
+  // 104.3 / 89.3 us; K = 1408, 333 rows: 2.88 / 2.53 us.
+  if (a.rows <= 152 && vecs <= 1024) return launch<1, false>(a, threads(1), st);
   if (vecs <= 1024) return launch<2, false>(a, threads(2), st);
   if (vecs <= 2048) return launch<4, false>(a, threads(4), st);
   return launch<8, false>(a, threads(8), st);

@@ -38,12 +38,12 @@ LinearShape shape_of(const moe_linear_dims& d) {
 }
 
 struct LinWs {
-  size_t flags, counters, partial, q, sf, total;
+  size_t flags, q, sf, total;
 };
 
 LinWs ws_layout(const moe_linear_dims& d) {
   const LinearShape s = shape_of(d);
-  const size_t slabs = (size_t)linear_slabs(s), Kp = (size_t)linear_padded_k(s);
+  const size_t Kp = (size_t)linear_padded_k(s);
   const size_t rows = (size_t)d.max_rows;
   LinWs L;
   size_t o = 0;
@@ -53,12 +53,6 @@ LinWs ws_layout(const moe_linear_dims& d) {
     return at;
   };
   L.flags = take(256);
-  L.counters = take(slabs * 4);
-  // fp32 sums of every part of a split K: [slab, part][row tile][128 features]
-  size_t parts = slabs * (size_t)linear_num_kb(s);
-  if (parts > (size_t)kLinMaxParts) parts = kLinMaxParts;
-  const size_t tn = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  L.partial = take(slabs < (size_t)kLinMaxParts ? parts * tn * 128 * 4 : 0);
   L.q = take(rows * (s.f8 ? Kp : Kp / 2));
   L.sf = take((rows + 127) / 128 * (Kp / 128) * kSFAtomBytes);
   L.total = o;
@@ -125,9 +119,10 @@ moe_status check_call(const moe_linear_dims* d, const void* prepared, int64_t ro
   return MOE_OK;
 }
 
+// The product of a pair (q, sf) or, q null, of a few bf16 rows x.
 moe_status forward(const moe_linear_dims* d, const void* prepared, const void* q, const void* sf,
-                   int64_t rows, void* out, int64_t ldo, int32_t out_type, void* ws,
-                   cudaStream_t st) {
+                   const void* x, int64_t ldx, int64_t rows, void* out, int64_t ldo,
+                   int32_t out_type, void* ws, cudaStream_t st) {
   const LinWs L = ws_layout(*d);
   uint8_t* b = static_cast<uint8_t*>(ws);
   LinearLaunch g;
@@ -135,12 +130,12 @@ moe_status forward(const moe_linear_dims* d, const void* prepared, const void* q
   g.w_codes = static_cast<const uint8_t*>(prepared);
   g.q = static_cast<const uint8_t*>(q);
   g.sf = static_cast<const uint8_t*>(sf);
+  g.x = x;
+  g.ldx = ldx;
   g.rows = rows;
   g.out = out;
   g.ldo = ldo;
   g.out_f32 = out_type == MOE_OUT_F32;
-  g.partial = reinterpret_cast<float*>(b + L.partial);
-  g.counters = reinterpret_cast<int32_t*>(b + L.counters);
   g.flags = reinterpret_cast<int32_t*>(b + L.flags);
   g.num_sms = moe_device_sm_count();
   if (g.num_sms <= 0) return fail(MOE_ERR_CUDA, "no CUDA device");
@@ -245,8 +240,8 @@ moe_status moe_linear_workspace_init(const moe_linear_dims* d, void* ws, size_t 
   if (ws_bytes < L.total)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", ws_bytes,
                 L.total);
-  // only the flags and the counters need a defined start
-  const cudaError_t e = cudaMemsetAsync(ws, 0, L.partial, static_cast<cudaStream_t>(stream));
+  // only the flags need a defined start
+  const cudaError_t e = cudaMemsetAsync(ws, 0, L.q, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "workspace clear");
   try {
     std::lock_guard<std::mutex> lk(g_mu);
@@ -268,10 +263,12 @@ moe_status moe_linear_forward(const moe_linear_dims* d, const void* prepared, co
   const LinWs L = ws_layout(*d);
   uint8_t* b = static_cast<uint8_t*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows <= kLinFusedRows)
+    return forward(d, prepared, nullptr, nullptr, x, ldx, rows, out, ldo, out_type, ws, st);
   const cudaError_t e =
       launch_linear_quantize(shape_of(*d), x, ldx, rows, b + L.q, b + L.sf, st);
   if (e != cudaSuccess) return cuda_fail(e, "linear quantise");
-  return forward(d, prepared, b + L.q, b + L.sf, rows, out, ldo, out_type, ws, st);
+  return forward(d, prepared, b + L.q, b + L.sf, nullptr, 0, rows, out, ldo, out_type, ws, st);
 }
 
 moe_status moe_linear_forward_pair(const moe_linear_dims* d, const void* prepared, const void* q,
@@ -285,7 +282,7 @@ moe_status moe_linear_forward_pair(const moe_linear_dims* d, const void* prepare
   if (rows == 0) return MOE_OK;
   if (!q || !sf || !aligned(q, 16) || !aligned(sf, 16))
     return fail(MOE_ERR_INVALID_ARG, "q and sf must be 16-byte aligned pointers");
-  return forward(d, prepared, q, sf, rows, out, ldo, out_type, ws,
+  return forward(d, prepared, q, sf, nullptr, 0, rows, out, ldo, out_type, ws,
                  static_cast<cudaStream_t>(stream));
 }
 

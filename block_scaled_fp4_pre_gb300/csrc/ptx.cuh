@@ -393,6 +393,14 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+// Store 16 bytes into the shared memory of another CTA of the cluster (a mapa_shared
+// address, 16-byte aligned).
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float x, float y, float z,
+                                                 float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y),
+               "f"(z), "f"(w)
+               : "memory");
+}
 // Every thread of both CTAs: release this CTA's earlier shared-memory writes, wait
 // for all threads of the cluster (a hardware barrier, like __syncthreads).
 __device__ __forceinline__ void cluster_sync() {
