@@ -100,15 +100,13 @@ WsLayout ws_layout(const moe_dims& d) {
   const int64_t few_t = L.T_cap < kFewTokens ? L.T_cap : kFewTokens;
   L.few_slots = few_t * k < E ? few_t * k : E;
   L.off_few_ctrl = take(256);
-  L.off_few_list = take((size_t)L.few_slots * 8);
-  L.off_few_wtab = take((size_t)L.few_slots * kFewTokens * 4);
   L.off_few_counters = take((size_t)(L.few_slots * (2 * I / kBM) + H / kBM) * 4);
   L.off_few_logits = take((size_t)kFewTokens * E * 4);
   L.off_few_xq = take((size_t)kFewTokens * act_row_bytes(d, H));
   L.off_few_xsf = take((size_t)sf_row_bytes(d, H) * 128);
   L.off_few_hq = take((size_t)L.few_slots * kFewTokens * act_row_bytes(d, I));
   L.off_few_hsf = take((size_t)L.few_slots * sf_row_bytes(d, I) * 128);
-  L.off_few_parts = take((size_t)kFewRanges * 4 * kFewTokens * kBM * 4);
+  L.off_few_parts = take((size_t)kFewBlocks * 4 * kFewTokens * kBM * 4);
   L.total = o;
   return L;
 }
@@ -671,12 +669,10 @@ moe_status moe_few_forward(const moe_dims* dims, const void* prepared, const voi
   a.logits = reinterpret_cast<float*>(b + L.off_few_logits);
   a.xq = b + L.off_few_xq;
   a.xsf = b + L.off_few_xsf;
-  a.list = reinterpret_cast<int2*>(b + L.off_few_list);
-  a.wtab = reinterpret_cast<float*>(b + L.off_few_wtab);
   a.hq = b + L.off_few_hq;
   a.hsf = b + L.off_few_hsf;
   a.parts0 = reinterpret_cast<float*>(b + L.off_few_parts);
-  a.parts1 = a.parts0 + (size_t)kFewRanges * 2 * kFewTokens * kBM;
+  a.parts1 = a.parts0 + (size_t)kFewBlocks * 2 * kFewTokens * kBM;
   a.counters = reinterpret_cast<int32_t*>(b + L.off_few_counters);
   a.counters1 = a.counters + L.few_slots * (2 * dims->inter / kBM);
   a.ctrl = reinterpret_cast<int32_t*>(b + L.off_few_ctrl);

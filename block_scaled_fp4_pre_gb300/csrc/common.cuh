@@ -117,7 +117,7 @@ struct WsLayout {
       off_local_rank, off_blk_base, off_tile_start,
       off_slot_token, off_slot_assign, off_slot_weight, off_xb, off_xsf, off_xq, off_xs, off_hb,
       off_hsf, off_acc, off_stage_x, off_stage_ids, off_stage_w, off_stage_out, off_few_ctrl,
-      off_few_list, off_few_wtab, off_few_counters, off_few_logits, off_few_xq, off_few_xsf,
+      off_few_counters, off_few_logits, off_few_xq, off_few_xsf,
       off_few_hq, off_few_hsf, off_few_parts, total;
   int64_t few_slots;      // experts the few-token form can touch
 };
@@ -330,7 +330,7 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st);
 // ---------------------------------------------------------------------------
 // The whole layer for a few tokens (few.cu).
 constexpr int kFewTokens = 16;     // tokens a call takes: the columns of one MMA
-constexpr int kFewRanges = 304;    // most ranges (blocks) of the expert kernel
+constexpr int kFewBlocks = 304;    // most blocks of the expert kernel
 struct FewArgs {
   const uint16_t* x;         // bf16 [T, H]
   const uint16_t* router;    // bf16 [E, H], or null: ids and weights are given
@@ -342,11 +342,9 @@ struct FewArgs {
   float* logits;             // [T, E]
   uint8_t* xq;               // [kFewTokens, H or H/2] and its scale blocks
   uint8_t* xsf;
-  int2* list;                // [slots] (expert, its tokens as bits), experts ascending
-  float* wtab;               // [slots][kFewTokens] routing weights
   uint8_t* hq;               // [slots * kFewTokens, I or I/2] and, a slot, its scale blocks
   uint8_t* hsf;
-  float* parts0;             // [kFewRanges][2][kFewTokens][128] fp32 sums of cut lines
+  float* parts0;             // [ranges][2][128][kFewTokens] fp32 sums of cut lines
   float* parts1;
   int32_t* counters;         // [slots * 2I/128], zero between calls
   int32_t* counters1;        // [H/128], zero between calls

@@ -1,10 +1,9 @@
 // The whole expert layer for a few tokens (up to kFewTokens), router included, in two
 // kernels for sm_103a:
 //
-//   few_route_kernel    logits = x Wr^T (fp32), top-k (ties to the lowest expert), softmax
-//                       over the chosen k; x quantised; the list of touched experts with
-//                       their tokens and weights
-//   few_expert_kernel   gate/up products, SwiGLU, requantisation; down products; the
+//   few_logits_kernel   logits = x Wr^T (fp32); x quantised
+//   few_expert_kernel   top-k (ties to the lowest expert) and softmax over the chosen k;
+//                       gate/up products, SwiGLU, requantisation; down products; the
 //                       weighted sum over the experts; bf16
 //
 // The same arithmetic and rounding points as the layer kernel (gemm.cu), on the same
@@ -15,22 +14,28 @@
 // - Every token is a column of every MMA (N = 16): no bucketing, no gather; an expert's
 //   columns of tokens that did not choose it are not used.  The tensor core takes the
 //   same time for 16 columns as for one.
-// - Work is cut into equal ranges of k-block tiles (one 16 KiB weight box each), one range
-//   a block and phase, whatever the number of experts: a range starts and ends inside a
-//   weight slab.  A slab that spans ranges leaves fp32 sums of each part in the workspace,
-//   and the part that finishes last adds them in the order of the ranges, so the result
-//   does not depend on timing.
+// - Every block works the routing out for itself, from the logits: some hundred loads and a
+//   few warp reductions, against an elected block's ticket, its list in global memory and
+//   a second read of it (5 us less at one token).
+// - Work is cut into ranges of k-block tiles (one 16 KiB weight box each), equal to a tile
+//   whatever the number of experts: a range starts and ends inside a weight slab.  A slab
+//   that spans ranges leaves fp32 sums of each part in the workspace, and the part that
+//   finishes last adds them in the order of the ranges, so the result does not depend on
+//   timing.
+// - Blocks claim ranges from a counter, all of phase 0 before any of phase 1, so the wait
+//   for the intermediate rows ends however many blocks are resident, and an SM that the
+//   memory serves faster takes more of them (equal shares ended 15% apart).  The first
+//   stages of a phase 1 range hold its weights before that wait.
 // - Phase 1 (down) runs slab by slab over the experts, so a block adds the experts'
 //   weighted products in registers and leaves one sum per slab it touches.
-// - Blocks claim ranges from a counter, all of phase 0 before any of phase 1, so the wait
-//   for the intermediate rows ends however many blocks are resident; the first stages of
-//   a phase 1 range hold its weights before that wait.
 //
 // Roles (192 threads, two blocks an SM): warp 0 claims and issues the TMA copies, warp 1
 // issues the MMAs, warps 2-5 read the accumulators (four of 16 columns each in flight).
 // Every wait is bounded (kWaitLimitNs); a timeout sets the workspace's error flag.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -40,22 +45,23 @@ namespace mxmoe {
 namespace {
 
 constexpr unsigned kFullW = 0xFFFFFFFFu;
-constexpr int kRouteThreads = 256;
-constexpr int kRouteExperts = 2;          // experts a block: four warps share a row of Wr
+constexpr int kLogitThreads = 512;
+constexpr int kLogitExperts = 2;          // experts a block
+constexpr int kLogitSplit = 4;            // warps that share a row of Wr (and 8 tokens each)
 constexpr int kFewThreads = 192;
 constexpr int kFewBlocksPerSM = 2;
 constexpr int kFewN = kFewTokens;         // MMA columns
 constexpr int kFewAccs = 4;
+constexpr int kFewLeast = 5;         // least tiles of a range (a whole line where that is less)
 constexpr int kFewTmemCols = 256;
 constexpr int kFewSfCol = kFewAccs * kFewN;   // two buffers of scale registers
 constexpr int kFewRing = 4;
+constexpr int kFewMaxSlots = kFewTokens * 32;
 
-// ws.ctrl words, all zero between calls but the last
-constexpr int kCtlTicket = 0;    // blocks of the routing kernel done
-constexpr int kCtlClaim = 1;     // next range
-constexpr int kCtlDone = 2;      // intermediate slabs written
-constexpr int kCtlExit = 3;      // blocks of the expert kernel done
-constexpr int kCtlSlots = 4;     // touched experts of the last routing
+// ws.ctrl words, all zero between calls
+constexpr int kCtlClaim = 0;     // next range
+constexpr int kCtlDone = 1;      // intermediate slabs written
+constexpr int kCtlExit = 2;      // blocks of the expert kernel done
 
 enum Fmt { kMx4 = 0, kMx8 = 1, kNv4 = 2 };
 
@@ -82,14 +88,17 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // One token's top-k by one warp: lane j ends with the j-th expert and its weight.
 // R: logits a lane holds (lane l: experts l, l + 32, ...).
 template <int R>
-__device__ __forceinline__ void top_k(const float* logits, int E, int k, int lane, int& id,
-                                      float& weight) {
-  uint32_t key[R];
+__device__ __forceinline__ void load_keys(const float* logits, int E, int lane,
+                                          uint32_t (&key)[R]) {
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int e = i * 32 + lane;
     key[i] = e < E ? order_key(__ldcg(logits + e)) : 0u;
   }
+}
+template <int R>
+__device__ __forceinline__ void top_k(uint32_t (&key)[R], int k, int lane, int& id,
+                                      float& weight) {
   uint32_t my_key = 0;
   id = -1;
   for (int j = 0; j < k; ++j) {
@@ -119,21 +128,17 @@ __device__ __forceinline__ void top_k(const float* logits, int E, int k, int lan
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const FewArgs a) {
-  __shared__ float part[8][kFewTokens];
-  __shared__ int last;
-  __shared__ uint32_t mask[1024];
-  __shared__ int16_t slot_of[1024];
-  __shared__ int warp_sum[8];
+__global__ void __launch_bounds__(kLogitThreads, 1) few_logits_kernel(const FewArgs a) {
+  __shared__ float part[kLogitThreads / 32][kFewTokens / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = a.T, H = a.H, E = a.E, k = a.k;
+  const int T = a.T, H = a.H, E = a.E;
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();   // after the wait: the expert kernel claims before its own
   // x quantised: a thread takes 8 elements, four lanes a scale (two for NVFP4)
   {
     const int vecs = H / 8, total = T * vecs;
-    for (int i = (int)(blockIdx.x * kRouteThreads) + tid; i - lane < total;
-         i += (int)gridDim.x * kRouteThreads) {
+    for (int i = (int)(blockIdx.x * kLogitThreads) + tid; i - lane < total;
+         i += (int)gridDim.x * kLogitThreads) {
       const bool live = i < total;
       const int t = live ? i / vecs : 0, c = live ? i - t * vecs : 0;
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -170,117 +175,79 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const FewArgs 
       }
     }
   }
-  if (a.router) {
-    const int e = (int)blockIdx.x * kRouteExperts + (warp >> 2);
-    float acc[kFewTokens];
+  if (!a.router) return;
+  // Warp (g, s, p): expert g of the block, half s of the tokens, part p of the row.  Loads
+  // come in batches of four 16-byte vectors of the row and of B tokens, before any
+  // arithmetic.
+  const int g = warp >> 3, half = (warp >> 2) & 1, p = warp & 3;
+  const int e = (int)blockIdx.x * kLogitExperts + g;
+  const int tok0 = half * (kFewTokens / 2);
+  float acc[kFewTokens / 2];
 #pragma unroll
-    for (int t = 0; t < kFewTokens; ++t) acc[t] = 0.f;
-    if (e < E) {
-      const uint16_t* wr = a.router + (size_t)e * H;
-      for (int c = (warp & 3) * 32 + lane; c < H / 8; c += 128) {
-        float w[8];
-        bf16x8(*reinterpret_cast<const uint4*>(wr + c * 8), w);
+  for (int t = 0; t < kFewTokens / 2; ++t) acc[t] = 0.f;
+  auto dots = [&](auto batch) {
+    constexpr int B = decltype(batch)::value;
+    const uint16_t* wr = a.router + (size_t)e * H;
+    const int vecs = H / 8;
+    for (int c0 = p * 32 + lane; c0 < vecs; c0 += 4 * kLogitSplit * 32) {
+      uint4 w[4];
 #pragma unroll
-        for (int t = 0; t < kFewTokens; ++t) {
-          if (t < T) {
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i * kLogitSplit * 32;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < vecs) w[i] = *reinterpret_cast<const uint4*>(wr + c * 8);
+      }
+#pragma unroll
+      for (int t0 = 0; t0 < kFewTokens / 2; t0 += B) {
+        if (tok0 + t0 >= T) break;
+        uint4 xv[B][4];
+#pragma unroll
+        for (int t = 0; t < B; ++t) {
+          const int tok = min(tok0 + t0 + t, T - 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * kLogitSplit * 32;
+            xv[t][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < vecs) xv[t][i] = *reinterpret_cast<const uint4*>(a.x + (size_t)tok * H + c * 8);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float wf[8];
+          bf16x8(w[i], wf);
+#pragma unroll
+          for (int t = 0; t < B; ++t) {
             float v[8];
-            bf16x8(*reinterpret_cast<const uint4*>(a.x + (size_t)t * H + c * 8), v);
+            bf16x8(xv[t][i], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[t] = fmaf(w[j], v[j], acc[t]);
+            for (int j = 0; j < 8; ++j) acc[t0 + t] = fmaf(wf[j], v[j], acc[t0 + t]);
           }
         }
       }
     }
+  };
+  if (e < E && tok0 < T) {
+    if (T == 1)
+      dots(std::integral_constant<int, 1>());
+    else
+      dots(std::integral_constant<int, 4>());
+  }
 #pragma unroll
-    for (int t = 0; t < kFewTokens; ++t) {
-      if (t < T) {
+  for (int t = 0; t < kFewTokens / 2; ++t) {
+    if (tok0 + t < T) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(kFullW, acc[t], o);
-        if (lane == 0) part[warp][t] = acc[t];
-      }
-    }
-    __syncthreads();
-    if (tid < kRouteExperts * kFewTokens) {
-      const int g = tid / kFewTokens, t = tid % kFewTokens;
-      const int ee = (int)blockIdx.x * kRouteExperts + g;
-      if (t < T && ee < E)
-        a.logits[(size_t)t * E + ee] = (part[4 * g][t] + part[4 * g + 1][t]) +
-                                       (part[4 * g + 2][t] + part[4 * g + 3][t]);
+      for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(kFullW, acc[t], o);
+      if (lane == 0) part[warp][t] = acc[t];
     }
   }
-  // The last block to get here routes.
-  __threadfence();
   __syncthreads();
-  if (tid == 0) {
-    last = atomicAdd(&a.ctrl[kCtlTicket], 1) == (int)gridDim.x - 1;
-    if (last) a.ctrl[kCtlTicket] = 0;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  for (int e = tid; e < E; e += kRouteThreads) mask[e] = 0u;
-  __syncthreads();
-  for (int t = warp; t < T; t += 8) {
-    int id = -1;
-    if (a.router) {
-      float w;
-      if (E <= 256)
-        top_k<8>(a.logits + (size_t)t * E, E, k, lane, id, w);
-      else
-        top_k<32>(a.logits + (size_t)t * E, E, k, lane, id, w);
-      if (lane < k) {
-        a.ids[t * k + lane] = id;
-        a.weights[t * k + lane] = w;
-      }
-    } else if (lane < k) {
-      id = a.ids[t * k + lane];
-      if (id < 0 || id >= E) {
-        atomicOr(&a.flags[0], kErrRouting);
-        id = -1;
-      }
-    }
-    if (lane < k && id >= 0) atomicOr(&mask[id], 1u << t);
-  }
-  __syncthreads();
-  // Touched experts in ascending order: four experts a thread.
-  {
-    int mine = 0;
-    for (int j = 0; j < 4; ++j) {
-      const int e = tid * 4 + j;
-      if (e < E && mask[e]) ++mine;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFullW, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += warp_sum[w];
-    for (int j = 0; j < 4; ++j) {
-      const int e = tid * 4 + j;
-      if (e < E && mask[e]) {
-        a.list[at] = make_int2(e, (int)mask[e]);
-        slot_of[e] = (int16_t)at;
-#pragma unroll
-        for (int t = 0; t < kFewTokens; t += 4)
-          *reinterpret_cast<float4*>(a.wtab + (size_t)at * kFewTokens + t) =
-              make_float4(0.f, 0.f, 0.f, 0.f);
-        ++at;
-      }
-    }
-    if (tid == kRouteThreads - 1) a.ctrl[kCtlSlots] = at;
-  }
-  __syncthreads();
-  // A token's weights by one thread, in order: an expert named twice gets their sum.
-  if (tid < T) {
-    for (int j = 0; j < k; ++j) {
-      const int id = a.ids[tid * k + j];
-      if (id >= 0 && id < E)
-        a.wtab[(size_t)slot_of[id] * kFewTokens + tid] += a.weights[tid * k + j];
-    }
+  if (tid < kLogitExperts * kFewTokens) {
+    const int gg = tid / kFewTokens, t = tid % kFewTokens;
+    const int ee = (int)blockIdx.x * kLogitExperts + gg;
+    const int w0 = gg * 8 + t / (kFewTokens / 2) * 4, tt = t % (kFewTokens / 2);
+    if (t < T && ee < E)
+      a.logits[(size_t)t * E + ee] =
+          (part[w0][tt] + part[w0 + 1][tt]) + (part[w0 + 2][tt] + part[w0 + 3][tt]);
   }
 }
 
@@ -307,7 +274,20 @@ struct __align__(16) FewTail {
   uint32_t tmem_base;
   int abort;
   int last;
+  int slots, weights_used;
   float h[kFewN][68];        // one slab's SwiGLU outputs (64 features, padded rows)
+  // Touched experts: (expert | first weight << 16, tokens as bits), and their tokens'
+  // routing weights.
+  int2 list[kFewMaxSlots];
+  float weight[kFewMaxSlots];
+};
+
+// Scratch of the routing, in the operand stages before any copy into them.
+struct RouteScratch {
+  uint32_t mask[1024];       // tokens of each expert
+  int16_t slot_of[1024];
+  int16_t id[kFewTokens][32];
+  float w[kFewTokens][32];
 };
 
 template <int FMT>
@@ -318,22 +298,132 @@ static_assert(2 * (few_smem_bytes<kMx4>() + 1024) <= 228 * 1024, "two blocks per
 static_assert(2 * (few_smem_bytes<kMx8>() + 1024) <= 228 * 1024, "two blocks per SM");
 static_assert(2 * (few_smem_bytes<kNv4>() + 1024) <= 228 * 1024, "two blocks per SM");
 
-// Tiles of a phase: `kb` of them a line (an expert's weight slab).  Phase 0 lines are
-// slot * m0 + slab, phase 1 lines slab * slots + slot.  No range is empty but those from
-// `ranges` on, which a phase of fewer tiles than blocks has.
+// Tiles of a phase: `kb` of them a line (an expert's weight slab), cut into `ranges` that
+// differ by at most one tile.  Phase 0 lines are slot * m0 + slab, phase 1 lines
+// slab * slots + slot.
 struct Plan {
-  int64_t n;       // tiles
-  int kb, ranges;
-  __device__ __forceinline__ Plan(int64_t tiles, int kb_line, int blocks)
-      : n(tiles), kb(kb_line), ranges((int)min(tiles, (int64_t)blocks)) {}
-  __device__ __forceinline__ int64_t start(int r) const {
-    return r >= ranges ? n : r * n / ranges;
+  int n, kb, ranges, q, rem;
+  // One range a block, of at least kFewLeast tiles or a line, since each cut costs a join
+  // (finer ranges measured slower: 16 tokens 213 to 225 us against 205, 1 token 46 against
+  // 33).  whole: phase 0 with four lines and more a block takes lines, which need no join
+  // and let a faster SM take more of them.
+  __device__ __forceinline__ Plan(int tiles, int kb_line, int blocks, bool whole)
+      : n(tiles), kb(kb_line) {
+    if (whole && tiles >= 4 * blocks * kb_line)
+      ranges = tiles / kb_line;
+    else
+      ranges = max(1, min(blocks, tiles / min(kb_line, kFewLeast)));
+    q = n / ranges;
+    rem = n - q * ranges;
   }
+  __device__ __forceinline__ int start(int r) const { return r * q + min(r, rem); }
   // the range that holds tile t
-  __device__ __forceinline__ int range_of(int64_t t) const {
-    return (int)(((t + 1) * ranges - 1) / n);
+  __device__ __forceinline__ int range_of(int t) const {
+    const int big = rem * (q + 1);
+    return t < big ? t / (q + 1) : rem + (t - big) / q;
   }
 };
+
+// Every block: each token's top-k (or the given ids), the list of touched experts.
+// All threads; ends with a block barrier.  `scratch.mask` is zero at the start.
+__device__ __forceinline__ void route(const FewArgs& a, RouteScratch& sc, FewTail* tail) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, k = a.k;
+  auto note = [&](int t, int id, float w) {   // lane j < k: assignment (t, j)
+    if (lane < k) {
+      sc.id[t][lane] = (int16_t)id;
+      sc.w[t][lane] = w;
+      if (id >= 0) atomicOr(&sc.mask[id], 1u << t);
+      if (a.router && blockIdx.x == 0) {
+        a.ids[t * k + lane] = id;
+        a.weights[t * k + lane] = w;
+      }
+    }
+  };
+  constexpr int kWarps = kFewThreads / 32, kRounds = (kFewTokens + kWarps - 1) / kWarps;
+  if (!a.router) {
+    for (int t = warp; t < a.T; t += kWarps) {
+      int id = lane < k ? a.ids[t * k + lane] : 0;
+      const float w = lane < k ? a.weights[t * k + lane] : 0.f;
+      if (id < 0 || id >= E) {
+        if (blockIdx.x == 0) atomicOr(&a.flags[0], kErrRouting);
+        id = -1;
+      }
+      note(t, id, w);
+    }
+  } else if (E <= 256) {
+    uint32_t key[kRounds][8];   // every token's loads before any selection
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (warp + r * kWarps < a.T)
+        load_keys<8>(a.logits + (size_t)(warp + r * kWarps) * E, E, lane, key[r]);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int t = warp + r * kWarps;
+      if (t < a.T) {
+        int id;
+        float w;
+        top_k<8>(key[r], k, lane, id, w);
+        note(t, id, w);
+      }
+    }
+  } else {
+    for (int t = warp; t < a.T; t += kWarps) {
+      uint32_t key[32];
+      int id;
+      float w;
+      load_keys<32>(a.logits + (size_t)t * E, E, lane, key);
+      top_k<32>(key, k, lane, id, w);
+      note(t, id, w);
+    }
+  }
+  __syncthreads();
+  // Slots in the order in which the assignments first name an expert.
+  const int n = a.T * k;
+  if (warp == 0) {
+    int at = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane, t = i / k, j = i - t * k;
+      const int id = i < n ? sc.id[t][j] : -1;
+      uint32_t m = 0;
+      if (id >= 0) {
+        m = sc.mask[id];
+        if (m & ((1u << t) - 1u)) m = 0;
+        if (!a.router)
+          for (int o = 0; o < j; ++o)
+            if (sc.id[t][o] == id) m = 0;
+      }
+      const uint32_t firsts = __ballot_sync(kFullW, m != 0);
+      if (m) {
+        const int s = at + __popc(firsts & ((1u << lane) - 1u));
+        // which stretch of the weights a slot gets does not matter
+        const int w0 = atomicAdd(&tail->weights_used, __popc(m));
+        tail->list[s] = make_int2(id | w0 << 16, (int)m);
+        sc.slot_of[id] = (int16_t)s;
+      }
+      at += __popc(firsts);
+    }
+    if (lane == 0) tail->slots = at;
+  }
+  __syncthreads();
+  // A token that names an expert twice gets the sum of the weights, in their order.
+  for (int i = threadIdx.x; i < n; i += kFewThreads) {
+    const int t = i / k, j = i - t * k, id = sc.id[t][j];
+    bool first = id >= 0;
+    float w = sc.w[t][j];
+    if (!a.router) {
+      for (int o = 0; o < j; ++o) first = first && sc.id[t][o] != id;
+      for (int o = j + 1; o < k; ++o)
+        if (sc.id[t][o] == id) w += sc.w[t][o];
+    }
+    if (first) {
+      const int2 l = tail->list[sc.slot_of[id]];
+      tail->weight[(l.x >> 16) + __popc((uint32_t)l.y & ((1u << t) - 1u))] = w;
+    }
+  }
+  ptx::fence_proxy_async_smem();   // the scratch is written by TMA copies next
+  __syncthreads();
+}
 
 template <int FMT>
 __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
@@ -381,19 +471,25 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
   ptx::tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
   volatile int* abort_flag = &tail->abort;
-  const int ranges = (int)gridDim.x;
-  // The first claim overlaps the routing kernel: that one started after the call before
+  RouteScratch& scratch = *reinterpret_cast<RouteScratch*>(smem);
+  for (int e = threadIdx.x; e < a.E; e += kFewThreads) scratch.mask[e] = 0u;
+  if (threadIdx.x == 0) tail->weights_used = 0;
+  __syncthreads();
+  // The first claim overlaps the kernel before: that one started after the call before
   // this one had reset the counter.
   int claim = 0;
   if (threadIdx.x == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
+  route(a, scratch, tail);
 
-  const int slots = a.ctrl[kCtlSlots];
+  const int slots = tail->slots;
   const int m0 = 2 * a.I / kBM, m1 = a.H / kBM;
   const int kb0 = (a.H + kKb - 1) / kKb, kb1 = (a.I + kKb - 1) / kKb;
-  const Plan P0((int64_t)slots * m0 * kb0, kb0, ranges);
-  const Plan P1((int64_t)slots * m1 * kb1, kb1, ranges);
+  const int blocks = (int)gridDim.x;
+  const Plan P0(slots * m0 * kb0, kb0, blocks, true);
+  const Plan P1(slots * m1 * kb1, kb1, blocks, false);
+  const int R0 = P0.ranges, R = R0 + P1.ranges;
 
   if (slots == 0) {
     // no valid assignment: zeros
@@ -404,36 +500,70 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
     if (lane == 0) {
       const uint64_t pol_w = ptx::policy_evict_first();
       const uint64_t pol_t = ptx::policy_evict_last();
+      // Where a range stands: its next tile.
+      struct Cursor {
+        int idx, t, t1, kb, slot, slab, wslab;
+        bool down;
+      };
+      auto weight_slab = [&](Cursor& c) {
+        c.wslab = (tail->list[c.slot].x & 0xFFFF) * (c.down ? m1 : m0) + c.slab;
+      };
+      auto open = [&](int idx) {
+        Cursor c = {};
+        c.idx = idx < R ? idx : -1;
+        c.down = idx >= R0;
+        if (c.idx < 0) return c;
+        const Plan& P = c.down ? P1 : P0;
+        const int rg = c.down ? idx - R0 : idx;
+        c.t = P.start(rg);
+        c.t1 = P.start(rg + 1);
+        const int line = c.t / P.kb, per = c.down ? slots : m0;
+        c.kb = c.t - line * P.kb;
+        (c.down ? c.slab : c.slot) = line / per;
+        (c.down ? c.slot : c.slab) = line % per;
+        weight_slab(c);
+        return c;
+      };
+      auto step = [&](Cursor& c) {
+        ++c.t;
+        if (++c.kb < (c.down ? kb1 : kb0)) return;
+        c.kb = 0;
+        if (c.down) {
+          if (++c.slot == slots) {
+            c.slot = 0;
+            ++c.slab;
+          }
+        } else if (++c.slab == m0) {
+          c.slab = 0;
+          ++c.slot;
+        }
+        if (c.t < c.t1) weight_slab(c);
+      };
       int stage = 0, r = 0;
       uint32_t phase = 0, rph = 0;
       int64_t issued = 0;
       bool ok = true, waited = false;
+      Cursor next = open(claim);
       while (true) {
-        const int idx = claim < 2 * ranges ? claim : -1;
+        Cursor c = next;
         ok = ptx::mbar_wait(&tail->ring_empty[r], rph ^ 1u, abort_flag, kWaitLimitNs);
         if (!ok) break;
-        tail->ring[r] = idx;
+        tail->ring[r] = c.idx;
         ptx::mbar_arrive(&tail->ring_full[r]);
         if (++r == kFewRing) {
           r = 0;
           rph ^= 1u;
         }
-        if (idx < 0) break;
-        claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
-        const bool down = idx >= ranges;
-        const Plan& P = down ? P1 : P0;
-        const int rg = down ? idx - ranges : idx;
-        const int64_t t0 = P.start(rg), t1 = P.start(rg + 1);
+        if (c.idx < 0) break;
+        const bool down = c.down;
+        const int kb_line = down ? kb1 : kb0;
         const CUtensorMap* tw = down ? &tmap_w2 : &tmap_w1;
         const CUtensorMap* tt = down ? &tmap_h : &tmap_x;
         const uint8_t* wsf0 = down ? a.w2_sf : a.w1_sf;
         const uint8_t* tsf0 = down ? a.hsf : a.xsf;
         const int K = down ? a.I : a.H, kc = K / kAtomK;
-        // The token side of tile t, into stage s: x's rows, or the expert's rows of h.
-        auto tokens = [&](int64_t t, int s) {
-          const int64_t line = t / P.kb;
-          const int kb = (int)(t - line * P.kb);
-          const int slot = down ? (int)(line % slots) : 0;
+        // The token side of a tile, into stage s: x's rows, or the expert's rows of h.
+        auto tokens = [&](int slot, int kb, int s) {
           const int atoms = min(kKb, K - kb * kKb) / kAtomK;
           ptx::tma_load_2d(smem + SM::kB + (size_t)s * SM::kBSlot, tt, kb * kBKBytes,
                            slot * kFewN, &tail->full[s], pol_t);
@@ -441,62 +571,52 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
                          tsf0 + ((size_t)slot * kc + (size_t)kb * (kKb / kAtomK)) * kSFAtomBytes,
                          atoms * kSFAtomBytes, &tail->full[s], pol_t);
         };
-        int64_t held = t0;          // tiles [held, t) have their weights only
-        int held_stage = stage;
-        int64_t cur_line = -1;
-        int wslab = 0;
-        for (int64_t t = t0; t < t1; ++t) {
-          const int64_t line = t / P.kb;
-          const int kb = (int)(t - line * P.kb);
-          if (line != cur_line) {
-            cur_line = line;
-            const int slot = (int)(down ? line % slots : line / m0);
-            const int slab = (int)(down ? line / slots : line % m0);
-            wslab = a.list[slot].x * (down ? m1 : m0) + slab;
+        // tiles [held, c.t) of a phase 1 range have their weights only, in stages from
+        // held_stage on
+        const int t0 = c.t;
+        int held = t0, held_stage = stage;
+        auto release = [&](int upto) {
+          ok = ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag, kWaitLimitNs);
+          if (!ok) return;
+          ptx::fence_proxy_async_global();
+          waited = true;
+          for (; held < upto; ++held) {
+            const int line = held / kb_line;
+            tokens(line % slots, held - line * kb_line, held_stage);
+            if (++held_stage == kSt) held_stage = 0;
           }
-          if (down && !waited && t - t0 == kSt) {
-            // every stage holds weights of this range: its intermediate rows next
-            ok = ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag, kWaitLimitNs);
+        };
+        for (; c.t < c.t1; step(c)) {
+          if (down && !waited && c.t - t0 == kSt) {
+            release(c.t);   // every stage holds weights of this range
             if (!ok) break;
-            ptx::fence_proxy_async_global();
-            waited = true;
-            for (; held < t; ++held) {
-              tokens(held, held_stage);
-              if (++held_stage == kSt) held_stage = 0;
-            }
           }
           ok = ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
           if (!ok) break;
-          const int atoms = min(kKb, K - kb * kKb) / kAtomK;
+          const int atoms = min(kKb, K - c.kb * kKb) / kAtomK;
           uint64_t* bar = &tail->full[stage];
           // a widened E2M1 box counts its packed bytes only
           ptx::mbar_arrive_expect_tx(
               bar, (uint32_t)((FMT == kMx8 ? kATileBytes / 2 : kATileBytes) +
                               a.t_rows * kBKBytes + 2 * atoms * kSFAtomBytes));
-          ptx::tma_load_2d(smem + (size_t)stage * kATileBytes, tw, 0, (wslab * P.kb + kb) * kBM,
-                           bar, pol_w);
-          ptx::bulk_load(smem + SM::kSFA + (size_t)stage * SM::kSF,
-                         wsf0 + ((size_t)wslab * kc + (size_t)kb * (kKb / kAtomK)) * kSFAtomBytes,
-                         atoms * kSFAtomBytes, bar, pol_w);
-          if (!down || waited) tokens(t, stage);
+          ptx::tma_load_2d(smem + (size_t)stage * kATileBytes, tw, 0,
+                           (c.wslab * kb_line + c.kb) * kBM, bar, pol_w);
+          ptx::bulk_load(
+              smem + SM::kSFA + (size_t)stage * SM::kSF,
+              wsf0 + ((size_t)c.wslab * kc + (size_t)c.kb * (kKb / kAtomK)) * kSFAtomBytes,
+              atoms * kSFAtomBytes, bar, pol_w);
+          if (!down || waited) tokens(down ? c.slot : 0, c.kb, stage);
+          // The next range, claimed late: a block that runs behind should not hold one.
+          if (c.t == max(t0, c.t1 - 2)) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
           ++issued;
           if (++stage == kSt) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok && down && !waited && t1 > t0) {   // a range shorter than the stages
-          ok = ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag, kWaitLimitNs);
-          if (ok) {
-            ptx::fence_proxy_async_global();
-            waited = true;
-          }
-          for (; ok && held < t1; ++held) {
-            tokens(held, held_stage);
-            if (++held_stage == kSt) held_stage = 0;
-          }
-        }
+        if (ok && down && !waited) release(c.t1);   // a range shorter than the stages
         if (!ok) break;
+        next = open(claim);
       }
       if (!ok) atomicOr(&a.flags[0], kErrTimeout);
       // Every copy issued here must have landed before the block exits.  (After a timeout
@@ -509,7 +629,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    // the whole warp runs the loop; one lane issues
+    {
       const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
       const uint64_t db0 = ptx::desc_sw128(ptx::smem_addr(smem + SM::kB));
       const uint64_t dsa0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFA));
@@ -521,30 +642,31 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       uint32_t phase = 0, rph = 0, acc_phase = 0, sfbuf = 0;
       bool ok = true;
       while (ok) {
-        ok = ptx::mbar_wait(&tail->ring_full[r], rph, abort_flag, kWaitLimitNs);
+        ok = __all_sync(kFullW, ptx::mbar_wait(&tail->ring_full[r], rph, abort_flag, kWaitLimitNs));
         if (!ok) break;
-        const int idx = tail->ring[r];
-        ptx::mbar_arrive(&tail->ring_empty[r]);
+        const int idx = __shfl_sync(kFullW, tail->ring[r], 0);
+        if (ptx::elect_one()) ptx::mbar_arrive(&tail->ring_empty[r]);
         if (++r == kFewRing) {
           r = 0;
           rph ^= 1u;
         }
         if (idx < 0) break;
-        const bool down = idx >= ranges;
+        const bool down = idx >= R0;
         const Plan& P = down ? P1 : P0;
-        const int rg = down ? idx - ranges : idx;
-        const int64_t t1 = P.start(rg + 1);
+        const int rg = down ? idx - R0 : idx;
+        const int t1 = P.start(rg + 1);
         const int K = down ? a.I : a.H;
-        for (int64_t t = P.start(rg); t < t1 && ok;) {
-          const int kbs = (int)(t % P.kb);
-          const int kbe = (int)min((int64_t)P.kb, kbs + (t1 - t));
+        for (int t = P.start(rg), kbs = t % P.kb; t < t1 && ok; kbs = 0) {
+          const int kbe = min(P.kb, kbs + t1 - t);
           t += kbe - kbs;
-          ok = ptx::mbar_wait(&tail->acc_empty[acc], acc_phase ^ 1u, abort_flag, kWaitLimitNs);
+          ok = __all_sync(kFullW, ptx::mbar_wait(&tail->acc_empty[acc], acc_phase ^ 1u, abort_flag,
+                                                 kWaitLimitNs));
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(acc * kFewN);
           for (int kb = kbs; kb < kbe; ++kb) {
-            ok = ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs);
+            ok = __all_sync(kFullW, ptx::mbar_wait(&tail->full[stage], phase, abort_flag,
+                                                   kWaitLimitNs));
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t sfa = tmem_base + (uint32_t)kFewSfCol + (sfbuf ? 2 * kSfCols : 0u);
@@ -555,41 +677,44 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
             const uint64_t db = db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4));
             const uint32_t on = kb != kbs ? 1u : 0u;
             const bool whole = K - kb * kKb >= kKb;   // a last k-block may be half wide
-            if constexpr (FMT == kMx8) {
-              ptx::tc_cp_sf(sfa, dsa);
-              ptx::tc_cp_sf(sfb, dsb);
-              ptx::tc_mma_f8f4(d, da, db, ptx::idesc_f8f4(kFewN, 0), sfa, sfb, on);
-              ptx::tc_mma_f8f4(d, da + 2, db + 2, ptx::idesc_f8f4(kFewN, 1), sfa, sfb, 1u);
-              ptx::tc_mma_f8f4(d, da + 4, db + 4, ptx::idesc_f8f4(kFewN, 2), sfa, sfb, 1u);
-              ptx::tc_mma_f8f4(d, da + 6, db + 6, ptx::idesc_f8f4(kFewN, 3), sfa, sfb, 1u);
-            } else if constexpr (FMT == kNv4) {
+            if (ptx::elect_one()) {
+              if constexpr (FMT == kMx8) {
+                ptx::tc_cp_sf(sfa, dsa);
+                ptx::tc_cp_sf(sfb, dsb);
+                ptx::tc_mma_f8f4(d, da, db, ptx::idesc_f8f4(kFewN, 0), sfa, sfb, on);
+                ptx::tc_mma_f8f4(d, da + 2, db + 2, ptx::idesc_f8f4(kFewN, 1), sfa, sfb, 1u);
+                ptx::tc_mma_f8f4(d, da + 4, db + 4, ptx::idesc_f8f4(kFewN, 2), sfa, sfb, 1u);
+                ptx::tc_mma_f8f4(d, da + 6, db + 6, ptx::idesc_f8f4(kFewN, 3), sfa, sfb, 1u);
+              } else if constexpr (FMT == kNv4) {
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                if (s < 2 || whole) {
-                  ptx::tc_cp_sf(sfa + s * 4, dsa + 32 * s);
-                  ptx::tc_cp_sf(sfb + s * 4, dsb + 32 * s);
+                for (int s = 0; s < 4; ++s) {
+                  if (s < 2 || whole) {
+                    ptx::tc_cp_sf(sfa + s * 4, dsa + 32 * s);
+                    ptx::tc_cp_sf(sfb + s * 4, dsb + 32 * s);
+                  }
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  if (s < 2 || whole)
+                    ptx::tc_mma_nvf4(d, da + 2 * s, db + 2 * s, idn, sfa + s * 4, sfb + s * 4,
+                                     s == 0 ? on : 1u);
+              } else {
+                ptx::tc_cp_sf(sfa, dsa);
+                ptx::tc_cp_sf(sfb, dsb);
+                if (whole) {
+                  ptx::tc_cp_sf(sfa + 4, dsa + 32);
+                  ptx::tc_cp_sf(sfb + 4, dsb + 32);
+                }
+                ptx::tc_mma_mxf4(d, da, db, id0, sfa, sfb, on);
+                ptx::tc_mma_mxf4(d, da + 2, db + 2, id2, sfa, sfb, 1u);
+                if (whole) {
+                  ptx::tc_mma_mxf4(d, da + 4, db + 4, id0, sfa + 4, sfb + 4, 1u);
+                  ptx::tc_mma_mxf4(d, da + 6, db + 6, id2, sfa + 4, sfb + 4, 1u);
                 }
               }
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                if (s < 2 || whole)
-                  ptx::tc_mma_nvf4(d, da + 2 * s, db + 2 * s, idn, sfa + s * 4, sfb + s * 4,
-                                   s == 0 ? on : 1u);
-            } else {
-              ptx::tc_cp_sf(sfa, dsa);
-              ptx::tc_cp_sf(sfb, dsb);
-              if (whole) {
-                ptx::tc_cp_sf(sfa + 4, dsa + 32);
-                ptx::tc_cp_sf(sfb + 4, dsb + 32);
-              }
-              ptx::tc_mma_mxf4(d, da, db, id0, sfa, sfb, on);
-              ptx::tc_mma_mxf4(d, da + 2, db + 2, id2, sfa, sfb, 1u);
-              if (whole) {
-                ptx::tc_mma_mxf4(d, da + 4, db + 4, id0, sfa + 4, sfb + 4, 1u);
-                ptx::tc_mma_mxf4(d, da + 6, db + 6, id2, sfa + 4, sfb + 4, 1u);
-              }
+              ptx::tc_commit(&tail->empty[stage]);
             }
-            ptx::tc_commit(&tail->empty[stage]);
+            __syncwarp();
             sfbuf ^= 1u;
             if (++stage == kSt) {
               stage = 0;
@@ -597,16 +722,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
             }
           }
           if (!ok) break;
-          ptx::tc_commit(&tail->acc_full[acc]);
+          if (ptx::elect_one()) ptx::tc_commit(&tail->acc_full[acc]);
+          __syncwarp();
           if (++acc == kFewAccs) {
             acc = 0;
             acc_phase ^= 1u;
           }
         }
       }
-      if (!ok) atomicOr(&a.flags[0], kErrTimeout);
+      if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
       // every MMA issued here has finished before the block frees its tensor memory
-      ptx::tc_commit(&tail->mma_done);
+      if (ptx::elect_one()) ptx::tc_commit(&tail->mma_done);
+      __syncwarp();
       int never = 0;
       ptx::mbar_wait(&tail->mma_done, 0, &never, kWaitLimitNs);
     }
@@ -635,34 +762,50 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
     // Adds the parts of tiles [lo, hi), which span ranges first..last, of which this block
     // has range rg's in v.  Returns false in every part but the last one to finish.
     auto join = [&](float (&v)[kFewN], const Plan& P, float* parts, int32_t* counter, int rg,
-                    int64_t lo, int64_t hi) {
+                    int lo, int hi) {
       const int first = P.range_of(lo), last = P.range_of(hi - 1);
       if (first == last) return true;
-      // a range's first line is its piece 0, a later one (its last) piece 1
+      // A range's first line is its piece 0, a later one (its last) piece 1; a piece is
+      // [128 features][16 columns].
       auto piece = [&](int rr) {
-        return parts + ((size_t)rr * 2 + (P.start(rr) >= lo ? 0 : 1)) * (kFewN * kBM) + row;
+        return reinterpret_cast<float4*>(
+            parts + ((size_t)rr * 2 + (P.start(rr) >= lo ? 0 : 1)) * (kFewN * kBM) + row * kFewN);
       };
-      float* mine = piece(rg);
+      float4* mine = piece(rg);
 #pragma unroll
-      for (int t = 0; t < kFewN; ++t)
-        if (t < T) __stcg(mine + t * kBM, v[t]);
+      for (int c = 0; c < kFewN; c += 4)
+        if (c < T) __stcg(mine + c / 4, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]));
       ptx::named_bar_sync(1, 128);
       if (ep == 0) {
-        __threadfence();
-        tail->last = atomicAdd(counter, 1) == last - first;
+        tail->last = ptx::atomic_add_acq_rel(counter, 1) == last - first;
         if (tail->last) *counter = 0;
-        __threadfence();
       }
       ptx::named_bar_sync(1, 128);
-      const bool mine_last = tail->last != 0;
-      if (!mine_last) return false;
+      if (tail->last == 0) return false;
+      // eight parts' loads in flight, added in the order of the ranges
 #pragma unroll
-      for (int t = 0; t < kFewN; ++t) v[t] = 0.f;
-      for (int rr = first; rr <= last; ++rr) {
-        const float* p = piece(rr);
+      for (int c = 0; c < kFewN; c += 4) {
+        if (c >= T) break;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r0 = first; r0 <= last; r0 += 8) {
+          float4 p[8];
 #pragma unroll
-        for (int t = 0; t < kFewN; ++t)
-          if (t < T) v[t] += __ldcg(p + t * kBM);
+          for (int i = 0; i < 8; ++i) {
+            p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r0 + i <= last) p[i] = __ldcg(piece(r0 + i) + c / 4);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s.x += p[i].x;
+            s.y += p[i].y;
+            s.z += p[i].z;
+            s.w += p[i].w;
+          }
+        }
+        v[c] = s.x;
+        v[c + 1] = s.y;
+        v[c + 2] = s.z;
+        v[c + 3] = s.w;
       }
       return true;
     };
@@ -679,15 +822,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       }
       if (idx < 0) break;
       float v[kFewN];
-      if (idx < ranges) {
+      if (idx < R0) {
         // ---- gate/up: sums, SwiGLU, requantisation
-        const int rg = idx;
-        const int64_t t1 = P0.start(rg + 1);
-        for (int64_t t = P0.start(rg); t < t1;) {
-          const int64_t line = t / kb0, lo = line * kb0, hi = lo + kb0;
+        const int rg = idx, t1 = P0.start(rg + 1);
+        int line = P0.start(rg) / kb0, slot = line / m0, slab = line - slot * m0;
+        for (int t = P0.start(rg); t < t1; ++line, ++slab) {
+          const int lo = line * kb0, hi = lo + kb0;
           t = min(hi, t1);
-          const int slot = (int)(line / m0), slab = (int)(line % m0);
-          const uint32_t chosen = (uint32_t)a.list[slot].y;
+          if (slab == m0) {
+            slab = 0;
+            ++slot;
+          }
+          const uint32_t chosen = (uint32_t)tail->list[slot].y;
           if (!(ok = take(v))) break;
           if (!join(v, P0, a.parts0, a.counters + line, rg, lo, hi)) continue;
           // Rows of this warp: [gate 8 | up 8 | gate 8 | up 8], so lane l and l ^ 8 hold
@@ -748,28 +894,26 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
         }
       } else {
         // ---- down: the experts' products, weighted, summed slab by slab
-        const int rg = idx - ranges;
-        const int64_t t1 = P1.start(rg + 1);
+        const int rg = idx - R0, t1 = P1.start(rg + 1);
         float sum[kFewN];
 #pragma unroll
-        for (int t = 0; t < kFewN; ++t) sum[t] = 0.f;
-        const int64_t span = (int64_t)slots * kb1;   // tiles of one output slab
-        for (int64_t t = P1.start(rg); t < t1;) {
-          const int64_t line = t / kb1;
+        for (int c = 0; c < kFewN; ++c) sum[c] = 0.f;
+        const int span = slots * kb1;   // tiles of one output slab
+        int line = P1.start(rg) / kb1, slab = line / slots, slot = line - slab * slots;
+        for (int t = P1.start(rg); t < t1; ++line, ++slot) {
           t = min((line + 1) * kb1, t1);
-          const int slot = (int)(line % slots), slab = (int)(line / slots);
-          const uint32_t chosen = (uint32_t)a.list[slot].y;
-          float w[kFewN];
-#pragma unroll
-          for (int c = 0; c < kFewN; c += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(a.wtab + (size_t)slot * kFewN + c);
-            w[c] = f.x; w[c + 1] = f.y; w[c + 2] = f.z; w[c + 3] = f.w;
+          if (slot == slots) {
+            slot = 0;
+            ++slab;
           }
+          const int2 l = tail->list[slot];
+          const uint32_t chosen = (uint32_t)l.y;
+          const float* w = tail->weight + (l.x >> 16);
           if (!(ok = take(v))) break;
           // columns of other tokens hold anything, NaN too: skipped, not multiplied by 0
 #pragma unroll
           for (int c = 0; c < kFewN; ++c)
-            if ((chosen >> c) & 1u) sum[c] = fmaf(w[c], v[c], sum[c]);
+            if ((chosen >> c) & 1u) sum[c] = fmaf(*w++, v[c], sum[c]);
           if (t == t1 || t == (slab + 1) * span) {
             if (join(sum, P1, a.parts1, a.counters1 + slab, rg, slab * span, (slab + 1) * span)) {
               const int n = slab * kBM + row;
@@ -800,7 +944,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       a.ctrl[kCtlClaim] = 0;
       a.ctrl[kCtlDone] = 0;
       a.ctrl[kCtlExit] = 0;
-      __threadfence();
     }
   }
 }
@@ -835,12 +978,12 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   if ((e = make_tmap(&mx, a.xq, f8 ? s.H : s.H / 2, kFewN, a.t_rows)) ||
       (e = make_tmap(&mh, a.hq, f8 ? s.I : s.I / 2, (uint64_t)g.slots_cap * kFewN, a.t_rows)))
     return e;
-  int blocks = a.router ? (s.E + kRouteExperts - 1) / kRouteExperts
-                        : (a.T * (s.H / 8) + kRouteThreads - 1) / kRouteThreads;
-  e = launch_pdl(few_route_kernel<FMT>, dim3(blocks), dim3(kRouteThreads), 0, st, a);
+  const int blocks = a.router ? (s.E + kLogitExperts - 1) / kLogitExperts
+                              : (a.T * (s.H / 8) + kLogitThreads - 1) / kLogitThreads;
+  e = launch_pdl(few_logits_kernel<FMT>, dim3(blocks), dim3(kLogitThreads), 0, st, a);
   if (e != cudaSuccess) return e;
   int grid = kFewBlocksPerSM * g.num_sms;
-  if (grid > kFewRanges) grid = kFewRanges;
+  if (grid > kFewBlocks) grid = kFewBlocks;
   return launch_pdl(few_expert_kernel<FMT>, dim3(grid), dim3(kFewThreads), kBytes, st, m1, mx, m2,
                     mh, a);
 }

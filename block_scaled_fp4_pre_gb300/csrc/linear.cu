@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    // the whole warp runs the loop; one lane issues
+    {
       const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
       const uint64_t db0 = ptx::desc_sw128(ptx::smem_addr(smem + SM::kB));
       const uint64_t dsa0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFA));
@@ -291,21 +292,26 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       uint32_t phase = 0, acc_phase = 0, sfbuf = 0;
       bool ok = true;
       for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
-        ok = ptx::mbar_wait(&tail->acc_empty, acc_phase ^ 1u, abort_flag, kWaitLimitNs);
+        ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->acc_empty, acc_phase ^ 1u, abort_flag,
+                                                  kWaitLimitNs));
         if (!ok) break;
         ptx::tc_fence_after();
         for (int kb = 0; kb < a.num_kb; ++kb) {
-          ok = ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs);
+          ok = __all_sync(kFullMask,
+                          ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs));
           if (!ok) break;
           ptx::tc_fence_after();
-          lin_mma<F8, TN>(tmem_base, da0 + (uint64_t)(stage * (kATileBytes >> 4)),
-                          db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4)),
-                          dsa0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
-                          dsb0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
-                          tmem_base + (uint32_t)kLinSfCol + (sfbuf ? 16u : 0u),
-                          TN == 64 ? (uint32_t)(g / a.slabs & 1) * 2u : 0u, kb ? 1u : 0u,
-                          a.K - kb * kKb >= kKb);
-          ptx::tc_commit(&tail->empty[stage]);
+          if (ptx::elect_one()) {
+            lin_mma<F8, TN>(tmem_base, da0 + (uint64_t)(stage * (kATileBytes >> 4)),
+                            db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4)),
+                            dsa0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
+                            dsb0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
+                            tmem_base + (uint32_t)kLinSfCol + (sfbuf ? 16u : 0u),
+                            TN == 64 ? (uint32_t)(g / a.slabs & 1) * 2u : 0u, kb ? 1u : 0u,
+                            a.K - kb * kKb >= kKb);
+            ptx::tc_commit(&tail->empty[stage]);
+          }
+          __syncwarp();
           sfbuf ^= 1u;
           if (++stage == kSt) {
             stage = 0;
@@ -313,12 +319,14 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
           }
         }
         if (!ok) break;
-        ptx::tc_commit(&tail->acc_full);
+        if (ptx::elect_one()) ptx::tc_commit(&tail->acc_full);
+        __syncwarp();
         acc_phase ^= 1u;
       }
-      if (!ok) atomicOr(&a.flags[0], kErrTimeout);
+      if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
       // every MMA issued here has finished before the block frees its tensor memory
-      ptx::tc_commit(&tail->mma_done);
+      if (ptx::elect_one()) ptx::tc_commit(&tail->mma_done);
+      __syncwarp();
       int never = 0;
       ptx::mbar_wait(&tail->mma_done, 0, &never, kWaitLimitNs);
     }
@@ -451,7 +459,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
       const uint64_t db0 = ptx::desc_sw128(ptx::smem_addr(smem + SM::kB));
       const uint64_t dsa0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFA));
@@ -459,23 +467,28 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       int stage = 0;
       uint32_t phase = 0, sfbuf = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs);
+        ok = __all_sync(kFullMask,
+                        ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs));
         if (!ok) break;
         ptx::tc_fence_after();
-        lin_mma<F8, TN>(tmem_base, da0 + (uint64_t)(stage * (kATileBytes >> 4)),
-                        db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4)),
-                        dsa0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
-                        dsb0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
-                        tmem_base + (uint32_t)kLinSfCol + (sfbuf ? 16u : 0u),
-                        TN == 64 ? (uint32_t)(tile & 1) * 2u : 0u, kb != kb0 ? 1u : 0u, a.K - kb * kKb >= kKb);
-        ptx::tc_commit(&tail->empty[stage]);
+        if (ptx::elect_one()) {
+          lin_mma<F8, TN>(tmem_base, da0 + (uint64_t)(stage * (kATileBytes >> 4)),
+                          db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4)),
+                          dsa0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
+                          dsb0 + (uint64_t)(stage * (int)(SM::kSF >> 4)),
+                          tmem_base + (uint32_t)kLinSfCol + (sfbuf ? 16u : 0u),
+                          TN == 64 ? (uint32_t)(tile & 1) * 2u : 0u, kb != kb0 ? 1u : 0u, a.K - kb * kKb >= kKb);
+          ptx::tc_commit(&tail->empty[stage]);
+        }
+        __syncwarp();
         sfbuf ^= 1u;
         if (++stage == kSt) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      ptx::tc_commit(&tail->acc_full);
+      if (ptx::elect_one()) ptx::tc_commit(&tail->acc_full);
+      __syncwarp();
     }
   } else {
     if constexpr (QUANT) {

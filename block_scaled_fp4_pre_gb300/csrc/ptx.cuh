@@ -27,6 +27,19 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // visible.  A no-op for kernels launched without the programmatic attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// True in one lane of a converged warp.  Code that all lanes reach together and that picks
+// its issuing lane this way keeps descriptors and addresses in uniform registers; inside a
+// branch on the lane id each tensor-core instruction first moves them there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---- mbarrier --------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
@@ -81,6 +94,14 @@ __device__ __forceinline__ int ld_acquire(const int32_t* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+// Adds to *p and returns the old value; releases this thread's earlier accesses (and those
+// a barrier ordered before it) and acquires those released by earlier adds.
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v)
+               : "memory");
+  return old;
 }
 // Waits until *p >= target (acquire), bounded like mbar_wait: gives up when *abort
 // becomes nonzero or after limit_ns, setting *abort in the latter case.
