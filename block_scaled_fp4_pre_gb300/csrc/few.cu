@@ -497,7 +497,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
          i += (int64_t)gridDim.x * kFewThreads)
       a.out[i] = 0;
   } else if (warp == 0) {
-    if (lane == 0) {
+    // the whole warp runs the loop; one lane issues
+    {
+      claim = __shfl_sync(kFullW, claim, 0);
       const uint64_t pol_w = ptx::policy_evict_first();
       const uint64_t pol_t = ptx::policy_evict_last();
       // Where a range stands: its next tile.
@@ -546,10 +548,14 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       Cursor next = open(claim);
       while (true) {
         Cursor c = next;
-        ok = ptx::mbar_wait(&tail->ring_empty[r], rph ^ 1u, abort_flag, kWaitLimitNs);
+        ok = __all_sync(kFullW, ptx::mbar_wait(&tail->ring_empty[r], rph ^ 1u, abort_flag,
+                                               kWaitLimitNs));
         if (!ok) break;
-        tail->ring[r] = c.idx;
-        ptx::mbar_arrive(&tail->ring_full[r]);
+        if (lane == 0) {
+          tail->ring[r] = c.idx;
+          ptx::mbar_arrive(&tail->ring_full[r]);
+        }
+        __syncwarp();
         if (++r == kFewRing) {
           r = 0;
           rph ^= 1u;
@@ -576,13 +582,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
         const int t0 = c.t;
         int held = t0, held_stage = stage;
         auto release = [&](int upto) {
-          ok = ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag, kWaitLimitNs);
+          ok = __all_sync(kFullW, ptx::wait_counter(&a.ctrl[kCtlDone], slots * m0, abort_flag,
+                                                    kWaitLimitNs));
           if (!ok) return;
           ptx::fence_proxy_async_global();
           waited = true;
           for (; held < upto; ++held) {
             const int line = held / kb_line;
-            tokens(line % slots, held - line * kb_line, held_stage);
+            if (ptx::elect_one()) tokens(line % slots, held - line * kb_line, held_stage);
+            __syncwarp();
             if (++held_stage == kSt) held_stage = 0;
           }
         };
@@ -591,23 +599,27 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
             release(c.t);   // every stage holds weights of this range
             if (!ok) break;
           }
-          ok = ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
+          ok = __all_sync(kFullW, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
+                                                 kWaitLimitNs));
           if (!ok) break;
-          const int atoms = min(kKb, K - c.kb * kKb) / kAtomK;
-          uint64_t* bar = &tail->full[stage];
-          // a widened E2M1 box counts its packed bytes only
-          ptx::mbar_arrive_expect_tx(
-              bar, (uint32_t)((FMT == kMx8 ? kATileBytes / 2 : kATileBytes) +
-                              a.t_rows * kBKBytes + 2 * atoms * kSFAtomBytes));
-          ptx::tma_load_2d(smem + (size_t)stage * kATileBytes, tw, 0,
-                           (c.wslab * kb_line + c.kb) * kBM, bar, pol_w);
-          ptx::bulk_load(
-              smem + SM::kSFA + (size_t)stage * SM::kSF,
-              wsf0 + ((size_t)c.wslab * kc + (size_t)c.kb * (kKb / kAtomK)) * kSFAtomBytes,
-              atoms * kSFAtomBytes, bar, pol_w);
-          if (!down || waited) tokens(down ? c.slot : 0, c.kb, stage);
+          if (ptx::elect_one()) {
+            const int atoms = min(kKb, K - c.kb * kKb) / kAtomK;
+            uint64_t* bar = &tail->full[stage];
+            // a widened E2M1 box counts its packed bytes only
+            ptx::mbar_arrive_expect_tx(
+                bar, (uint32_t)((FMT == kMx8 ? kATileBytes / 2 : kATileBytes) +
+                                a.t_rows * kBKBytes + 2 * atoms * kSFAtomBytes));
+            ptx::tma_load_2d(smem + (size_t)stage * kATileBytes, tw, 0,
+                             (c.wslab * kb_line + c.kb) * kBM, bar, pol_w);
+            ptx::bulk_load(
+                smem + SM::kSFA + (size_t)stage * SM::kSF,
+                wsf0 + ((size_t)c.wslab * kc + (size_t)c.kb * (kKb / kAtomK)) * kSFAtomBytes,
+                atoms * kSFAtomBytes, bar, pol_w);
+            if (!down || waited) tokens(down ? c.slot : 0, c.kb, stage);
+          }
+          __syncwarp();
           // The next range, claimed late: a block that runs behind should not hold one.
-          if (c.t == max(t0, c.t1 - 2)) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
+          if (c.t == max(t0, c.t1 - 2) && lane == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
           ++issued;
           if (++stage == kSt) {
             stage = 0;
@@ -616,9 +628,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
         }
         if (ok && down && !waited) release(c.t1);   // a range shorter than the stages
         if (!ok) break;
+        claim = __shfl_sync(kFullW, claim, 0);
         next = open(claim);
       }
-      if (!ok) atomicOr(&a.flags[0], kErrTimeout);
+      if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
       // Every copy issued here must have landed before the block exits.  (After a timeout
       // some stages may lack their token side: their waits run out.)
       const int64_t first = issued > kSt ? issued - kSt : 0;

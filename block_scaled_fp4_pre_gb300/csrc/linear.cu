@@ -13,6 +13,7 @@
 // - linear_quantize_kernel writes the activation codes and their scale blocks, for more
 //   than 32 bf16 rows.
 // - linear_kernel: persistent, one block's epilogue overlapping the other's MMAs.
+// - linear_pair_kernel: tiles of 256 features by 192 rows over SM pairs, for large products.
 // - linear_split_kernel: where there are too few tiles for the SMs, a cluster of up to
 //   eight blocks splits a tile's K.  The blocks exchange their sums through distributed
 //   shared memory, each adding the parts of its share of the features in order: no
@@ -77,29 +78,36 @@ __global__ void linear_scales_kernel(const uint8_t* __restrict__ src, uint32_t* 
 }
 
 // ---------------------------------------------------------------------------
-// Activations: a thread takes 8 elements of a row, four lanes a scale, sixteen a scale
-// word.  Elements past K (to the next multiple of 128) are zero.
-template <bool F8>
+// Activations: a thread takes 8 elements of a row at a time, four lanes a scale, sixteen a
+// scale word.  Elements past K (to the next multiple of 128) are zero.  A block covers
+// 2^span_log vectors of kQuantThreads >> span_log rows at a time and R times as many rows,
+// all of a thread's loads before any arithmetic; rows and columns need no division.
+template <bool F8, int R>
 __global__ void __launch_bounds__(kQuantThreads)
     linear_quantize_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows, int K,
-                           int Kp, uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
+                           int Kp, uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
+                           int span_log) {
   ptx::pdl_wait();
-  ptx::pdl_launch_dependents();   // after the wait: see linear_kernel's weight loads
-  const int vecs = Kp / 8, words = Kp / 128;
-  const int64_t total = rows * vecs;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  // whole warps stay in the loop: the shuffles below need every lane
-  for (int64_t i = first; i - (threadIdx.x & 31) < total; i += step) {
-    const bool live = i < total;
-    const int64_t row = live ? i / vecs : 0;
-    const int c = live ? (int)(i - row * vecs) : 0;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (live && c * 8 < K) w = *reinterpret_cast<const uint4*>(x + row * ldx + c * 8);
-    float v[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                  __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u),
-                  __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
-                  __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u)};
+  ptx::pdl_launch_dependents();   // after the wait: see the split kernel's weight loads
+  const int words = Kp / 128;
+  const int c = ((int)blockIdx.y << span_log) + (threadIdx.x & ((1 << span_log) - 1));
+  const int rows_once = kQuantThreads >> span_log;
+  const int64_t row0 = (int64_t)blockIdx.x * R * rows_once + (threadIdx.x >> span_log);
+  const bool in_k = c * 8 < K, in_kp = c * 8 < Kp;
+  uint4 w[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = row0 + i * rows_once;
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < rows && in_k) w[i] = __ldcs(reinterpret_cast<const uint4*>(x + row * ldx + c * 8));
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = row0 + i * rows_once;
+    float v[8] = {__uint_as_float(w[i].x << 16), __uint_as_float(w[i].x & 0xFFFF0000u),
+                  __uint_as_float(w[i].y << 16), __uint_as_float(w[i].y & 0xFFFF0000u),
+                  __uint_as_float(w[i].z << 16), __uint_as_float(w[i].z & 0xFFFF0000u),
+                  __uint_as_float(w[i].w << 16), __uint_as_float(w[i].w & 0xFFFF0000u)};
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     uint32_t s = (uint32_t)(e + 127) << (((threadIdx.x >> 2) & 3) * 8);
     s |= __shfl_xor_sync(kFullMask, s, 4);
     s |= __shfl_xor_sync(kFullMask, s, 8);
-    if (live) {
+    if (row < rows && in_kp) {
       if (F8)
         *reinterpret_cast<uint2*>(q + row * Kp + c * 8) = ptx::e4m3x8(v);
       else
@@ -136,6 +144,7 @@ struct LinArgs {
   int k_live;            // K as given
   int slabs, tiles, num_kb, kc4;
   int out_f32;
+  int pairs16;           // bf16 rows whose features can be stored two at a time
 };
 
 __host__ __device__ constexpr int lin_stages(int tn) { return tn == 128 ? 3 : tn == 64 ? 4 : 5; }
@@ -166,6 +175,36 @@ __device__ __forceinline__ void lin_store(const LinArgs& a, int m, int n, float 
     static_cast<float*>(a.out)[(int64_t)m * a.ldo + n] = v;
   else
     static_cast<__nv_bfloat16*>(a.out)[(int64_t)m * a.ldo + n] = __float2bfloat16(v);
+}
+
+// Stores up to 16 rows' values of feature n (a warp's lanes hold 32 consecutive features).
+// bf16 pairs where rows allow it: neighbouring lanes exchange, so that each stores two
+// features of every other row, and a whole block of 16 x 32 goes through one pointer.
+__device__ __forceinline__ void lin_store16(const LinArgs& a, int m, int rows, int n,
+                                            const float (&v)[16]) {
+  if (a.pairs16) {
+    const int odd = threadIdx.x & 1;
+    __nv_bfloat162 w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float got = __shfl_xor_sync(kFullMask, odd ? v[2 * j] : v[2 * j + 1], 1);
+      w[j] = odd ? __floats2bfloat162_rn(got, v[2 * j + 1]) : __floats2bfloat162_rn(v[2 * j], got);
+    }
+    __nv_bfloat162* p =
+        static_cast<__nv_bfloat162*>(a.out) + (((int64_t)(m + odd) * a.ldo + (n & ~1)) >> 1);
+    if (rows == 16 && (n | 31) < a.N) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j * a.ldo] = w[j];   // two rows further on each time
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (2 * j + odd < rows && n < a.N) p[j * a.ldo] = w[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < rows && n < a.N) lin_store(a, m + j, n, v[j]);
+  }
 }
 
 // The MMAs of one k-block: four, 32 bytes (+2 in a descriptor) further along every row.
@@ -236,50 +275,52 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
   const int total = a.slabs * a.tiles;   // the slabs of a row tile follow one another
 
   if (warp == 0) {
-    if (lane == 0) {
-      ptx::pdl_wait();
-      const uint64_t pol_w = ptx::policy_evict_normal();
-      const uint64_t pol_t = ptx::policy_evict_last();
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
-        const int slab = g % a.slabs, tile = g / a.slabs;
-        const uint8_t* wsf = a.w_sf + (size_t)slab * a.kc4 * kSFAtomBytes;
-        const uint8_t* tsf = a.t_sf + (size_t)(tile * TN >> 7) * a.kc4 * kSFAtomBytes;
-        for (int kb = 0; kb < a.num_kb; ++kb) {
-          ok = ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
-          if (!ok) break;
+    // the whole warp runs the loop; one lane issues
+    ptx::pdl_wait();
+    const uint64_t pol_w = ptx::policy_evict_normal();
+    const uint64_t pol_t = ptx::policy_evict_last();
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
+      const int slab = g % a.slabs, tile = g / a.slabs;
+      const uint8_t* wsf = a.w_sf + (size_t)slab * a.kc4 * kSFAtomBytes;
+      const uint8_t* tsf = a.t_sf + (size_t)(tile * TN >> 7) * a.kc4 * kSFAtomBytes;
+      for (int kb = 0; kb < a.num_kb; ++kb) {
+        ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
+                                                  kWaitLimitNs));
+        if (!ok) break;
+        if (ptx::elect_one()) {
           const int atoms = min(kKb, a.K - kb * kKb) / 128;
+          const size_t at = (size_t)kb * (kKb / 128) * kSFAtomBytes;
           uint64_t* bar = &tail->full[stage];
           // a widened E2M1 box (F8) counts its packed bytes only
           ptx::mbar_arrive_expect_tx(bar, (uint32_t)((F8 ? kATileBytes / 2 : kATileBytes) +
                                                      SM::kBSlot + 2 * atoms * kSFAtomBytes));
           ptx::tma_load_2d(smem + (size_t)stage * kATileBytes, &tmap_w, 0,
                            (slab * a.num_kb + kb) * kBM, bar, pol_w);
-          ptx::bulk_load(smem + SM::kSFA + (size_t)stage * SM::kSF,
-                         wsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes, bar,
-                         pol_w);
+          ptx::bulk_load(smem + SM::kSFA + (size_t)stage * SM::kSF, wsf + at,
+                         atoms * kSFAtomBytes, bar, pol_w);
           ptx::tma_load_2d(smem + SM::kB + (size_t)stage * SM::kBSlot, &tmap_x, kb * kBKBytes,
                            tile * TN, bar, pol_t);
-          ptx::bulk_load(smem + SM::kSFB + (size_t)stage * SM::kSF,
-                         tsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes, bar,
-                         pol_t);
-          ++issued;
-          if (++stage == kSt) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          ptx::bulk_load(smem + SM::kSFB + (size_t)stage * SM::kSF, tsf + at,
+                         atoms * kSFAtomBytes, bar, pol_t);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == kSt) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) atomicOr(&a.flags[0], kErrTimeout);
-      // every copy issued here must have landed before the block exits
-      const int64_t first = issued > kSt ? issued - kSt : 0;
-      for (int64_t i = first; i < issued; ++i) {
-        int never = 0;
-        ptx::mbar_wait(&tail->full[i % kSt], (uint32_t)((i / kSt) & 1), &never, kWaitLimitNs);
-      }
+    }
+    if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
+    // every copy issued here must have landed before the block exits
+    const int64_t first = issued > kSt ? issued - kSt : 0;
+    for (int64_t i = first; i < issued; ++i) {
+      int never = 0;
+      ptx::mbar_wait(&tail->full[i % kSt], (uint32_t)((i / kSt) & 1), &never, kWaitLimitNs);
     }
   } else if (warp == 1) {
     // the whole warp runs the loop; one lane issues
@@ -349,9 +390,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       for (int c0 = 0; c0 < cols; c0 += 16) {
         float v[16];
         ptx::tmem_ld16(taddr + (uint32_t)c0, v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c0 + j < cols && n < a.N) lin_store(a, m0 + c0 + j, n, v[j]);
+        lin_store16(a, m0 + c0, min(16, cols - c0), n, v);
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(&tail->acc_empty);
@@ -362,6 +401,279 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, kLinTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Large products: a pair of SMs (a 2-CTA cluster) shares a tile of 256 features by up to
+// 192 rows, each MMA spanning both (tcgen05 cta_group::2, M = 256): each SM stages its own
+// 128-feature slab and half of the rows, so it writes and reads 60% of the shared-memory
+// bytes a 128 x 128 tile takes per product.  Two accumulators, seven stages.  Roles (320
+// threads, one block an SM): warp 0 producer, warp 1 of the leader MMA issue, warps 2-9
+// epilogue, two a lane quarter.
+constexpr int kPairThreads = 320;
+constexpr int kPairTmemCols = 512;
+constexpr int kPairStages = 7;
+constexpr int kPairRows = kBNPair;                // 192
+constexpr int kPairHalf = kPairRows / 2;
+constexpr int kPairEpiWarps = 8;
+constexpr uint32_t kPairSfCol = 2 * kPairRows;    // two buffers of scale registers:
+constexpr uint32_t kPairSfCols = 24;              // 8 of the slab's, 16 of the rows'
+
+struct __align__(16) LinPairTail {
+  uint64_t full[kPairStages];     // leader: both CTAs' loads of a stage landed
+  uint64_t empty[kPairStages];    // each CTA: the pair's MMAs are done with its stage
+  uint64_t acc_full[2];           // each CTA: the accumulator is complete
+  uint64_t acc_empty[2];          // leader: all 16 epilogue warps have read it
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <bool F8>
+struct LinPairSmem {
+  static constexpr size_t kSF = (size_t)(F8 ? 1 : 2) * kSFAtomBytes;   // one 128-row block
+  static constexpr size_t kBSlot = (size_t)kPairHalf * kBKBytes;
+  static constexpr size_t kB = (size_t)kPairStages * kATileBytes;
+  static constexpr size_t kSFA = kB + kPairStages * kBSlot;
+  static constexpr size_t kSFB = kSFA + kPairStages * kSF;
+  static constexpr size_t kTail = kSFB + kPairStages * 2 * kSF;
+  static constexpr size_t kBytes = kTail + sizeof(LinPairTail) + 1024;
+  static_assert(kBytes <= 227 * 1024, "one block per SM");
+};
+
+struct LinPairMaps {
+  CUtensorMap w, x, wsf, tsf;
+};
+
+template <bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ LinPairMaps maps, const LinArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  using SM = LinPairSmem<F8>;
+  constexpr int kKb = F8 ? 128 : kBK;
+  constexpr int kSt = kPairStages;
+  LinPairTail* tail = reinterpret_cast<LinPairTail*>(smem + SM::kTail);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      ptx::mbar_init(&tail->full[s], 1);
+      ptx::mbar_init(&tail->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&tail->acc_full[b], 1);
+      ptx::mbar_init(&tail->acc_empty[b], 2 * kPairEpiWarps);
+    }
+    ptx::mbar_init(&tail->mma_done, 1);
+    tail->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&maps.w);
+    ptx::prefetch_tmap(&maps.x);
+    ptx::prefetch_tmap(&maps.wsf);
+    ptx::prefetch_tmap(&maps.tsf);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&tail->tmem_base, kPairTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // both CTAs' barriers exist before either signals the other's
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = tail->tmem_base;
+  volatile int* abort_flag = &tail->abort;
+  ptx::pdl_launch_dependents();
+  const int pairs = (a.slabs + 1) / 2, total = pairs * a.tiles;
+
+  if (warp == 0) {
+    // the whole warp runs the loop; one lane issues
+    ptx::pdl_wait();
+    const uint64_t pol = ptx::policy_evict_normal();
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&tail->full[0]), 0);
+    const uint32_t s_a = ptx::smem_addr(smem), s_b = ptx::smem_addr(smem + SM::kB);
+    const uint32_t s_sfa = ptx::smem_addr(smem + SM::kSFA);
+    const uint32_t s_sfb = ptx::smem_addr(smem + SM::kSFB);
+    // Both CTAs' bytes of a stage, all counted on the leader's barrier (a widened E2M1
+    // box counts its packed bytes only).
+    constexpr uint32_t kStageBytes = 2u * (uint32_t)((F8 ? kATileBytes / 2 : kATileBytes) +
+                                                     SM::kBSlot + 3 * SM::kSF);
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int g = first; g < total && ok; g += step) {
+      // an odd last slab is multiplied twice, and stored once
+      const int slab = min(g % pairs * 2 + (int)rank, a.slabs - 1), m0 = g / pairs * kPairRows;
+      int wy = slab * a.num_kb * kBM, say = slab * a.kc4 * 2, sby = 0;
+      const int row = m0 + (int)rank * kPairHalf, blk = m0 >> 7;
+      for (int kb = 0; kb < a.num_kb; ++kb) {
+        ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
+                                                  kWaitLimitNs));
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          const uint32_t bar = full0 + (uint32_t)stage * 8u;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&tail->full[stage], kStageBytes);
+          ptx::tma_load_2d_pair(s_a + (uint32_t)stage * kATileBytes, &maps.w, 0, wy, bar, pol);
+          ptx::tma_load_2d_pair(s_b + (uint32_t)(stage * SM::kBSlot), &maps.x, kb * kBKBytes, row,
+                                bar, pol);
+          ptx::tma_load_3d_pair(s_sfa + (uint32_t)(stage * SM::kSF), &maps.wsf, 0, say, 0, bar, pol);
+          // every MMA reads all the rows' scales in both CTAs
+          ptx::tma_load_3d_pair(s_sfb + (uint32_t)(stage * 2 * SM::kSF), &maps.tsf, 0, sby, blk, bar,
+                                pol);
+        }
+        __syncwarp();
+        wy += kBM;
+        say += F8 ? 2 : 4;
+        sby += F8 ? 2 : 4;
+        ++issued;
+        if (++stage == kSt) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
+    // the pair's MMAs are done reading this CTA's last stages before the block leaves
+    const int64_t from = issued > kSt ? issued - kSt : 0;
+    for (int64_t i = from; i < issued; ++i) {
+      int never = 0;
+      ptx::mbar_wait(&tail->empty[i % kSt], (uint32_t)((i / kSt) & 1), &never, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // the whole warp runs the loop; one lane issues
+      const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
+      const uint64_t db0 = ptx::desc_sw128(ptx::smem_addr(smem + SM::kB));
+      const uint64_t dsa0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFA));
+      const uint64_t dsb0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFB));
+      const uint32_t id0 = ptx::idesc_mxf4_m(2 * kBM, kPairRows, 0);
+      const uint32_t id2 = ptx::idesc_mxf4_m(2 * kBM, kPairRows, 2);
+      int stage = 0, ab = 0;
+      uint32_t phase = 0, acc_phase = 0, sfbuf = 0;
+      bool ok = true;
+      for (int g = first; g < total && ok; g += step) {
+        // tiles start at a 128-row scale block or in the middle of one
+        const uint32_t shift = (uint32_t)((g / pairs * kPairRows & 127) >> 5);
+        ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->acc_empty[ab], acc_phase ^ 1u, abort_flag,
+                                                  kWaitLimitNs));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(ab * kPairRows);
+        for (int kb = 0; kb < a.num_kb; ++kb) {
+          ok = __all_sync(kFullMask,
+                          ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t da = da0 + (uint64_t)(stage * (kATileBytes >> 4));
+          const uint64_t db = db0 + (uint64_t)(stage * (int)(SM::kBSlot >> 4));
+          const uint64_t dsa = dsa0 + (uint64_t)(stage * (int)(SM::kSF >> 4));
+          const uint64_t dsb = dsb0 + (uint64_t)(stage * (int)(2 * SM::kSF >> 4));
+          const uint32_t fa = tmem_base + kPairSfCol + (sfbuf ? kPairSfCols : 0u);
+          const uint32_t fb0 = fa + 8, fb = fb0 + shift;
+          const uint32_t acc = kb ? 1u : 0u;
+          const bool whole = a.K - kb * kKb >= kKb;   // a last k-block may be half wide
+          if (ptx::elect_one()) {
+            constexpr int kBlk = (int)(SM::kSF >> 4);
+            ptx::tc_cp_sf_pair(fa, dsa);
+            ptx::tc_cp_sf_pair(fb0, dsb);
+            ptx::tc_cp_sf_pair(fb0 + 4, dsb + kBlk);
+            if constexpr (F8) {
+              ptx::tc_mma_f8f4_pair(d, da, db, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 0), fa, fb, acc);
+              ptx::tc_mma_f8f4_pair(d, da + 2, db + 2, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 1), fa,
+                                    fb, 1u);
+              ptx::tc_mma_f8f4_pair(d, da + 4, db + 4, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 2), fa,
+                                    fb, 1u);
+              ptx::tc_mma_f8f4_pair(d, da + 6, db + 6, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 3), fa,
+                                    fb, 1u);
+            } else {
+              if (whole) {
+                ptx::tc_cp_sf_pair(fa + 4, dsa + 32);
+                ptx::tc_cp_sf_pair(fb0 + 8, dsb + 32);
+                ptx::tc_cp_sf_pair(fb0 + 12, dsb + kBlk + 32);
+              }
+              ptx::tc_mma_mxf4_pair(d, da, db, id0, fa, fb, acc);
+              ptx::tc_mma_mxf4_pair(d, da + 2, db + 2, id2, fa, fb, 1u);
+              if (whole) {
+                ptx::tc_mma_mxf4_pair(d, da + 4, db + 4, id0, fa + 4, fb + 8, 1u);
+                ptx::tc_mma_mxf4_pair(d, da + 6, db + 6, id2, fa + 4, fb + 8, 1u);
+              }
+            }
+            ptx::tc_commit_pair_both(&tail->empty[stage]);
+          }
+          __syncwarp();
+          sfbuf ^= 1u;
+          if (++stage == kSt) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (ptx::elect_one()) ptx::tc_commit_pair_both(&tail->acc_full[ab]);
+        __syncwarp();
+        if (ab) acc_phase ^= 1u;
+        ab ^= 1;
+      }
+      if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
+      // every MMA issued here finishes before the pair's memory goes
+      if (ptx::elect_one()) ptx::tc_commit_pair(ptx::mapa_shared(ptx::smem_addr(&tail->mma_done), 0));
+      __syncwarp();
+      int never = 0;
+      ptx::mbar_wait(&tail->mma_done, 0, &never, kWaitLimitNs);
+    }
+  } else {
+    const int q = warp & 3, hh = (warp - 2) >> 2;   // lane quarter; even or odd chunks
+    const uint32_t acc_empty_l = ptx::mapa_shared(ptx::smem_addr(&tail->acc_empty[0]), 0);
+    int ab = 0;
+    uint32_t acc_phase = 0;
+    for (int g = first; g < total; g += step) {
+      const int m0 = g / pairs * kPairRows, cols = min(kPairRows, a.M - m0);
+      const int n0 = (g % pairs * 2 + (int)rank) * 128 + q * 32, n = n0 + lane;
+      if (!ptx::mbar_wait(&tail->acc_full[ab], acc_phase, abort_flag, kWaitLimitNs)) {
+        if (lane == 0) atomicOr(&a.flags[0], kErrTimeout);
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * kPairRows);
+      if (n0 < a.N) {
+        // two chunks of 16 rows a turn, the second's load behind the first's stores
+#pragma unroll 1
+        for (int c0 = hh * 16; c0 < cols; c0 += 64) {
+          uint32_t r0[16], r1[16];
+          const bool two = c0 + 32 < cols;
+          ptx::tmem_ld16_issue(taddr + (uint32_t)c0, r0);
+          ptx::tmem_wait_ld(r0);
+          if (two) ptx::tmem_ld16_issue(taddr + (uint32_t)(c0 + 32), r1);
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r0[j]);
+          lin_store16(a, m0 + c0, min(16, cols - c0), n, v);
+          if (two) {
+            ptx::tmem_wait_ld(r1);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r1[j]);
+            lin_store16(a, m0 + c0 + 32, min(16, cols - c0 - 32), n, v);
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(acc_empty_l + (uint32_t)ab * 8u);
+      if (ab) acc_phase ^= 1u;
+      ab ^= 1;
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves, nor frees its tensor memory, while the pair may still use it
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, kPairTmemCols);
   }
 }
 
@@ -412,30 +724,34 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_w = ptx::policy_evict_normal();
-      const uint64_t pol_t = ptx::policy_evict_last();
-      const uint8_t* wsf = a.w_sf + (size_t)slab * a.kc4 * kSFAtomBytes;
-      const uint8_t* tsf = a.t_sf + (size_t)(tile * TN >> 7) * a.kc4 * kSFAtomBytes;
-      auto tokens = [&](int kb, int s) {
-        const int atoms = min(kKb, a.K - kb * kKb) / 128;
-        ptx::tma_load_2d(smem + SM::kB + (size_t)s * SM::kBSlot, &tmap_x, kb * kBKBytes, m0,
-                         &tail->full[s], pol_t);
-        ptx::bulk_load(smem + SM::kSFB + (size_t)s * SM::kSF,
-                       tsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes,
+    // the whole warp runs the loop; one lane issues
+    const uint64_t pol_w = ptx::policy_evict_normal();
+    const uint64_t pol_t = ptx::policy_evict_last();
+    const uint8_t* wsf = a.w_sf + (size_t)slab * a.kc4 * kSFAtomBytes;
+    const uint8_t* tsf = a.t_sf + (size_t)(tile * TN >> 7) * a.kc4 * kSFAtomBytes;
+    auto tokens = [&](int kb, int s) {
+      const int atoms = min(kKb, a.K - kb * kKb) / 128;
+      ptx::tma_load_2d(smem + SM::kB + (size_t)s * SM::kBSlot, &tmap_x, kb * kBKBytes, m0,
                        &tail->full[s], pol_t);
-      };
-      int stage = 0;
-      uint32_t phase = 0;
-      int kb = kb0;
-      for (; kb < kb1; ++kb) {
-        // The first stages' weights do not wait for the kernel before this one.
-        if (!QUANT && kb - kb0 == kSt) {
-          ptx::pdl_wait();
-          for (int j = 0; j < kSt; ++j) tokens(kb0 + j, j);
-        }
-        ok = ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
-        if (!ok) break;
+      ptx::bulk_load(smem + SM::kSFB + (size_t)s * SM::kSF,
+                     tsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes,
+                     &tail->full[s], pol_t);
+    };
+    // The first stages' weights do not wait for the kernel before this one; their rows do.
+    auto release = [&](int n) {
+      ptx::pdl_wait();
+      if (ptx::elect_one())
+        for (int j = 0; j < n; ++j) tokens(kb0 + j, j);
+      __syncwarp();
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!QUANT && kb - kb0 == kSt) release(kSt);
+      ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
+                                                kWaitLimitNs));
+      if (!ok) break;
+      if (ptx::elect_one()) {
         const int atoms = min(kKb, a.K - kb * kKb) / 128;
         uint64_t* bar = &tail->full[stage];
         // a widened E2M1 box (F8) counts its packed bytes only
@@ -448,16 +764,14 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
                        wsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes, bar,
                        pol_w);
         if (!QUANT && kb - kb0 >= kSt) tokens(kb, stage);
-        if (++stage == kSt) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      if (!QUANT && kb1 - kb0 <= kSt) {
-        ptx::pdl_wait();
-        for (int j = 0; j < kb1 - kb0; ++j) tokens(kb0 + j, j);
+      __syncwarp();
+      if (++stage == kSt) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
+    if (!QUANT && kb1 - kb0 <= kSt) release(kb1 - kb0);
   } else if (warp == 1) {
     {
       const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
@@ -566,9 +880,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       for (int c0 = 0; c0 < cols; c0 += 16) {
         float v[16];
         ptx::tmem_ld16(taddr + (uint32_t)c0, v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c0 + j < cols && n < a.N) lin_store(a, m0 + c0 + j, n, v[j]);
+        lin_store16(a, m0 + c0, min(16, cols - c0), n, v);
       }
     }
   } else {
@@ -702,6 +1014,43 @@ cudaError_t launch_tile(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
   }
 }
 
+template <bool F8>
+cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
+  constexpr size_t kBytes = LinPairSmem<F8>::kBytes;
+  LinPairMaps m;
+  const uint64_t w_rows = (uint64_t)a.slabs * a.num_kb * kBM;
+  if (w_rows > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  cudaError_t e = F8 ? make_tmap_e2m1_wide(&m.w, g.w_codes, 128, w_rows)
+                     : make_tmap(&m.w, g.w_codes, kBKBytes, w_rows, kBM);
+  const uint64_t row_blocks = (uint64_t)(a.M + 127) / 128;
+  if (e != cudaSuccess ||
+      (e = make_tmap(&m.x, g.q, F8 ? (uint64_t)a.K : (uint64_t)a.K / 2, (uint64_t)a.M,
+                     kPairHalf)) ||
+      (e = make_tmap_scales(&m.wsf, a.w_sf, (uint64_t)a.slabs * a.kc4, 1, F8 ? 1 : 2, 1)) ||
+      (e = make_tmap_scales(&m.tsf, a.t_sf, (uint64_t)a.kc4, row_blocks, F8 ? 1 : 2, 2)))
+    return e;
+  a.tiles = (a.M + kPairRows - 1) / kPairRows;
+  const int64_t items = (int64_t)a.tiles * ((a.slabs + 1) / 2);
+  if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  // clusters that fit at once (a GPC may have an odd number of SMs), for the device of
+  // the first launch
+  static int clusters = 0;
+  if (clusters == 0) {
+    if ((e = allow_smem(linear_pair_kernel<F8>, kBytes)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(g.num_sms);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    int c = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&c, linear_pair_kernel<F8>, &cfg)) != cudaSuccess)
+      return e;
+    if (c < 1) return cudaErrorInvalidConfiguration;
+    clusters = c < g.num_sms / 2 ? c : g.num_sms / 2;
+  }
+  const int grid = 2 * (int)(items < clusters ? items : clusters);
+  return launch_pdl(linear_pair_kernel<F8>, dim3(grid), dim3(kPairThreads), kBytes, st, m, a);
+}
+
 int grid_for(int64_t n) {
   const int64_t b = (n + 255) / 256;
   return (int)(b < 1 ? 1 : b > 16384 ? 16384 : b);
@@ -727,13 +1076,19 @@ cudaError_t launch_linear_prepare(const LinearShape& s, const uint8_t* codes,
 cudaError_t launch_linear_quantize(const LinearShape& s, const void* x, int64_t ldx, int64_t rows,
                                    uint8_t* q, uint8_t* sf, cudaStream_t st) {
   const int Kp = linear_padded_k(s);
-  const int64_t vecs = rows * (Kp / 8);
-  const dim3 grid((unsigned)grid_for(vecs));
   auto* xp = static_cast<const uint16_t*>(x);
-  return s.f8 ? launch_pdl(linear_quantize_kernel<true>, grid, dim3(kQuantThreads), 0, st, xp, ldx,
-                           rows, s.K, Kp, q, sf)
-              : launch_pdl(linear_quantize_kernel<false>, grid, dim3(kQuantThreads), 0, st, xp,
-                           ldx, rows, s.K, Kp, q, sf);
+  int span_log = 4;   // columns of a block: a power of two, at least a scale word
+  while (span_log < 8 && (8 << span_log) < Kp) ++span_log;
+  const unsigned spans = (unsigned)((Kp / 8 + (1 << span_log) - 1) >> span_log);
+  auto go = [&](auto kernel, int r) {
+    const int64_t per = (int64_t)r * (kQuantThreads >> span_log);
+    return launch_pdl(kernel, dim3((unsigned)((rows + per - 1) / per), spans), dim3(kQuantThreads),
+                      0, st, xp, ldx, rows, s.K, Kp, q, sf, span_log);
+  };
+  // four rows a thread once that leaves blocks enough for every SM
+  if (rows * (Kp / 8) >= (int64_t)1 << 20)
+    return s.f8 ? go(linear_quantize_kernel<true, 4>, 4) : go(linear_quantize_kernel<false, 4>, 4);
+  return s.f8 ? go(linear_quantize_kernel<true, 1>, 1) : go(linear_quantize_kernel<false, 1>, 1);
 }
 
 cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
@@ -744,6 +1099,8 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
   a.out = g.out;
   a.ldo = g.ldo;
   a.out_f32 = g.out_f32;
+  a.pairs16 = !g.out_f32 && s.N % 2 == 0 && g.ldo % 2 == 0 &&
+              reinterpret_cast<uintptr_t>(g.out) % 4 == 0;
   a.x = static_cast<const uint16_t*>(g.x);
   a.ldx = g.ldx;
   a.flags = g.flags;
@@ -754,15 +1111,29 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
   a.slabs = (s.N + 127) / 128;
   a.num_kb = linear_num_kb(s);
   a.kc4 = a.K / 128;
-  // Rows a tile: few rows take the narrowest that holds them; while 128-row tiles would not
-  // give every SM one, 64-row tiles (317 x 1001 x 1056: 8.3 against 10.8 us; 512 x 4096 x
-  // 4096: 14.5 against 17.6).
-  const int tn = a.M <= 32 ? 32 : (int64_t)((a.M + 127) / 128) * a.slabs <= g.num_sms ? 64 : 128;
-  if (s.f8)
-    return tn == 32 ? launch_tile<true, 32>(g, a, st)
-           : tn == 64 ? launch_tile<true, 64>(g, a, st) : launch_tile<true, 128>(g, a, st);
-  return tn == 32 ? launch_tile<false, 32>(g, a, st)
-         : tn == 64 ? launch_tile<false, 64>(g, a, st) : launch_tile<false, 128>(g, a, st);
+  if (a.M <= 32) return s.f8 ? launch_tile<true, 32>(g, a, st) : launch_tile<false, 32>(g, a, st);
+  // Tiles: 64 rows while 128-row tiles would not give every SM one, else 128, or SM pairs'
+  // 256 x 192, by an estimate in cycles: rounds of tiles times (k-blocks times a tile's
+  // cycles a k-block, plus a tile's fixed part), all fitted to timings.  Measured (us, pair
+  // against the other; MXFP4, then MXFP8 pairs in): 1024 x 4096 x 4096 16.6 / 13.3 and 18.8 /
+  // 15.5 (one round of 128-row tiles, two of pairs); 1536 x 4096 x 4096 18.7 / 21.1 and 20.2 /
+  // 27.5; 4096 x 4096 x 512 16.3 / 14.3 and 15.3 / 14.3; 4096 x 4096 x 2048 26.0 / 27.2 and
+  // 25.1 / 31.6; 16384 x 4096 x 4096 124.8 / 145.4 and 166.4 / 199.0.  Fewer than 24 pairs
+  // leave most of the weights' reads to too few SMs (317 x 1001 x 1056: 12.9 / 8.8).
+  const bool narrow = (int64_t)((a.M + 127) / 128) * a.slabs <= g.num_sms;
+  const int64_t pair_tiles =
+      (int64_t)((a.M + kPairRows - 1) / kPairRows) * ((a.slabs + 1) / 2);
+  const int64_t tiles =
+      (int64_t)(narrow ? (a.M + 63) / 64 : (a.M + 127) / 128) * a.slabs;
+  auto rounds = [](int64_t n, int64_t at_once) { return (n + at_once - 1) / at_once; };
+  const int64_t kb_pair = s.f8 ? 430 : 490;
+  const int64_t kb_tile = narrow ? (s.f8 ? 750 : 600) : (s.f8 ? 850 : 1100);
+  const int64_t t_pair = rounds(pair_tiles, g.num_sms / 2) * (a.num_kb * kb_pair + 2500);
+  const int64_t t_tile = rounds(tiles, 2 * g.num_sms) * (a.num_kb * kb_tile + (narrow ? 1200 : 1500));
+  if (pair_tiles >= 24 && t_pair < t_tile)
+    return s.f8 ? launch_pair<true>(g, a, st) : launch_pair<false>(g, a, st);
+  if (narrow) return s.f8 ? launch_tile<true, 64>(g, a, st) : launch_tile<false, 64>(g, a, st);
+  return s.f8 ? launch_tile<true, 128>(g, a, st) : launch_tile<false, 128>(g, a, st);
 }
 
 }  // namespace mxmoe

@@ -62,4 +62,22 @@ inline cudaError_t make_tmap_e2m1_wide(CUtensorMap* m, const void* base, uint64_
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// 128x4 scale blocks of `row_blocks` 128-row groups of `per_row` 512-byte blocks each, as
+// 256-byte rows in three dimensions, read `blocks` along K by `rows` groups at a time;
+// blocks past the end read as zeros.
+inline cudaError_t make_tmap_scales(CUtensorMap* m, const void* base, uint64_t per_row,
+                                    uint64_t row_blocks, uint32_t blocks, uint32_t rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {256, 2 * per_row, row_blocks};
+  const cuuint64_t strides[2] = {256, 512 * per_row};
+  const cuuint32_t box[3] = {256, 2 * blocks, rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace mxmoe

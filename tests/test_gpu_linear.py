@@ -210,3 +210,33 @@ def test_refusals():
         dims = mx.make_linear_dims(*bad)
         assert mx.moe_linear_workspace_size(dims) == 0 and mx.moe_linear_weights_size(dims) == 0
         refused(status, mx.moe_linear_workspace_init, dims, lin.ws)
+
+
+@pytest.mark.parametrize("mma", [F4, F8])
+@pytest.mark.parametrize("rows,N,K", [(700, 2048, 416), (1300, 2200, 256), (577, 4100, 768),
+                                      (1153, 3201, 1120)])
+def test_tiles_over_sm_pairs(rows, N, K, mma):
+    # several 192-row tiles that start in the middle of a scale block, an odd number of
+    # weight slabs, features past the last whole slab, a last k-block of half width
+    lin = Linear(N, K, rows, mma)
+    x = inputs(rows, K)
+    for dtype in (torch.bfloat16, torch.float32):
+        out = torch.full((rows, N), float("nan"), dtype=dtype, device="cuda")
+        mx.moe_linear_forward(lin.dims, lin.prepared, x, out, lin.ws)
+        mx.moe_linear_check(lin.ws)
+        lin.check(out, x)
+
+
+def test_pair_in_on_sm_pairs_does_not_read_past_its_scales():
+    # 577 rows: the last tile's second scale block lies past the end of sf
+    rows, N, K = 577, 4096, 512
+    lin = Linear(N, K, rows, F8)
+    x = inputs(rows, K)
+    q = torch.empty(rows, K, dtype=torch.uint8, device="cuda")
+    n = mx.moe_mxfp8_scale_bytes(rows, K, mx.MOE_SF_128X4)
+    buf = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    mx.moe_mxfp8_quantize(x, rows, K, q, buf[:n], mx.MOE_SF_128X4)
+    out = torch.empty(rows, N, dtype=torch.float32, device="cuda")
+    mx.moe_linear_forward_pair(lin.dims, lin.prepared, q, buf[:n], rows, out, lin.ws)
+    mx.moe_linear_check(lin.ws)
+    lin.check(out, x)
