@@ -35,6 +35,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -340,6 +341,29 @@ __device__ __forceinline__ void route(const FewArgs& a, RouteScratch& sc, FewTai
       }
     }
   };
+  if (a.router && a.T == 1 && E <= 256) {
+    // One token: its j-th expert is slot j, straight from the warp that chose it (2.4 us of
+    // routing with the steps below, 1.9 so).
+    if (warp == 0) {
+      uint32_t key[8];
+      int id;
+      float w;
+      load_keys<8>(a.logits, E, lane, key);
+      top_k<8>(key, k, lane, id, w);
+      if (lane < k) {
+        tail->list[lane] = make_int2(id | lane << 16, 1);
+        tail->weight[lane] = w;
+        if (blockIdx.x == 0) {
+          a.ids[lane] = id;
+          a.weights[lane] = w;
+        }
+      }
+      if (lane == 0) tail->slots = k;
+    }
+    ptx::fence_proxy_async_smem();   // the cleared scratch is written by TMA copies next
+    __syncthreads();
+    return;
+  }
   constexpr int kWarps = kFewThreads / 32, kRounds = (kFewTokens + kWarps - 1) / kWarps;
   if (!a.router) {
     for (int t = warp; t < a.T; t += kWarps) {
@@ -856,9 +880,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
                                               : (lane & 7) * 2 + (lane >> 4));
 #pragma unroll
           for (int p = 0; p < kFewN / 2; ++p) {
-            const float x = __shfl_xor_sync(kFullW, up ? v[2 * p] : v[2 * p + 1], 8);
-            const float g = up ? x : v[2 * p], u = up ? v[2 * p + 1] : x;
-            tail->h[2 * p + (up ? 1 : 0)][f] = __fdividef(g, 1.0f + __expf(-g)) * u;
+            if (2 * p < T) {
+              const float x = __shfl_xor_sync(kFullW, up ? v[2 * p] : v[2 * p + 1], 8);
+              const float g = up ? x : v[2 * p], u = up ? v[2 * p + 1] : x;
+              tail->h[2 * p + (up ? 1 : 0)][f] = __fdividef(g, 1.0f + __expf(-g)) * u;
+            }
           }
           ptx::named_bar_sync(1, 128);
           // 16 columns x 64 features: eight threads a column, eight features each
@@ -900,9 +926,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
           }
           ptx::named_bar_sync(1, 128);   // all stored; the buffer is free again
           if (ep == 0) {
-            __threadfence();
             ptx::fence_proxy_async_global();
-            atomicAdd(&a.ctrl[kCtlDone], 1);
+            ptx::red_add_release(&a.ctrl[kCtlDone], 1);
           }
         }
       } else {
@@ -964,12 +989,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
 template <int FMT>
 cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   constexpr size_t kBytes = few_smem_bytes<FMT>();
-  static bool set = false;
-  if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(few_expert_kernel<FMT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+  static std::atomic<bool> set{false};   // once a process; a failure is tried again
+  if (!set.load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        few_expert_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
     if (e != cudaSuccess) return e;
-    set = true;
+    set.store(true, std::memory_order_relaxed);
   }
   FewArgs a = g.args;
   const Shape& s = g.shape;

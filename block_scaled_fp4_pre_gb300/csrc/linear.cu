@@ -25,6 +25,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "ptx.cuh"
 #include "tmap.cuh"
@@ -952,17 +954,23 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int cluster, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Raises a kernel's shared-memory limit once a process; a failure is tried again.
 template <typename K>
-cudaError_t allow_smem(K* kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<bool>& done) {
+  if (done.load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.store(true, std::memory_order_relaxed);
+  return e;
 }
 
 template <bool F8, int TN, bool QUANT>
 cudaError_t launch_split(const CUtensorMap& tw, const CUtensorMap& tx, const LinArgs& a, int parts,
                          cudaStream_t st) {
   constexpr size_t kBytes = LinSmem<F8, TN>::kBytes;
-  static const cudaError_t allowed = allow_smem(linear_split_kernel<F8, TN, QUANT>, kBytes);
-  if (allowed != cudaSuccess) return allowed;
+  static std::atomic<bool> set{false};
+  const cudaError_t e = allow_smem(linear_split_kernel<F8, TN, QUANT>, kBytes, set);
+  if (e != cudaSuccess) return e;
   return launch_cluster(linear_split_kernel<F8, TN, QUANT>, a.tiles * a.slabs * parts, parts,
                         kBytes, st, tw, tx, a, parts);
 }
@@ -1006,8 +1014,8 @@ cudaError_t launch_tile(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
                  : launch_split<F8, TN, false>(tw, tx, a, parts, st);
   } else {
     if (parts > 1) return launch_split<F8, TN, false>(tw, tx, a, parts, st);
-    static const cudaError_t allowed = allow_smem(linear_kernel<F8, TN>, kBytes);
-    if (allowed != cudaSuccess) return allowed;
+    static std::atomic<bool> set{false};
+    if ((e = allow_smem(linear_kernel<F8, TN>, kBytes, set)) != cudaSuccess) return e;
     const int grid = (int)(items < blocks ? items : blocks);
     return launch_pdl(linear_kernel<F8, TN>, dim3(grid), dim3(kLinThreads), kBytes, st, tw, tx,
                       a);
@@ -1034,9 +1042,11 @@ cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
   // clusters that fit at once (a GPC may have an odd number of SMs), for the device of
   // the first launch
-  static int clusters = 0;
+  static std::atomic<int> fit{0};
+  int clusters = fit.load(std::memory_order_relaxed);
   if (clusters == 0) {
-    if ((e = allow_smem(linear_pair_kernel<F8>, kBytes)) != cudaSuccess) return e;
+    static std::atomic<bool> set{false};
+    if ((e = allow_smem(linear_pair_kernel<F8>, kBytes, set)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(g.num_sms);
     cfg.blockDim = dim3(kPairThreads);
@@ -1046,6 +1056,7 @@ cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
       return e;
     if (c < 1) return cudaErrorInvalidConfiguration;
     clusters = c < g.num_sms / 2 ? c : g.num_sms / 2;
+    fit.store(clusters, std::memory_order_relaxed);
   }
   const int grid = 2 * (int)(items < clusters ? items : clusters);
   return launch_pdl(linear_pair_kernel<F8>, dim3(grid), dim3(kPairThreads), kBytes, st, m, a);

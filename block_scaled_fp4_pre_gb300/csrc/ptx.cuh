@@ -103,6 +103,10 @@ __device__ __forceinline__ int atomic_add_acq_rel(int32_t* p, int v) {
                : "memory");
   return old;
 }
+// Adds to *p; releases as above.
+__device__ __forceinline__ void red_add_release(int32_t* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 // Waits until *p >= target (acquire), bounded like mbar_wait: gives up when *abort
 // becomes nonzero or after limit_ns, setting *abort in the latter case.
 __device__ __forceinline__ bool wait_counter(const int32_t* p, int target, volatile int* abort,
