@@ -46,9 +46,8 @@ namespace mxmoe {
 namespace {
 
 constexpr unsigned kFullW = 0xFFFFFFFFu;
-constexpr int kLogitThreads = 512;
 constexpr int kLogitExperts = 2;          // experts a block
-constexpr int kLogitSplit = 4;            // warps that share a row of Wr (and 8 tokens each)
+constexpr int kLogitSplit = 4;            // warps that share a row of Wr
 constexpr int kFewThreads = 192;
 constexpr int kFewBlocksPerSM = 2;
 constexpr int kFewN = kFewTokens;         // MMA columns
@@ -59,10 +58,9 @@ constexpr int kFewSfCol = kFewAccs * kFewN;   // two buffers of scale registers
 constexpr int kFewRing = 4;
 constexpr int kFewMaxSlots = kFewTokens * 32;
 
-// ws.ctrl words, all zero between calls
+// ws.ctrl words, cleared by the logits kernel
 constexpr int kCtlClaim = 0;     // next range
-constexpr int kCtlDone = 1;      // intermediate slabs written
-constexpr int kCtlExit = 2;      // blocks of the expert kernel done
+constexpr int kCtlDone = 32;     // intermediate slabs written (a cache line of its own)
 
 enum Fmt { kMx4 = 0, kMx8 = 1, kNv4 = 2 };
 
@@ -128,18 +126,29 @@ __device__ __forceinline__ void top_k(uint32_t (&key)[R], int k, int lane, int& 
   weight = w / sum;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kLogitThreads, 1) few_logits_kernel(const FewArgs a) {
-  __shared__ float part[kLogitThreads / 32][kFewTokens / 2];
+// LIGHT: at most two tokens, in blocks small enough (64 registers, 256 threads) to sit
+// beside the expert kernel's two: in a decode loop the next call's blocks then wait on the
+// SMs when an expert kernel ends, instead of being launched (1 token 32.8 -> @LIGHT@ us).
+// Otherwise 512 threads, the second half of the warps for tokens 8 to 15.
+template <int FMT, bool LIGHT>
+__global__ void __launch_bounds__(LIGHT ? 256 : 512, LIGHT ? 4 : 1)
+    few_logits_kernel(const FewArgs a) {
+  constexpr int kThreads = LIGHT ? 256 : 512, kHalves = LIGHT ? 1 : 2;
+  constexpr int kTok = LIGHT ? 2 : kFewTokens / 2;   // tokens a warp takes
+  __shared__ float part[kThreads / 32][kTok];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = a.T, H = a.H, E = a.E;
   ptx::pdl_wait();
-  ptx::pdl_launch_dependents();   // after the wait: the expert kernel claims before its own
+  ptx::pdl_launch_dependents();
+  if (blockIdx.x == 0 && tid == 0) {   // the expert kernel's counters, for this call
+    a.ctrl[kCtlClaim] = 0;
+    a.ctrl[kCtlDone] = 0;
+  }
   // x quantised: a thread takes 8 elements, four lanes a scale (two for NVFP4)
   {
     const int vecs = H / 8, total = T * vecs;
-    for (int i = (int)(blockIdx.x * kLogitThreads) + tid; i - lane < total;
-         i += (int)gridDim.x * kLogitThreads) {
+    for (int i = (int)(blockIdx.x * kThreads) + tid; i - lane < total;
+         i += (int)gridDim.x * kThreads) {
       const bool live = i < total;
       const int t = live ? i / vecs : 0, c = live ? i - t * vecs : 0;
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -180,12 +189,12 @@ __global__ void __launch_bounds__(kLogitThreads, 1) few_logits_kernel(const FewA
   // Warp (g, s, p): expert g of the block, half s of the tokens, part p of the row.  Loads
   // come in batches of four 16-byte vectors of the row and of B tokens, before any
   // arithmetic.
-  const int g = warp >> 3, half = (warp >> 2) & 1, p = warp & 3;
+  const int g = warp / (kLogitSplit * kHalves), half = (warp >> 2) & (kHalves - 1), p = warp & 3;
   const int e = (int)blockIdx.x * kLogitExperts + g;
-  const int tok0 = half * (kFewTokens / 2);
-  float acc[kFewTokens / 2];
+  const int tok0 = half * kTok;
+  float acc[kTok];
 #pragma unroll
-  for (int t = 0; t < kFewTokens / 2; ++t) acc[t] = 0.f;
+  for (int t = 0; t < kTok; ++t) acc[t] = 0.f;
   auto dots = [&](auto batch) {
     constexpr int B = decltype(batch)::value;
     const uint16_t* wr = a.router + (size_t)e * H;
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) few_logits_kernel(const FewA
         if (c < vecs) w[i] = *reinterpret_cast<const uint4*>(wr + c * 8);
       }
 #pragma unroll
-      for (int t0 = 0; t0 < kFewTokens / 2; t0 += B) {
+      for (int t0 = 0; t0 < kTok; t0 += B) {
         if (tok0 + t0 >= T) break;
         uint4 xv[B][4];
 #pragma unroll
@@ -228,13 +237,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1) few_logits_kernel(const FewA
     }
   };
   if (e < E && tok0 < T) {
-    if (T == 1)
-      dots(std::integral_constant<int, 1>());
-    else
-      dots(std::integral_constant<int, 4>());
+    dots(std::integral_constant<int, LIGHT ? 1 : 4>());
   }
 #pragma unroll
-  for (int t = 0; t < kFewTokens / 2; ++t) {
+  for (int t = 0; t < kTok; ++t) {
     if (tok0 + t < T) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(kFullW, acc[t], o);
@@ -242,10 +248,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1) few_logits_kernel(const FewA
     }
   }
   __syncthreads();
-  if (tid < kLogitExperts * kFewTokens) {
-    const int gg = tid / kFewTokens, t = tid % kFewTokens;
+  if (tid < kLogitExperts * kHalves * kTok) {
+    const int gg = tid / (kHalves * kTok), t = tid % (kHalves * kTok);
     const int ee = (int)blockIdx.x * kLogitExperts + gg;
-    const int w0 = gg * 8 + t / (kFewTokens / 2) * 4, tt = t % (kFewTokens / 2);
+    const int w0 = (gg * kHalves + t / kTok) * kLogitSplit, tt = t % kTok;
     if (t < T && ee < E)
       a.logits[(size_t)t * E + ee] =
           (part[w0][tt] + part[w0 + 1][tt]) + (part[w0 + 2][tt] + part[w0 + 3][tt]);
@@ -499,12 +505,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
   for (int e = threadIdx.x; e < a.E; e += kFewThreads) scratch.mask[e] = 0u;
   if (threadIdx.x == 0) tail->weights_used = 0;
   __syncthreads();
-  // The first claim overlaps the kernel before: that one started after the call before
-  // this one had reset the counter.
-  int claim = 0;
-  if (threadIdx.x == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
+  int claim = 0;
+  if (threadIdx.x == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);   // answered during route()
   route(a, scratch, tail);
 
   const int slots = tail->slots;
@@ -643,7 +647,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
           }
           __syncwarp();
           // The next range, claimed late: a block that runs behind should not hold one.
-          if (c.t == max(t0, c.t1 - 2) && lane == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
+          // (In phase 1 after the last tile, so that no block takes two ranges while it
+          // waits for the intermediate rows.)
+          if (!down && c.t == max(t0, c.t1 - 2) && lane == 0)
+            claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
           ++issued;
           if (++stage == kSt) {
             stage = 0;
@@ -652,6 +659,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
         }
         if (ok && down && !waited) release(c.t1);   // a range shorter than the stages
         if (!ok) break;
+        if (down && lane == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
         claim = __shfl_sync(kFullW, claim, 0);
         next = open(claim);
       }
@@ -975,15 +983,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, kFewTmemCols);
   }
-  if (threadIdx.x == 0) {
-    // the last block out resets the counters for the next call
-    __threadfence();
-    if (atomicAdd(&a.ctrl[kCtlExit], 1) == (int)gridDim.x - 1) {
-      a.ctrl[kCtlClaim] = 0;
-      a.ctrl[kCtlDone] = 0;
-      a.ctrl[kCtlExit] = 0;
-    }
-  }
 }
 
 template <int FMT>
@@ -1016,9 +1015,12 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   if ((e = make_tmap(&mx, a.xq, f8 ? s.H : s.H / 2, kFewN, a.t_rows)) ||
       (e = make_tmap(&mh, a.hq, f8 ? s.I : s.I / 2, (uint64_t)g.slots_cap * kFewN, a.t_rows)))
     return e;
+  const bool light = a.T <= 2;
+  const int threads = light ? 256 : 512;
   const int blocks = a.router ? (s.E + kLogitExperts - 1) / kLogitExperts
-                              : (a.T * (s.H / 8) + kLogitThreads - 1) / kLogitThreads;
-  e = launch_pdl(few_logits_kernel<FMT>, dim3(blocks), dim3(kLogitThreads), 0, st, a);
+                              : (a.T * (s.H / 8) + threads - 1) / threads;
+  e = light ? launch_pdl(few_logits_kernel<FMT, true>, dim3(blocks), dim3(threads), 0, st, a)
+            : launch_pdl(few_logits_kernel<FMT, false>, dim3(blocks), dim3(threads), 0, st, a);
   if (e != cudaSuccess) return e;
   int grid = kFewBlocksPerSM * g.num_sms;
   if (grid > kFewBlocks) grid = kFewBlocks;
