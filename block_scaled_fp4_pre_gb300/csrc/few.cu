@@ -27,13 +27,17 @@
 //   memory serves faster takes more of them (equal shares ended 15% apart).  The first
 //   stages of a phase 1 range hold its weights before that wait.
 // - Phase 1 (down) runs slab by slab over the experts, so a block adds the experts'
-//   weighted products in registers and leaves one sum per slab it touches.
+//   weighted products in registers and leaves one sum per slab it touches.  With up to
+//   kClusterTokens tokens, where those joins at the end are a large part of the time, a
+//   cluster of eight blocks takes a slab and adds its eight sums in shared memory.
 //
 // Roles (192 threads, two blocks an SM): warp 0 claims and issues the TMA copies, warp 1
 // issues the MMAs, warps 2-5 read the accumulators (four of 16 columns each in flight).
 // Every wait is bounded (kWaitLimitNs); a timeout sets the workspace's error flag.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <stddef.h>
 
 #include <atomic>
 #include <type_traits>
@@ -56,6 +60,8 @@ constexpr int kFewLeast = 5;         // least tiles of a range (a whole line whe
 constexpr int kFewTmemCols = 256;
 constexpr int kFewSfCol = kFewAccs * kFewN;   // two buffers of scale registers
 constexpr int kFewRing = 4;
+constexpr int kClusterTokens = 4;
+constexpr int kFewCluster = 8;
 constexpr int kFewMaxSlots = kFewTokens * 32;
 
 // ws.ctrl words, cleared by the logits kernel
@@ -282,12 +288,18 @@ struct __align__(16) FewTail {
   int abort;
   int last;
   int slots, weights_used;
-  float h[kFewN][68];        // one slab's SwiGLU outputs (64 features, padded rows)
+  // One slab's SwiGLU outputs (64 features, padded rows); at the end of a clustered call the
+  // cluster's sums, stored 16 bytes at a time.
+  alignas(16) float h[kFewN][68];
   // Touched experts: (expert | first weight << 16, tokens as bits), and their tokens'
   // routing weights.
   int2 list[kFewMaxSlots];
   float weight[kFewMaxSlots];
 };
+
+static_assert(offsetof(FewTail, h) % 16 == 0 && FewSmem<kMx4>::kTail % 16 == 0 &&
+                  FewSmem<kMx8>::kTail % 16 == 0 && FewSmem<kNv4>::kTail % 16 == 0,
+              "the cluster's sums are stored 16 bytes at a time");
 
 // Scratch of the routing, in the operand stages before any copy into them.
 struct RouteScratch {
@@ -310,6 +322,7 @@ static_assert(2 * (few_smem_bytes<kNv4>() + 1024) <= 228 * 1024, "two blocks per
 // slab * slots + slot.
 struct Plan {
   int n, kb, ranges, q, rem;
+  int span = 0;   // not 0: eight ranges to each `span` tiles (clusters' slabs)
   // One range a block, of at least kFewLeast tiles or a line, since each cut costs a join
   // (finer ranges measured slower: 16 tokens 213 to 225 us against 205, 1 token 46 against
   // 33).  whole: phase 0 with four lines and more a block takes lines, which need no join
@@ -323,7 +336,14 @@ struct Plan {
     q = n / ranges;
     rem = n - q * ranges;
   }
-  __device__ __forceinline__ int start(int r) const { return r * q + min(r, rem); }
+  // One slab of `slab_tiles` tiles a cluster.
+  __device__ __forceinline__ Plan(int slabs, int slab_tiles, int kb_line)
+      : n(slabs * slab_tiles), kb(kb_line), ranges(slabs * kFewCluster), q(0), rem(0),
+        span(slab_tiles) {}
+  __device__ __forceinline__ int start(int r) const {
+    if (span) return r / kFewCluster * span + r % kFewCluster * span / kFewCluster;
+    return r * q + min(r, rem);
+  }
   // the range that holds tile t
   __device__ __forceinline__ int range_of(int t) const {
     const int big = rem * (q + 1);
@@ -455,7 +475,8 @@ __device__ __forceinline__ void route(const FewArgs& a, RouteScratch& sc, FewTai
   __syncthreads();
 }
 
-template <int FMT>
+// CLUSTER: launched in clusters of kFewCluster; phase 1 slab c is cluster c's.
+template <int FMT, bool CLUSTER>
 __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
     few_expert_kernel(const __grid_constant__ CUtensorMap tmap_w1,
                       const __grid_constant__ CUtensorMap tmap_x,
@@ -516,8 +537,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
   const int kb0 = (a.H + kKb - 1) / kKb, kb1 = (a.I + kKb - 1) / kKb;
   const int blocks = (int)gridDim.x;
   const Plan P0(slots * m0 * kb0, kb0, blocks, true);
-  const Plan P1(slots * m1 * kb1, kb1, blocks, false);
+  const Plan P1 = CLUSTER ? Plan(m1, slots * kb1, kb1) : Plan(slots * m1 * kb1, kb1, blocks, false);
   const int R0 = P0.ranges, R = R0 + P1.ranges;
+  float sum[kFewN];   // phase 1: weighted sums of this thread's output feature
+#pragma unroll
+  for (int c = 0; c < kFewN; ++c) sum[c] = 0.f;
 
   if (slots == 0) {
     // no valid assignment: zeros
@@ -572,8 +596,17 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       int stage = 0, r = 0;
       uint32_t phase = 0, rph = 0;
       int64_t issued = 0;
-      bool ok = true, waited = false;
-      Cursor next = open(claim);
+      bool ok = true, waited = false, own_left = true;
+      // The range of a claim; past phase 0, with clusters, the block's own, once.
+      auto take_claim = [&]() {
+        if (CLUSTER && claim >= R0) {
+          const int own = own_left && (int)blockIdx.x < P1.ranges ? R0 + (int)blockIdx.x : R;
+          own_left = false;
+          return open(own);
+        }
+        return open(claim);
+      };
+      Cursor next = take_claim();
       while (true) {
         Cursor c = next;
         ok = __all_sync(kFullW, ptx::mbar_wait(&tail->ring_empty[r], rph ^ 1u, abort_flag,
@@ -659,9 +692,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
         }
         if (ok && down && !waited) release(c.t1);   // a range shorter than the stages
         if (!ok) break;
-        if (down && lane == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
+        if (!CLUSTER && down && lane == 0) claim = atomicAdd(&a.ctrl[kCtlClaim], 1);
         claim = __shfl_sync(kFullW, claim, 0);
-        next = open(claim);
+        next = take_claim();
       }
       if (!ok && lane == 0) atomicOr(&a.flags[0], kErrTimeout);
       // Every copy issued here must have landed before the block exits.  (After a timeout
@@ -941,9 +974,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
       } else {
         // ---- down: the experts' products, weighted, summed slab by slab
         const int rg = idx - R0, t1 = P1.start(rg + 1);
-        float sum[kFewN];
-#pragma unroll
-        for (int c = 0; c < kFewN; ++c) sum[c] = 0.f;
         const int span = slots * kb1;   // tiles of one output slab
         int line = P1.start(rg) / kb1, slab = line / slots, slot = line - slab * slots;
         for (int t = P1.start(rg); t < t1; ++line, ++slot) {
@@ -960,7 +990,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
 #pragma unroll
           for (int c = 0; c < kFewN; ++c)
             if ((chosen >> c) & 1u) sum[c] = fmaf(*w++, v[c], sum[c]);
-          if (t == t1 || t == (slab + 1) * span) {
+          if (!CLUSTER && (t == t1 || t == (slab + 1) * span)) {
             if (join(sum, P1, a.parts1, a.counters1 + slab, rg, slab * span, (slab + 1) * span)) {
               const int n = slab * kBM + row;
 #pragma unroll
@@ -977,6 +1007,32 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
     if (!ok && ep == 0) atomicOr(&a.flags[0], kErrTimeout);
   }
 
+  if (CLUSTER && slots > 0 && (int)blockIdx.x < P1.ranges) {
+    // The cluster's sums of its slab: block p adds features [16 p, 16 p + 16), in the order
+    // of the blocks.  The buffer is [part][feature][token], in the room of phase 0's h,
+    // which every block has left: their sums rest on all of it.
+    constexpr int kShare = kBM / kFewCluster;
+    float* const sums = &tail->h[0][0];
+    const int part = (int)blockIdx.x % kFewCluster, slab = (int)blockIdx.x / kFewCluster;
+    __syncwarp();
+    if (warp >= 2) {
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t to = ptx::mapa_shared(
+          ptx::smem_addr(sums + (part * kShare + row % kShare) * kClusterTokens),
+          (uint32_t)(row / kShare));
+      ptx::st_cluster_f32x4(to, sum[0], sum[1], sum[2], sum[3]);
+    }
+    ptx::cluster_sync();
+    if (threadIdx.x < kShare * kClusterTokens) {
+      const int f = threadIdx.x % kShare, c = threadIdx.x / kShare;
+      float v = 0.f;
+#pragma unroll
+      for (int p = 0; p < kFewCluster; ++p) v += sums[(p * kShare + f) * kClusterTokens + c];
+      if (c < T)
+        a.out[(size_t)c * a.H + slab * kBM + part * kShare + f] =
+            __bfloat16_as_ushort(__float2bfloat16(v));
+    }
+  }
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -985,16 +1041,53 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
   }
 }
 
+// Launch attributes of the expert kernel in clusters: the cluster, then programmatic
+// stream serialisation.
+struct ClusterConfig {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  ClusterConfig(int blocks, size_t smem, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kFewCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+// Blocks of the expert kernel that run at once (found once a process; a failure is tried
+// again), at most `most`.
+template <int FMT, bool CLUSTER>
+cudaError_t resident_blocks(int most, int& blocks) {
+  static std::atomic<int> fit{0};
+  constexpr size_t kBytes = few_smem_bytes<FMT>();
+  blocks = fit.load(std::memory_order_relaxed);
+  if (blocks == 0) {
+    cudaError_t e = cudaFuncSetAttribute(few_expert_kernel<FMT, CLUSTER>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+    if (e != cudaSuccess) return e;
+    blocks = most;
+    if (CLUSTER) {
+      int n = 0;
+      ClusterConfig c(most / kFewCluster * kFewCluster, kBytes, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&n, few_expert_kernel<FMT, CLUSTER>, &c.cfg);
+      if (e != cudaSuccess) return e;
+      blocks = n < 1 ? -1 : n * kFewCluster;
+      if (blocks > most) blocks = most / kFewCluster * kFewCluster;
+    }
+    fit.store(blocks, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
-  constexpr size_t kBytes = few_smem_bytes<FMT>();
-  static std::atomic<bool> set{false};   // once a process; a failure is tried again
-  if (!set.load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        few_expert_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
-    if (e != cudaSuccess) return e;
-    set.store(true, std::memory_order_relaxed);
-  }
   FewArgs a = g.args;
   const Shape& s = g.shape;
   constexpr bool f8 = FMT == kMx8;
@@ -1022,10 +1115,21 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   e = light ? launch_pdl(few_logits_kernel<FMT, true>, dim3(blocks), dim3(threads), 0, st, a)
             : launch_pdl(few_logits_kernel<FMT, false>, dim3(blocks), dim3(threads), 0, st, a);
   if (e != cudaSuccess) return e;
-  int grid = kFewBlocksPerSM * g.num_sms;
-  if (grid > kFewBlocks) grid = kFewBlocks;
-  return launch_pdl(few_expert_kernel<FMT>, dim3(grid), dim3(kFewThreads), kBytes, st, m1, mx, m2,
-                    mh, a);
+  constexpr size_t kBytes = few_smem_bytes<FMT>();
+  int most = kFewBlocksPerSM * g.num_sms, grid = 0;
+  if (most > kFewBlocks) most = kFewBlocks;
+  if (a.T <= kClusterTokens) {
+    // a slab a cluster: as many clusters as slabs (36 fit: H up to 4608)
+    if ((e = resident_blocks<FMT, true>(most, grid)) != cudaSuccess) return e;
+    if (s.H / kBM * kFewCluster <= grid) {
+      ClusterConfig c(grid, kBytes, st);
+      c.cfg.numAttrs = 2;
+      return cudaLaunchKernelEx(&c.cfg, few_expert_kernel<FMT, true>, m1, mx, m2, mh, a);
+    }
+  }
+  if ((e = resident_blocks<FMT, false>(most, grid)) != cudaSuccess) return e;
+  return launch_pdl(few_expert_kernel<FMT, false>, dim3(grid), dim3(kFewThreads), kBytes, st, m1,
+                    mx, m2, mh, a);
 }
 
 }  // namespace
