@@ -164,7 +164,7 @@ def _nbytes(t) -> int:
 def _stream(stream) -> int | None:
     if stream is None:
         # the current stream's handle without building a Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -315,12 +315,13 @@ def moe_mxfp8_quantize(x, rows: int, K: int, q, sf, layout: int, rows_cap: int |
 
 def _matrix(t, shape, dtypes, name: str) -> int:
     """Row stride of a 2-D tensor of this shape and one of the dtypes, its rows contiguous."""
-    if t.shape != shape or t.dtype not in dtypes:
-        raise ValueError(f"{name}: need {list(shape)} of {dtypes}, got {list(t.shape)} of {t.dtype}")
-    ld, step = t.stride()
-    if step != 1 and shape[1] > 1:
+    if t.dtype in dtypes and t.shape == shape:
+        ld, step = t.stride()
+        if step == 1 or shape[1] == 1:
+            # a single row may have any stride; of more, the library checks it
+            return ld if shape[0] > 1 or ld >= shape[1] else shape[1]
         raise ValueError(f"{name}: rows must be contiguous")
-    return ld if shape[0] > 1 else max(ld, shape[1])
+    raise ValueError(f"{name}: need {list(shape)} of {dtypes}, got {list(t.shape)} of {t.dtype}")
 
 
 _BF16 = (torch.bfloat16,)
@@ -337,15 +338,20 @@ def moe_rmsnorm_mxfp8(x, gamma, eps: float, q=None, sf=None, layout: int = MOE_S
     shape = x.shape
     rows, K = shape
     ldx = _matrix(x, shape, _BF16, "x")
-    ldr = 0 if residual is None else _matrix(residual, shape, _BF16, "residual")
-    ldro = 0 if residual_out is None else _matrix(residual_out, shape, _BF16, "residual_out")
-    ldy = 0 if y is None else _matrix(y, shape, _BF16, "y")
-    if gamma.dtype != torch.bfloat16 or gamma.shape != (K,) or not gamma.is_contiguous():
+    px = x.data_ptr()
+    pr = pro = py = None
+    ldr = ldro = ldy = 0
+    if residual is not None:
+        ldr, pr = _matrix(residual, shape, _BF16, "residual"), residual.data_ptr()
+    if residual_out is not None:
+        ldro, pro = _matrix(residual_out, shape, _BF16, "residual_out"), residual_out.data_ptr()
+    if y is not None:
+        ldy, py = _matrix(y, shape, _BF16, "y"), y.data_ptr()
+    if gamma.dtype is not torch.bfloat16 or gamma.shape != (K,) or not gamma.is_contiguous():
         raise ValueError(f"gamma: need contiguous bf16 [{K}]")
-    _check(lib().moe_rmsnorm_mxfp8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(gamma), eps, rows, K,
-                                   _ptr(residual_out), ldro, _ptr(y), ldy, _ptr(q), _ptr(sf),
-                                   layout, rows if rows_cap is None else rows_cap,
-                                   _stream(stream)))
+    _check(lib().moe_rmsnorm_mxfp8(px, ldx, pr, ldr, gamma.data_ptr(), eps, rows, K, pro, ldro, py,
+                                   ldy, _ptr(q), _ptr(sf), layout,
+                                   rows if rows_cap is None else rows_cap, _stream(stream)))
 
 
 def moe_linear_weights_size(dims: LinearDims) -> int:

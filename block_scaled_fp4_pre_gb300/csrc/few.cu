@@ -27,9 +27,10 @@
 //   memory serves faster takes more of them (equal shares ended 15% apart).  The first
 //   stages of a phase 1 range hold its weights before that wait.
 // - Phase 1 (down) runs slab by slab over the experts, so a block adds the experts'
-//   weighted products in registers and leaves one sum per slab it touches.  With up to
-//   kClusterTokens tokens, where those joins at the end are a large part of the time, a
-//   cluster of eight blocks takes a slab and adds its eight sums in shared memory.
+//   weighted products in registers and leaves one sum per slab.  A cluster of eight blocks
+//   takes a slab and adds its eight sums in shared memory (joins through global memory at
+//   the end took 3 us of 29 at one token, 10 of 175 at sixteen); where there are more slabs
+//   than clusters fit (H above 4480), phase 1 is cut into ranges as phase 0 is.
 //
 // Roles (192 threads, two blocks an SM): warp 0 claims and issues the TMA copies, warp 1
 // issues the MMAs, warps 2-5 read the accumulators (four of 16 columns each in flight).
@@ -60,8 +61,8 @@ constexpr int kFewLeast = 5;         // least tiles of a range (a whole line whe
 constexpr int kFewTmemCols = 256;
 constexpr int kFewSfCol = kFewAccs * kFewN;   // two buffers of scale registers
 constexpr int kFewRing = 4;
-constexpr int kClusterTokens = 4;
 constexpr int kFewCluster = 8;
+constexpr int kTailTokens = 4;   // tokens whose cluster sums fit the block's tail
 constexpr int kFewMaxSlots = kFewTokens * 32;
 
 // ws.ctrl words, cleared by the logits kernel
@@ -1009,28 +1010,33 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
 
   if (CLUSTER && slots > 0 && (int)blockIdx.x < P1.ranges) {
     // The cluster's sums of its slab: block p adds features [16 p, 16 p + 16), in the order
-    // of the blocks.  The buffer is [part][feature][token], in the room of phase 0's h,
-    // which every block has left: their sums rest on all of it.
+    // of the blocks; the buffer is [part][feature][token].  Few tokens fit the room of phase
+    // 0's h, which every block has left (their sums rest on all of it); more take the
+    // operand stages, free once every block has read its accumulators.
     constexpr int kShare = kBM / kFewCluster;
-    float* const sums = &tail->h[0][0];
+    const int cols = T <= kTailTokens ? kTailTokens : kFewN;
+    float* const sums = T <= kTailTokens ? &tail->h[0][0] : reinterpret_cast<float*>(smem);
     const int part = (int)blockIdx.x % kFewCluster, slab = (int)blockIdx.x / kFewCluster;
     __syncwarp();
+    if (T > kTailTokens) ptx::cluster_sync();
     if (warp >= 2) {
       const int row = (warp & 3) * 32 + lane;
-      const uint32_t to = ptx::mapa_shared(
-          ptx::smem_addr(sums + (part * kShare + row % kShare) * kClusterTokens),
-          (uint32_t)(row / kShare));
-      ptx::st_cluster_f32x4(to, sum[0], sum[1], sum[2], sum[3]);
+      const uint32_t to =
+          ptx::mapa_shared(ptx::smem_addr(sums + (part * kShare + row % kShare) * cols),
+                           (uint32_t)(row / kShare));
+#pragma unroll
+      for (int c = 0; c < kFewN; c += 4)
+        if (c < T)
+          ptx::st_cluster_f32x4(to + (uint32_t)c * 4, sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
     }
     ptx::cluster_sync();
-    if (threadIdx.x < kShare * kClusterTokens) {
-      const int f = threadIdx.x % kShare, c = threadIdx.x / kShare;
+    for (int i = threadIdx.x; i < kShare * T; i += kFewThreads) {
+      const int f = i % kShare, c = i / kShare;
       float v = 0.f;
 #pragma unroll
-      for (int p = 0; p < kFewCluster; ++p) v += sums[(p * kShare + f) * kClusterTokens + c];
-      if (c < T)
-        a.out[(size_t)c * a.H + slab * kBM + part * kShare + f] =
-            __bfloat16_as_ushort(__float2bfloat16(v));
+      for (int p = 0; p < kFewCluster; ++p) v += sums[(p * kShare + f) * cols + c];
+      a.out[(size_t)c * a.H + slab * kBM + part * kShare + f] =
+          __bfloat16_as_ushort(__float2bfloat16(v));
     }
   }
   ptx::tc_fence_before();
@@ -1061,6 +1067,14 @@ struct ClusterConfig {
   }
 };
 
+// Stands for the expert kernel's threads and shared memory when asking how many clusters fit:
+// for kernels that allocate tensor memory the runtime answers as if one block filled an SM
+// (15 clusters instead of 36).  Never launched.
+__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM) few_shape_kernel(int* p) {
+  extern __shared__ int shape_smem[];
+  if (p) *p = shape_smem[0];
+}
+
 // Blocks of the expert kernel that run at once (found once a process; a failure is tried
 // again), at most `most`.
 template <int FMT, bool CLUSTER>
@@ -1076,8 +1090,10 @@ cudaError_t resident_blocks(int most, int& blocks) {
     if (CLUSTER) {
       int n = 0;
       ClusterConfig c(most / kFewCluster * kFewCluster, kBytes, nullptr);
-      e = cudaOccupancyMaxActiveClusters(&n, few_expert_kernel<FMT, CLUSTER>, &c.cfg);
-      if (e != cudaSuccess) return e;
+      if ((e = cudaFuncSetAttribute(few_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kBytes)) != cudaSuccess ||
+          (e = cudaOccupancyMaxActiveClusters(&n, few_shape_kernel, &c.cfg)) != cudaSuccess)
+        return e;
       blocks = n < 1 ? -1 : n * kFewCluster;
       if (blocks > most) blocks = most / kFewCluster * kFewCluster;
     }
@@ -1118,14 +1134,16 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   constexpr size_t kBytes = few_smem_bytes<FMT>();
   int most = kFewBlocksPerSM * g.num_sms, grid = 0;
   if (most > kFewBlocks) most = kFewBlocks;
-  if (a.T <= kClusterTokens) {
-    // a slab a cluster: as many clusters as slabs (36 fit: H up to 4608)
-    if ((e = resident_blocks<FMT, true>(most, grid)) != cudaSuccess) return e;
-    if (s.H / kBM * kFewCluster <= grid) {
-      ClusterConfig c(grid, kBytes, st);
-      c.cfg.numAttrs = 2;
-      return cudaLaunchKernelEx(&c.cfg, few_expert_kernel<FMT, true>, m1, mx, m2, mh, a);
-    }
+  // A slab a cluster: as many clusters as slabs, at least 32 (phase 0 wants the blocks), and
+  // fewer than fit an empty GPU, where the last one started late (1 token: 25.2 us with 32
+  // clusters, 25.5 with 35, 27.8 with all 36).
+  if ((e = resident_blocks<FMT, true>(most, grid)) != cudaSuccess) return e;
+  const int slabs = s.H / kBM, fit = grid / kFewCluster - 1;
+  if (slabs <= fit) {
+    const int clusters = slabs > 32 ? slabs : fit < 32 ? fit : 32;
+    ClusterConfig c(clusters * kFewCluster, kBytes, st);
+    c.cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&c.cfg, few_expert_kernel<FMT, true>, m1, mx, m2, mh, a);
   }
   if ((e = resident_blocks<FMT, false>(most, grid)) != cudaSuccess) return e;
   return launch_pdl(few_expert_kernel<FMT, false>, dim3(grid), dim3(kFewThreads), kBytes, st, m1,

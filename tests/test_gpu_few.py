@@ -123,7 +123,7 @@ def check_close(got, want):
 
 SHAPES = [(1, 256, 128, 8, 2), (3, 640, 384, 12, 3), (16, 512, 256, 40, 6), (8, 1024, 640, 5, 5),
           (9, 384, 128, 300, 8), (2, 4096, 512, 16, 6), (5, 256, 2048, 7, 1), (16, 256, 128, 1, 1),
-          (16, 256, 128, 1024, 32)]
+          (16, 256, 128, 1024, 32), (3, 4736, 128, 6, 2), (16, 8192, 256, 10, 4), (1, 4480, 256, 9, 3)]
 
 
 @pytest.mark.parametrize("mma", [F4, F8, NV])

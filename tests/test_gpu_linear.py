@@ -194,6 +194,8 @@ def test_refusals():
             torch.empty(9, 128, dtype=torch.bfloat16, device="cuda"), lin.ws)
     refused(inv, mx.moe_linear_forward, d, lin.prepared[16:], x, out, lin.ws)
     refused(inv, mx.moe_linear_forward, d, lin.prepared, inputs(8, 260)[:, :256], out, lin.ws)
+    refused(inv, mx.moe_linear_forward, d, lin.prepared, x[:1].expand(8, 256), out, lin.ws)
+    refused(inv, mx.moe_linear_forward, d, lin.prepared, x, out[:1].expand(8, 128), lin.ws)
     refused(inv, mx.moe_linear_prepare, d, q, sf, lin.prepared[:1024])
     f4 = Linear(128, 256, 8, F4)
     refused(mx.MOE_ERR_UNSUPPORTED, mx.moe_linear_forward_pair, f4.dims, f4.prepared, q, sf, 8,

@@ -197,8 +197,12 @@ def test_refusals():
     refused(wide[:, :256], gamma, EPS, q, sf)                # stride not a multiple of 8
     odd = torch.empty(4 * 256 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(4, 256)
     refused(odd, gamma, EPS, q, sf)                          # not 16-byte aligned
+    refused(x[:1].expand(4, 256), gamma, EPS, q, sf)         # rows that overlap
+    refused(x, gamma, EPS, q, sf, residual=r[:1].expand(4, 256))
     with pytest.raises(ValueError):
         mx.moe_rmsnorm_mxfp8(x.float(), gamma, EPS, q, sf)
+    with pytest.raises(ValueError):
+        mx.moe_rmsnorm_mxfp8(x.t().contiguous().t(), gamma, EPS, q, sf)
     with pytest.raises(ValueError):
         mx.moe_rmsnorm_mxfp8(x, gamma, EPS, q, sf, residual=r[:3])
     with pytest.raises(ValueError):
