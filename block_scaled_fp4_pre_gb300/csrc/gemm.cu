@@ -39,7 +39,6 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
-#include "tmap.cuh"
 
 namespace mxmoe {
 namespace {
@@ -996,7 +995,61 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM)
 }
 
 // ---------------------------------------------------------------------------
-// Host side.
+// Host side: tensor maps through the driver entry point (no libcuda link).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  return fn;
+}
+
+// Row-major uint8 matrix [rows, row_bytes] read in boxes of 128 bytes x box_rows,
+// 128-byte swizzle.
+cudaError_t make_tmap(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+                      uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// kb_elems: K elements per k-block (256 for packed E2M1 tokens, 128 for E4M3).
+// Packed E2M1 matrix [rows, K elements] (K/2 bytes a row), read in boxes of 128
+// elements x 128 rows that land one element per byte: each 16 elements' 8 packed
+// bytes followed by 8 unused bytes (CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B), the
+// operand layout of kind::mxf8f6f4 for E2M1; 128-byte swizzle, 16 KiB a box.
+cudaError_t make_tmap_e2m1_wide(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {K, rows};
+  const cuuint64_t strides[1] = {K / 2};
+  const cuuint32_t box[2] = {128, kBM};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // atom_k: K elements of one 128x4 scale block (128, or 64 for NVFP4's scale per 16).
 PhaseArgs phase_args(const uint8_t* w_sf, const uint8_t* t_sf, int rows_per_expert, int K,
                      int kb_elems, int atom_k) {

@@ -1,4 +1,5 @@
-// Tensor maps on the host, through the driver entry point (no libcuda link).
+// Tensor maps on the host, through the driver entry point (no libcuda link).  (gemm.cu keeps
+// its own copies: recorded traffic measurements are matched to that file by its hash.)
 #pragma once
 
 #include <cuda.h>
