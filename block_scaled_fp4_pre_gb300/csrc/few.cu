@@ -58,11 +58,12 @@ constexpr int kFewBlocksPerSM = 2;
 constexpr int kFewN = kFewTokens;         // MMA columns
 constexpr int kFewAccs = 4;
 constexpr int kFewLeast = 5;         // least tiles of a range (a whole line where that is less)
+constexpr int kFewLong = 20;         // tiles of a line from which cutting it pays (see Plan)
 constexpr int kFewTmemCols = 256;
 constexpr int kFewSfCol = kFewAccs * kFewN;   // two buffers of scale registers
 constexpr int kFewRing = 4;
 constexpr int kFewCluster = 8;
-constexpr int kTailTokens = 4;   // tokens whose cluster sums fit the block's tail
+constexpr int kTailTokens = 8;   // tokens whose cluster sums fit the block's tail
 constexpr int kFewMaxSlots = kFewTokens * 32;
 
 // ws.ctrl words, cleared by the logits kernel
@@ -135,7 +136,7 @@ __device__ __forceinline__ void top_k(uint32_t (&key)[R], int k, int lane, int& 
 
 // LIGHT: at most two tokens, in blocks small enough (64 registers, 256 threads) to sit
 // beside the expert kernel's two: in a decode loop the next call's blocks then wait on the
-// SMs when an expert kernel ends, instead of being launched (1 token 32.8 -> @LIGHT@ us).
+// SMs when an expert kernel ends, instead of being launched (1 token 23.5 -> 22.6 us).
 // Otherwise 512 threads, the second half of the warps for tokens 8 to 15.
 template <int FMT, bool LIGHT>
 __global__ void __launch_bounds__(LIGHT ? 256 : 512, LIGHT ? 4 : 1)
@@ -318,35 +319,47 @@ static_assert(2 * (few_smem_bytes<kMx4>() + 1024) <= 228 * 1024, "two blocks per
 static_assert(2 * (few_smem_bytes<kMx8>() + 1024) <= 228 * 1024, "two blocks per SM");
 static_assert(2 * (few_smem_bytes<kNv4>() + 1024) <= 228 * 1024, "two blocks per SM");
 
-// Tiles of a phase: `kb` of them a line (an expert's weight slab), cut into `ranges` that
-// differ by at most one tile.  Phase 0 lines are slot * m0 + slab, phase 1 lines
-// slab * slots + slot.
+// Tiles of a phase: `kb` of them a line (an expert's weight slab), cut into ranges.  Phase 0
+// lines are slot * m0 + slab, phase 1 lines slab * slots + slot.
+//
+// A cut line costs a join of about 3.5 us, the time of a dozen tiles of one block.  So
+// phase 0 takes whole lines where every block gets one or none, cut into `per` equal parts
+// where lines are long and leave blocks idle, and where blocks take many (they claim as
+// they finish, so a faster SM takes more).  In between, equal ranges that start and end
+// anywhere.  1 token of the full-size layer (192 lines): 25.4 us with equal ranges, 22.6
+// with whole lines; 3 tokens of 2176 x 256, MXFP8: 18.1 and 16.1.  Ranges smaller than a
+// block's share measured slower: 1 token 46 us against 33, 16 tokens 213 to 225 against 205
+// (before the changes since).
 struct Plan {
   int n, kb, ranges, q, rem;
-  int span = 0;   // not 0: eight ranges to each `span` tiles (clusters' slabs)
-  // One range a block, of at least kFewLeast tiles or a line, since each cut costs a join
-  // (finer ranges measured slower: 16 tokens 213 to 225 us against 205, 1 token 46 against
-  // 33).  whole: phase 0 with four lines and more a block takes lines, which need no join
-  // and let a faster SM take more of them.
-  __device__ __forceinline__ Plan(int tiles, int kb_line, int blocks, bool whole)
-      : n(tiles), kb(kb_line) {
-    if (whole && tiles >= 4 * blocks * kb_line)
-      ranges = tiles / kb_line;
-    else
-      ranges = max(1, min(blocks, tiles / min(kb_line, kFewLeast)));
+  int span = 0, per = 0;   // per > 0: each `span` tiles are `per` ranges
+  // Equal ranges of at least kFewLeast tiles (or a line).
+  __device__ __forceinline__ Plan(int tiles, int kb_line, int blocks) : n(tiles), kb(kb_line) {
+    ranges = max(1, min(blocks, tiles / min(kb_line, kFewLeast)));
     q = n / ranges;
     rem = n - q * ranges;
   }
-  // One slab of `slab_tiles` tiles a cluster.
-  __device__ __forceinline__ Plan(int slabs, int slab_tiles, int kb_line)
-      : n(slabs * slab_tiles), kb(kb_line), ranges(slabs * kFewCluster), q(0), rem(0),
-        span(slab_tiles) {}
+  // `spans` times `tiles` tiles of `parts` ranges each.
+  __device__ __forceinline__ Plan(int spans, int tiles, int kb_line, int parts)
+      : n(spans * tiles), kb(kb_line), ranges(spans * parts), q(0), rem(0), span(tiles),
+        per(parts) {}
+  static __device__ __forceinline__ Plan phase0(int lines, int kb_line, int blocks) {
+    if (lines > blocks && lines < 4 * blocks) return Plan(lines * kb_line, kb_line, blocks);
+    const int parts = lines > blocks || kb_line < kFewLong ? 1 : min(blocks / max(lines, 1), kb_line / 6);
+    return Plan(lines, kb_line, kb_line, max(parts, 1));
+  }
   __device__ __forceinline__ int start(int r) const {
-    if (span) return r / kFewCluster * span + r % kFewCluster * span / kFewCluster;
+    if (per == 1) return r * span;
+    if (per) return r / per * span + r % per * span / per;
     return r * q + min(r, rem);
   }
   // the range that holds tile t
   __device__ __forceinline__ int range_of(int t) const {
+    if (per == 1) return t / span;
+    if (per) {
+      const int s = t / span;
+      return s * per + ((t - s * span + 1) * per - 1) / span;
+    }
     const int big = rem * (q + 1);
     return t < big ? t / (q + 1) : rem + (t - big) / q;
   }
@@ -369,8 +382,8 @@ __device__ __forceinline__ void route(const FewArgs& a, RouteScratch& sc, FewTai
     }
   };
   if (a.router && a.T == 1 && E <= 256) {
-    // One token: its j-th expert is slot j, straight from the warp that chose it (2.4 us of
-    // routing with the steps below, 1.9 so).
+    // One token: its j-th expert is slot j, straight from the warp that chose it (1.7 us of
+    // routing against 2.4 with the steps below).
     if (warp == 0) {
       uint32_t key[8];
       int id;
@@ -477,8 +490,10 @@ __device__ __forceinline__ void route(const FewArgs& a, RouteScratch& sc, FewTai
 }
 
 // CLUSTER: launched in clusters of kFewCluster; phase 1 slab c is cluster c's.
+// 128 registers at most (the bound for two blocks of 256 threads), so that the next call's
+// light logits blocks find room beside two of these.
 template <int FMT, bool CLUSTER>
-__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
+__global__ void __launch_bounds__(256, kFewBlocksPerSM)
     few_expert_kernel(const __grid_constant__ CUtensorMap tmap_w1,
                       const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ CUtensorMap tmap_w2,
@@ -537,8 +552,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
   const int m0 = 2 * a.I / kBM, m1 = a.H / kBM;
   const int kb0 = (a.H + kKb - 1) / kKb, kb1 = (a.I + kKb - 1) / kKb;
   const int blocks = (int)gridDim.x;
-  const Plan P0(slots * m0 * kb0, kb0, blocks, true);
-  const Plan P1 = CLUSTER ? Plan(m1, slots * kb1, kb1) : Plan(slots * m1 * kb1, kb1, blocks, false);
+  const Plan P0 = Plan::phase0(slots * m0, kb0, blocks);
+  const Plan P1 =
+      CLUSTER ? Plan(m1, slots * kb1, kb1, kFewCluster) : Plan(slots * m1 * kb1, kb1, blocks);
   const int R0 = P0.ranges, R = R0 + P1.ranges;
   float sum[kFewN];   // phase 1: weighted sums of this thread's output feature
 #pragma unroll
@@ -1014,7 +1030,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM)
     // 0's h, which every block has left (their sums rest on all of it); more take the
     // operand stages, free once every block has read its accumulators.
     constexpr int kShare = kBM / kFewCluster;
-    const int cols = T <= kTailTokens ? kTailTokens : kFewN;
+    const int cols = T <= 4 ? 4 : T <= kTailTokens ? kTailTokens : kFewN;
+    static_assert(kFewCluster * kShare * kTailTokens * 4 <= sizeof(tail->h), "room of h");
     float* const sums = T <= kTailTokens ? &tail->h[0][0] : reinterpret_cast<float*>(smem);
     const int part = (int)blockIdx.x % kFewCluster, slab = (int)blockIdx.x / kFewCluster;
     __syncwarp();
@@ -1126,8 +1143,10 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
     return e;
   const bool light = a.T <= 2;
   const int threads = light ? 256 : 512;
-  const int blocks = a.router ? (s.E + kLogitExperts - 1) / kLogitExperts
-                              : (a.T * (s.H / 8) + threads - 1) / threads;
+  // enough blocks for the experts' logits and for a vector of x a thread
+  int blocks = (a.T * (s.H / 8) + threads - 1) / threads;
+  if (a.router && blocks < (s.E + kLogitExperts - 1) / kLogitExperts)
+    blocks = (s.E + kLogitExperts - 1) / kLogitExperts;
   e = light ? launch_pdl(few_logits_kernel<FMT, true>, dim3(blocks), dim3(threads), 0, st, a)
             : launch_pdl(few_logits_kernel<FMT, false>, dim3(blocks), dim3(threads), 0, st, a);
   if (e != cudaSuccess) return e;
@@ -1138,9 +1157,16 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   // fewer than fit an empty GPU, where the last one started late (1 token: 25.2 us with 32
   // clusters, 25.5 with 35, 27.8 with all 36).
   if ((e = resident_blocks<FMT, true>(most, grid)) != cudaSuccess) return e;
+  // Small layers launch no more than phase 0 has ranges for.
   const int slabs = s.H / kBM, fit = grid / kFewCluster - 1;
   if (slabs <= fit) {
-    const int clusters = slabs > 32 ? slabs : fit < 32 ? fit : 32;
+    const int64_t touched = (int64_t)a.T * s.k < s.E ? (int64_t)a.T * s.k : s.E;
+    const int64_t kb0 = weight_num_kb(s, s.H);
+    const int64_t ranges0 = touched * (2 * s.I / kBM) * (kb0 < kFewLong ? 1 : kb0 / 6);
+    const int64_t want = (ranges0 + kFewCluster - 1) / kFewCluster;
+    int clusters = want < 32 ? (int)want : 32;
+    if (clusters > fit) clusters = fit;
+    if (clusters < slabs) clusters = slabs;
     ClusterConfig c(clusters * kFewCluster, kBytes, st);
     c.cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&c.cfg, few_expert_kernel<FMT, true>, m1, mx, m2, mh, a);
