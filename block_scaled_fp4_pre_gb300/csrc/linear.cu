@@ -663,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(acc_empty_l + (uint32_t)ab * 8u);
+      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(acc_empty_l + (uint32_t)ab * 8u);
       if (ab) acc_phase ^= 1u;
       ab ^= 1;
     }

@@ -242,3 +242,18 @@ def test_pair_in_on_sm_pairs_does_not_read_past_its_scales():
     mx.moe_linear_forward_pair(lin.dims, lin.prepared, q, buf[:n], rows, out, lin.ws)
     mx.moe_linear_check(lin.ws)
     lin.check(out, x)
+
+
+@pytest.mark.parametrize("rows,N,K,mma", [(70000, 128, 32768, F4), (270000, 8192, 32, F8)])
+def test_offsets_past_32_bits(rows, N, K, mma):
+    # 2.3e9 elements of x, and 2.2e9 of out
+    lin = Linear(N, K, rows, mma)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(rows // 100, K, generator=g, device="cuda").bfloat16().repeat(100, 1)
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    mx.moe_linear_forward(lin.dims, lin.prepared, x, out, lin.ws)
+    mx.moe_linear_check(lin.ws)
+    n = rows // 100
+    assert torch.equal(out[-n:], out[:n])
+    pick = [0, n // 2, rows - n // 3, rows - 1]
+    lin.check(out[pick], x[pick])

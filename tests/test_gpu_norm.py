@@ -207,3 +207,18 @@ def test_refusals():
         mx.moe_rmsnorm_mxfp8(x, gamma, EPS, q, sf, residual=r[:3])
     with pytest.raises(ValueError):
         mx.moe_rmsnorm_mxfp8(x, gamma[:128], EPS, q, sf)
+
+
+def test_offsets_past_32_bits():
+    rows, K = 33000, 65536                                   # 2.16e9 elements
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[:-3] = 1
+    x[-3:] = torch.randn(3, K, generator=g, device="cuda").bfloat16()
+    gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    q, sf, ro, y = run(x, x, gamma, mx.MOE_SF_128X4)
+    q1, sf1, ro1, y1 = run(x[-3:].contiguous(), x[-3:].contiguous(), gamma, mx.MOE_SF_128X4)
+    assert torch.equal(q[-3:], q1) and torch.equal(y[-3:], y1) and torch.equal(ro[-3:], ro1)
+    at, at1 = (torch.from_numpy(micro64.sf_offsets(n, K // 32)[-3:]).cuda() for n in (rows, 3))
+    assert torch.equal(sf[at], sf1[at1])
+    assert torch.all(y[:-3] == 1)

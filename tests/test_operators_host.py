@@ -1,0 +1,124 @@
+"""Host-side checks of the operators around the expert layer: sizes and refusals that need
+no GPU."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def mx():
+    from block_scaled_fp4_pre_gb300 import build
+
+    build.build()
+    import block_scaled_fp4_pre_gb300 as m
+
+    m.lib()
+    return m
+
+
+def linear(mx, n=256, k=512, rows=8, mma=None):
+    return mx.make_linear_dims(n, k, rows, mx.MOE_MMA_MXF4xMXF4 if mma is None else mma)
+
+
+@pytest.mark.parametrize("n,k,slabs,kp", [(1, 32, 1, 128), (128, 128, 1, 128), (129, 160, 2, 256),
+                                          (1001, 1056, 8, 1152), (4096, 4096, 32, 4096)])
+def test_weight_sizes(mx, n, k, slabs, kp):
+    # whole slabs of 128 rows, K in whole k-blocks (256 elements of 4 bits, 128 for MXFP8
+    # activations) and a scale byte per 32 elements of K in whole 128-element blocks
+    scales = slabs * 128 * kp // 32
+    f4 = slabs * 128 * (-(-kp // 256) * 128) + scales
+    f8 = slabs * 128 * (kp // 128 * 64) + scales
+    assert mx.moe_linear_weights_size(linear(mx, n, k)) == f4
+    assert mx.moe_linear_weights_size(linear(mx, n, k, mma=mx.MOE_MMA_FP8xFP4)) == f8
+
+
+def test_workspace_holds_the_quantised_rows(mx):
+    for mma, per in ((mx.MOE_MMA_MXF4xMXF4, 2), (mx.MOE_MMA_FP8xFP4, 1)):
+        for rows in (1, 129, 4096):
+            size = mx.moe_linear_workspace_size(linear(mx, 64, 4096, rows, mma))
+            assert size >= rows * 4096 // per + -(-rows // 128) * 32 * 512
+            assert size <= rows * 4096 // per + -(-rows // 128) * 32 * 512 + 4096
+
+
+@pytest.mark.parametrize("change", [dict(n=0), dict(n=-3), dict(n=(1 << 20) + 1), dict(k=0),
+                                    dict(k=48), dict(k=65568), dict(rows=0), dict(rows=(1 << 20) + 1)])
+def test_linear_dims_out_of_range(mx, change):
+    d = linear(mx, **change)
+    assert mx.moe_linear_weights_size(d) == 0 and mx.moe_linear_workspace_size(d) == 0
+    assert mx.lib().moe_linear_workspace_init(ctypes.byref(d), 1024, 1 << 30, None) \
+        == mx.MOE_ERR_INVALID_ARG
+    assert mx.moe_last_error()
+
+
+def test_linear_types(mx):
+    for mma in (mx.MOE_MMA_NVF4xNVF4, 0, 9):
+        d = linear(mx, mma=mma)
+        assert mx.moe_linear_weights_size(d) == 0
+        assert mx.lib().moe_linear_prepare(ctypes.byref(d), 1024, 1024, 1024, 1 << 30, None) \
+            == mx.MOE_ERR_UNSUPPORTED
+
+
+def test_linear_calls_refuse_before_they_launch(mx):
+    d = linear(mx, mma=mx.MOE_MMA_FP8xFP4)
+    ref, f = ctypes.byref(d), mx.lib()
+    big = 1 << 30
+    assert f.moe_linear_forward(None, 1024, 1024, 512, 8, 1024, 256, 0, 1024, big, None) \
+        == mx.MOE_ERR_INVALID_ARG
+    assert f.moe_linear_forward(ref, 1024, 1024, 512, 8, 1024, 256, 0, None, big, None) \
+        == mx.MOE_ERR_INVALID_ARG
+    assert f.moe_linear_forward(ref, 1024, 1024, 512, 8, 1024, 256, 0, 1028, big, None) \
+        == mx.MOE_ERR_INVALID_ARG                            # workspace not aligned
+    assert f.moe_linear_forward(ref, 1024, 1024, 512, 8, 1024, 256, 0, 1024, 16, None) \
+        == mx.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert f.moe_linear_forward(ref, 1024, 1024, 512, 8, 1024, 256, 0, 1024, big, None) \
+        == mx.MOE_ERR_WORKSPACE_MISMATCH                     # never initialised
+    assert f.moe_linear_check(1024, None) == mx.MOE_ERR_WORKSPACE_MISMATCH
+    assert f.moe_linear_workspace_init(ref, None, big, None) == mx.MOE_ERR_INVALID_ARG
+    assert f.moe_linear_workspace_init(ref, 1024, 16, None) == mx.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("change", [dict(K=0), dict(K=100), dict(K=65664), dict(rows=-1),
+                                    dict(rows=9), dict(cap=(1 << 23) + 1), dict(eps=-1e-6),
+                                    dict(eps=float("nan")), dict(eps=float("inf")), dict(sf=None),
+                                    dict(layout=2), dict(q=1032), dict(x=None), dict(gamma=None),
+                                    dict(x=1030), dict(ldx=120), dict(ldx=250), dict(ldy=100),
+                                    dict(q=None, sf=None, y=None, ro=None)])
+def test_norm_arguments(mx, change):
+    a = dict(x=1024, ldx=256, r=1024, ldr=256, gamma=1024, eps=1e-6, rows=8, K=256, ro=1024,
+             ldro=256, y=1024, ldy=256, q=1024, sf=1024, layout=mx.MOE_SF_128X4, cap=8) | change
+    status = mx.lib().moe_rmsnorm_mxfp8(a["x"], a["ldx"], a["r"], a["ldr"], a["gamma"], a["eps"],
+                                        a["rows"], a["K"], a["ro"], a["ldro"], a["y"], a["ldy"],
+                                        a["q"], a["sf"], a["layout"], a["cap"], None)
+    assert status == mx.MOE_ERR_INVALID_ARG
+    assert mx.moe_last_error()
+
+
+def test_few_arguments(mx):
+    d = mx.make_dims(256, 128, 8, 2, 16)
+    f, ref = mx.lib().moe_few_forward, ctypes.byref(d)
+    big = 1 << 33
+    assert f(None, 1024, 1024, 1024, 1024, 1024, 1, 1024, big, 1024, None) == mx.MOE_ERR_INVALID_ARG
+    assert f(ref, 1024, 1024, 1024, 1024, 1024, 1, None, big, 1024, None) == mx.MOE_ERR_INVALID_ARG
+    assert f(ref, 1024, 1024, 1024, 1024, 1024, 1, 1024, 16, 1024, None) \
+        == mx.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert f(ref, 1024, 1024, 1024, 1024, 1024, 1, 1024, big, 1024, None) \
+        == mx.MOE_ERR_WORKSPACE_MISMATCH
+
+
+def test_matrix_strides(mx):
+    import torch
+
+    t = torch.zeros(6, 40, dtype=torch.bfloat16)
+    check = mx._matrix
+    assert check(t, (6, 40), (torch.bfloat16,), "t") == 40
+    assert check(t[:, 8:24], (6, 16), (torch.bfloat16,), "t") == 40
+    assert check(t[:1, :32].expand(6, 32), (6, 32), (torch.bfloat16,), "t") == 0   # refused by the C side
+    assert check(t[2:3], (1, 40), (torch.bfloat16,), "t") == 40
+    assert check(t[0].expand(1, 40), (1, 40), (torch.bfloat16,), "t") == 40
+    for bad in (t.t(), t.float(), t[0], t[:, :39]):
+        with pytest.raises(ValueError):
+            check(bad, (6, 40), (torch.bfloat16,), "t")
+    with pytest.raises(ValueError):
+        check(torch.zeros(40, 6, dtype=torch.bfloat16).t(), (6, 40), (torch.bfloat16,), "t")
