@@ -17,15 +17,14 @@
 // - Every block works the routing out for itself, from the logits: some hundred loads and a
 //   few warp reductions, against an elected block's ticket, its list in global memory and
 //   a second read of it (5 us less at one token).
-// - Work is cut into ranges of k-block tiles (one 16 KiB weight box each), equal to a tile
-//   whatever the number of experts: a range starts and ends inside a weight slab.  A slab
-//   that spans ranges leaves fp32 sums of each part in the workspace, and the part that
-//   finishes last adds them in the order of the ranges, so the result does not depend on
-//   timing.
+// - Work is cut into ranges of k-block tiles (one 16 KiB weight box each): whole weight
+//   slabs where that spreads well, else equal ranges that start and end inside a slab (see
+//   Plan).  A slab that spans ranges leaves fp32 sums of each part in the workspace, and
+//   the part that finishes last adds them in the order of the ranges, so the result does
+//   not depend on timing.
 // - Blocks claim ranges from a counter, all of phase 0 before any of phase 1, so the wait
-//   for the intermediate rows ends however many blocks are resident, and an SM that the
-//   memory serves faster takes more of them (equal shares ended 15% apart).  The first
-//   stages of a phase 1 range hold its weights before that wait.
+//   for the intermediate rows ends however many blocks are resident.  The first stages of
+//   a phase 1 range hold its weights before that wait.
 // - Phase 1 (down) runs slab by slab over the experts, so a block adds the experts'
 //   weighted products in registers and leaves one sum per slab.  A cluster of eight blocks
 //   takes a slab and adds its eight sums in shared memory (joins through global memory at
@@ -34,6 +33,13 @@
 //
 // Roles (192 threads, two blocks an SM): warp 0 claims and issues the TMA copies, warp 1
 // issues the MMAs, warps 2-5 read the accumulators (four of 16 columns each in flight).
+//
+// Measured (4096 x 2048, 256 experts, top-6): 16 tokens 170 us, 0.94 of the measured copy
+// bandwidth on the touched experts' weights; 5 tokens with MXFP8 activations 75 us, 0.76; 1
+// token 22.6 us, 0.54: 9 of them stream weights, the rest is the chain logits (2.4), routing
+// (1.7), first copy (2.3), SwiGLU and the step to phase 1 (2), its five tiles (2), the
+// cluster's sum and the launch (3).  A small layer (12 experts of 640 x 384) takes 12.7 us,
+// all of it that chain.
 // Every wait is bounded (kWaitLimitNs); a timeout sets the workspace's error flag.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

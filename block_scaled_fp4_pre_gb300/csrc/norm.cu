@@ -8,15 +8,25 @@
 // quantisation, so each input element is read once and each output written once.  y is
 // quantised from its fp32 value, not from the bf16 one, so q carries one rounding.  The
 // sum is fp32 in a fixed order (per thread, then a shuffle tree, then the warps in
-// order): the same input gives the same bits, whatever else runs.  An element that lies
-// next to a rounding boundary of E4M3 flips with the last bit of y, so what follows the
-// sum keeps the rounding errors: the warps' sums, the mean and the reciprocal root are
-// pairs of floats, and y is rounded to fp32 once.
+// order): the same input gives the same bits, whatever else runs.
+//
+// An element next to a rounding boundary of E4M3, or a group's largest next to a power of
+// two's, flips with the last bits of y.  So the sums, the mean and the reciprocal root are
+// pairs of floats, and where the nearest float of some y lies on a boundary (its last 19
+// bits are 0, one float in 2^19) it is rounded to odd instead: a value that is not exactly a
+// float gets the float next to it towards zero with its last bit set, which is on no
+// boundary, and E4M3 of that is E4M3 of the unrounded value.  Against 64 bits, 67.1e6
+// elements at K = 4096: 38 codes differ in plain fp32, 8 here, for 4 us of 93 (trees of pairs
+// all through: 9 for 7 us).
 //
 // Layout: a thread holds V vectors of 8 consecutive elements (16 bytes of bf16), so four
 // lanes hold a scale's 32 elements and reduce its amax with two shuffles, and sixteen
 // lanes a whole scale word (four scales), which is stored as one 32-bit word in either
-// layout.  Bound by HBM at large row counts and by launch and load latency at few.
+// layout.
+//
+// Bound by HBM at large row counts: 16384 x 4096 with residual and both outputs (606 MB)
+// 93 us, 0.96 of the measured copy bandwidth; by launch and load latency at few: one row
+// of 4096 2.2 us.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -64,6 +74,29 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
   const float s = a + b, t = s - a;
   return {s, (a - (s - t)) + (b - t)};
 }
+// Adds the pairs of the lanes that differ in `o`.
+__device__ __forceinline__ Two lane_sum(Two a, int o) {
+  const Two s = two_sum(a.hi, __shfl_xor_sync(kAll, a.hi, o));
+  return {s.hi, s.lo + (a.lo + __shfl_xor_sync(kAll, a.lo, o))};
+}
+// r * g * inv, to nearest but for some 2^-24 of the cases next to a tie.
+__device__ __forceinline__ float times(float r, float g, Two inv) {
+  const float p = r * g, pl = fmaf(r, g, -p);
+  return fmaf(p, inv.hi, fmaf(p, inv.lo, pl * inv.hi));
+}
+// The same rounded to odd.  hi is the product to nearest and lo what is left of it, to
+// about 2^-45 of it: where lo is not 0 the value towards zero is hi, or one below where
+// lo's sign differs.
+__device__ __forceinline__ float times_to_odd(float r, float g, Two inv) {
+  const float p = r * g, pl = fmaf(r, g, -p);
+  const float t = p * inv.hi;
+  const float tl = fmaf(p, inv.hi, -t) + fmaf(p, inv.lo, pl * inv.hi);
+  const float hi = t + tl, lo = (t - hi) + tl;
+  const uint32_t h = __float_as_uint(hi), l = __float_as_uint(lo);
+  const uint32_t odd = (h - ((h ^ l) >> 31)) | 1u;
+  // (NaN and infinities, whose lo is NaN, stay as they are)
+  return fabsf(lo) > 0.f ? __uint_as_float(odd) : hi;
+}
 // 1 / sqrt(s / K + eps): the hardware's approximate root improved by one Newton step in
 // two-float form (inv_k is 1 / K so).  Every thread of a row does this, so it has no
 // division: with IEEE divisions and root here the large rows took 120 us instead of 96.
@@ -82,10 +115,13 @@ __device__ __forceinline__ Two inverse_root(Two s, Two inv_k, float eps) {
 }
 
 // WARP_ROW: one warp a row (kWarpRowThreads / 32 rows a block); otherwise one block a row.
+// V = 2 serves at most 512 threads; three such blocks an SM leave each thread 42 registers
+// (without the bound: 50, and 104 us instead of 96 at 16384 x 4096).
 template <int V, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
+__global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : V == 2 ? 512 : 1024,
+                                  WARP_ROW ? 5 : V == 2 ? 3 : 1)
     rmsnorm_mxfp8_kernel(const RmsnormArgs a) {
-  __shared__ float part[32];
+  __shared__ float2 part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nt = WARP_ROW ? 32 : (int)blockDim.x;       // threads of a row
   const int t = WARP_ROW ? lane : (int)threadIdx.x;
@@ -113,7 +149,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
     }
   }
   float r[V][8];
-  float ss = 0.f;
+  Two sum = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * nt + t;
@@ -126,23 +162,34 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
     }
     if (a.residual_out && c < vecs)
       *reinterpret_cast<uint4*>(a.residual_out + row * a.ldro + c * 8) = pack8(r[i]);
+    if (WARP_ROW) {   // eight squares as a tree, the vectors' sums as pairs
+      float s[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+      for (int j = 0; j < 4; ++j)
+        s[j] = fmaf(r[i][2 * j], r[i][2 * j], r[i][2 * j + 1] * r[i][2 * j + 1]);
+      const Two v = two_sum(sum.hi, (s[0] + s[1]) + (s[2] + s[3]));
+      sum = {v.hi, sum.lo + v.lo};
+    } else {          // over many threads the chains' roundings average out
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum.hi = fmaf(r[i][j], r[i][j], sum.hi);
+    }
   }
+  if (WARP_ROW || nt <= 128) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-  Two sum = {ss, 0.f};
+    for (int o = 16; o > 0; o >>= 1) sum = lane_sum(sum, o);
+  } else {   // and so do the warps' trees'
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum.hi += __shfl_xor_sync(kAll, sum.hi, o);
+  }
   if (!WARP_ROW) {
-    if (lane == 0) part[warp] = ss;
+    if (lane == 0) part[warp] = make_float2(sum.hi, sum.lo);
     __syncthreads();
     // every warp adds the warps' sums, a lane each, as a tree of pairs
-    sum.hi = lane < (nt >> 5) ? part[lane] : 0.f;
+    const float2 mine = lane < (nt >> 5) ? part[lane] : make_float2(0.f, 0.f);
+    sum = {mine.x, mine.y};
     const int top = 31 - __clz((nt >> 5) * 2 - 1);   // levels: 2^top lanes cover the warps
 #pragma unroll 1
-    for (int o = (1 << top) >> 1; o > 0; o >>= 1) {
-      const Two s = two_sum(sum.hi, __shfl_xor_sync(kAll, sum.hi, o));
-      sum = {s.hi, s.lo + (sum.lo + __shfl_xor_sync(kAll, sum.lo, o))};
-    }
+    for (int o = (1 << top) >> 1; o > 0; o >>= 1) sum = lane_sum(sum, o);
     sum.hi = __shfl_sync(kAll, sum.hi, 0);   // lanes past the 2^top hold other sums
     sum.lo = __shfl_sync(kAll, sum.lo, 0);
   }
@@ -156,13 +203,18 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : 1024)
     if (live) gw = *reinterpret_cast<const uint4*>(a.gamma + c * 8);
     unpack8(gw, g);
     float amax = 0.f;
+    uint32_t tail = 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      // r * gamma exactly, as two floats, times the root, rounded once
-      const float p = r[i][j] * g[j], pl = fmaf(r[i][j], g[j], -p);
-      y[j] = fmaf(p, inv.hi, fmaf(p, inv.lo, pl * inv.hi));
-      amax = fmaxf(amax, fabsf(y[j]));
+      y[j] = times(r[i][j], g[j], inv);
+      tail = min(tail, __float_as_uint(y[j]) & 0x7FFFFu);
     }
+    if (tail == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = times_to_odd(r[i][j], g[j], inv);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
     if (a.y && live) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c * 8) = pack8(y);
     if (a.q) {
       amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
@@ -214,8 +266,8 @@ cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& args, int64_t rows_cap, cuda
   auto threads = [&](int v) { return (vecs + v * 32 - 1) / (v * 32) * 32; };
   // With at most one block an SM the latency of a row counts: as many threads as the row
   // feeds.  With more, a row's fixed work (the sums' trees) is shared by more elements a
-  // thread.  K = 4096, one vector a thread against two: 1 row 2.06 / 2.49 us, 16384 rows
-  // 104.3 / 89.3 us; K = 1408, 333 rows: 2.88 / 2.53 us.
+  // thread.  K = 4096, one vector a thread against two (before the care for ties): 1 row
+  // 2.06 / 2.49 us, 16384 rows 104.3 / 89.3 us; K = 1408, 333 rows: 2.88 / 2.53 us.
   if (a.rows <= 152 && vecs <= 1024) return launch<1, false>(a, threads(1), st);
   if (vecs <= 1024) return launch<2, false>(a, threads(2), st);
   if (vecs <= 2048) return launch<4, false>(a, threads(4), st);
