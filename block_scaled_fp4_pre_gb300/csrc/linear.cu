@@ -13,7 +13,7 @@
 // - linear_quantize_kernel writes the activation codes and their scale blocks, for more
 //   than 32 bf16 rows.
 // - linear_kernel: persistent, one block's epilogue overlapping the other's MMAs.
-// - linear_pair_kernel: tiles of 256 features by 192 rows over SM pairs, for large products.
+// - linear_pair_kernel: tiles of 256 features by 192 or 256 rows over SM pairs, for large products.
 // - linear_split_kernel: where there are too few tiles for the SMs, a cluster of up to
 //   eight blocks splits a tile's K.  The blocks exchange their sums through distributed
 //   shared memory, each adding the parts of its share of the features in order: no
@@ -84,6 +84,7 @@ __global__ void linear_scales_kernel(const uint8_t* __restrict__ src, uint32_t* 
 // scale word.  Elements past K (to the next multiple of 128) are zero.  A block covers
 // 2^span_log vectors of kQuantThreads >> span_log rows at a time and R times as many rows,
 // all of a thread's loads before any arithmetic; rows and columns need no division.
+// Bound by HBM: 16384 x 4096 in 33 us, 172 MB at 0.77 of the measured copy bandwidth.
 template <bool F8, int R>
 __global__ void __launch_bounds__(kQuantThreads)
     linear_quantize_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows, int K,
@@ -408,38 +409,47 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
 
 // ---------------------------------------------------------------------------
 // Large products: a pair of SMs (a 2-CTA cluster) shares a tile of 256 features by up to
-// 192 rows, each MMA spanning both (tcgen05 cta_group::2, M = 256): each SM stages its own
-// 128-feature slab and half of the rows, so it writes and reads 60% of the shared-memory
-// bytes a 128 x 128 tile takes per product.  Two accumulators, seven stages.  Roles (320
+// ROWS (192 or 256) rows, each MMA spanning both (tcgen05 cta_group::2, M = 256): each SM
+// stages its own 128-feature slab and half of the rows, so it writes and reads 60% (192)
+// or half (256) of the shared-memory bytes a 128 x 128 tile takes per product.  Two
+// accumulators: two of 256 rows and the scale registers are more than the 512 columns of
+// tensor memory, so these share 48 columns, which the epilogue reads first.  Roles (320
 // threads, one block an SM): warp 0 producer, warp 1 of the leader MMA issue, warps 2-9
 // epilogue, two a lane quarter.
+// Bound by the tensor pipe and the power cap: 16384 x 4096 x 4096 in 85 us behind the
+// quantisation (6.4 PFLOP/s) at 1.95 GHz and 1370 W of 1400; with no weight loads it takes 4%
+// less, with no stores 10%, with neither 11%.
 constexpr int kPairThreads = 320;
 constexpr int kPairTmemCols = 512;
-constexpr int kPairStages = 7;
-constexpr int kPairRows = kBNPair;                // 192
-constexpr int kPairHalf = kPairRows / 2;
 constexpr int kPairEpiWarps = 8;
-constexpr uint32_t kPairSfCol = 2 * kPairRows;    // two buffers of scale registers:
-constexpr uint32_t kPairSfCols = 24;              // 8 of the slab's, 16 of the rows'
+constexpr uint32_t kPairSfCols = 24;                // a buffer of scale registers: 8 of the
+constexpr uint32_t kPairSfCol = kPairTmemCols - 2 * kPairSfCols;   // slab's, 16 of the rows'
+__host__ __device__ constexpr int lin_pair_stages(int rows) { return rows == 256 ? 6 : 7; }
+// first column of the second accumulator
+__host__ __device__ constexpr uint32_t lin_pair_acc(int rows) {
+  return 2 * rows <= (int)kPairSfCol ? (uint32_t)rows : kPairSfCol - (uint32_t)rows;
+}
 
 struct __align__(16) LinPairTail {
-  uint64_t full[kPairStages];     // leader: both CTAs' loads of a stage landed
-  uint64_t empty[kPairStages];    // each CTA: the pair's MMAs are done with its stage
+  uint64_t full[7];               // leader: both CTAs' loads of a stage landed
+  uint64_t empty[7];              // each CTA: the pair's MMAs are done with its stage
   uint64_t acc_full[2];           // each CTA: the accumulator is complete
-  uint64_t acc_empty[2];          // leader: all 16 epilogue warps have read it
+  uint64_t acc_empty[2];          // leader: all 16 epilogue warps have read it, or what
+                                  // the other accumulator shares with it
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
 };
 
-template <bool F8>
+template <bool F8, int ROWS>
 struct LinPairSmem {
+  static constexpr int kSt = lin_pair_stages(ROWS);
   static constexpr size_t kSF = (size_t)(F8 ? 1 : 2) * kSFAtomBytes;   // one 128-row block
-  static constexpr size_t kBSlot = (size_t)kPairHalf * kBKBytes;
-  static constexpr size_t kB = (size_t)kPairStages * kATileBytes;
-  static constexpr size_t kSFA = kB + kPairStages * kBSlot;
-  static constexpr size_t kSFB = kSFA + kPairStages * kSF;
-  static constexpr size_t kTail = kSFB + kPairStages * 2 * kSF;
+  static constexpr size_t kBSlot = (size_t)(ROWS / 2) * kBKBytes;
+  static constexpr size_t kB = (size_t)kSt * kATileBytes;
+  static constexpr size_t kSFA = kB + kSt * kBSlot;
+  static constexpr size_t kSFB = kSFA + kSt * kSF;
+  static constexpr size_t kTail = kSFB + kSt * 2 * kSF;
   static constexpr size_t kBytes = kTail + sizeof(LinPairTail) + 1024;
   static_assert(kBytes <= 227 * 1024, "one block per SM");
 };
@@ -448,15 +458,17 @@ struct LinPairMaps {
   CUtensorMap w, x, wsf, tsf;
 };
 
-template <bool F8>
+template <bool F8, int ROWS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinPairMaps maps, const LinArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  using SM = LinPairSmem<F8>;
+  using SM = LinPairSmem<F8, ROWS>;
   constexpr int kKb = F8 ? 128 : kBK;
-  constexpr int kSt = kPairStages;
+  constexpr int kSt = SM::kSt;
+  constexpr uint32_t kAcc2 = lin_pair_acc(ROWS);
+  constexpr bool kShared = kAcc2 < ROWS;   // the accumulators share columns
   LinPairTail* tail = reinterpret_cast<LinPairTail*>(smem + SM::kTail);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -509,9 +521,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     for (int g = first; g < total && ok; g += step) {
       // an odd last slab is multiplied twice, and stored once
-      const int slab = min(g % pairs * 2 + (int)rank, a.slabs - 1), m0 = g / pairs * kPairRows;
+      const int slab = min(g % pairs * 2 + (int)rank, a.slabs - 1), m0 = g / pairs * ROWS;
       int wy = slab * a.num_kb * kBM, say = slab * a.kc4 * 2, sby = 0;
-      const int row = m0 + (int)rank * kPairHalf, blk = m0 >> 7;
+      const int row = m0 + (int)rank * (ROWS / 2), blk = m0 >> 7;
       for (int kb = 0; kb < a.num_kb; ++kb) {
         ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
                                                   kWaitLimitNs));
@@ -552,19 +564,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint64_t db0 = ptx::desc_sw128(ptx::smem_addr(smem + SM::kB));
       const uint64_t dsa0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFA));
       const uint64_t dsb0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFB));
-      const uint32_t id0 = ptx::idesc_mxf4_m(2 * kBM, kPairRows, 0);
-      const uint32_t id2 = ptx::idesc_mxf4_m(2 * kBM, kPairRows, 2);
+      const uint32_t id0 = ptx::idesc_mxf4_m(2 * kBM, ROWS, 0);
+      const uint32_t id2 = ptx::idesc_mxf4_m(2 * kBM, ROWS, 2);
       int stage = 0, ab = 0;
       uint32_t phase = 0, acc_phase = 0, sfbuf = 0;
       bool ok = true;
       for (int g = first; g < total && ok; g += step) {
         // tiles start at a 128-row scale block or in the middle of one
-        const uint32_t shift = (uint32_t)((g / pairs * kPairRows & 127) >> 5);
-        ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->acc_empty[ab], acc_phase ^ 1u, abort_flag,
-                                                  kWaitLimitNs));
+        const uint32_t shift = (uint32_t)((g / pairs * ROWS & 127) >> 5);
+        // free: read by the epilogue in its last tile, or, with shared columns, what the
+        // tile before has in them
+        ok = __all_sync(kFullMask,
+                        kShared ? ptx::mbar_wait(&tail->acc_empty[ab ^ 1],
+                                                 ab ? acc_phase : acc_phase ^ 1u, abort_flag,
+                                                 kWaitLimitNs)
+                                : ptx::mbar_wait(&tail->acc_empty[ab], acc_phase ^ 1u, abort_flag,
+                                                 kWaitLimitNs));
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(ab * kPairRows);
+        const uint32_t d = tmem_base + (ab ? kAcc2 : 0u);
         for (int kb = 0; kb < a.num_kb; ++kb) {
           ok = __all_sync(kFullMask,
                           ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs));
@@ -584,12 +602,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             ptx::tc_cp_sf_pair(fb0, dsb);
             ptx::tc_cp_sf_pair(fb0 + 4, dsb + kBlk);
             if constexpr (F8) {
-              ptx::tc_mma_f8f4_pair(d, da, db, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 0), fa, fb, acc);
-              ptx::tc_mma_f8f4_pair(d, da + 2, db + 2, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 1), fa,
+              ptx::tc_mma_f8f4_pair(d, da, db, ptx::idesc_f8f4_m(2 * kBM, ROWS, 0), fa, fb, acc);
+              ptx::tc_mma_f8f4_pair(d, da + 2, db + 2, ptx::idesc_f8f4_m(2 * kBM, ROWS, 1), fa,
                                     fb, 1u);
-              ptx::tc_mma_f8f4_pair(d, da + 4, db + 4, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 2), fa,
+              ptx::tc_mma_f8f4_pair(d, da + 4, db + 4, ptx::idesc_f8f4_m(2 * kBM, ROWS, 2), fa,
                                     fb, 1u);
-              ptx::tc_mma_f8f4_pair(d, da + 6, db + 6, ptx::idesc_f8f4_m(2 * kBM, kPairRows, 3), fa,
+              ptx::tc_mma_f8f4_pair(d, da + 6, db + 6, ptx::idesc_f8f4_m(2 * kBM, ROWS, 3), fa,
                                     fb, 1u);
             } else {
               if (whole) {
@@ -632,38 +650,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int ab = 0;
     uint32_t acc_phase = 0;
     for (int g = first; g < total; g += step) {
-      const int m0 = g / pairs * kPairRows, cols = min(kPairRows, a.M - m0);
+      const int m0 = g / pairs * ROWS, cols = min(ROWS, a.M - m0);
       const int n0 = (g % pairs * 2 + (int)rank) * 128 + q * 32, n = n0 + lane;
       if (!ptx::mbar_wait(&tail->acc_full[ab], acc_phase, abort_flag, kWaitLimitNs)) {
         if (lane == 0) atomicOr(&a.flags[0], kErrTimeout);
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * kPairRows);
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (ab ? kAcc2 : 0u);
+      // Two chunks of 16 rows a turn; shared columns first, and handed back once read (a
+      // half's two of the three chunks at that end).
+      bool held = true;
+      auto hand_back = [&] {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(acc_empty_l + (uint32_t)ab * 8u);
+        held = false;
+      };
       if (n0 < a.N) {
-        // two chunks of 16 rows a turn, the second's load behind the first's stores
+        const bool down = kShared && ab == 0;
 #pragma unroll 1
-        for (int c0 = hh * 16; c0 < cols; c0 += 64) {
-          uint32_t r0[16], r1[16];
-          const bool two = c0 + 32 < cols;
-          ptx::tmem_ld16_issue(taddr + (uint32_t)c0, r0);
-          ptx::tmem_wait_ld(r0);
-          if (two) ptx::tmem_ld16_issue(taddr + (uint32_t)(c0 + 32), r1);
-          float v[16];
+        for (int u = 0; u < ROWS / 64; ++u) {
+          const int c0 = (down ? ROWS - 64 - 64 * u : 64 * u) + hh * 16, c1 = c0 + 32;
+          if (c0 < cols) {
+            uint32_t r0[16], r1[16];
+            const bool two = c1 < cols;
+            ptx::tmem_ld16_issue(taddr + (uint32_t)c0, r0);
+            if (two) ptx::tmem_ld16_issue(taddr + (uint32_t)c1, r1);
+            ptx::tmem_wait_ld(r0);
+            if (two) ptx::tmem_wait_ld(r1);
+            if (held && (kShared || u == ROWS / 64 - 1)) hand_back();
+            float v[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r0[j]);
-          lin_store16(a, m0 + c0, min(16, cols - c0), n, v);
-          if (two) {
-            ptx::tmem_wait_ld(r1);
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r0[j]);
+            lin_store16(a, m0 + c0, min(16, cols - c0), n, v);
+            if (two) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r1[j]);
-            lin_store16(a, m0 + c0 + 32, min(16, cols - c0 - 32), n, v);
+              for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r1[j]);
+              lin_store16(a, m0 + c1, min(16, cols - c1), n, v);
+            }
           }
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(acc_empty_l + (uint32_t)ab * 8u);
+      if (held) hand_back();
       if (ab) acc_phase ^= 1u;
       ab ^= 1;
     }
@@ -1022,9 +1051,9 @@ cudaError_t launch_tile(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
   }
 }
 
-template <bool F8>
+template <bool F8, int ROWS>
 cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
-  constexpr size_t kBytes = LinPairSmem<F8>::kBytes;
+  constexpr size_t kBytes = LinPairSmem<F8, ROWS>::kBytes;
   LinPairMaps m;
   const uint64_t w_rows = (uint64_t)a.slabs * a.num_kb * kBM;
   if (w_rows > 0x7FFFFFFFull) return cudaErrorInvalidValue;
@@ -1033,11 +1062,11 @@ cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
   const uint64_t row_blocks = (uint64_t)(a.M + 127) / 128;
   if (e != cudaSuccess ||
       (e = make_tmap(&m.x, g.q, F8 ? (uint64_t)a.K : (uint64_t)a.K / 2, (uint64_t)a.M,
-                     kPairHalf)) ||
+                     ROWS / 2)) ||
       (e = make_tmap_scales(&m.wsf, a.w_sf, (uint64_t)a.slabs * a.kc4, 1, F8 ? 1 : 2, 1)) ||
       (e = make_tmap_scales(&m.tsf, a.t_sf, (uint64_t)a.kc4, row_blocks, F8 ? 1 : 2, 2)))
     return e;
-  a.tiles = (a.M + kPairRows - 1) / kPairRows;
+  a.tiles = (a.M + ROWS - 1) / ROWS;
   const int64_t items = (int64_t)a.tiles * ((a.slabs + 1) / 2);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
   // clusters that fit at once (a GPC may have an odd number of SMs), for the device of
@@ -1046,20 +1075,20 @@ cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
   int clusters = fit.load(std::memory_order_relaxed);
   if (clusters == 0) {
     static std::atomic<bool> set{false};
-    if ((e = allow_smem(linear_pair_kernel<F8>, kBytes, set)) != cudaSuccess) return e;
+    if ((e = allow_smem(linear_pair_kernel<F8, ROWS>, kBytes, set)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(g.num_sms);
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = kBytes;
     int c = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&c, linear_pair_kernel<F8>, &cfg)) != cudaSuccess)
+    if ((e = cudaOccupancyMaxActiveClusters(&c, linear_pair_kernel<F8, ROWS>, &cfg)) != cudaSuccess)
       return e;
     if (c < 1) return cudaErrorInvalidConfiguration;
     clusters = c < g.num_sms / 2 ? c : g.num_sms / 2;
     fit.store(clusters, std::memory_order_relaxed);
   }
   const int grid = 2 * (int)(items < clusters ? items : clusters);
-  return launch_pdl(linear_pair_kernel<F8>, dim3(grid), dim3(kPairThreads), kBytes, st, m, a);
+  return launch_pdl(linear_pair_kernel<F8, ROWS>, dim3(grid), dim3(kPairThreads), kBytes, st, m, a);
 }
 
 int grid_for(int64_t n) {
@@ -1124,25 +1153,31 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
   a.kc4 = a.K / 128;
   if (a.M <= 32) return s.f8 ? launch_tile<true, 32>(g, a, st) : launch_tile<false, 32>(g, a, st);
   // Tiles: 64 rows while 128-row tiles would not give every SM one, else 128, or SM pairs'
-  // 256 x 192, by an estimate in cycles: rounds of tiles times (k-blocks times a tile's
-  // cycles a k-block, plus a tile's fixed part), all fitted to timings.  Measured (us, pair
-  // against the other; MXFP4, then MXFP8 pairs in): 1024 x 4096 x 4096 16.6 / 13.3 and 18.8 /
-  // 15.5 (one round of 128-row tiles, two of pairs); 1536 x 4096 x 4096 18.7 / 21.1 and 20.2 /
-  // 27.5; 4096 x 4096 x 512 16.3 / 14.3 and 15.3 / 14.3; 4096 x 4096 x 2048 26.0 / 27.2 and
-  // 25.1 / 31.6; 16384 x 4096 x 4096 124.8 / 145.4 and 166.4 / 199.0.  Fewer than 24 pairs
-  // leave most of the weights' reads to too few SMs (317 x 1001 x 1056: 12.9 / 8.8).
+  // 256 features by 192 or 256 rows, by an estimate in cycles: rounds of tiles times
+  // (k-blocks times a tile's cycles a k-block, plus a tile's fixed part), all fitted to
+  // timings.  Measured (us, 256 / 192 / 128 rows; MXFP4, then MXFP8 pairs in): 1024 x 4096 x
+  // 4096 13.0 / 16.6 / 13.3 and 14.2 / 19.5 / 15.5; 1536 x 4096 x 4096 19.8 / 18.5 / 21.1 and
+  // 23.4 / 20.0 / 27.5; 4096 x 4096 x 512 14.2 / 15.8 / 14.3 and 12.7 / 14.3 / 14.3; 4096 x
+  // 4096 x 4096 45.5 / 44.0 / - and 47.2 / 44.3 / -; 16384 x 4096 x 4096 116.6 / 124.1 / 145.4
+  // and 163 / 165 / 199; 8192 x 8192 x 8192 181 / 198 / - and 328 / 336 / -.  Fewer than 24
+  // pairs leave most of the weights' reads to too few SMs (317 x 1001 x 1056: 12.9 / 8.8).
   const bool narrow = (int64_t)((a.M + 127) / 128) * a.slabs <= g.num_sms;
-  const int64_t pair_tiles =
-      (int64_t)((a.M + kPairRows - 1) / kPairRows) * ((a.slabs + 1) / 2);
   const int64_t tiles =
       (int64_t)(narrow ? (a.M + 63) / 64 : (a.M + 127) / 128) * a.slabs;
   auto rounds = [](int64_t n, int64_t at_once) { return (n + at_once - 1) / at_once; };
-  const int64_t kb_pair = s.f8 ? 430 : 490;
   const int64_t kb_tile = narrow ? (s.f8 ? 750 : 600) : (s.f8 ? 850 : 1100);
-  const int64_t t_pair = rounds(pair_tiles, g.num_sms / 2) * (a.num_kb * kb_pair + 2500);
   const int64_t t_tile = rounds(tiles, 2 * g.num_sms) * (a.num_kb * kb_tile + (narrow ? 1200 : 1500));
-  if (pair_tiles >= 24 && t_pair < t_tile)
-    return s.f8 ? launch_pair<true>(g, a, st) : launch_pair<false>(g, a, st);
+  auto pair_tiles = [&](int rows) {
+    return (int64_t)((a.M + rows - 1) / rows) * ((a.slabs + 1) / 2);
+  };
+  auto t_pair = [&](int rows, int64_t kb) {
+    return rounds(pair_tiles(rows), g.num_sms / 2) * (a.num_kb * kb + 1500);
+  };
+  const int64_t t192 = t_pair(192, s.f8 ? 560 : 590), t256 = t_pair(256, s.f8 ? 745 : 762);
+  if (pair_tiles(256) >= 24 && t256 < t_tile && t256 < t192)
+    return s.f8 ? launch_pair<true, 256>(g, a, st) : launch_pair<false, 256>(g, a, st);
+  if (pair_tiles(192) >= 24 && t192 < t_tile)
+    return s.f8 ? launch_pair<true, 192>(g, a, st) : launch_pair<false, 192>(g, a, st);
   if (narrow) return s.f8 ? launch_tile<true, 64>(g, a, st) : launch_tile<false, 64>(g, a, st);
   return s.f8 ? launch_tile<true, 128>(g, a, st) : launch_tile<false, 128>(g, a, st);
 }
