@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kQuantThreads)
                            int Kp, uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
                            int span_log) {
   ptx::pdl_wait();
-  ptx::pdl_launch_dependents();   // after the wait: see the split kernel's weight loads
+  ptx::pdl_launch_dependents();
   const int words = Kp / 128;
   const int c = ((int)blockIdx.y << span_log) + (threadIdx.x & ((1 << span_log) - 1));
   const int rows_once = kQuantThreads >> span_log;
@@ -760,25 +760,20 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
     const uint64_t pol_t = ptx::policy_evict_last();
     const uint8_t* wsf = a.w_sf + (size_t)slab * a.kc4 * kSFAtomBytes;
     const uint8_t* tsf = a.t_sf + (size_t)(tile * TN >> 7) * a.kc4 * kSFAtomBytes;
-    auto tokens = [&](int kb, int s) {
-      const int atoms = min(kKb, a.K - kb * kKb) / 128;
-      ptx::tma_load_2d(smem + SM::kB + (size_t)s * SM::kBSlot, &tmap_x, kb * kBKBytes, m0,
-                       &tail->full[s], pol_t);
-      ptx::bulk_load(smem + SM::kSFB + (size_t)s * SM::kSF,
-                     tsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes,
-                     &tail->full[s], pol_t);
-    };
-    // The first stages' weights do not wait for the kernel before this one; their rows do.
-    auto release = [&](int n) {
-      ptx::pdl_wait();
-      if (ptx::elect_one())
-        for (int j = 0; j < n; ++j) tokens(kb0 + j, j);
-      __syncwarp();
-    };
+    // The first stages' weights are asked into L2 while the kernel before this one ends.
+    if (ptx::elect_one()) {
+      const int first = min(kb1 - kb0, kSt);
+      for (int j = 0; j < first; ++j)
+        ptx::tma_prefetch_2d(&tmap_w, 0, (slab * a.num_kb + kb0 + j) * kBM);
+      const int atom0 = kb0 * (kKb / 128);
+      ptx::bulk_prefetch(wsf + (size_t)atom0 * kSFAtomBytes,
+                         (uint32_t)(min(first * (kKb / 128), a.kc4 - atom0) * kSFAtomBytes));
+    }
+    __syncwarp();
+    ptx::pdl_wait();
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!QUANT && kb - kb0 == kSt) release(kSt);
       ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
                                                 kWaitLimitNs));
       if (!ok) break;
@@ -794,7 +789,13 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
         ptx::bulk_load(smem + SM::kSFA + (size_t)stage * SM::kSF,
                        wsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes, bar,
                        pol_w);
-        if (!QUANT && kb - kb0 >= kSt) tokens(kb, stage);
+        if (!QUANT) {
+          ptx::tma_load_2d(smem + SM::kB + (size_t)stage * SM::kBSlot, &tmap_x, kb * kBKBytes, m0,
+                           bar, pol_t);
+          ptx::bulk_load(smem + SM::kSFB + (size_t)stage * SM::kSF,
+                         tsf + (size_t)kb * (kKb / 128) * kSFAtomBytes, atoms * kSFAtomBytes, bar,
+                         pol_t);
+        }
       }
       __syncwarp();
       if (++stage == kSt) {
@@ -802,7 +803,6 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
         phase ^= 1u;
       }
     }
-    if (!QUANT && kb1 - kb0 <= kSt) release(kb1 - kb0);
   } else if (warp == 1) {
     {
       const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));

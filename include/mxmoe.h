@@ -257,7 +257,7 @@ MXMOE_API moe_status moe_run_host(const moe_dims *dims, const void *prepared_dev
  * Uses regions of the workspace of its own: a moe_pre_dispatch made before it can still be
  * followed by its moe_forward.  One call at a time may use a workspace.  After
  * MOE_ERR_TIMEOUT initialise the workspace again.  x_dev, router_dev and out_dev 16-byte
- * aligned; prepared_dev must not be written by a kernel still running. */
+ * aligned. */
 MXMOE_API moe_status moe_few_forward(const moe_dims *dims, const void *prepared_dev,
                                      const void *router_dev, const void *x_dev,
                                      int32_t *topk_ids_dev, float *topk_weights_dev,
@@ -391,9 +391,8 @@ MXMOE_API moe_status moe_linear_workspace_init(const moe_linear_dims *dims, void
 /* The product on bf16 rows x_dev [rows, K] (row stride ldx elements, a multiple of 8 and at
  * least K; 16-byte aligned; finite), quantised into the workspace first.  out_dev is
  * [rows, N] with row stride ldo >= N elements, bf16 (MOE_OUT_BF16) or fp32 (MOE_OUT_F32),
- * aligned to its element.  0 <= rows <= max_rows; 0 rows is a no-op.  prepared_dev must
- * not be written by a kernel still running when the call's kernels start.  Results do not
- * depend on timing. */
+ * aligned to its element; it shares no memory with x_dev or the workspace.  0 <= rows <=
+ * max_rows; 0 rows is a no-op.  Results do not depend on timing. */
 enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
 MXMOE_API moe_status moe_linear_forward(const moe_linear_dims *dims, const void *prepared_dev,
                                         const void *x_dev, int64_t ldx, int64_t rows,

@@ -257,3 +257,48 @@ def test_offsets_past_32_bits(rows, N, K, mma):
     assert torch.equal(out[-n:], out[:n])
     pick = [0, n // 2, rows - n // 3, rows - 1]
     lin.check(out[pick], x[pick])
+
+
+@pytest.mark.parametrize("mma", [F4, F8])
+@pytest.mark.parametrize("rows", [4864, 4870, 5000, 5094])
+def test_rounds_of_256_row_tiles(rows, mma):
+    # three rounds of tiles through accumulators that share columns; a last tile of 6 rows,
+    # 136 (the shared columns unused) and 230
+    N, K = 2300, 160
+    lin = Linear(N, K, rows, mma)
+    x = inputs(rows, K)
+    out = torch.full((rows, N), float("nan"), dtype=torch.float32, device="cuda")
+    again = torch.empty_like(out)
+    mx.moe_linear_forward(lin.dims, lin.prepared, x, out, lin.ws)
+    mx.moe_linear_forward(lin.dims, lin.prepared, x, again, lin.ws)
+    mx.moe_linear_check(lin.ws)
+    lin.check(out, x)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_weights_written_just_before(rows):
+    # the weights change on the same stream between calls, with no wait in between
+    N, K = 1024, 2048
+    lins = [Linear(N, K, rows, F4, seed=s) for s in (1, 2)]
+    src = [(torch.from_numpy(l.codes).cuda(), torch.from_numpy(l.scales).cuda()) for l in lins]
+    x = inputs(rows, K)
+    want = [torch.empty(rows, N, device="cuda") for _ in lins]
+    for l, w in zip(lins, want):
+        mx.moe_linear_forward(l.dims, l.prepared, x, w, l.ws)
+    a = lins[0]
+    outs = [torch.empty_like(want[0]) for _ in range(20)]
+    for i, out in enumerate(outs):
+        if i % 3:
+            mx.moe_linear_prepare(a.dims, *src[i & 1], a.prepared)
+        else:
+            a.prepared.copy_(lins[1].prepared if i & 1 else want_prepared(a, src[0]))
+        mx.moe_linear_forward(a.dims, a.prepared, x, out, a.ws)
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i & 1])
+
+
+def want_prepared(lin, src):
+    p = torch.empty_like(lin.prepared)
+    mx.moe_linear_prepare(lin.dims, *src, p)
+    return p
