@@ -413,15 +413,16 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
 // stages its own 128-feature slab and half of the rows, so it writes and reads 60% (192)
 // or half (256) of the shared-memory bytes a 128 x 128 tile takes per product.  Two
 // accumulators: two of 256 rows and the scale registers are more than the 512 columns of
-// tensor memory, so these share 48 columns, which the epilogue reads first.  Roles (320
-// threads, one block an SM): warp 0 producer, warp 1 of the leader MMA issue, warps 2-9
-// epilogue, two a lane quarter.
-// Bound by the tensor pipe and the power cap: 16384 x 4096 x 4096 in 85 us behind the
-// quantisation (6.4 PFLOP/s) at 1.95 GHz and 1370 W of 1400; with no weight loads it takes 4%
-// less, with no stores 10%, with neither 11%.
-constexpr int kPairThreads = 320;
+// tensor memory, so these share 48 columns, which the epilogue reads first.  Roles (576
+// threads, one block an SM): warp 0 producer, warp 1 of the leader MMA issue, warps 2-17
+// epilogue, four a lane quarter (two: 39.5 us against 34.2 at 16384 x 4096 x 512).
+// Bound by the tensor pipe and power: 16384 x 4096 x 4096 in 85 us behind the quantisation
+// (6.4 PFLOP/s).  On zeros, which draw less, 3% less, with MXFP8 rows 17% (8192 cubed: 331 us
+// and 253, 0.89 of what the MMA alone reaches); of that, no loads at all 3 to 4%, no
+// copies of scales nothing, no stores 10%.
+constexpr int kPairEpiWarps = 16;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr int kPairTmemCols = 512;
-constexpr int kPairEpiWarps = 8;
 constexpr uint32_t kPairSfCols = 24;                // a buffer of scale registers: 8 of the
 constexpr uint32_t kPairSfCol = kPairTmemCols - 2 * kPairSfCols;   // slab's, 16 of the rows'
 __host__ __device__ constexpr int lin_pair_stages(int rows) { return rows == 256 ? 6 : 7; }
@@ -434,7 +435,7 @@ struct __align__(16) LinPairTail {
   uint64_t full[7];               // leader: both CTAs' loads of a stage landed
   uint64_t empty[7];              // each CTA: the pair's MMAs are done with its stage
   uint64_t acc_full[2];           // each CTA: the accumulator is complete
-  uint64_t acc_empty[2];          // leader: all 16 epilogue warps have read it, or what
+  uint64_t acc_empty[2];          // leader: both CTAs' epilogue warps have read it, or what
                                   // the other accumulator shares with it
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -645,7 +646,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ptx::mbar_wait(&tail->mma_done, 0, &never, kWaitLimitNs);
     }
   } else {
-    const int q = warp & 3, hh = (warp - 2) >> 2;   // lane quarter; even or odd chunks
+    constexpr int kShare = kPairEpiWarps / 4;        // warps a lane quarter
+    const int q = warp & 3, hh = (warp - 2) >> 2;    // lane quarter; first chunk
     const uint32_t acc_empty_l = ptx::mapa_shared(ptx::smem_addr(&tail->acc_empty[0]), 0);
     int ab = 0;
     uint32_t acc_phase = 0;
@@ -669,9 +671,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       };
       if (n0 < a.N) {
         const bool down = kShared && ab == 0;
+        constexpr int kTurns = (ROWS + 32 * kShare - 1) / (32 * kShare);
 #pragma unroll 1
-        for (int u = 0; u < ROWS / 64; ++u) {
-          const int c0 = (down ? ROWS - 64 - 64 * u : 64 * u) + hh * 16, c1 = c0 + 32;
+        for (int u = 0; u < kTurns; ++u) {
+          const int c0 = (down ? kTurns - 1 - u : u) * 32 * kShare + hh * 16, c1 = c0 + 16 * kShare;
           if (c0 < cols) {
             uint32_t r0[16], r1[16];
             const bool two = c1 < cols;
@@ -679,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (two) ptx::tmem_ld16_issue(taddr + (uint32_t)c1, r1);
             ptx::tmem_wait_ld(r0);
             if (two) ptx::tmem_wait_ld(r1);
-            if (held && (kShared || u == ROWS / 64 - 1)) hand_back();
+            if (held && (kShared || u == kTurns - 1)) hand_back();
             float v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r0[j]);
