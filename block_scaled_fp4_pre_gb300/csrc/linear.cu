@@ -1158,7 +1158,8 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
   // Tiles: 64 rows while 128-row tiles would not give every SM one, else 128, or SM pairs'
   // 256 features by 192 or 256 rows, by an estimate in cycles: rounds of tiles times
   // (k-blocks times a tile's cycles a k-block, plus a tile's fixed part), all fitted to
-  // timings.  Measured (us, 256 / 192 / 128 rows; MXFP4, then MXFP8 pairs in): 1024 x 4096 x
+  // timings.  Measured (us, 256 / 192 / 128 rows, pairs with eight epilogue warps; MXFP4, then
+  // MXFP8 pairs in): 1024 x 4096 x
   // 4096 13.0 / 16.6 / 13.3 and 14.2 / 19.5 / 15.5; 1536 x 4096 x 4096 19.8 / 18.5 / 21.1 and
   // 23.4 / 20.0 / 27.5; 4096 x 4096 x 512 14.2 / 15.8 / 14.3 and 12.7 / 14.3 / 14.3; 4096 x
   // 4096 x 4096 45.5 / 44.0 / - and 47.2 / 44.3 / -; 16384 x 4096 x 4096 116.6 / 124.1 / 145.4
