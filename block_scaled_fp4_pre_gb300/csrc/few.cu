@@ -542,6 +542,8 @@ __global__ void __launch_bounds__(256, kFewBlocksPerSM)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  // Met before the cluster's sums are exchanged: every block has started by then.
+  if (CLUSTER) ptx::cluster_arrive_relaxed();
   const uint32_t tmem_base = tail->tmem_base;
   volatile int* abort_flag = &tail->abort;
   RouteScratch& scratch = *reinterpret_cast<RouteScratch*>(smem);
@@ -1030,6 +1032,8 @@ __global__ void __launch_bounds__(256, kFewBlocksPerSM)
     if (!ok && ep == 0) atomicOr(&a.flags[0], kErrTimeout);
   }
 
+  __syncwarp();
+  if (CLUSTER) ptx::cluster_wait();
   if (CLUSTER && slots > 0 && (int)blockIdx.x < P1.ranges) {
     // The cluster's sums of its slab: block p adds features [16 p, 16 p + 16), in the order
     // of the blocks; the buffer is [part][feature][token].  Few tokens fit the room of phase
@@ -1040,7 +1044,6 @@ __global__ void __launch_bounds__(256, kFewBlocksPerSM)
     static_assert(kFewCluster * kShare * kTailTokens * 4 <= sizeof(tail->h), "room of h");
     float* const sums = T <= kTailTokens ? &tail->h[0][0] : reinterpret_cast<float*>(smem);
     const int part = (int)blockIdx.x % kFewCluster, slab = (int)blockIdx.x / kFewCluster;
-    __syncwarp();
     if (T > kTailTokens) ptx::cluster_sync();
     if (warp >= 2) {
       const int row = (warp & 3) * 32 + lane;
