@@ -117,6 +117,7 @@ def lib() -> ctypes.CDLL:
             "moe_linear_forward": ([LD, vp, vp, i64, i64, vp, i64, i32, vp, sz, vp], i32),
             "moe_linear_forward_pair": ([LD, vp, vp, vp, i64, vp, i64, i32, vp, sz, vp], i32),
             "moe_linear_check": ([vp, vp], i32),
+            "moe_debug_linear_give_up": ([vp, i32], i32),
         }
         for name, (args, res) in sigs.items():
             f = getattr(l, name)
@@ -394,6 +395,11 @@ def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, w
 
 def moe_linear_check(ws, stream=None) -> None:
     _check(lib().moe_linear_check(_ptr(ws), _stream(stream)))
+
+
+def moe_debug_linear_give_up(ws, on: bool) -> None:
+    """Calls on this linear workspace behave as if a device wait had run out."""
+    _check(lib().moe_debug_linear_give_up(_ptr(ws), int(on)))
 
 
 def moe_fp4_mma_probe(ws, n: int, blocks_per_sm: int, blocks: int, mma_count: int,

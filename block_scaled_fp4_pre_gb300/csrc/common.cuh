@@ -319,6 +319,7 @@ struct LinearLaunch {
   int64_t ldo;
   int out_f32;
   int32_t* flags;
+  int give_up;               // as LinArgs
   int num_sms;
 };
 cudaError_t launch_linear_prepare(const LinearShape& s, const uint8_t* codes,

@@ -21,7 +21,8 @@
 //   epilogue warps quantise bf16 rows into the operand stages themselves, so that the
 //   call is one kernel.
 //
-// Every wait is bounded (kWaitLimitNs); a timeout sets the workspace's error flag.
+// Every wait is bounded (kWaitLimitNs); a timeout sets the workspace's error flag, and a block
+// leaves only when its copies and MMAs have ended.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -148,6 +149,7 @@ struct LinArgs {
   int slabs, tiles, num_kb, kc4;
   int out_f32;
   int pairs16;           // bf16 rows whose features can be stored two at a time
+  int give_up;           // the MMA warps give up before their first wait (a test of that path)
 };
 
 __host__ __device__ constexpr int lin_stages(int tn) { return tn == 128 ? 3 : tn == 64 ? 4 : 5; }
@@ -158,6 +160,7 @@ struct __align__(16) LinTail {
   uint64_t acc_full, acc_empty, mma_done;
   uint32_t tmem_base;
   int abort;
+  int issued;   // k-blocks whose copies were issued (linear_split_kernel)
 };
 
 template <bool F8, int TN>
@@ -334,7 +337,8 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       const uint64_t dsb0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFB));
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0, sfbuf = 0;
-      bool ok = true;
+      bool ok = !a.give_up;
+      if (!ok) *abort_flag = 1;
       for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
         ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->acc_empty, acc_phase ^ 1u, abort_flag,
                                                   kWaitLimitNs));
@@ -738,6 +742,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       ptx::mbar_init(&tail->empty[s], 1);
     }
     ptx::mbar_init(&tail->acc_full, 1);
+    ptx::mbar_init(&tail->mma_done, 1);
     tail->abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_w);
@@ -756,6 +761,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
   const int m0 = tile * TN, cols = min(TN, a.M - m0);
   const int q = warp & 3, ep = (int)threadIdx.x - 64, row = q * 32 + lane;
   bool ok = true;
+  int done = 0;   // k-blocks issued (warp 0) or quantised (warps 2-5)
 
   if (warp == 0) {
     // the whole warp runs the loop; one lane issues
@@ -776,7 +782,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
     ptx::pdl_wait();
     int stage = 0;
     uint32_t phase = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int kb = kb0; kb < kb1; ++kb, ++done) {
       ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
                                                 kWaitLimitNs));
       if (!ok) break;
@@ -806,6 +812,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
         phase ^= 1u;
       }
     }
+    if (lane == 0) tail->issued = done;
   } else if (warp == 1) {
     {
       const uint64_t da0 = ptx::desc_sw128(ptx::smem_addr(smem));
@@ -814,7 +821,9 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       const uint64_t dsb0 = ptx::desc_sf(ptx::smem_addr(smem + SM::kSFB));
       int stage = 0;
       uint32_t phase = 0, sfbuf = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      ok = !a.give_up;
+      if (!ok) *abort_flag = 1;
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
         ok = __all_sync(kFullMask,
                         ptx::mbar_wait(&tail->full[stage], phase, abort_flag, kWaitLimitNs));
         if (!ok) break;
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
       constexpr int kMost = TN * kVecs / 128;     // of a thread
       int stage = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb, ++done) {
         uint4 w[kMost];
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
@@ -854,8 +863,9 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
           if (r < cols && c * 8 < a.k_live)
             w[i] = *reinterpret_cast<const uint4*>(a.x + (m0 + r) * a.ldx + c * 8);
         }
-        ok = ok && ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
-        __syncwarp();
+        ok = __all_sync(kFullMask, ptx::mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag,
+                                                  kWaitLimitNs));
+        if (!ok) break;
         uint8_t* b = smem + SM::kB + (size_t)stage * SM::kBSlot;
         uint8_t* sf = smem + SM::kSFB + (size_t)stage * SM::kSF;
 #pragma unroll
@@ -878,17 +888,15 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
           uint32_t s = (uint32_t)(e + 127) << ((v >> 2 & 3) * 8);
           s |= __shfl_xor_sync(kFullMask, s, 4);
           s |= __shfl_xor_sync(kFullMask, s, 8);
-          if (ok) {
-            // 128-byte swizzle: 16-byte chunk c of row r at chunk c ^ (r % 8)
-            if constexpr (F8)
-              *reinterpret_cast<uint2*>(b + r * 128 + (((v >> 1) ^ (r & 7)) << 4) + (v & 1) * 8) =
-                  ptx::e4m3x8(f);
-            else
-              *reinterpret_cast<uint32_t*>(b + r * 128 + (((v >> 2) ^ (r & 7)) << 4) +
-                                           (v & 3) * 4) = ptx::e2m1x8(f);
-            if ((v & 15) == 0)
-              *reinterpret_cast<uint32_t*>(sf + (v >> 4) * kSFAtomBytes + r * 16) = s;
-          }
+          // 128-byte swizzle: 16-byte chunk c of row r at chunk c ^ (r % 8)
+          if constexpr (F8)
+            *reinterpret_cast<uint2*>(b + r * 128 + (((v >> 1) ^ (r & 7)) << 4) + (v & 1) * 8) =
+                ptx::e4m3x8(f);
+          else
+            *reinterpret_cast<uint32_t*>(b + r * 128 + (((v >> 2) ^ (r & 7)) << 4) +
+                                         (v & 3) * 4) = ptx::e2m1x8(f);
+          if ((v & 15) == 0)
+            *reinterpret_cast<uint32_t*>(sf + (v >> 4) * kSFAtomBytes + r * 16) = s;
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&tail->full[stage]);
@@ -904,7 +912,8 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
   __syncwarp();
   // The accumulator is complete, so every copy has landed and every MMA has read its
   // operands: the stages are free for the other blocks' sums.  (After a timeout the sums
-  // are worthless and the flag says so; all barriers are still met.)
+  // are worthless and the flag says so; all barriers are still met, and copies and MMAs in
+  // flight touch this block's memory only, which it keeps until they have ended.)
   if (!ok) atomicOr(&a.flags[0], kErrTimeout);
   const int n = slab * 128 + row;
   if (parts == 1) {
@@ -961,6 +970,22 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {   // the same in every thread: all waits that set it lie before the barrier
+    int never = 0;
+    // A stage's phase ends with its bytes and, with QUANT, every quantiser's arrival: those
+    // that gave up arrive for what was issued, at most kSt k-blocks, a stage each.
+    if (QUANT && warp >= 2)
+      for (int i = done; i < tail->issued; ++i) ptx::mbar_arrive(&tail->full[i % kSt]);
+    if (warp == 0)
+      for (int i = max(done - kSt, 0); i < done; ++i)
+        ptx::mbar_wait(&tail->full[i % kSt], (uint32_t)((i / kSt) & 1), &never, kWaitLimitNs);
+    if (warp == 1) {
+      if (ptx::elect_one()) ptx::tc_commit(&tail->mma_done);
+      __syncwarp();
+      ptx::mbar_wait(&tail->mma_done, 0, &never, kWaitLimitNs);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, kLinTmemCols);
@@ -1147,6 +1172,7 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
   a.x = static_cast<const uint16_t*>(g.x);
   a.ldx = g.ldx;
   a.flags = g.flags;
+  a.give_up = g.give_up;
   a.M = (int)g.rows;
   a.N = s.N;
   a.K = linear_padded_k(s);

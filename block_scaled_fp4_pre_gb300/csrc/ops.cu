@@ -59,8 +59,12 @@ LinWs ws_layout(const moe_linear_dims& d) {
   return L;
 }
 
+struct LinState {
+  moe_linear_dims dims;
+  bool give_up;   // moe_debug_linear_give_up
+};
 std::mutex g_mu;
-std::map<const void*, moe_linear_dims> g_linear;
+std::map<const void*, LinState> g_linear;
 
 moe_status check_dims(const moe_linear_dims* d) {
   if (!d) return fail(MOE_ERR_INVALID_ARG, "dims is NULL");
@@ -79,7 +83,8 @@ moe_status check_dims(const moe_linear_dims* d) {
   return MOE_OK;
 }
 
-moe_status check_ws(const moe_linear_dims* d, const void* ws, size_t ws_bytes) {
+moe_status check_ws(const moe_linear_dims* d, const void* ws, size_t ws_bytes,
+                    bool* give_up) {
   if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
   const size_t need = ws_layout(*d).total;
@@ -90,19 +95,20 @@ moe_status check_ws(const moe_linear_dims* d, const void* ws, size_t ws_bytes) {
   if (it == g_linear.end())
     return fail(MOE_ERR_WORKSPACE_MISMATCH,
                 "workspace %p was not initialised by moe_linear_workspace_init", ws);
-  const moe_linear_dims& w = it->second;
+  const moe_linear_dims& w = it->second.dims;
   if (w.out_features != d->out_features || w.in_features != d->in_features ||
       w.max_rows != d->max_rows || w.mma_type != d->mma_type)
     return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was initialised for other dims", ws);
+  *give_up = it->second.give_up;
   return MOE_OK;
 }
 
 moe_status check_call(const moe_linear_dims* d, const void* prepared, int64_t rows,
                       const void* out, int64_t ldo, int32_t out_type, const void* ws,
-                      size_t ws_bytes) {
+                      size_t ws_bytes, bool* give_up) {
   moe_status s = check_dims(d);
   if (s) return s;
-  if ((s = check_ws(d, ws, ws_bytes))) return s;
+  if ((s = check_ws(d, ws, ws_bytes, give_up))) return s;
   if (rows < 0 || rows > d->max_rows)
     return fail(MOE_ERR_INVALID_ARG, "rows %lld outside [0, max_rows=%d]", (long long)rows,
                 d->max_rows);
@@ -122,7 +128,7 @@ moe_status check_call(const moe_linear_dims* d, const void* prepared, int64_t ro
 // The product of a pair (q, sf) or, q null, of a few bf16 rows x.
 moe_status forward(const moe_linear_dims* d, const void* prepared, const void* q, const void* sf,
                    const void* x, int64_t ldx, int64_t rows, void* out, int64_t ldo,
-                   int32_t out_type, void* ws, cudaStream_t st) {
+                   int32_t out_type, void* ws, bool give_up, cudaStream_t st) {
   const LinWs L = ws_layout(*d);
   uint8_t* b = static_cast<uint8_t*>(ws);
   LinearLaunch g;
@@ -137,6 +143,7 @@ moe_status forward(const moe_linear_dims* d, const void* prepared, const void* q
   g.ldo = ldo;
   g.out_f32 = out_type == MOE_OUT_F32;
   g.flags = reinterpret_cast<int32_t*>(b + L.flags);
+  g.give_up = give_up;
   g.num_sms = moe_device_sm_count();
   if (g.num_sms <= 0) return fail(MOE_ERR_CUDA, "no CUDA device");
   const cudaError_t e = launch_linear(g, st);
@@ -245,7 +252,7 @@ moe_status moe_linear_workspace_init(const moe_linear_dims* d, void* ws, size_t 
   if (e != cudaSuccess) return cuda_fail(e, "workspace clear");
   try {
     std::lock_guard<std::mutex> lk(g_mu);
-    g_linear[ws] = *d;
+    g_linear[ws] = LinState{*d, false};
   } catch (...) {
     return fail(MOE_ERR_CUDA, "out of host memory for the workspace registry");
   }
@@ -255,7 +262,8 @@ moe_status moe_linear_workspace_init(const moe_linear_dims* d, void* ws, size_t 
 moe_status moe_linear_forward(const moe_linear_dims* d, const void* prepared, const void* x,
                               int64_t ldx, int64_t rows, void* out, int64_t ldo, int32_t out_type,
                               void* ws, size_t ws_bytes, void* stream) {
-  moe_status s = check_call(d, prepared, rows, out, ldo, out_type, ws, ws_bytes);
+  bool give_up = false;
+  moe_status s = check_call(d, prepared, rows, out, ldo, out_type, ws, ws_bytes, &give_up);
   if (s || rows == 0) return s;
   if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x NULL or not 16-byte aligned");
   if (!good_stride(ldx, d->in_features))
@@ -264,17 +272,20 @@ moe_status moe_linear_forward(const moe_linear_dims* d, const void* prepared, co
   uint8_t* b = static_cast<uint8_t*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows <= kLinFusedRows)
-    return forward(d, prepared, nullptr, nullptr, x, ldx, rows, out, ldo, out_type, ws, st);
+    return forward(d, prepared, nullptr, nullptr, x, ldx, rows, out, ldo, out_type, ws, give_up,
+                   st);
   const cudaError_t e =
       launch_linear_quantize(shape_of(*d), x, ldx, rows, b + L.q, b + L.sf, st);
   if (e != cudaSuccess) return cuda_fail(e, "linear quantise");
-  return forward(d, prepared, b + L.q, b + L.sf, nullptr, 0, rows, out, ldo, out_type, ws, st);
+  return forward(d, prepared, b + L.q, b + L.sf, nullptr, 0, rows, out, ldo, out_type, ws,
+                 give_up, st);
 }
 
 moe_status moe_linear_forward_pair(const moe_linear_dims* d, const void* prepared, const void* q,
                                    const void* sf, int64_t rows, void* out, int64_t ldo,
                                    int32_t out_type, void* ws, size_t ws_bytes, void* stream) {
-  moe_status s = check_call(d, prepared, rows, out, ldo, out_type, ws, ws_bytes);
+  bool give_up = false;
+  moe_status s = check_call(d, prepared, rows, out, ldo, out_type, ws, ws_bytes, &give_up);
   if (s) return s;
   if (d->mma_type != MOE_MMA_FP8xFP4 || d->in_features % 128)
     return fail(MOE_ERR_UNSUPPORTED,
@@ -282,7 +293,7 @@ moe_status moe_linear_forward_pair(const moe_linear_dims* d, const void* prepare
   if (rows == 0) return MOE_OK;
   if (!q || !sf || !aligned(q, 16) || !aligned(sf, 16))
     return fail(MOE_ERR_INVALID_ARG, "q and sf must be 16-byte aligned pointers");
-  return forward(d, prepared, q, sf, nullptr, 0, rows, out, ldo, out_type, ws,
+  return forward(d, prepared, q, sf, nullptr, 0, rows, out, ldo, out_type, ws, give_up,
                  static_cast<cudaStream_t>(stream));
 }
 
@@ -300,6 +311,16 @@ moe_status moe_linear_check(void* ws, void* stream) {
     return cuda_fail(e, "flag read");
   if ((e = cudaMemset(ws, 0, sizeof(flag)))) return cuda_fail(e, "flag clear");
   if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a device wait ran past its limit");
+  return MOE_OK;
+}
+
+moe_status moe_debug_linear_give_up(void* ws, int32_t on) {
+  if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_linear.find(ws);
+  if (it == g_linear.end())
+    return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was not initialised", ws);
+  it->second.give_up = on != 0;
   return MOE_OK;
 }
 

@@ -411,6 +411,14 @@ MXMOE_API moe_status moe_linear_forward_pair(const moe_linear_dims *dims, const 
  * MOE_ERR_TIMEOUT or MOE_OK. */
 MXMOE_API moe_status moe_linear_check(void *ws_dev, void *stream);
 
+/* Debug: exercises the failure path of this workspace's products without any fault.  While it
+ * is on, the blocks of a call behave as if their first wait for an operand had run out: they
+ * end the copies they have begun, record a timeout and leave.  The call's output is
+ * worthless, the next moe_linear_check returns MOE_ERR_TIMEOUT, and the context and the
+ * workspace stay usable.  Without effect on products large enough for tiles over SM pairs.
+ * Host only. */
+MXMOE_API moe_status moe_debug_linear_give_up(void *ws_dev, int32_t on);
+
 /* FP4 tensor-core throughput probe (measurement only; the denominator of the
  * layer's compute roofline).  Launches `blocks` blocks of 128 threads on `stream`,
  * blocks_per_sm (1 or 2) of them resident per SM, each of which issues mma_count

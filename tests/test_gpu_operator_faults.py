@@ -1,0 +1,45 @@
+"""The operators around the expert layer where something goes wrong: waits that run out."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import block_scaled_fp4_pre_gb300 as mx
+from tests.test_gpu_linear import F4, F8, Linear, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+# the product that quantises bf16 rows itself, over eight blocks and in one; the split one on
+# quantised rows; whole tiles of 64 and 128 rows
+@pytest.mark.parametrize("mma", [F4, F8])
+@pytest.mark.parametrize("rows,N,K", [(5, 512, 4096), (32, 5000, 8192), (3, 100, 256),
+                                      (48, 256, 4096), (100, 2048, 8192), (300, 2000, 1024),
+                                      (20102, 810, 160)])
+def test_a_product_whose_waits_run_out_leaves_nothing_behind(rows, N, K, mma):
+    lin = Linear(N, K, rows, mma)
+    x = inputs(rows, K)
+    want = torch.empty(rows, N, dtype=torch.float32, device="cuda")
+    mx.moe_linear_forward(lin.dims, lin.prepared, x, want, lin.ws)
+    mx.moe_linear_check(lin.ws)
+    out = torch.empty_like(want)
+    for _ in range(3):
+        mx.moe_debug_linear_give_up(lin.ws, True)
+        mx.moe_linear_forward(lin.dims, lin.prepared, x, out, lin.ws)
+        mx.moe_debug_linear_give_up(lin.ws, False)
+        # the next call's blocks take the shared and tensor memory that the last ones left
+        mx.moe_linear_forward(lin.dims, lin.prepared, x, out, lin.ws)
+        with pytest.raises(mx.MoeError) as e:
+            mx.moe_linear_check(lin.ws)
+        assert e.value.status == mx.MOE_ERR_TIMEOUT
+        assert torch.equal(out, want)
+    mx.moe_linear_check(lin.ws)                 # cleared
+
+
+def test_give_up_refusals():
+    for ws, status in ((None, mx.MOE_ERR_INVALID_ARG),
+                       (torch.empty(1024, dtype=torch.uint8, device="cuda"),
+                        mx.MOE_ERR_WORKSPACE_MISMATCH)):
+        with pytest.raises(mx.MoeError) as e:
+            mx.moe_debug_linear_give_up(ws, True)
+        assert e.value.status == status

@@ -61,3 +61,15 @@ def test_no_store_to_another_block_before_every_block_runs(name):
             seen += 1
             assert met_always(body, at), kernel
     assert seen
+
+
+@pytest.mark.parametrize("name", ["few.cu", "linear.cu"])
+def test_no_block_leaves_with_copies_in_flight(name):
+    # also after a wait that ran out: waits with a flag of their own, not the block's abort
+    seen = 0
+    for kernel, body in kernels(name).items():
+        issue = [body.rfind(f) for f in ("tma_load_2d", "tma_load_3d", "bulk_load")]
+        if max(issue) >= 0:
+            seen += 1
+            assert "&never" in body[max(issue):], kernel
+    assert seen
