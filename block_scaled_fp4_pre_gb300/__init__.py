@@ -9,6 +9,7 @@ library is missing, importing the functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -171,6 +172,38 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _elements(t, dtype, n: int, name: str, last: int | None = None) -> int | None:
+    """Address of a contiguous CUDA tensor of this dtype that holds n elements, rows of `last`.
+
+    The library sees addresses only: it would read another type as this one, and run past a
+    tensor that is too small.  None and raw addresses pass."""
+    if not isinstance(t, torch.Tensor):
+        return None if t is None else int(t)
+    if (t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda
+            or (last is not None and t.dim() > 1 and t.shape[-1] != last)):
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"{name}: need a contiguous CUDA tensor of {dtype}, {n} elements or more"
+                       f"{f' in rows of {last}' if last is not None else ''}; got {t.dtype} "
+                       f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
+
+def _bytes(t, n: int, name: str) -> int | None:
+    """The same of n bytes, whatever the dtype."""
+    if not isinstance(t, torch.Tensor):
+        return None if t is None else int(t)
+    if t.numel() * t.element_size() < n or not t.is_contiguous() or not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"{name}: need {n} contiguous bytes on the GPU; got {t.dtype} "
+                       f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _prepared_bytes(hidden: int, inter: int, num_experts: int, mma_type: int) -> int:
+    return moe_prepared_weights_size(make_dims(hidden, inter, num_experts, 1, 1, mma_type))
+
+
 # ---------------------------------------------------------------------------
 # Entry points (same names as the C ABI)
 
@@ -233,10 +266,19 @@ def moe_run_host(dims: MoeDims, prepared, ws, x_host, topk_ids_host, topk_weight
 def moe_few_forward(dims: MoeDims, prepared, router, x, topk_ids, topk_weights, num_tokens: int,
                     ws, out, stream=None) -> None:
     """The whole layer for up to 16 tokens: router (or, with router None, given ids and
-    weights), experts and their weighted sum."""
-    _check(lib().moe_few_forward(ctypes.byref(dims), _ptr(prepared), _ptr(router), _ptr(x),
-                                 _ptr(topk_ids), _ptr(topk_weights), num_tokens, _ptr(ws),
-                                 _nbytes(ws), _ptr(out), _stream(stream)))
+    weights), experts and their weighted sum.
+
+    x and out are bf16 [tokens, hidden], router bf16 [experts, hidden], topk_ids int32 and
+    topk_weights fp32 [tokens, topk], each contiguous."""
+    T, H, E, k = num_tokens, dims.hidden, dims.num_experts, dims.topk
+    bf16 = torch.bfloat16
+    _check(lib().moe_few_forward(
+        ctypes.byref(dims),
+        _bytes(prepared, _prepared_bytes(H, dims.inter, E, dims.mma_type), "prepared"),
+        _elements(router, bf16, E * H, "router", H), _elements(x, bf16, T * H, "x", H),
+        _elements(topk_ids, torch.int32, T * k, "topk_ids"),
+        _elements(topk_weights, torch.float32, T * k, "topk_weights"), T, _ptr(ws), _nbytes(ws),
+        _elements(out, bf16, T * H, "out", H), _stream(stream)))
 
 
 def moe_check(ws, stream=None) -> None:

@@ -72,7 +72,14 @@ class ExpertBlock:
         """attn bf16 [T, features], residual bf16 [T, H] (updated in place) -> bf16 [T, next
         features], a view of a buffer that the next call overwrites.  routing: (ids, weights)
         for the expert layer instead of the block's router; needed above 16 tokens."""
-        T = attn.shape[0]
+        T, k = attn.shape[0], self.dims.topk
+        # before the residual changes
+        if routing is None and T > FEW_TOKENS:
+            raise ValueError(f"{T} tokens: above {FEW_TOKENS} the routing is the caller's")
+        for t, dtype in zip(routing or (), (torch.int32, torch.float32)):
+            if t.dtype is not dtype or t.shape != (T, k) or not t.is_contiguous():
+                raise ValueError(f"routing: need contiguous {dtype} [{T}, {k}], got {t.dtype} "
+                                 f"{list(t.shape)}")
         o, h, m, q, out = (b[:T] for b in (self.o, self.h, self.m, self.q, self.out))
         mx.moe_linear_forward(self.wo.dims, self.wo.prepared, attn, o, self.wo.ws, stream)
         mx.moe_rmsnorm_mxfp8(o, self.gamma_in, self.eps, residual=residual, residual_out=residual,
@@ -81,8 +88,6 @@ class ExpertBlock:
             ids, weights = routing or (self.ids, self.weights)
             mx.moe_few_forward(self.dims, self.prepared, None if routing else self.router, h, ids,
                                weights, T, self.ws, m, stream)
-        elif routing is None:
-            raise ValueError(f"{T} tokens: above {FEW_TOKENS} the routing is the caller's")
         else:
             mx.moe_pre_dispatch(self.dims, h, *routing, T, self.ws, stream)
             mx.moe_forward(self.dims, self.prepared, self.ws, m, T, stream)

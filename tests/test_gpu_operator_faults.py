@@ -1,10 +1,12 @@
-"""The operators around the expert layer where something goes wrong: waits that run out."""
+"""The operators around the expert layer where something goes wrong: waits that run out and
+tensors that are not what a call needs."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 import block_scaled_fp4_pre_gb300 as mx
+from tests.test_gpu_block import make as make_block
 from tests.test_gpu_linear import F4, F8, Linear, inputs
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,17 @@ def test_give_up_refusals():
         with pytest.raises(mx.MoeError) as e:
             mx.moe_debug_linear_give_up(ws, True)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("T", [4, 20])
+def test_block_refuses_routing_of_other_types(T):
+    b, attn, res = make_block(T)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w, ids = torch.topk(torch.rand(T, 16, generator=g, device="cuda"), 4)     # int64 ids
+    b.forward(attn, res.clone(), (ids.int(), w))
+    b.check()
+    for routing in ((ids, w), (ids.int(), w.bfloat16()), (ids.int()[:, :2].contiguous(), w)):
+        kept = res.clone()
+        with pytest.raises(ValueError):
+            b.forward(attn, kept, routing)
+        assert torch.equal(kept, res)

@@ -122,3 +122,41 @@ def test_matrix_strides(mx):
             check(bad, (6, 40), (torch.bfloat16,), "t")
     with pytest.raises(ValueError):
         check(torch.zeros(40, 6, dtype=torch.bfloat16).t(), (6, 40), (torch.bfloat16,), "t")
+
+
+def few_args(mx, torch, T=3, H=256, I=128, E=8, k=2):
+    """Arguments of moe_few_forward that lack nothing but a GPU."""
+    d = mx.make_dims(H, I, E, k, 16)
+    bf = torch.bfloat16
+    return d, dict(
+        prepared=torch.zeros(mx.moe_prepared_weights_size(d), dtype=torch.uint8),
+        router=torch.zeros(E, H, dtype=bf), x=torch.zeros(T, H, dtype=bf),
+        topk_ids=torch.zeros(T, k, dtype=torch.int32), topk_weights=torch.zeros(T, k),
+        num_tokens=T, ws=torch.zeros(1024, dtype=torch.uint8), out=torch.zeros(T, H, dtype=bf))
+
+
+@pytest.mark.parametrize("name,change", [
+    ("prepared", lambda t: t[1:]), ("router", lambda t: t.float()), ("router", lambda t: t[1:]),
+    ("router", lambda t: t.t().contiguous().t()), ("router", lambda t: t.view(16, 128)),
+    ("x", lambda t: t.half()), ("x", lambda t: t[:2]), ("x", lambda t: t.repeat(1, 2)[:, :256]),
+    ("x", lambda t: t.repeat(1, 2)), ("topk_ids", lambda t: t.long()),
+    ("topk_ids", lambda t: t[:, :1].contiguous()), ("topk_ids", lambda t: t.t().contiguous().t()),
+    ("topk_weights", lambda t: t.bfloat16()), ("topk_weights", lambda t: t[:2]),
+    ("out", lambda t: t.float()), ("out", lambda t: t[:2]), ("out", lambda t: t.repeat(1, 2)[:, :256])])
+def test_few_refuses_tensors_the_library_would_misread(mx, monkeypatch, name, change):
+    import torch
+
+    class OnGpu(torch.Tensor):      # a host tensor that says it is on the GPU
+        is_cuda = True
+
+    monkeypatch.setattr(mx, "_stream", lambda s: 0)
+    d, a = few_args(mx, torch)
+    gpu = {n: t.as_subclass(OnGpu) if isinstance(t, torch.Tensor) else t for n, t in a.items()}
+    with pytest.raises(mx.MoeError) as e:        # nothing to refuse but the workspace
+        mx.moe_few_forward(d, **gpu)
+    assert e.value.status in (mx.MOE_ERR_WORKSPACE_TOO_SMALL, mx.MOE_ERR_INVALID_ARG)
+    assert "workspace" in str(e.value)
+    for bad in (change(gpu[name]), a[name]):     # wrong, and right but on the host
+        with pytest.raises(mx.MoeError) as e:
+            mx.moe_few_forward(d, **{**gpu, name: bad})
+        assert e.value.status == mx.MOE_ERR_INVALID_ARG and f"{name}:" in str(e.value)
