@@ -367,6 +367,12 @@ def _matrix(t, shape, dtypes, name: str) -> int:
     raise ValueError(f"{name}: need {list(shape)} of {dtypes}, got {list(t.shape)} of {t.dtype}")
 
 
+def _on_gpu(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: need a CUDA tensor, got one on {t.device}")
+
+
 _BF16 = (torch.bfloat16,)
 _OUT = (torch.bfloat16, torch.float32)
 
@@ -407,32 +413,50 @@ def moe_linear_workspace_size(dims: LinearDims) -> int:
 
 def moe_linear_prepare(dims: LinearDims, codes, scales, prepared, stream=None) -> None:
     """Canonical MXFP4 codes [N, K/2] and scales [N, K/32] into the product's layout."""
-    _check(lib().moe_linear_prepare(ctypes.byref(dims), _ptr(codes), _ptr(scales), _ptr(prepared),
-                                    _nbytes(prepared), _stream(stream)))
+    N, K = dims.out_features, dims.in_features
+    _check(lib().moe_linear_prepare(ctypes.byref(dims), _bytes(codes, N * K // 2, "codes"),
+                                    _bytes(scales, N * K // 32, "scales"),
+                                    _bytes(prepared, 0, "prepared"), _nbytes(prepared),
+                                    _stream(stream)))
 
 
 def moe_linear_workspace_init(dims: LinearDims, ws, stream=None) -> None:
-    _check(lib().moe_linear_workspace_init(ctypes.byref(dims), _ptr(ws), _nbytes(ws),
-                                           _stream(stream)))
+    _check(lib().moe_linear_workspace_init(ctypes.byref(dims), _bytes(ws, 0, "workspace"),
+                                           _nbytes(ws), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=None)
+def _linear_bytes(out_features: int, in_features: int, mma_type: int) -> int:
+    return moe_linear_weights_size(make_linear_dims(out_features, in_features, 1, mma_type))
 
 
 def moe_linear_forward(dims: LinearDims, prepared, x, out, ws, stream=None) -> None:
     """out = Q(x) W^T: x bf16 [rows, K], out bf16 or fp32 [rows, N], contiguous rows each."""
-    rows = x.shape[0]
-    ldx = _matrix(x, (rows, dims.in_features), _BF16, "x")
-    ldo = _matrix(out, (rows, dims.out_features), _OUT, "out")
-    _check(lib().moe_linear_forward(ctypes.byref(dims), _ptr(prepared), _ptr(x), ldx, rows,
-                                    _ptr(out), ldo, int(out.dtype == torch.float32), _ptr(ws),
+    rows, N, K = x.shape[0], dims.out_features, dims.in_features
+    ldx = _matrix(x, (rows, K), _BF16, "x")
+    ldo = _matrix(out, (rows, N), _OUT, "out")
+    if not (x.is_cuda and out.is_cuda):
+        _on_gpu(x=x, out=out)
+    blob = _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared")
+    _check(lib().moe_linear_forward(ctypes.byref(dims), blob, x.data_ptr(), ldx, rows,
+                                    out.data_ptr(), ldo, int(out.dtype is torch.float32), _ptr(ws),
                                     _nbytes(ws), _stream(stream)))
 
 
 def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, ws,
                             stream=None) -> None:
     """The product on an MXFP8 pair (q [rows, K], sf in MOE_SF_128X4 layout)."""
-    ldo = _matrix(out, (rows, dims.out_features), _OUT, "out")
-    _check(lib().moe_linear_forward_pair(ctypes.byref(dims), _ptr(prepared), _ptr(q), _ptr(sf),
-                                         rows, _ptr(out), ldo, int(out.dtype == torch.float32),
-                                         _ptr(ws), _nbytes(ws), _stream(stream)))
+    N, K = dims.out_features, dims.in_features
+    ldo = _matrix(out, (rows, N), _OUT, "out")
+    if not out.is_cuda:
+        _on_gpu(out=out)
+    blob = _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared")
+    # (K not in whole scale blocks: the library refuses it)
+    _check(lib().moe_linear_forward_pair(ctypes.byref(dims), blob, _bytes(q, rows * K, "q"),
+                                         _bytes(sf, (rows + 127) // 128 * (K // 128) * 512, "sf"),
+                                         rows, out.data_ptr(), ldo,
+                                         int(out.dtype is torch.float32), _ptr(ws), _nbytes(ws),
+                                         _stream(stream)))
 
 
 def moe_linear_check(ws, stream=None) -> None:

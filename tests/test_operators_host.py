@@ -135,6 +135,24 @@ def few_args(mx, torch, T=3, H=256, I=128, E=8, k=2):
         num_tokens=T, ws=torch.zeros(1024, dtype=torch.uint8), out=torch.zeros(T, H, dtype=bf))
 
 
+def refuses(mx, monkeypatch, f, d, args, name, change):
+    """f refuses `change` of one tensor, and the right tensor where it is on the host."""
+    import torch
+
+    class OnGpu(torch.Tensor):      # a host tensor that says it is on the GPU
+        is_cuda = True
+
+    monkeypatch.setattr(mx, "_stream", lambda s: 0)
+    gpu = {n: t.as_subclass(OnGpu) if isinstance(t, torch.Tensor) else t for n, t in args.items()}
+    with pytest.raises(mx.MoeError) as e:        # all right, but for an unknown workspace
+        f(d, **gpu)
+    assert "workspace" in str(e.value)
+    for bad in (change(gpu[name]), args[name]):
+        with pytest.raises(mx.MoeError) as e:
+            f(d, **{**gpu, name: bad})
+        assert e.value.status == mx.MOE_ERR_INVALID_ARG and f"{name}:" in str(e.value)
+
+
 @pytest.mark.parametrize("name,change", [
     ("prepared", lambda t: t[1:]), ("router", lambda t: t.float()), ("router", lambda t: t[1:]),
     ("router", lambda t: t.t().contiguous().t()), ("router", lambda t: t.view(16, 128)),
@@ -146,17 +164,60 @@ def few_args(mx, torch, T=3, H=256, I=128, E=8, k=2):
 def test_few_refuses_tensors_the_library_would_misread(mx, monkeypatch, name, change):
     import torch
 
-    class OnGpu(torch.Tensor):      # a host tensor that says it is on the GPU
-        is_cuda = True
-
-    monkeypatch.setattr(mx, "_stream", lambda s: 0)
     d, a = few_args(mx, torch)
-    gpu = {n: t.as_subclass(OnGpu) if isinstance(t, torch.Tensor) else t for n, t in a.items()}
-    with pytest.raises(mx.MoeError) as e:        # nothing to refuse but the workspace
-        mx.moe_few_forward(d, **gpu)
-    assert e.value.status in (mx.MOE_ERR_WORKSPACE_TOO_SMALL, mx.MOE_ERR_INVALID_ARG)
-    assert "workspace" in str(e.value)
-    for bad in (change(gpu[name]), a[name]):     # wrong, and right but on the host
-        with pytest.raises(mx.MoeError) as e:
-            mx.moe_few_forward(d, **{**gpu, name: bad})
-        assert e.value.status == mx.MOE_ERR_INVALID_ARG and f"{name}:" in str(e.value)
+    refuses(mx, monkeypatch, mx.moe_few_forward, d, a, name, change)
+
+
+def linear_args(mx, torch, pair, rows=5, N=256, K=512):
+    d = mx.make_linear_dims(N, K, 8, mx.MOE_MMA_FP8xFP4)
+    u8 = torch.uint8
+    a = dict(prepared=torch.zeros(mx.moe_linear_weights_size(d), dtype=u8),
+             out=torch.zeros(rows, N), ws=torch.zeros(mx.moe_linear_workspace_size(d), dtype=u8))
+    if pair:
+        return d, a | dict(q=torch.zeros(rows, K, dtype=u8), rows=rows,
+                           sf=torch.zeros(mx.moe_mxfp8_scale_bytes(rows, K, mx.MOE_SF_128X4), dtype=u8))
+    return d, a | dict(x=torch.zeros(rows, K, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("name,change", [
+    ("prepared", lambda t: t[1:]), ("prepared", lambda t: t.repeat(2)[::2]),
+    ("q", lambda t: t[:4]), ("q", lambda t: t.t().contiguous().t()), ("q", lambda t: t[:, :256]),
+    ("sf", lambda t: t[:-4]), ("sf", lambda t: t.repeat(2)[::2])])
+def test_linear_refuses_buffers_it_would_run_past(mx, monkeypatch, name, change):
+    import torch
+
+    d, a = linear_args(mx, torch, True)
+    refuses(mx, monkeypatch, mx.moe_linear_forward_pair, d, a, name, change)
+    d, a = linear_args(mx, torch, False)
+    if name in a:
+        refuses(mx, monkeypatch, mx.moe_linear_forward, d, a, name, change)
+
+
+@pytest.mark.parametrize("name,change", [
+    ("codes", lambda t: t[1:]), ("codes", lambda t: t.t().contiguous().t()),
+    ("scales", lambda t: t[1:]), ("scales", lambda t: t.repeat(1, 2)[:, :16])])
+def test_linear_prepare_refuses_buffers_it_would_run_past(mx, monkeypatch, name, change):
+    import torch
+
+    d, u8 = linear(mx), torch.uint8
+    # prepared too small to be written, so that the right buffers go no further either
+    a = dict(codes=torch.zeros(256, 256, dtype=u8), scales=torch.zeros(256, 16, dtype=u8),
+             prepared=torch.zeros(512, dtype=u8))
+
+    def prepare(d, **kw):
+        try:
+            mx.moe_linear_prepare(d, **kw)
+        except mx.MoeError as e:
+            if "prepared has 512 bytes" in str(e) or "aligned" in str(e):
+                raise mx.MoeError(e.status, "the call itself, like an unknown workspace") from e
+            raise
+
+    refuses(mx, monkeypatch, prepare, d, a, name, change)
+
+
+@pytest.mark.parametrize("name", ["x", "out"])
+def test_linear_refuses_host_rows(mx, monkeypatch, name):
+    import torch
+
+    d, a = linear_args(mx, torch, False)
+    refuses(mx, monkeypatch, mx.moe_linear_forward, d, a, name, lambda t: t.as_subclass(torch.Tensor))
