@@ -192,11 +192,11 @@ def _bytes(t, n: int, name: str) -> int | None:
     """The same of n bytes, whatever the dtype."""
     if not isinstance(t, torch.Tensor):
         return None if t is None else int(t)
-    if t.numel() * t.element_size() < n or not t.is_contiguous() or not t.is_cuda:
-        raise MoeError(MOE_ERR_INVALID_ARG,
-                       f"{name}: need {n} contiguous bytes on the GPU; got {t.dtype} "
-                       f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.data_ptr()
+    if t.nbytes >= n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID_ARG,
+                   f"{name}: need {n} contiguous bytes on the GPU; got {t.dtype} "
+                   f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
 @functools.lru_cache(maxsize=None)
@@ -438,9 +438,11 @@ def moe_linear_forward(dims: LinearDims, prepared, x, out, ws, stream=None) -> N
     if not (x.is_cuda and out.is_cuda):
         _on_gpu(x=x, out=out)
     blob = _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared")
-    _check(lib().moe_linear_forward(ctypes.byref(dims), blob, x.data_ptr(), ldx, rows,
-                                    out.data_ptr(), ldo, int(out.dtype is torch.float32), _ptr(ws),
-                                    _nbytes(ws), _stream(stream)))
+    status = (_lib or lib()).moe_linear_forward(
+        ctypes.byref(dims), blob, x.data_ptr(), ldx, rows, out.data_ptr(), ldo,
+        out.dtype is torch.float32, ws.data_ptr(), ws.nbytes, _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, ws,
@@ -452,11 +454,12 @@ def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, w
         _on_gpu(out=out)
     blob = _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared")
     # (K not in whole scale blocks: the library refuses it)
-    _check(lib().moe_linear_forward_pair(ctypes.byref(dims), blob, _bytes(q, rows * K, "q"),
-                                         _bytes(sf, (rows + 127) // 128 * (K // 128) * 512, "sf"),
-                                         rows, out.data_ptr(), ldo,
-                                         int(out.dtype is torch.float32), _ptr(ws), _nbytes(ws),
-                                         _stream(stream)))
+    status = (_lib or lib()).moe_linear_forward_pair(
+        ctypes.byref(dims), blob, _bytes(q, rows * K, "q"),
+        _bytes(sf, (rows + 127) // 128 * (K // 128) * 512, "sf"), rows, out.data_ptr(), ldo,
+        out.dtype is torch.float32, ws.data_ptr(), ws.nbytes, _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_linear_check(ws, stream=None) -> None:
