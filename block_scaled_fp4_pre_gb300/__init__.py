@@ -163,10 +163,13 @@ def _nbytes(t) -> int:
     raise TypeError("need a tensor or array to know its size")
 
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         # the current stream's handle without building a Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -179,13 +182,13 @@ def _elements(t, dtype, n: int, name: str, last: int | None = None) -> int | Non
     tensor that is too small.  None and raw addresses pass."""
     if not isinstance(t, torch.Tensor):
         return None if t is None else int(t)
-    if (t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda
-            or (last is not None and t.dim() > 1 and t.shape[-1] != last)):
-        raise MoeError(MOE_ERR_INVALID_ARG,
-                       f"{name}: need a contiguous CUDA tensor of {dtype}, {n} elements or more"
-                       f"{f' in rows of {last}' if last is not None else ''}; got {t.dtype} "
-                       f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.data_ptr()
+    if (t.dtype is dtype and t.numel() >= n and t.is_cuda and t.is_contiguous()
+            and (last is None or t.size(-1) == last or t.dim() == 1)):
+        return t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID_ARG,
+                   f"{name}: need a contiguous CUDA tensor of {dtype}, {n} elements or more"
+                   f"{f' in rows of {last}' if last is not None else ''}; got {t.dtype} "
+                   f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
 def _bytes(t, n: int, name: str) -> int | None:
@@ -272,13 +275,15 @@ def moe_few_forward(dims: MoeDims, prepared, router, x, topk_ids, topk_weights, 
     topk_weights fp32 [tokens, topk], each contiguous."""
     T, H, E, k = num_tokens, dims.hidden, dims.num_experts, dims.topk
     bf16 = torch.bfloat16
-    _check(lib().moe_few_forward(
+    status = (_lib or lib()).moe_few_forward(
         ctypes.byref(dims),
         _bytes(prepared, _prepared_bytes(H, dims.inter, E, dims.mma_type), "prepared"),
         _elements(router, bf16, E * H, "router", H), _elements(x, bf16, T * H, "x", H),
         _elements(topk_ids, torch.int32, T * k, "topk_ids"),
-        _elements(topk_weights, torch.float32, T * k, "topk_weights"), T, _ptr(ws), _nbytes(ws),
-        _elements(out, bf16, T * H, "out", H), _stream(stream)))
+        _elements(topk_weights, torch.float32, T * k, "topk_weights"), T, ws.data_ptr(), ws.nbytes,
+        _elements(out, bf16, T * H, "out", H), _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_check(ws, stream=None) -> None:
