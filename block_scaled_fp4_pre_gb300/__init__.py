@@ -403,9 +403,21 @@ def moe_rmsnorm_mxfp8(x, gamma, eps: float, q=None, sf=None, layout: int = MOE_S
         ldy, py = _matrix(y, shape, _BF16, "y"), y.data_ptr()
     if gamma.dtype is not torch.bfloat16 or gamma.shape != (K,) or not gamma.is_contiguous():
         raise ValueError(f"gamma: need contiguous bf16 [{K}]")
-    _check(lib().moe_rmsnorm_mxfp8(px, ldx, pr, ldr, gamma.data_ptr(), eps, rows, K, pro, ldro, py,
-                                   ldy, _ptr(q), _ptr(sf), layout,
-                                   rows if rows_cap is None else rows_cap, _stream(stream)))
+    if not (x.is_cuda and gamma.is_cuda and (pr is None or residual.is_cuda)
+            and (pro is None or residual_out.is_cuda) and (py is None or y.is_cuda)):
+        _on_gpu(x=x, gamma=gamma, residual=residual, residual_out=residual_out, y=y)
+    cap = rows if rows_cap is None else rows_cap
+    pq = psf = None
+    if q is not None:
+        pq = _bytes(q, rows * K, "q")
+    if sf is not None:   # (K not in whole scale words: the library refuses it)
+        sf_rows = (cap + 127) // 128 * 128 if layout == MOE_SF_128X4 else cap
+        psf = _bytes(sf, sf_rows * (K // 128) * 4, "sf")
+    status = (_lib or lib()).moe_rmsnorm_mxfp8(px, ldx, pr, ldr, gamma.data_ptr(), eps, rows, K,
+                                               pro, ldro, py, ldy, pq, psf, layout, cap,
+                                               _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_linear_weights_size(dims: LinearDims) -> int:

@@ -221,3 +221,31 @@ def test_linear_refuses_host_rows(mx, monkeypatch, name):
 
     d, a = linear_args(mx, torch, False)
     refuses(mx, monkeypatch, mx.moe_linear_forward, d, a, name, lambda t: t.as_subclass(torch.Tensor))
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("name,change", [
+    ("q", lambda t: t[:4]), ("q", lambda t: t.t().contiguous().t()), ("sf", lambda t: t[:-4]),
+    ("sf", lambda t: t.repeat(2)[::2]), ("x", None), ("gamma", None), ("residual", None),
+    ("residual_out", None), ("y", None)])
+def test_norm_refuses_buffers_it_would_run_past(mx, monkeypatch, layout, name, change):
+    import torch
+
+    rows, cap, K = 5, 200, 256
+    bf, u8 = torch.bfloat16, torch.uint8
+    # eps below 0, so that the right buffers go no further either
+    a = dict(x=torch.zeros(rows, K, dtype=bf), gamma=torch.zeros(K, dtype=bf), eps=-1.0,
+             q=torch.zeros(rows, K, dtype=u8), layout=layout, rows_cap=cap,
+             sf=torch.zeros(mx.moe_mxfp8_scale_bytes(cap, K, layout), dtype=u8),
+             **{n: torch.zeros(rows, K, dtype=bf) for n in ("residual", "residual_out", "y")})
+
+    def norm(d, **kw):
+        try:
+            mx.moe_rmsnorm_mxfp8(**kw)
+        except mx.MoeError as e:
+            if "eps must be" in str(e):
+                raise mx.MoeError(e.status, "the call itself, like an unknown workspace") from e
+            raise
+
+    refuses(mx, monkeypatch, norm, None, a, name,
+            change or (lambda t: t.as_subclass(torch.Tensor)))
