@@ -657,7 +657,8 @@ moe_status moe_few_forward(const moe_dims* dims, const void* prepared, const voi
   g.w2_codes = prep + P.off_w2c;
   g.slots_cap = L.few_slots;
   g.num_sms = sm_count();
-  if (g.num_sms <= 0) return fail(MOE_ERR_CUDA, "no CUDA device");
+  if (g.num_sms <= 0 || cudaGetDevice(&g.device) != cudaSuccess)
+    return fail(MOE_ERR_CUDA, "no CUDA device");
   FewArgs& a = g.args;
   a.x = static_cast<const uint16_t*>(x);
   a.router = static_cast<const uint16_t*>(router);

@@ -320,7 +320,7 @@ struct LinearLaunch {
   int out_f32;
   int32_t* flags;
   int give_up;               // as LinArgs
-  int num_sms;
+  int device, num_sms;       // the current device
 };
 cudaError_t launch_linear_prepare(const LinearShape& s, const uint8_t* codes,
                                   const uint8_t* scales, uint8_t* prep, cudaStream_t st);
@@ -360,7 +360,7 @@ struct FewLaunch {
   const uint8_t* w1_codes;
   const uint8_t* w2_codes;
   int64_t slots_cap;
-  int num_sms;
+  int device, num_sms;       // the current device
 };
 cudaError_t launch_few(const FewLaunch& g, cudaStream_t st);
 

@@ -46,10 +46,10 @@
 
 #include <stddef.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tmap.cuh"
 
@@ -1101,13 +1101,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSM) few_shape_kernel
   if (p) *p = shape_smem[0];
 }
 
-// Blocks of the expert kernel that run at once (found once a process; a failure is tried
-// again), at most `most`.
+// Blocks of the expert kernel that run at once on the current device, `dev` (found once; a
+// failure is tried again), at most `most`.
 template <int FMT, bool CLUSTER>
-cudaError_t resident_blocks(int most, int& blocks) {
-  static std::atomic<int> fit{0};
+cudaError_t resident_blocks(int dev, int most, int& blocks) {
+  static PerDevice<int> fit;
   constexpr size_t kBytes = few_smem_bytes<FMT>();
-  blocks = fit.load(std::memory_order_relaxed);
+  blocks = fit.get(dev);
   if (blocks == 0) {
     cudaError_t e = cudaFuncSetAttribute(few_expert_kernel<FMT, CLUSTER>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
@@ -1123,7 +1123,7 @@ cudaError_t resident_blocks(int most, int& blocks) {
       blocks = n < 1 ? -1 : n * kFewCluster;
       if (blocks > most) blocks = most / kFewCluster * kFewCluster;
     }
-    fit.store(blocks, std::memory_order_relaxed);
+    fit.set(dev, blocks);
   }
   return cudaSuccess;
 }
@@ -1165,7 +1165,7 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
   // A slab a cluster: as many clusters as slabs, at least 32 (phase 0 wants the blocks), and
   // fewer than fit an empty GPU, where the last one started late (1 token: 25.2 us with 32
   // clusters, 25.5 with 35, 27.8 with all 36).
-  if ((e = resident_blocks<FMT, true>(most, grid)) != cudaSuccess) return e;
+  if ((e = resident_blocks<FMT, true>(g.device, most, grid)) != cudaSuccess) return e;
   // Small layers launch no more than phase 0 has ranges for.
   const int slabs = s.H / kBM, fit = grid / kFewCluster - 1;
   if (slabs <= fit) {
@@ -1180,7 +1180,7 @@ cudaError_t launch_fmt(const FewLaunch& g, cudaStream_t st) {
     c.cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&c.cfg, few_expert_kernel<FMT, true>, m1, mx, m2, mh, a);
   }
-  if ((e = resident_blocks<FMT, false>(most, grid)) != cudaSuccess) return e;
+  if ((e = resident_blocks<FMT, false>(g.device, most, grid)) != cudaSuccess) return e;
   return launch_pdl(few_expert_kernel<FMT, false>, dim3(grid), dim3(kFewThreads), kBytes, st, m1,
                     mx, m2, mh, a);
 }

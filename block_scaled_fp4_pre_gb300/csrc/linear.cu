@@ -26,9 +26,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "common.cuh"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tmap.cuh"
 
@@ -1011,22 +1010,21 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int cluster, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Raises a kernel's shared-memory limit once a process; a failure is tried again.
+// Raises a kernel's shared-memory limit on the current device, `dev`, once; a failure is tried
+// again.
 template <typename K>
-cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<bool>& done) {
-  if (done.load(std::memory_order_relaxed)) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.store(true, std::memory_order_relaxed);
-  return e;
+cudaError_t allow_smem(K* kernel, size_t bytes, PerDevice<bool>& done, int dev) {
+  return once_a_device(done, dev, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
 }
 
 template <bool F8, int TN, bool QUANT>
 cudaError_t launch_split(const CUtensorMap& tw, const CUtensorMap& tx, const LinArgs& a, int parts,
-                         cudaStream_t st) {
+                         int dev, cudaStream_t st) {
   constexpr size_t kBytes = LinSmem<F8, TN>::kBytes;
-  static std::atomic<bool> set{false};
-  const cudaError_t e = allow_smem(linear_split_kernel<F8, TN, QUANT>, kBytes, set);
+  static PerDevice<bool> set;
+  const cudaError_t e = allow_smem(linear_split_kernel<F8, TN, QUANT>, kBytes, set, dev);
   if (e != cudaSuccess) return e;
   return launch_cluster(linear_split_kernel<F8, TN, QUANT>, a.tiles * a.slabs * parts, parts,
                         kBytes, st, tw, tx, a, parts);
@@ -1067,12 +1065,12 @@ cudaError_t launch_tile(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
     parts *= 2;
   }
   if constexpr (TN == 32) {
-    return quant ? launch_split<F8, TN, true>(tw, tx, a, parts, st)
-                 : launch_split<F8, TN, false>(tw, tx, a, parts, st);
+    return quant ? launch_split<F8, TN, true>(tw, tx, a, parts, g.device, st)
+                 : launch_split<F8, TN, false>(tw, tx, a, parts, g.device, st);
   } else {
-    if (parts > 1) return launch_split<F8, TN, false>(tw, tx, a, parts, st);
-    static std::atomic<bool> set{false};
-    if ((e = allow_smem(linear_kernel<F8, TN>, kBytes, set)) != cudaSuccess) return e;
+    if (parts > 1) return launch_split<F8, TN, false>(tw, tx, a, parts, g.device, st);
+    static PerDevice<bool> set;
+    if ((e = allow_smem(linear_kernel<F8, TN>, kBytes, set, g.device)) != cudaSuccess) return e;
     const int grid = (int)(items < blocks ? items : blocks);
     return launch_pdl(linear_kernel<F8, TN>, dim3(grid), dim3(kLinThreads), kBytes, st, tw, tx,
                       a);
@@ -1097,13 +1095,14 @@ cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
   a.tiles = (a.M + ROWS - 1) / ROWS;
   const int64_t items = (int64_t)a.tiles * ((a.slabs + 1) / 2);
   if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  // clusters that fit at once (a GPC may have an odd number of SMs), for the device of
-  // the first launch
-  static std::atomic<int> fit{0};
-  int clusters = fit.load(std::memory_order_relaxed);
+  // clusters that fit at once (a GPC may have an odd number of SMs)
+  static PerDevice<int> fit;
+  int clusters = fit.get(g.device);
   if (clusters == 0) {
-    static std::atomic<bool> set{false};
-    if ((e = allow_smem(linear_pair_kernel<F8, ROWS>, kBytes, set)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(linear_pair_kernel<F8, ROWS>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes)) !=
+        cudaSuccess)
+      return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(g.num_sms);
     cfg.blockDim = dim3(kPairThreads);
@@ -1113,7 +1112,7 @@ cudaError_t launch_pair(const LinearLaunch& g, LinArgs a, cudaStream_t st) {
       return e;
     if (c < 1) return cudaErrorInvalidConfiguration;
     clusters = c < g.num_sms / 2 ? c : g.num_sms / 2;
-    fit.store(clusters, std::memory_order_relaxed);
+    fit.set(g.device, clusters);
   }
   const int grid = 2 * (int)(items < clusters ? items : clusters);
   return launch_pdl(linear_pair_kernel<F8, ROWS>, dim3(grid), dim3(kPairThreads), kBytes, st, m, a);

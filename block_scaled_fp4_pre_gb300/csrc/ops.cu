@@ -145,7 +145,7 @@ moe_status forward(const moe_linear_dims* d, const void* prepared, const void* q
   g.flags = reinterpret_cast<int32_t*>(b + L.flags);
   g.give_up = give_up;
   g.num_sms = moe_device_sm_count();
-  if (g.num_sms <= 0) return fail(MOE_ERR_CUDA, "no CUDA device");
+  if (g.num_sms <= 0 || cudaGetDevice(&g.device) != cudaSuccess) return fail(MOE_ERR_CUDA, "no CUDA device");
   const cudaError_t e = launch_linear(g, st);
   if (e != cudaSuccess) return cuda_fail(e, "linear kernel");
   return MOE_OK;

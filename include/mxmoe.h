@@ -22,6 +22,9 @@
  *     buffers are allocated and freed by the caller; no hot entry point allocates.
  *   - Device pointers passed to kernels must be 16-byte aligned (256-byte for the
  *     prepared weights and the workspace); otherwise MOE_ERR_INVALID_ARG.
+ *   - A call works on the calling thread's current device, where its buffers lie.  The
+ *     expert layer (moe_forward, moe_run_host, moe_debug_gate_up) serves one device a
+ *     process, that of its first launch; the other operators serve any.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is enqueued
  *     asynchronously and stream-ordered; only moe_check, moe_run_host and the
  *     moe_read_* debug calls synchronise.

@@ -249,3 +249,55 @@ def test_norm_refuses_buffers_it_would_run_past(mx, monkeypatch, layout, name, c
 
     refuses(mx, monkeypatch, norm, None, a, name,
             change or (lambda t: t.as_subclass(torch.Tensor)))
+
+
+def test_what_a_launcher_keeps_belongs_to_a_device(tmp_path):
+    import os
+    import shutil
+    import subprocess
+
+    from block_scaled_fp4_pre_gb300 import build
+
+    cc = shutil.which("g++") or pytest.skip("no g++")
+    src = tmp_path / "t.cc"
+    src.write_text(r"""
+#include "per_device.h"
+#include <cstdio>
+#define REQUIRE(c) if (!(c)) { std::printf("line %d: %s\n", __LINE__, #c); return 1; }
+using namespace mxmoe;
+int main() {
+  static PerDevice<int> fit;
+  REQUIRE(fit.get(0) == 0 && fit.get(1) == 0);
+  fit.set(0, 36);
+  REQUIRE(fit.get(0) == 36 && fit.get(1) == 0 && fit.get(63) == 0);
+  fit.set(63, 7);
+  fit.set(64, 8); fit.set(-1, 9);              // kept nowhere, and nothing written past the end
+  REQUIRE(fit.get(63) == 7 && fit.get(64) == 0 && fit.get(-1) == 0 && fit.get(0) == 36);
+  static PerDevice<bool> done;
+  enum Err { kOk = 0, kBad = 3 };
+  int calls = 0;
+  Err answer = kOk;
+  auto raise = [&] { ++calls; return answer; };
+  REQUIRE(once_a_device(done, 0, raise) == kOk && calls == 1);
+  REQUIRE(once_a_device(done, 0, raise) == kOk && calls == 1);
+  answer = kBad;                               // a second device is asked for itself
+  REQUIRE(once_a_device(done, 1, raise) == kBad && calls == 2);
+  answer = kOk;                                // and again after a failure
+  REQUIRE(once_a_device(done, 1, raise) == kOk && calls == 3);
+  REQUIRE(once_a_device(done, 1, raise) == kOk && calls == 3);
+  REQUIRE(once_a_device(done, 64, raise) == kOk && calls == 4);
+  REQUIRE(once_a_device(done, 64, raise) == kOk && calls == 5);
+  return 0;
+}
+""")
+    exe = str(tmp_path / "t")
+    subprocess.run([cc, "-std=c++17", "-Wall", "-Werror", "-I", build.CSRC, str(src), "-o", exe],
+                   check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    # and the operators' launchers keep nothing in any other way
+    for name in ("linear.cu", "few.cu", "norm.cu"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            kept = [l for l in f if l.lstrip().startswith("static ") and "PerDevice<" not in l
+                    and "constexpr" not in l and "static __device__" not in l]
+        assert not kept, kept
