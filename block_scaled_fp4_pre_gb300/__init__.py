@@ -364,10 +364,11 @@ def moe_mxfp8_quantize(x, rows: int, K: int, q, sf, layout: int, rows_cap: int |
 def _matrix(t, shape, dtypes, name: str) -> int:
     """Row stride of a 2-D tensor of this shape and one of the dtypes, its rows contiguous."""
     if t.dtype in dtypes and t.shape == shape:
+        if t.is_contiguous():   # a single row is, whatever its stride says
+            return shape[1]
         ld, step = t.stride()
         if step == 1 or shape[1] == 1:
-            # a single row may have any stride; of more, the library checks it
-            return ld if shape[0] > 1 or ld >= shape[1] else shape[1]
+            return ld           # checked by the library
         raise ValueError(f"{name}: rows must be contiguous")
     raise ValueError(f"{name}: need {list(shape)} of {dtypes}, got {list(t.shape)} of {t.dtype}")
 
@@ -391,8 +392,7 @@ def moe_rmsnorm_mxfp8(x, gamma, eps: float, q=None, sf=None, layout: int = MOE_S
     as moe_mxfp8_quantize writes them.  Any output may be left out."""
     shape = x.shape
     rows, K = shape
-    ldx = _matrix(x, shape, _BF16, "x")
-    px = x.data_ptr()
+    px, ldx = x.data_ptr(), _matrix(x, shape, _BF16, "x")
     pr = pro = py = None
     ldr = ldro = ldy = 0
     if residual is not None:

@@ -301,3 +301,15 @@ int main() {
             kept = [l for l in f if l.lstrip().startswith("static ") and "PerDevice<" not in l
                     and "constexpr" not in l and "static __device__" not in l]
         assert not kept, kept
+
+
+def test_a_single_row_may_have_any_stride(mx):
+    import torch
+
+    t = torch.zeros(6, 44, dtype=torch.bfloat16)
+    for row in (t[2:3, :40], t[2:3, :40].expand(1, 40), t[2, :40].view(1, 40),
+                torch.as_strided(t, (1, 40), (7, 1)), torch.as_strided(t, (1, 40), (0, 1))):
+        assert mx._matrix(row, (1, 40), (torch.bfloat16,), "t") == 40
+    assert mx._matrix(t[:2, :40], (2, 40), (torch.bfloat16,), "t") == 44    # refused by the library
+    assert mx._matrix(t[:0, :40], (0, 40), (torch.bfloat16,), "t") >= 0
+    assert mx._matrix(t[:, :1], (6, 1), (torch.bfloat16,), "t") == 44
