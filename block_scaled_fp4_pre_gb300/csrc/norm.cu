@@ -7,17 +7,21 @@
 // One pass: a row's values stay in registers between the sum of squares and the
 // quantisation, so each input element is read once and each output written once.  y is
 // quantised from its fp32 value, not from the bf16 one, so q carries one rounding.  The
-// sum is fp32 in a fixed order (per thread, then a shuffle tree, then the warps in
-// order): the same input gives the same bits, whatever else runs.
+// sum is fp32 in a fixed order (per thread, then a shuffle tree, then a tree over the
+// warps) that depends on K and, above K = 1024, on whether the call has more rows than the
+// device has SMs: the same call gives the same bits, whatever else runs.
 //
 // An element next to a rounding boundary of E4M3, or a group's largest next to a power of
 // two's, flips with the last bits of y.  So the sums, the mean and the reciprocal root are
 // pairs of floats, and where the nearest float of some y lies on a boundary (its last 19
 // bits are 0, one float in 2^19) it is rounded to odd instead: a value that is not exactly a
 // float gets the float next to it towards zero with its last bit set, which is on no
-// boundary, and E4M3 of that is E4M3 of the unrounded value.  Against 64 bits, 67.1e6
-// elements at K = 4096: 38 codes differ in plain fp32, 8 here, for 4 us of 93 (trees of pairs
-// all through: 9 for 7 us).
+// boundary, and E4M3 of that is E4M3 of the unrounded value.  What is left are the sums' own
+// roundings.  Codes a million that differ from those of 64 bits, on rows whose squares a few
+// large channels dominate, here and in plain fp32: K = 768 0.08 and 1.2, 1152 0.18 and 0.87,
+// 1408 0.12 and 0.70, 2048 0.16 and 0.60, 4096 0.15 and 0.64, for 4 us of 93 at 16384 x 4096.
+// With the squares of each vector as a tree and pairs all through: 0.06, 0.10, 0.13 and 0.03
+// from K = 1152 on, for another 1 us of 38 at 16384 x 1408 and 4 of 94 at 16384 x 4096.
 //
 // Layout: a thread holds V vectors of 8 consecutive elements (16 bytes of bf16), so four
 // lanes hold a scale's 32 elements and reduce its amax with two shuffles, and sixteen
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : V == 2 ? 512 : 10
         s[j] = fmaf(r[i][2 * j], r[i][2 * j], r[i][2 * j + 1] * r[i][2 * j + 1]);
       const Two v = two_sum(sum.hi, (s[0] + s[1]) + (s[2] + s[3]));
       sum = {v.hi, sum.lo + v.lo};
-    } else {          // over many threads the chains' roundings average out
+    } else {          // one chain a thread: see the rates at the top of the file
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum.hi = fmaf(r[i][j], r[i][j], sum.hi);
     }
@@ -268,7 +272,7 @@ cudaError_t launch_rmsnorm_mxfp8(const RmsnormArgs& args, int64_t rows_cap, cuda
   // feeds.  With more, a row's fixed work (the sums' trees) is shared by more elements a
   // thread.  K = 4096, one vector a thread against two (before the care for ties): 1 row
   // 2.06 / 2.49 us, 16384 rows 104.3 / 89.3 us; K = 1408, 333 rows: 2.88 / 2.53 us.
-  if (a.rows <= 152 && vecs <= 1024) return launch<1, false>(a, threads(1), st);
+  if (vecs <= 1024 && a.rows <= moe_device_sm_count()) return launch<1, false>(a, threads(1), st);
   if (vecs <= 1024) return launch<2, false>(a, threads(2), st);
   if (vecs <= 2048) return launch<4, false>(a, threads(4), st);
   return launch<8, false>(a, threads(8), st);

@@ -343,15 +343,17 @@ MXMOE_API moe_status moe_mxfp8_quantize(const void *x, int64_t rows, int64_t K, 
  *   y            = r * gamma / sqrt(mean(r^2) + eps), fp32; also stored as bf16(y)
  *   (q, sf)      = the MXFP8 pair of the fp32 y: codes, scales and scale layouts as
  *                  moe_mxfp8_quantize writes them
- * in one pass over the row; sums are fp32 in a fixed order.  x, residual, residual_out and
+ * in one pass over the row; sums are fp32 in a fixed order, the same for every call of up
+ * to as many rows as the device has SMs and the same for every call of more.  x, residual, residual_out and
  * y are bf16 [rows, K] with row strides ldx, ldr, ldro, ldy (elements, multiples of 8, at
  * least K); gamma is bf16 [K]; q is contiguous.  All device pointers, 16-byte aligned.
  * residual and residual_out may be NULL (either alone: r = x, or r is not stored), so may
  * y, and so may q with sf (then sf_layout and rows_cap are not read); at least one output
  * must be given.  residual_out and y may be x or residual themselves (same stride).
  * 0 <= rows <= rows_cap <= 2^23, K a multiple of 128 in [128, 65536], eps >= 0.  rows =
- * 0 only clears the scales.  A row that holds an infinity or a NaN, or whose squares
- * overflow fp32, spoils its own outputs and no other row's.  MOE_ERR_INVALID_ARG
+ * 0 only clears the scales.  A row that holds an infinity or a NaN, or whose squares or
+ * products r * gamma overflow fp32, spoils its own outputs and no other row's; products
+ * below fp32's normal range lose digits.  MOE_ERR_INVALID_ARG
  * otherwise.  Stream-ordered, no allocation, no synchronisation. */
 MXMOE_API moe_status moe_rmsnorm_mxfp8(const void *x, int64_t ldx, const void *residual,
                                        int64_t ldr, const void *gamma, float eps, int64_t rows,
