@@ -59,3 +59,21 @@ def test_block_refuses_routing_of_other_types(T):
         with pytest.raises(ValueError):
             b.forward(attn, kept, routing)
         assert torch.equal(kept, res)
+
+
+@pytest.mark.parametrize("change", [dict(max_rows=7), dict(mma_type=F4), dict(out_features=127),
+                                    dict(in_features=224)])
+def test_a_workspace_of_other_dims_is_refused(change):
+    # dims whose own workspace would fit this one
+    lin = Linear(128, 256, 8, F8)
+    d = dict(out_features=128, in_features=256, max_rows=8, mma_type=F8) | change
+    other = mx.make_linear_dims(**d)
+    assert mx.moe_linear_workspace_size(other) <= lin.ws.numel()
+    x = inputs(7, d["in_features"])
+    out = torch.full((7, d["out_features"]), 3.0, dtype=torch.float32, device="cuda")
+    prepared = torch.empty(mx.moe_linear_weights_size(other), dtype=torch.uint8, device="cuda")
+    with pytest.raises(mx.MoeError) as e:
+        mx.moe_linear_forward(other, prepared, x, out, lin.ws)
+    assert e.value.status == mx.MOE_ERR_WORKSPACE_MISMATCH
+    torch.cuda.synchronize()
+    assert torch.all(out == 3)
