@@ -193,10 +193,11 @@ def _elements(t, dtype, n: int, name: str, last: int | None = None) -> int | Non
 
 def _bytes(t, n: int, name: str) -> int | None:
     """The same of n bytes, whatever the dtype."""
-    if not isinstance(t, torch.Tensor):
+    try:
+        if t.nbytes >= n and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
         return None if t is None else int(t)
-    if t.nbytes >= n and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
     raise MoeError(MOE_ERR_INVALID_ARG,
                    f"{name}: need {n} contiguous bytes on the GPU; got {t.dtype} "
                    f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
@@ -281,7 +282,8 @@ def moe_few_forward(dims: MoeDims, prepared, router, x, topk_ids, topk_weights, 
         _elements(router, bf16, E * H, "router", H), _elements(x, bf16, T * H, "x", H),
         _elements(topk_ids, torch.int32, T * k, "topk_ids"),
         _elements(topk_weights, torch.float32, T * k, "topk_weights"), T, ws.data_ptr(), ws.nbytes,
-        _elements(out, bf16, T * H, "out", H), _stream(stream))
+        _elements(out, bf16, T * H, "out", H),
+        _raw_stream(_current_device()) if stream is None else _stream(stream))
     if status:
         _check(status)
 
@@ -415,7 +417,8 @@ def moe_rmsnorm_mxfp8(x, gamma, eps: float, q=None, sf=None, layout: int = MOE_S
         psf = _bytes(sf, sf_rows * (K // 128) * 4, "sf")
     status = (_lib or lib()).moe_rmsnorm_mxfp8(px, ldx, pr, ldr, gamma.data_ptr(), eps, rows, K,
                                                pro, ldro, py, ldy, pq, psf, layout, cap,
-                                               _stream(stream))
+                                               _raw_stream(_current_device()) if stream is None
+                                               else _stream(stream))
     if status:
         _check(status)
 
@@ -457,7 +460,8 @@ def moe_linear_forward(dims: LinearDims, prepared, x, out, ws, stream=None) -> N
     blob = _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared")
     status = (_lib or lib()).moe_linear_forward(
         ctypes.byref(dims), blob, x.data_ptr(), ldx, rows, out.data_ptr(), ldo,
-        out.dtype is torch.float32, ws.data_ptr(), ws.nbytes, _stream(stream))
+        out.dtype is torch.float32, ws.data_ptr(), ws.nbytes,
+        _raw_stream(_current_device()) if stream is None else _stream(stream))
     if status:
         _check(status)
 
@@ -469,12 +473,13 @@ def moe_linear_forward_pair(dims: LinearDims, prepared, q, sf, rows: int, out, w
     ldo = _matrix(out, (rows, N), _OUT, "out")
     if not out.is_cuda:
         _on_gpu(out=out)
-    blob = _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared")
-    # (K not in whole scale blocks: the library refuses it)
     status = (_lib or lib()).moe_linear_forward_pair(
-        ctypes.byref(dims), blob, _bytes(q, rows * K, "q"),
+        ctypes.byref(dims), _bytes(prepared, _linear_bytes(N, K, dims.mma_type), "prepared"),
+        _bytes(q, rows * K, "q"),
+        # (K not in whole scale blocks: the library refuses it)
         _bytes(sf, (rows + 127) // 128 * (K // 128) * 512, "sf"), rows, out.data_ptr(), ldo,
-        out.dtype is torch.float32, ws.data_ptr(), ws.nbytes, _stream(stream))
+        out.dtype is torch.float32, ws.data_ptr(), ws.nbytes,
+        _raw_stream(_current_device()) if stream is None else _stream(stream))
     if status:
         _check(status)
 

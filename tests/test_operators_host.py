@@ -135,15 +135,15 @@ def few_args(mx, torch, T=3, H=256, I=128, E=8, k=2):
         num_tokens=T, ws=torch.zeros(1024, dtype=torch.uint8), out=torch.zeros(T, H, dtype=bf))
 
 
-def refuses(mx, monkeypatch, f, d, args, name, change):
+def refuses(mx, f, d, args, name, change):
     """f refuses `change` of one tensor, and the right tensor where it is on the host."""
     import torch
 
     class OnGpu(torch.Tensor):      # a host tensor that says it is on the GPU
         is_cuda = True
 
-    monkeypatch.setattr(mx, "_stream", lambda s: 0)
     gpu = {n: t.as_subclass(OnGpu) if isinstance(t, torch.Tensor) else t for n, t in args.items()}
+    gpu["stream"] = 0                            # no current stream without a GPU
     with pytest.raises(mx.MoeError) as e:        # all right, but for an unknown workspace
         f(d, **gpu)
     assert "workspace" in str(e.value)
@@ -161,11 +161,11 @@ def refuses(mx, monkeypatch, f, d, args, name, change):
     ("topk_ids", lambda t: t[:, :1].contiguous()), ("topk_ids", lambda t: t.t().contiguous().t()),
     ("topk_weights", lambda t: t.bfloat16()), ("topk_weights", lambda t: t[:2]),
     ("out", lambda t: t.float()), ("out", lambda t: t[:2]), ("out", lambda t: t.repeat(1, 2)[:, :256])])
-def test_few_refuses_tensors_the_library_would_misread(mx, monkeypatch, name, change):
+def test_few_refuses_tensors_the_library_would_misread(mx, name, change):
     import torch
 
     d, a = few_args(mx, torch)
-    refuses(mx, monkeypatch, mx.moe_few_forward, d, a, name, change)
+    refuses(mx, mx.moe_few_forward, d, a, name, change)
 
 
 def linear_args(mx, torch, pair, rows=5, N=256, K=512):
@@ -183,20 +183,20 @@ def linear_args(mx, torch, pair, rows=5, N=256, K=512):
     ("prepared", lambda t: t[1:]), ("prepared", lambda t: t.repeat(2)[::2]),
     ("q", lambda t: t[:4]), ("q", lambda t: t.t().contiguous().t()), ("q", lambda t: t[:, :256]),
     ("sf", lambda t: t[:-4]), ("sf", lambda t: t.repeat(2)[::2])])
-def test_linear_refuses_buffers_it_would_run_past(mx, monkeypatch, name, change):
+def test_linear_refuses_buffers_it_would_run_past(mx, name, change):
     import torch
 
     d, a = linear_args(mx, torch, True)
-    refuses(mx, monkeypatch, mx.moe_linear_forward_pair, d, a, name, change)
+    refuses(mx, mx.moe_linear_forward_pair, d, a, name, change)
     d, a = linear_args(mx, torch, False)
     if name in a:
-        refuses(mx, monkeypatch, mx.moe_linear_forward, d, a, name, change)
+        refuses(mx, mx.moe_linear_forward, d, a, name, change)
 
 
 @pytest.mark.parametrize("name,change", [
     ("codes", lambda t: t[1:]), ("codes", lambda t: t.t().contiguous().t()),
     ("scales", lambda t: t[1:]), ("scales", lambda t: t.repeat(1, 2)[:, :16])])
-def test_linear_prepare_refuses_buffers_it_would_run_past(mx, monkeypatch, name, change):
+def test_linear_prepare_refuses_buffers_it_would_run_past(mx, name, change):
     import torch
 
     d, u8 = linear(mx), torch.uint8
@@ -212,15 +212,15 @@ def test_linear_prepare_refuses_buffers_it_would_run_past(mx, monkeypatch, name,
                 raise mx.MoeError(e.status, "the call itself, like an unknown workspace") from e
             raise
 
-    refuses(mx, monkeypatch, prepare, d, a, name, change)
+    refuses(mx, prepare, d, a, name, change)
 
 
 @pytest.mark.parametrize("name", ["x", "out"])
-def test_linear_refuses_host_rows(mx, monkeypatch, name):
+def test_linear_refuses_host_rows(mx, name):
     import torch
 
     d, a = linear_args(mx, torch, False)
-    refuses(mx, monkeypatch, mx.moe_linear_forward, d, a, name, lambda t: t.as_subclass(torch.Tensor))
+    refuses(mx, mx.moe_linear_forward, d, a, name, lambda t: t.as_subclass(torch.Tensor))
 
 
 @pytest.mark.parametrize("layout", [0, 1])
@@ -228,7 +228,7 @@ def test_linear_refuses_host_rows(mx, monkeypatch, name):
     ("q", lambda t: t[:4]), ("q", lambda t: t.t().contiguous().t()), ("sf", lambda t: t[:-4]),
     ("sf", lambda t: t.repeat(2)[::2]), ("x", None), ("gamma", None), ("residual", None),
     ("residual_out", None), ("y", None)])
-def test_norm_refuses_buffers_it_would_run_past(mx, monkeypatch, layout, name, change):
+def test_norm_refuses_buffers_it_would_run_past(mx, layout, name, change):
     import torch
 
     rows, cap, K = 5, 200, 256
@@ -247,7 +247,7 @@ def test_norm_refuses_buffers_it_would_run_past(mx, monkeypatch, layout, name, c
                 raise mx.MoeError(e.status, "the call itself, like an unknown workspace") from e
             raise
 
-    refuses(mx, monkeypatch, norm, None, a, name,
+    refuses(mx, norm, None, a, name,
             change or (lambda t: t.as_subclass(torch.Tensor)))
 
 
