@@ -328,7 +328,7 @@ moe_status check_tokens(const moe_dims* d, int32_t T) {
 
 __global__ void write_header_kernel(int32_t* hdr, moe_dims d, unsigned long long total) {
   hdr[0] = 0x454F4D58;  // "XMOE"
-  hdr[1] = 1;           // layout version
+  hdr[1] = 2;           // layout version (2: with the few-token form's regions)
   hdr[2] = d.hidden;
   hdr[3] = d.inter;
   hdr[4] = d.num_experts;

@@ -121,3 +121,13 @@ def test_norm_of_a_row_among_few_and_among_many(K):
         norm.check_pair(q, sf, ref, sms, K, mx.MOE_SF_PACKED)
         lo, hi = (micro64.bf16(ref + s * norm.DELTA * np.abs(ref)) for s in (-1, 1))
         assert np.all((lo <= y) & (y <= hi))
+
+
+def test_layer_workspace_says_its_layout():
+    # the regions of the few-token form made it another layout than version 1
+    d = mx.make_dims(256, 128, 8, 2, 16)
+    ws = torch.zeros(mx.moe_workspace_size(d), dtype=torch.uint8, device="cuda")
+    mx.moe_workspace_init(d, ws)
+    assert ws[:32].view(torch.int32).tolist() == [0x454F4D58, 2, 256, 128, 8, 2, 16,
+                                                  mx.MOE_MMA_MXF4xMXF4]
+    assert ws[32:40].view(torch.int64).item() == ws.numel()
