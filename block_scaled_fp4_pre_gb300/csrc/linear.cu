@@ -419,10 +419,12 @@ __global__ void __launch_bounds__(kLinThreads, kLinBlocksPerSM)
 // tensor memory, so these share 48 columns, which the epilogue reads first.  Roles (576
 // threads, one block an SM): warp 0 producer, warp 1 of the leader MMA issue, warps 2-17
 // epilogue, four a lane quarter (two: 39.5 us against 34.2 at 16384 x 4096 x 512).
-// Bound by the tensor pipe and power: 16384 x 4096 x 4096 in 85 us behind the quantisation
-// (6.4 PFLOP/s).  On zeros, which draw less, 3% less, with MXFP8 rows 17% (8192 cubed: 331 us
-// and 253, 0.89 of what the MMA alone reaches); of that, no loads at all 3 to 4%, no
-// copies of scales nothing, no stores 10%.
+// MXFP4, 16384 x 4096 x 4096: 85 us behind the quantisation (6.4 PFLOP/s, 0.66 of what the MMA
+// alone reaches).  No unit is saturated (8192 rows: tensor pipe 64% of the launch, L2 54%,
+// DRAM 12%), and what was measured explains half of the rest: without stores 10% less, without
+// loads 3 to 4%, without copies of scales about 1%, on zeros, which draw less power, 3%.
+// MXFP8: 78% of the launch in the tensor pipe, and bound by power (8192 cubed 331 us, on zeros
+// 253, 0.89 of what the MMA alone reaches).
 constexpr int kPairEpiWarps = 16;
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr int kPairTmemCols = 512;
@@ -1182,13 +1184,22 @@ cudaError_t launch_linear(const LinearLaunch& g, cudaStream_t st) {
   if (a.M <= 32) return s.f8 ? launch_tile<true, 32>(g, a, st) : launch_tile<false, 32>(g, a, st);
   // Tiles: 64 rows while 128-row tiles would not give every SM one, else 128, or SM pairs'
   // 256 features by 192 or 256 rows, by an estimate in cycles: rounds of tiles times
-  // (k-blocks times a tile's cycles a k-block, plus a tile's fixed part), all fitted to
-  // timings.  Measured (us, 256 / 192 / 128 rows, pairs with eight epilogue warps; MXFP4, then
-  // MXFP8 pairs in): 1024 x 4096 x
-  // 4096 13.0 / 16.6 / 13.3 and 14.2 / 19.5 / 15.5; 1536 x 4096 x 4096 19.8 / 18.5 / 21.1 and
-  // 23.4 / 20.0 / 27.5; 4096 x 4096 x 512 14.2 / 15.8 / 14.3 and 12.7 / 14.3 / 14.3; 4096 x
-  // 4096 x 4096 45.5 / 44.0 / - and 47.2 / 44.3 / -; 16384 x 4096 x 4096 116.6 / 124.1 / 145.4
-  // and 163 / 165 / 199; 8192 x 8192 x 8192 181 / 198 / - and 328 / 336 / -.  Fewer than 24
+  // (k-blocks times a tile's cycles a k-block, plus a tile's fixed part), fitted to timings of
+  // pairs with eight epilogue warps.  Measured with the present sixteen (us, 256 / 192 / 128 / 64
+  // rows; MXFP4 from bf16 rows, then MXFP8 pairs in):
+  //   1024 x 4096 x 4096   12.7 / 16.2 / 13.3 / 17.9    14.1 / 18.8 / 14.8 / 24.7
+  //   1536 x 4096 x 4096   19.7 / 18.2 / 20.8 / 25.5    23.7 / 19.7 / 26.9 / 35.7
+  //   4096 x 4096 x 512    12.7 / 12.8 / 14.3 / 16.9    11.8 / 11.8 / 14.4 / 19.2
+  //   4096 x 4096 x 2048   23.3 / 23.8 / 27.2 / 34.7    25.8 / 25.0 / 31.0 / 45.2
+  //   4096 x 4096 x 4096   36.7 / 37.6 / 42.9 / 56.4    43.5 / 42.7 / 55.3 / 79.8
+  //   16384 x 4096 x 512   34.1 / 35.6 / 42.3 / 55.7    32.2 / 32.9 / 44.1 / 66.4
+  //   16384 x 4096 x 4096   118 / 127 / 145 / 203        154 / 160 / 188 / 299
+  //   16384 x 512 x 1024   22.9 / 24.0 / 23.3 / 23.2    14.1 / 15.1 / 16.1 / 18.6
+  //   8192 x 8192 x 8192    198 / 209 / 250 / 336        321 / 321 / 378 / 562
+  //   700 x 2048 x 512      7.9 / 6.5 / 5.9 / 5.1        6.3 / 4.9 / 5.4 / 4.4
+  //   1300 x 2200 x 256     7.4 / 6.8 / 6.3 / 5.7        6.0 / 5.3 / 5.3 / 5.4
+  // The estimate takes the fastest but at 4096 cubed (192 rows, 2% slower in MXFP4) and in small
+  // products, where it takes pairs that are 1 to 1.4 us behind 64-row tiles.  Fewer than 24
   // pairs leave most of the weights' reads to too few SMs (317 x 1001 x 1056: 12.9 / 8.8).
   const bool narrow = (int64_t)((a.M + 127) / 128) * a.slabs <= g.num_sms;
   const int64_t tiles =

@@ -44,7 +44,6 @@ inline cudaError_t make_tmap(CUtensorMap* m, const void* base, uint64_t row_byte
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// kb_elems: K elements per k-block (256 for packed E2M1 tokens, 128 for E4M3).
 // Packed E2M1 matrix [rows, K elements] (K/2 bytes a row), read in boxes of 128
 // elements x 128 rows that land one element per byte: each 16 elements' 8 packed
 // bytes followed by 8 unused bytes (CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B), the

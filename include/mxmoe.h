@@ -26,8 +26,8 @@
  *     expert layer (moe_forward, moe_run_host, moe_debug_gate_up) serves one device a
  *     process, that of its first launch; the other operators serve any.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is enqueued
- *     asynchronously and stream-ordered; only moe_check, moe_run_host and the
- *     moe_read_* debug calls synchronise.
+ *     asynchronously and stream-ordered; only moe_check, moe_linear_check, moe_run_host
+ *     and the moe_read_* debug calls synchronise.
  *   - A failing call returns a nonzero moe_status and records a message readable
  *     with moe_last_error() (per thread).  Nothing is enqueued after a failed
  *     argument check.
@@ -111,6 +111,8 @@ MXMOE_API moe_status moe_validate_dims(const moe_dims *dims);
 MXMOE_API size_t moe_prepared_weights_size(const moe_dims *dims);
 
 /* Bytes of the workspace for dims->max_tokens tokens; 0 for bad dims.  Host only.
+ * (10 MB of them, and the intermediate rows of up to min(E, 16 k) experts of 16 tokens, serve
+ * moe_few_forward only.)
  * (The pages' symmetric buffer sized by num_max_tokens_per_rank, one per
  * mma_type; this library runs on one GPU, so it is plain device memory.) */
 MXMOE_API size_t moe_workspace_size(const moe_dims *dims);
@@ -376,7 +378,9 @@ typedef struct moe_linear_dims {
     int32_t mma_type;
 } moe_linear_dims;
 
-/* Bytes of the prepared weights and of the workspace; 0 for bad dims.  Host only. */
+/* Bytes of the prepared weights and of the workspace; 0 for bad dims.  Host only.  All but
+ * 1 KiB of the workspace holds the quantised rows of moe_linear_forward: max_rows of K or K / 2
+ * bytes and their scales.  Where only moe_linear_forward_pair is called it is not touched. */
 MXMOE_API size_t moe_linear_weights_size(const moe_linear_dims *dims);
 MXMOE_API size_t moe_linear_workspace_size(const moe_linear_dims *dims);
 
