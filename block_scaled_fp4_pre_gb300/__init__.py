@@ -29,6 +29,7 @@ MOE_ERR_WORKSPACE_MISMATCH = 4
 MOE_ERR_CUDA = 5
 MOE_ERR_ROUTING = 6
 MOE_ERR_TIMEOUT = 7
+MOE_ERR_PAGE = 8
 
 
 class MoeDims(ctypes.Structure):
@@ -60,6 +61,60 @@ def make_linear_dims(out_features: int, in_features: int, max_rows: int,
     return LinearDims(out_features, in_features, max_rows, mma_type)
 
 
+class RopeDims(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+    def __repr__(self):
+        return "RopeDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+MOE_ROPE_HALF = 0
+MOE_ROPE_INTERLEAVED = 1
+MOE_ROPE_UNSCALED = 0
+MOE_ROPE_LINEAR = 1
+MOE_ROPE_NTK = 2
+MOE_ROPE_YARN = 3
+
+
+def make_rope_dims(head_dim: int, rotary_dim: int | None = None, layout: int = MOE_ROPE_HALF,
+                   base: float = 10000.0, scaling: int = MOE_ROPE_UNSCALED, factor: float = 1.0,
+                   original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                   magnitude: float = 0.0) -> RopeDims:
+    return RopeDims(head_dim, head_dim if rotary_dim is None else rotary_dim, layout, scaling,
+                    base, factor, original_length, beta_fast, beta_slow, magnitude)
+
+
+class AttentionDims(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("max_shared_tokens", ctypes.c_int32)]
+
+    def __repr__(self):
+        return ("AttentionDims("
+                + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")")
+
+
+def make_attention_dims(q_heads: int, kv_heads: int, head_dim: int, num_pages: int,
+                        page_size: int, max_tokens: int, max_shared_tokens: int = 0
+                        ) -> AttentionDims:
+    return AttentionDims(q_heads, kv_heads, head_dim, num_pages, page_size, max_tokens,
+                         max_shared_tokens)
+
+
+class KvBatch(ctypes.Structure):
+    """A step's batch (make_kv_batch).  It holds the addresses of its tensors and keeps them
+    alive; their contents may change between calls."""
+    _fields_ = [("seq_lens_dev", ctypes.c_void_p), ("cu_new_dev", ctypes.c_void_p),
+                ("pages_dev", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("tokens", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("pages_ld", ctypes.c_int32), ("shared_len", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{status_string(status)}: {message}")
@@ -78,6 +133,7 @@ def lib() -> ctypes.CDLL:
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         l = ctypes.CDLL(LIB_PATH)
         D, LD = ctypes.POINTER(MoeDims), ctypes.POINTER(LinearDims)
+        RD, AD, KB = (ctypes.POINTER(t) for t in (RopeDims, AttentionDims, KvBatch))
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sigs = {
             "moe_last_error": ([], ctypes.c_char_p),
@@ -119,6 +175,16 @@ def lib() -> ctypes.CDLL:
             "moe_linear_forward_pair": ([LD, vp, vp, vp, i64, vp, i64, i32, vp, sz, vp], i32),
             "moe_linear_check": ([vp, vp], i32),
             "moe_debug_linear_give_up": ([vp, i32], i32),
+            "moe_rope_table_size": ([RD], sz),
+            "moe_rope_prepare": ([RD, vp, sz, vp], i32),
+            "moe_rope": ([RD, vp, vp, i64, vp, i64, i32, vp, i64, vp], i32),
+            "moe_attention_workspace_size": ([AD], sz),
+            "moe_attention_workspace_init": ([AD, vp, sz, vp], i32),
+            "moe_kv_append": ([AD, KB, RD, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
+                               vp, sz, vp], i32),
+            "moe_attention": ([AD, KB, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
+                              i32),
+            "moe_attention_check": ([vp, vp], i32),
         }
         for name, (args, res) in sigs.items():
             f = getattr(l, name)
@@ -491,6 +557,156 @@ def moe_linear_check(ws, stream=None) -> None:
 def moe_debug_linear_give_up(ws, on: bool) -> None:
     """Calls on this linear workspace behave as if a device wait had run out."""
     _check(lib().moe_debug_linear_give_up(_ptr(ws), int(on)))
+
+
+def moe_rope_table_size(dims: RopeDims) -> int:
+    return int(lib().moe_rope_table_size(ctypes.byref(dims)))
+
+
+def moe_rope_prepare(dims: RopeDims, table, stream=None) -> None:
+    """Writes the rotation's table, once for the calls that take it with these dims."""
+    _check(lib().moe_rope_prepare(ctypes.byref(dims), _bytes(table, 0, "table"), _nbytes(table),
+                                  _stream(stream)))
+
+
+def _here(t, name: str) -> int:
+    """Address of a tensor on the current device."""
+    if t.get_device() == _current_device():
+        return t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: need a tensor on the current CUDA device "
+                                        f"{_current_device()}, got one on {t.device}")
+
+
+def _heads(t, tokens: int, heads: int, D: int, name: str) -> int:
+    """Token stride of bf16 [tokens, heads, D] or [tokens, heads * D], a token's row contiguous."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is torch.bfloat16:
+        if shape == (tokens, heads, D):
+            if (strides[2] == 1 or D == 1) and (strides[1] == D or heads == 1):
+                return strides[0] if tokens > 1 else heads * D
+        elif shape == (tokens, heads * D) and (strides[1] == 1 or heads * D == 1):
+            return strides[0] if tokens > 1 else heads * D
+    raise ValueError(f"{name}: need bf16 [{tokens}, {heads}, {D}] with contiguous tokens, got "
+                     f"{t.dtype} {list(shape)}, strides {strides}")
+
+
+def _ints(t, n: int, name: str) -> int:
+    if t.dtype is torch.int32 and t.numel() == n and t.is_contiguous():
+        return _here(t, name)
+    raise ValueError(f"{name}: need {n} contiguous int32, got {t.dtype} {list(t.shape)}")
+
+
+def moe_rope(dims: RopeDims, table, x, positions, out=None, stream=None) -> None:
+    """Rotates x, bf16 [tokens, heads, head_dim] with contiguous tokens, by each token's int32
+    position, into out or in place."""
+    out = x if out is None else out
+    if x.dim() != 3:
+        raise ValueError(f"x: need [tokens, heads, head_dim], got {list(x.shape)}")
+    T, heads, D = x.shape
+    if D != dims.head_dim:
+        raise ValueError(f"x: heads of {D} elements, the rotation's of {dims.head_dim}")
+    ldx, ldo = _heads(x, T, heads, D, "x"), _heads(out, T, heads, D, "out")
+    status = (_lib or lib()).moe_rope(
+        ctypes.byref(dims), _bytes(table, 4 * dims.rotary_dim, "table"), _here(x, "x"), ldx,
+        _ints(positions, T, "positions"), T, heads, _here(out, "out"), ldo,
+        _raw_stream(_current_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status)
+
+
+def make_kv_batch(seq_lens, pages, tokens: int, cu_new=None, max_new: int | None = None,
+                  shared_len: int = 0) -> KvBatch:
+    """A step's batch: seq_lens int32 [batch], pages int32 [batch, n], and, unless every sequence
+    has tokens / batch new tokens, cu_new int32 [batch + 1] with the most of one, max_new."""
+    batch = seq_lens.numel()
+    if pages.dim() != 2 or pages.shape[0] != batch:
+        raise ValueError(f"pages: need [{batch}, n], got {list(pages.shape)}")
+    if cu_new is not None and max_new is None:
+        raise ValueError("max_new: needed with cu_new")
+    b = KvBatch(_ints(seq_lens, batch, "seq_lens"),
+                None if cu_new is None else _ints(cu_new, batch + 1, "cu_new"),
+                _ints(pages, pages.numel(), "pages"), batch, tokens,
+                1 if max_new is None else max_new, pages.shape[1], shared_len)
+    b.tensors, b.device = (seq_lens, cu_new, pages), seq_lens.get_device()
+    return b
+
+
+def moe_attention_workspace_size(dims: AttentionDims) -> int:
+    return int(lib().moe_attention_workspace_size(ctypes.byref(dims)))
+
+
+def moe_attention_workspace_init(dims: AttentionDims, ws, stream=None) -> None:
+    _check(lib().moe_attention_workspace_init(ctypes.byref(dims), _bytes(ws, 0, "workspace"),
+                                              _nbytes(ws), _stream(stream)))
+
+
+def _cache(t, dims: AttentionDims, name: str) -> int:
+    shape = (dims.num_pages, dims.kv_heads, dims.page_size, dims.head_dim)
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous():
+        return _here(t, name)
+    raise ValueError(f"{name}: need contiguous bf16 {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _on_device(batch: KvBatch) -> None:
+    if batch.device != _current_device():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"batch: its tensors lie on device {batch.device}, "
+                                            f"current is {_current_device()}")
+
+
+def moe_kv_append(dims: AttentionDims, batch: KvBatch, k, v, k_cache, v_cache, ws, *, rope=None,
+                  table=None, positions=None, q=None, q_out=None, stream=None) -> None:
+    """Appends keys (rotated, given rope and its table) and values to the paged cache, and
+    rotates q into q_out (or in place).  q, k and v are bf16 [tokens, heads, head_dim]."""
+    T, D, hk, hq = batch.tokens, dims.head_dim, dims.kv_heads, dims.q_heads
+    _on_device(batch)
+    pq = pqo = pt = None
+    ldq = ldqo = 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        ldq, ldqo = _heads(q, T, hq, D, "q"), _heads(q_out, T, hq, D, "q_out")
+        pq, pqo = _here(q, "q"), _here(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    if rope is not None:
+        pt = _bytes(table, 4 * rope.rotary_dim, "table")
+        rope = ctypes.byref(rope)
+    ldk, ldv = _heads(k, T, hk, D, "k"), _heads(v, T, hk, D, "v")
+    status = (_lib or lib()).moe_kv_append(
+        ctypes.byref(dims), ctypes.byref(batch), rope, pt,
+        None if positions is None else _ints(positions, T, "positions"), pq, ldq, pqo, ldqo,
+        _here(k, "k"), ldk, _here(v, "v"), ldv, _cache(k_cache, dims, "k_cache"),
+        _cache(v_cache, dims, "v_cache"), _here(ws, "workspace"), ws.nbytes,
+        _raw_stream(_current_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_attention(dims: AttentionDims, batch: KvBatch, q, k_cache, v_cache, out, ws, *,
+                  scale: float | None = None, lse=None, stream=None) -> None:
+    """Attention of the batch's new tokens over the paged cache, which holds them already.
+
+    q and out are bf16 [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads] or None; scale is
+    head_dim ** -0.5 unless given."""
+    T, D, hq = batch.tokens, dims.head_dim, dims.q_heads
+    _on_device(batch)
+    ldq, ldo = _heads(q, T, hq, D, "q"), _heads(out, T, hq, D, "out")
+    pl = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, hq) or not lse.is_contiguous():
+            raise ValueError(f"lse: need contiguous fp32 [{T}, {hq}]")
+        pl = _here(lse, "lse")
+    status = (_lib or lib()).moe_attention(
+        ctypes.byref(dims), ctypes.byref(batch), _here(q, "q"), ldq,
+        _cache(k_cache, dims, "k_cache"), _cache(v_cache, dims, "v_cache"),
+        D ** -0.5 if scale is None else scale, _here(out, "out"), ldo, pl,
+        _here(ws, "workspace"), ws.nbytes,
+        _raw_stream(_current_device()) if stream is None else _stream(stream))
+    if status:
+        _check(status)
+
+
+def moe_attention_check(ws, stream=None) -> None:
+    _check(lib().moe_attention_check(_ptr(ws), _stream(stream)))
 
 
 def moe_fp4_mma_probe(ws, n: int, blocks_per_sm: int, blocks: int, mma_count: int,

@@ -423,6 +423,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
     case MOE_ERR_ROUTING: return "MOE_ERR_ROUTING";
     case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
+    case MOE_ERR_PAGE: return "MOE_ERR_PAGE";
     default: return "MOE_ERR_UNKNOWN";
   }
 }

@@ -53,6 +53,7 @@ __host__ __device__ __forceinline__ int segment_rows(int n, int tile_rows) {
 // Device error bits in ws.flags[0].
 constexpr int kErrRouting = 1;
 constexpr int kErrTimeout = 2;
+constexpr int kErrPage = 4;
 
 // Other words of ws.flags: [1] number of token tiles, [2] valid assignments,
 // [3] next work item of the layer kernel, [4] blocks of the layer kernel done.
@@ -363,5 +364,75 @@ struct FewLaunch {
   int device, num_sms;       // the current device
 };
 cudaError_t launch_few(const FewLaunch& g, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// Rotary positions and the append to a paged cache (rope.cu).
+constexpr int kMostSequences = 4096;
+constexpr int kMostPairs = 256;    // rotated pairs of a head of at most 512 elements
+struct RopeTable {
+  uint64_t turn[kMostPairs];       // 2^64 w / (2 pi): the angle of one position
+};
+// The step's batch on the device; pages through row 0 below shared_len.
+struct KvBatch {
+  const int32_t* seq_lens;
+  const int32_t* cu_new;           // or null: n_each tokens a sequence
+  const int32_t* pages;
+  int batch, tokens, max_new, n_each, pages_ld, shared_len;
+};
+struct RopeSection {               // heads of one tensor
+  const uint16_t* src;
+  uint16_t* dst;                   // null in the cache's sections
+  int64_t lds, ldd;
+  int heads;
+};
+struct RopeArgs {
+  const uint64_t* turn;            // table, or null: nothing is rotated
+  const int32_t* positions;        // or null: the place in the sequence
+  RopeSection q, k, v;             // moe_rope: q alone
+  uint16_t* k_cache;               // [num_pages, k.heads, page_size, head_dim]
+  uint16_t* v_cache;
+  KvBatch batch;                   // append only
+  int32_t* flags;
+  int64_t tokens;
+  float magnitude;
+  int head_dim, rotary_dim, layout;
+  int num_pages, page_shift;
+};
+cudaError_t launch_rope_prepare(const RopeTable& t, int pairs, void* table, cudaStream_t st);
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+cudaError_t launch_kv_append(const RopeArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// Attention over a paged cache (attention.cu).
+struct AttnArgs {
+  const uint16_t* q;               // [tokens, q_heads, head_dim], stride ldq
+  const uint16_t* k_cache;         // [num_pages, kv_heads, page_size, head_dim]
+  const uint16_t* v_cache;
+  uint16_t* out;
+  float* lse;                      // [tokens, q_heads], or null
+  int64_t ldq, ldo;
+  float scale_log2;                // scale * log2(e)
+  KvBatch batch;
+  int q_heads, kv_heads, group, num_pages, page_shift;
+  int32_t* flags;
+};
+struct AttnLaunch {
+  AttnArgs args;
+  int head_dim;
+  bool shared;                     // the shared prefix is computed once for the batch
+  int device, num_sms;             // the current device
+};
+cudaError_t launch_attention(const AttnLaunch& g, cudaStream_t st);
+
+// A sequence's new tokens in a call: the first, how many, and how many of them are computed.
+struct NewTokens {
+  int first, n, taken;
+};
+__device__ __forceinline__ NewTokens new_tokens(const KvBatch& b, int seq) {
+  if (!b.cu_new) return {seq * b.n_each, b.n_each, b.n_each};
+  const int first = min(max(b.cu_new[seq], 0), b.tokens);
+  const int n = min(max(b.cu_new[seq + 1], first), b.tokens) - first;
+  return {first, n, min(n, b.max_new)};
+}
 
 }  // namespace mxmoe

@@ -26,8 +26,8 @@
  *     expert layer (moe_forward, moe_run_host, moe_debug_gate_up) serves one device a
  *     process, that of its first launch; the other operators serve any.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is enqueued
- *     asynchronously and stream-ordered; only moe_check, moe_linear_check, moe_run_host
- *     and the moe_read_* debug calls synchronise.
+ *     asynchronously and stream-ordered; only moe_check, moe_linear_check,
+ *     moe_attention_check, moe_run_host and the moe_read_* debug calls synchronise.
  *   - A failing call returns a nonzero moe_status and records a message readable
  *     with moe_last_error() (per thread).  Nothing is enqueued after a failed
  *     argument check.
@@ -63,7 +63,9 @@ enum {
     MOE_ERR_WORKSPACE_MISMATCH = 4,  /* workspace initialised for other dims/mma    */
     MOE_ERR_CUDA = 5,                /* a CUDA runtime/driver call failed            */
     MOE_ERR_ROUTING = 6,             /* device saw topk ids outside [0, E)           */
-    MOE_ERR_TIMEOUT = 7              /* a device wait ran past its limit             */
+    MOE_ERR_TIMEOUT = 7,             /* a device wait ran past its limit             */
+    MOE_ERR_PAGE = 8                 /* device saw a token outside its pages or a page
+                                        outside the cache                            */
 };
 
 /* Operand types of the expert GEMMs (digest of PR #37279, items 1-4: the explicit
@@ -427,6 +429,149 @@ MXMOE_API moe_status moe_linear_check(void *ws_dev, void *stream);
  * workspace stay usable.  Without effect on products large enough for tiles over SM pairs.
  * Host only. */
 MXMOE_API moe_status moe_debug_linear_give_up(void *ws_dev, int32_t on);
+
+/* ---- rotary positions ----
+ * Rotates pairs of a head's first rotary_dim elements by an angle that grows with the token's
+ * position p: pair i by p * w_i, of (x[i], x[i + rotary_dim/2]) in MOE_ROPE_HALF layout, of
+ * (x[2i], x[2i + 1]) in MOE_ROPE_INTERLEAVED:
+ *   (a, b) -> m * (a cos - b sin, b cos + a sin),    w_i = base^(-2i / rotary_dim)
+ * The rest of the head is copied.  For contexts longer than the trained one w is scaled:
+ *   MOE_ROPE_UNSCALED  as it is
+ *   MOE_ROPE_LINEAR    w / factor
+ *   MOE_ROPE_NTK       base * factor^(rotary_dim / (rotary_dim - 2)) in base's place
+ *                      (rotary_dim > 2)
+ *   MOE_ROPE_YARN      w * g + w / factor * (1 - g), g = clamp((t - beta_slow) / (beta_fast -
+ *                      beta_slow), 0, 1) with t = original_length * w / (2 pi), the turns over
+ *                      the trained length (Peng et al. 2023, "YaRN")
+ * magnitude m: 0 means 1, for MOE_ROPE_YARN 0.1 ln(factor) + 1.  Angles are exact to 2^-52 of
+ * a turn times the position: they are whole products modulo one turn in 64-bit fixed point, w in
+ * double.  Cosines, sines and the rotation are fp32, rounded once to bf16.
+ * Ranges: head_dim a multiple of 8 in [8, 512]; rotary_dim even in [2, head_dim]; base > 1,
+ * factor >= 1, original_length > 0, beta_fast > beta_slow >= 0, magnitude >= 0, all finite and
+ * each read only where its scaling uses it. */
+enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 };
+enum { MOE_ROPE_UNSCALED = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3 };
+typedef struct moe_rope_dims {
+    int32_t head_dim;
+    int32_t rotary_dim;
+    int32_t layout;
+    int32_t scaling;
+    double base;
+    double factor;
+    double original_length;
+    double beta_fast;
+    double beta_slow;
+    double magnitude;
+} moe_rope_dims;
+
+/* Bytes of the table of w (0 for bad dims; host only), and the call that writes it, once for
+ * the calls that take it with the same dims.  table_dev is 16-byte aligned. */
+MXMOE_API size_t moe_rope_table_size(const moe_rope_dims *dims);
+MXMOE_API moe_status moe_rope_prepare(const moe_rope_dims *dims, void *table_dev,
+                                      size_t table_bytes, void *stream);
+
+/* Rotates x_dev, bf16 [tokens, heads, head_dim] with ldx elements from token to token, into
+ * out_dev (ldo; out may be x itself with the same stride, and shares no memory with it
+ * otherwise).  Both 16-byte aligned, strides multiples of 8 and at least heads * head_dim;
+ * positions_dev int32 [tokens] (a negative position rotates back).  0 <= tokens < 2^31,
+ * 1 <= heads <= 65536; no tokens is a no-op. */
+MXMOE_API moe_status moe_rope(const moe_rope_dims *dims, const void *table_dev, const void *x_dev,
+                              int64_t ldx, const int32_t *positions_dev, int64_t tokens,
+                              int32_t heads, void *out_dev, int64_t ldo, void *stream);
+
+/* ---- paged cache of keys and values, and attention over it ----
+ * The cache is two bf16 arrays [num_pages, kv_heads, page_size, head_dim], contiguous and
+ * 128-byte aligned: the rows of one page and head lie together.  A sequence's token p is row
+ * p % page_size of the page that entry p / page_size of its page table row names.
+ * Ranges: head_dim 64 or 128; q_heads a multiple of kv_heads, at most 1024; page_size a power of
+ * two in [16, 256]; num_pages >= 1 with num_pages * kv_heads * page_size < 2^31; max_tokens (of
+ * one call) in [1, 2^20]; 0 <= max_shared_tokens <= max_tokens. */
+typedef struct moe_attention_dims {
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t max_tokens;
+    int32_t max_shared_tokens;
+} moe_attention_dims;
+
+/* One step's batch: `batch` sequences (1 .. 4096) with `tokens` new tokens (0 .. max_tokens),
+ * packed sequence after sequence.
+ *   seq_lens_dev  int32 [batch]      tokens of each sequence, the new ones among them
+ *   cu_new_dev    int32 [batch + 1]  first new token of each sequence and, last, their number;
+ *                                    NULL: tokens / batch each (a whole number)
+ *   pages_dev     int32 [batch, pages_ld]  page tables, at least 1 entry a row
+ *   max_new       an upper bound of a sequence's new tokens, 1 .. max_tokens (with cu_new_dev;
+ *                 without, not read).  A sequence's new tokens past it are left out.
+ *   shared_len    the first tokens that all sequences have in common: a multiple of page_size,
+ *                 0 for none.  Their pages are read through the first sequence's row, which
+ *                 must name them; other rows' entries for them are not read.
+ * New token i of a sequence of length L with n new ones is at position p = L - n + i: it sees
+ * the keys 0 .. p.  Positions below 0 (a padded batch: length 0, one token) see nothing: zeros,
+ * lse minus infinity.  Rows of q, k, v and the outputs behind cu_new_dev's last entry are
+ * neither read nor written.  Values outside their ranges in these arrays are cut to them or
+ * raise MOE_ERR_PAGE at the next moe_attention_check; nothing outside the given buffers is
+ * accessed. */
+typedef struct moe_kv_batch {
+    const int32_t *seq_lens_dev;
+    const int32_t *cu_new_dev;
+    const int32_t *pages_dev;
+    int32_t batch;
+    int32_t tokens;
+    int32_t max_new;
+    int32_t pages_ld;
+    int32_t shared_len;
+} moe_kv_batch;
+
+/* Bytes of the workspace; 0 for bad dims.  Host only.  max_shared_tokens sizes the part that
+ * calls with a shared prefix use; calls of more tokens read the prefix once for each sequence
+ * instead, with the same results up to fp32 summation order. */
+MXMOE_API size_t moe_attention_workspace_size(const moe_attention_dims *dims);
+/* Clears and registers a workspace (256-byte aligned), as moe_workspace_init does for the
+ * layer's.  One call at a time may use a workspace. */
+MXMOE_API moe_status moe_attention_workspace_init(const moe_attention_dims *dims, void *ws_dev,
+                                                  size_t ws_bytes, void *stream);
+
+/* Writes the new tokens' keys and values into the cache, the keys rotated on the way, and
+ * rotates the queries:
+ *   rope, table_dev  the rotation (its head_dim the cache's), or both NULL: keys are copied
+ *   positions_dev    int32 [tokens] for the angles, or NULL: each token's place p
+ *   q_dev, q_out_dev bf16 [tokens, q_heads, head_dim], rotated from the one into the other (may be
+ *                    the same, see moe_rope); both NULL: keys and values only
+ *   k_dev, v_dev     bf16 [tokens, kv_heads, head_dim]
+ * Token strides ldq, ldk, ldv, ldqo in elements, multiples of 8 and at least a row; pointers
+ * 16-byte aligned.  k, v and q share no memory with the caches.  Tokens with a negative p are
+ * left out; a token whose page is missing is left out of the cache and raises MOE_ERR_PAGE.  No
+ * two tokens may have the same place in the cache (sequences that share a page they write to);
+ * with shared_len, no place lies in the shared pages. */
+MXMOE_API moe_status moe_kv_append(const moe_attention_dims *dims, const moe_kv_batch *batch,
+                                   const moe_rope_dims *rope, const void *table_dev,
+                                   const int32_t *positions_dev, const void *q_dev, int64_t ldq,
+                                   void *q_out_dev, int64_t ldqo, const void *k_dev, int64_t ldk,
+                                   const void *v_dev, int64_t ldv, void *k_cache_dev,
+                                   void *v_cache_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* out[t, h] = sum over the keys j that token t sees of softmax(scale * q[t, h] . k[j])_j v[j],
+ * with kv head h / (q_heads / kv_heads):
+ *   q_dev    bf16 [tokens, q_heads, head_dim], token stride ldq
+ *   out_dev  bf16, the same with ldo; shares no memory with q or the caches
+ *   lse_dev  fp32 [tokens, q_heads], ln of the sum of exp(scale * q . k), or NULL
+ *   scale    finite and positive
+ * Strides are multiples of 8 and at least a row, pointers 16-byte aligned.  The caches hold the new tokens' keys and
+ * values already (moe_kv_append).  Rows of the cache that no token of the call sees may hold
+ * anything, those that one sees finite values; q is finite.  Products of bf16 values
+ * are summed in fp32, the probabilities rounded to bf16 for theirs with the values, their sum
+ * taken in fp32.  Results do not depend on timing. */
+MXMOE_API moe_status moe_attention(const moe_attention_dims *dims, const moe_kv_batch *batch,
+                                   const void *q_dev, int64_t ldq, const void *k_cache_dev,
+                                   const void *v_cache_dev, float scale, void *out_dev,
+                                   int64_t ldo, float *lse_dev, void *ws_dev, size_t ws_bytes,
+                                   void *stream);
+
+/* Synchronises `stream`, then reads and clears the workspace's error flags: MOE_ERR_PAGE,
+ * MOE_ERR_TIMEOUT or MOE_OK. */
+MXMOE_API moe_status moe_attention_check(void *ws_dev, void *stream);
 
 /* FP4 tensor-core throughput probe (measurement only; the denominator of the
  * layer's compute roofline).  Launches `blocks` blocks of 128 threads on `stream`,
