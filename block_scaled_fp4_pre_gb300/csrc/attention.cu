@@ -5,8 +5,8 @@
 // One warp a query head of a token: a pass over its keys with the running maximum and sum.
 #include <cuda_runtime.h>
 
-#include "common.cuh"
-#include "ptx.cuh"
+#include "attn.cuh"
+#include "tmap.cuh"
 
 namespace mxmoe {
 namespace {
@@ -66,6 +66,15 @@ __global__ void __launch_bounds__(256) attention_row_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_attention(const AttnLaunch& g, cudaStream_t st) {
+  const AttnArgs& a = g.args;
+  const uint64_t rows = ((uint64_t)a.num_pages * a.kv_heads) << a.page_shift;
+  const uint32_t box = a.page_shift < 7 ? 1u << a.page_shift : kAttnTile;
+  CUtensorMap k, v;
+  cudaError_t e = make_tmap_bf16(&k, a.k_cache, g.head_dim, rows, box);
+  if (e == cudaSuccess) e = make_tmap_bf16(&v, a.v_cache, g.head_dim, rows, box);
+  if (e != cudaSuccess) return e;
+  if ((int64_t)a.batch.max_new * a.group <= kAttnFewRows)
+    return launch_attention_few(g, k, v, st);
   const int64_t warps = (int64_t)g.args.batch.tokens * g.args.q_heads;
   const dim3 grid((unsigned)((warps + 7) / 8));
   if (g.head_dim == 64) return launch_pdl(attention_row_kernel<64>, grid, dim3(256), 0, st, g.args);

@@ -1,0 +1,145 @@
+// What the attention kernels share: the line of work that they cut into equal ranges, and the
+// loads of keys and values by page.
+//
+// The work of a call is a line of tiles (128 keys of one item), item after item; block c of N
+// takes the tiles [c W / N, (c + 1) W / N).  So every block streams the same number of keys,
+// whatever the sequences' lengths, and an item is cut only where a block's range ends: a block
+// has at most two parts of items, its first and its last.  Parts go to the workspace, and the
+// block that finishes an item's last part joins them, in the order of the line.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace mxmoe {
+
+constexpr int kAttnTile = 128;            // keys of a tile
+constexpr unsigned long long kAttnWaitNs = 2000000000ull;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A sequence in a call: its new tokens, and the keys [.., kend) that the last of them sees.
+struct Sequence {
+  NewTokens t;
+  int len, kend;
+};
+__device__ __forceinline__ Sequence sequence(const AttnArgs& a, int b) {
+  Sequence s;
+  s.t = new_tokens(a.batch, b);
+  s.len = a.batch.seq_lens[b];
+  const int64_t cap = (int64_t)a.batch.pages_ld << a.page_shift;
+  int64_t end = (int64_t)s.len - s.t.n + s.t.taken;
+  if (end > cap) {
+    atomicOr(a.flags, kErrPage);
+    end = cap;
+  }
+  s.kend = end > 0 && s.t.taken > 0 ? (int)end : 0;
+  return s;
+}
+// Keys that new token i sees.
+__device__ __forceinline__ int limit_of(const Sequence& s, int i) {
+  const int64_t l = (int64_t)s.len - s.t.n + i + 1;
+  return l > s.kend ? s.kend : l > 0 ? (int)l : 0;
+}
+
+// Position of a block's range on a line of W tiles, and the block that has position p.
+__device__ __forceinline__ int64_t range_start(int64_t W, int N, int c) { return c * W / N; }
+__device__ __forceinline__ int block_of(int64_t W, int N, int64_t p) {
+  return (int)(((p + 1) * N - 1) / W);
+}
+
+// Sums of each thread's value over the threads before it; total in *total.  All threads of
+// the block (a whole number of warps, at most 32).
+__device__ __forceinline__ int64_t block_exclusive_sum(int64_t v, int64_t* warp_sums,
+                                                       int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int64_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += warp_sums[w];
+    all += warp_sums[w];
+  }
+  *total = all;
+  return before + s - v;
+}
+
+// A sequence's row of the page table, 32 entries at a time in the lanes of a warp.
+struct Pages {
+  const int32_t* row;
+  const int32_t* shared;    // the first sequence's, for entries below shared_pages
+  int shared_pages, base, mine;
+  __device__ __forceinline__ void start(const AttnArgs& a, int b) {
+    row = a.batch.pages + (int64_t)b * a.batch.pages_ld;
+    shared = a.batch.pages;
+    shared_pages = a.batch.shared_len >> a.page_shift;
+    base = -64;
+  }
+  // Entry first + i, i in [0, n), n at most 32, each lane its own i (converged warp).
+  __device__ __forceinline__ int get(const AttnArgs& a, int first, int n, int i) {
+    if (first < base || first + n > base + 32) {
+      base = first;
+      const int at = first + (int)(threadIdx.x & 31);
+      mine = -1;
+      if (at < a.batch.pages_ld) mine = at < shared_pages ? shared[at] : row[at];
+    }
+    return __shfl_sync(0xFFFFFFFFu, mine, first - base + i);
+  }
+};
+
+// Row of the cache's arrays, as the tensor map counts them, of row r of a page and head; the
+// row behind the last, which loads read as zeros, for a page outside the cache.
+__device__ __forceinline__ int cache_row(const AttnArgs& a, int page, int head, int r) {
+  if (page < 0 || page >= a.num_pages) {
+    atomicOr(a.flags, kErrPage);
+    return (a.num_pages * a.kv_heads) << a.page_shift;
+  }
+  return ((page * a.kv_heads + head) << a.page_shift) + r;
+}
+
+// Loads the boxes of one tile of keys (or values) from key k0 of a sequence, `keys` of them
+// (1 .. kAttnTile), into dst: [D / 64][kAttnTile rows][128 bytes], swizzled.  A converged
+// warp; what no box covers keeps its old contents.
+template <int D>
+__device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* map, Pages& pages,
+                                          int head, int k0, int keys, uint8_t* dst,
+                                          uint64_t* bar) {
+  constexpr int HALVES = D / 64;
+  const int lane = threadIdx.x & 31;
+  const int box = min(1 << a.page_shift, kAttnTile);
+  const int boxes = (keys + box - 1) / box;
+  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, boxes * HALVES * box * 128);
+  __syncwarp();
+  const int i = min(lane / HALVES, boxes - 1), half = lane % HALVES;
+  const int page = pages.get(a, k0 >> a.page_shift, boxes, i);
+  if (lane < boxes * HALVES) {
+    const int y = cache_row(a, page, head, k0 & ((1 << a.page_shift) - 1));
+    ptx::tma_load_2d(dst + (half * kAttnTile + i * box) * 128, map, half * 64, y, bar,
+                     ptx::policy_evict_normal());
+  }
+}
+
+// Items of at most 16 rows (attn_few.cu).
+constexpr int kAttnFewRows = 16;
+cudaError_t launch_attention_few(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap& v,
+                                 cudaStream_t st);
+
+}  // namespace mxmoe

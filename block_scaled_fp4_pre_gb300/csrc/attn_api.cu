@@ -99,13 +99,22 @@ void set_rope(RopeArgs& a, const moe_rope_dims& d, const void* table) {
 // ---- workspaces ----
 
 struct AttnWs {
-  size_t flags, total;
+  size_t flags, counters, stats, parts, total;
 };
 
 AttnWs ws_layout(const moe_attention_dims& d) {
   AttnWs L;
-  L.flags = 0;
-  L.total = 1024;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 1023) / 1024 * 1024;
+    return at;
+  };
+  L.flags = take(4);
+  L.counters = take(kAttnBlocks * sizeof(int32_t));
+  L.stats = take((size_t)kAttnBlocks * 2 * kAttnRows * sizeof(float2));
+  L.parts = take((size_t)kAttnBlocks * 2 * kAttnRows * d.head_dim * sizeof(float));
+  L.total = o;
   return L;
 }
 
@@ -273,8 +282,8 @@ moe_status moe_attention_workspace_init(const moe_attention_dims* d, void* ws, s
   if (ws_bytes < L.total)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", ws_bytes,
                 L.total);
-  // only the flags need a defined start
-  const cudaError_t e = cudaMemsetAsync(ws, 0, 1024, static_cast<cudaStream_t>(stream));
+  // only the flags and counters need a defined start
+  const cudaError_t e = cudaMemsetAsync(ws, 0, L.stats, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "workspace clear");
   try {
     std::lock_guard<std::mutex> lk(g_mu);
@@ -374,7 +383,12 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
   a.group = d->q_heads / d->kv_heads;
   a.num_pages = d->num_pages;
   a.page_shift = shift_of(d->page_size);
-  a.flags = flags_of(*d, ws);
+  const AttnWs L = ws_layout(*d);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.flags = reinterpret_cast<int32_t*>(w + L.flags);
+  a.counters = reinterpret_cast<int32_t*>(w + L.counters);
+  a.part_stats = reinterpret_cast<float2*>(w + L.stats);
+  a.parts = reinterpret_cast<float*>(w + L.parts);
   g.head_dim = d->head_dim;
   g.shared = batch->shared_len > 0 && batch->tokens <= d->max_shared_tokens;
   g.num_sms = moe_device_sm_count();

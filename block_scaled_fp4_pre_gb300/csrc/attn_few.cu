@@ -1,0 +1,447 @@
+// Attention with at most 16 query rows an item (a sequence's new tokens times the heads that
+// share a kv head): decode steps and short drafts, for sm_103a.
+//
+//   S = scale q K^T, p = exp2(S - m), O = sum p V, l = sum p over an item's keys in one pass
+//
+// Bound by the cache's bytes: 16 rows use each loaded key and value 16 times, far below what
+// the tensor cores take, so tiles arrive by TMA into a ring as deep as shared memory holds
+// (six of 32 KiB at D = 128) and eight warps go through each tile together, 16 keys a warp,
+// with mma.sync on registers: M = 16 is the rows there are, where a tcgen05 tile would carry 112
+// rows of padding through tensor memory.  Each warp keeps its own running maximum, sum and output; they
+// meet in shared memory at the end of an item.  The maximum is raised, and the output scaled,
+// only where a logit passes it by 2^8: the sums have room for that in fp32, and so has a
+// probability in bf16, whose rounding is relative.
+//
+// Work is cut as attn.cuh says; a cut item's parts are joined by the block that comes last.
+#include "attn.cuh"
+#include "per_device.h"
+#include "tmap.cuh"
+
+namespace mxmoe {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kWarps = 8;                       // of consumers; one more loads
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kGroup = 8;                       // rows that the warps add up at a time
+
+template <int D>
+struct Ring {
+  static constexpr int kBytes = kAttnTile * D * 2;
+  static constexpr int kStages = 196608 / kBytes;
+};
+
+template <int D>
+struct Smem {
+  uint8_t ring[Ring<D>::kStages][Ring<D>::kBytes];
+  float sums[kWarps][kGroup][D];
+  float2 stats[kWarps][kRows];
+  int64_t scan[kThreads / 32];
+  uint64_t full[Ring<D>::kStages], empty[Ring<D>::kStages];
+  int64_t start_left;                           // tiles of the block's range
+  int start_seq, start_head, start_tile;
+  int abort, joins;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Tiles of a sequence's items; one, of no keys, where its tokens see none.
+__device__ __forceinline__ int tiles_of(const Sequence& s) {
+  if (s.t.taken == 0) return 0;
+  return max(1, (s.kend + kAttnTile - 1) / kAttnTile);
+}
+
+// Walks the items of a block's range.
+struct Walk {
+  int64_t left;       // tiles of the range not yet given out
+  int seq, head, tile;
+  int64_t at;         // position of the current item on the line
+  Sequence s;
+  int tiles, first, last;   // the current item's tiles, and those of them in the range
+  __device__ __forceinline__ bool next(const AttnArgs& a, bool begin) {
+    if (left <= 0) return false;
+    if (begin) {
+      s = sequence(a, seq);
+      tiles = tiles_of(s);
+    } else {
+      at += tiles;
+      tile = 0;
+      if (++head == a.kv_heads) {
+        head = 0;
+        do {
+          s = sequence(a, ++seq);
+          tiles = tiles_of(s);
+        } while (tiles == 0);
+      }
+    }
+    first = tile;
+    last = (int)min((int64_t)tiles, tile + left);
+    left -= last - first;
+    return true;
+  }
+};
+
+// Four elements of a finished row: its sums divided by the probabilities' sum.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs& a, const Sequence& s, int kv_head, int r,
+                                          int quad, float4 acc, float sum, float top) {
+  const int64_t t = s.t.first + r / a.group;
+  const int head = kv_head * a.group + r % a.group;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2*>(a.out + t * a.ldo + head * D + quad * 4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && quad == 0)
+    a.lse[t * a.q_heads + head] =
+        sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_few_kernel(const __grid_constant__ AttnArgs a,
+                         const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
+  constexpr int STAGES = Ring<D>::kStages;
+  extern __shared__ uint8_t raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
+      raw + ((1024 - (ptx::smem_addr(raw) & 1023)) & 1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      ptx::mbar_init(&sm.full[i], 1);
+      ptx::mbar_init(&sm.empty[i], kWarps);
+    }
+    ptx::fence_mbar_init();
+    sm.abort = 0;
+    ptx::prefetch_tmap(&kmap);
+    ptx::prefetch_tmap(&vmap);
+  }
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait();
+
+  // The block's range of the line.
+  const int per = (a.batch.batch + kThreads - 1) / kThreads;
+  const int b0 = min((int)threadIdx.x * per, a.batch.batch), b1 = min(b0 + per, a.batch.batch);
+  int64_t mine = 0, line = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of(sequence(a, b));
+  int64_t at = block_exclusive_sum(mine, sm.scan, &line) * a.kv_heads;
+  line *= a.kv_heads;
+  const int N = (int)min((int64_t)gridDim.x, line);
+  if (line == 0 || (int)blockIdx.x >= N) return;
+  const int64_t begin = range_start(line, N, blockIdx.x);
+  const int64_t end = range_start(line, N, blockIdx.x + 1);
+  if (begin >= at && begin < at + mine * a.kv_heads) {
+    int b = b0, t = 0;
+    for (;; ++b) {
+      t = tiles_of(sequence(a, b));
+      if (begin < at + (int64_t)t * a.kv_heads) break;
+      at += (int64_t)t * a.kv_heads;
+    }
+    sm.start_seq = b;
+    sm.start_head = (int)((begin - at) / t);
+    sm.start_tile = (int)((begin - at) % t);
+    sm.start_left = end - begin;
+  }
+  __syncthreads();
+  Walk w;
+  w.left = sm.start_left;
+  w.seq = sm.start_seq;
+  w.head = sm.start_head;
+  w.tile = sm.start_tile;
+  w.at = begin - w.tile;
+  volatile int* abort = &sm.abort;
+  int stage = 0;
+  uint32_t phase = 0;
+  auto advance = [&] {
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+
+  if (warp == kWarps) {
+    // ---- loads: keys and values of a tile, one stage each ----
+    Pages pages;
+    int seq = -1;
+    for (bool first = true; w.next(a, first); first = false) {
+      if (w.seq != seq) pages.start(a, seq = w.seq);
+      for (int t = w.first; t < w.last; ++t) {
+        const int keys = min(kAttnTile, w.s.kend - t * kAttnTile);
+        if (keys <= 0) continue;
+        for (int v = 0; v < 2; ++v) {
+          ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
+          load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, t * kAttnTile, keys, sm.ring[stage],
+                       &sm.full[stage]);
+          advance();
+        }
+      }
+    }
+    // After a wait that ran out, copies may still be in flight: the block stays for them.
+    if (*abort) {
+      int never = 0;
+      for (int i = 0; i < STAGES; ++i) {
+        ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
+        advance();
+      }
+    }
+    return;
+  }
+
+  // ---- rows against tiles: 16 keys of a tile a warp ----
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t ring = ptx::smem_addr(sm.ring);
+  const int k_row = (lane >> 4) * 8 + (lane & 7), k_chunk = (lane >> 3) & 1;
+  const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
+  const uint32_t k_base = (warp * 16 + k_row) * 128, v_base = (warp * 16 + v_row) * 128;
+  const int swizzle = lane & 7;
+  for (bool first = true; w.next(a, first); first = false) {
+    const Sequence& s = w.s;
+    const int rows = s.t.taken * a.group;
+    uint32_t q[D / 16][4];
+    int limit[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      const bool live = r < rows;
+      const int token = r / a.group, head = w.head * a.group + r % a.group;
+      const uint16_t* src = a.q + (int64_t)(s.t.first + token) * a.ldq + head * D + 2 * c;
+      limit[i] = live ? limit_of(s, token) : 0;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][i] = live ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+        q[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+      }
+    }
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
+
+    for (int t = w.first; t < w.last; ++t) {
+      if (t * kAttnTile >= s.kend) continue;
+      const int tok = t * kAttnTile + warp * 16;      // the warp's first key
+      const bool some = tok < s.kend;
+      float x[2][4] = {};
+      ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+      if (some) {
+        float y[2][4] = {};                            // two chains a key group
+        const uint32_t base = ring + stage * Ring<D>::kBytes + k_base;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t f[4];
+          const int chunk = 2 * k + k_chunk;
+          ldmatrix4(base + (chunk >> 3) * (kAttnTile * 128) + (((chunk & 7) ^ swizzle) << 4), f);
+          if (k & 1) {
+            mma(y[0], q[k], f[0], f[1]);
+            mma(y[1], q[k], f[2], f[3]);
+          } else {
+            mma(x[0], q[k], f[0], f[1]);
+            mma(x[1], q[k], f[2], f[3]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[n][j] += y[n][j];
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.empty[stage]);
+      advance();
+      uint32_t p[4] = {};
+      if (some) {
+        const int key = tok + 2 * c;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[n][j] = key + n * 8 + (j & 1) < limit[j >> 1] ? x[n][j] * a.scale_log2 : -INFINITY;
+        float top[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float up = fmaxf(m[i], top[i]);
+            const float f = up == m[i] ? 1.f : exp2_approx(m[i] - up);
+            m[i] = up;
+            l[i] *= f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              o[n][2 * i] *= f;
+              o[n][2 * i + 1] *= f;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float from = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float u = exp2_approx(x[n][2 * i] - from), v = exp2_approx(x[n][2 * i + 1] - from);
+            l[i] += u + v;
+            p[2 * n + i] = pack_bf16(u, v);
+          }
+        }
+      }
+      ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+      if (some) {
+        const uint32_t base = ring + stage * Ring<D>::kBytes + v_base;
+        // values behind the last key may be anything: 0 times them must be 0
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        const bool tail = tok + 16 > s.kend;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = tok + i * 8 + 2 * c;
+          keep[i] = (key < s.kend ? 0xFFFFu : 0u) | (key + 1 < s.kend ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t f[4];
+          const int chunk = 2 * n + v_chunk;
+          ldmatrix4_t(base + (chunk >> 3) * (kAttnTile * 128) + (((chunk & 7) ^ swizzle) << 4), f);
+          if (tail) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] &= keep[j & 1];
+          }
+          mma(o[2 * n], p, f[0], f[1]);
+          mma(o[2 * n + 1], p, f[2], f[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.empty[stage]);
+      advance();
+    }
+
+    // ---- the warps' sums to one, eight rows at a time ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+      if (c == 0) sm.stats[warp][g + 8 * i] = make_float2(m[i], l[i]);
+    }
+    ptx::named_bar_sync(1, 32 * kWarps);
+    const bool whole = w.first == 0 && w.last == w.tiles;
+    // parts: a block's second is one that begins an item, its first one that does not
+    const int slot = 2 * blockIdx.x + (w.first == 0);
+    constexpr int kQuads = D / 4;
+    const int quad = threadIdx.x % kQuads, row8 = threadIdx.x / kQuads;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kGroup) {
+      const int i = r0 / kGroup;
+      float top = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) top = fmaxf(top, sm.stats[v][r0 + g].x);
+      const float f = top == -INFINITY ? 0.f : exp2_approx((i ? m[1] : m[0]) - top);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const int pair = (n * 4 + c) ^ ((g & 3) * 4);     // spreads the rows over the banks
+        *reinterpret_cast<float2*>(&sm.sums[warp][g][2 * pair]) =
+            make_float2((i ? o[n][2] : o[n][0]) * f, (i ? o[n][3] : o[n][1]) * f);
+      }
+      ptx::named_bar_sync(1, 32 * kWarps);
+      for (int rr = row8; rr < kGroup; rr += 32 * kWarps / kQuads) {
+        const int r = r0 + rr;
+        if (r >= rows) continue;
+        float rowtop = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) rowtop = fmaxf(rowtop, sm.stats[v][r].x);
+        const float from = rowtop == -INFINITY ? 0.f : rowtop;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          const float2 st = sm.stats[v][r];
+          sum += st.y * exp2_approx(st.x - from);
+          const float4 y = *reinterpret_cast<const float4*>(
+              &sm.sums[v][rr][4 * (quad ^ ((rr & 3) * 2))]);
+          acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+        }
+        if (whole) {
+          store_row<D>(a, s, w.head, r, quad, acc, sum, rowtop);
+        } else {
+          *reinterpret_cast<float4*>(a.parts + ((int64_t)slot * kRows + r) * D + quad * 4) = acc;
+          if (quad == 0) a.part_stats[slot * kRows + r] = make_float2(rowtop, sum);
+        }
+      }
+      ptx::named_bar_sync(1, 32 * kWarps);
+    }
+    if (whole) continue;
+
+    // ---- a cut item: the block that comes last joins its parts ----
+    const int from = block_of(line, N, w.at), to = block_of(line, N, w.at + w.tiles - 1);
+    __threadfence();
+    ptx::named_bar_sync(1, 32 * kWarps);
+    if (threadIdx.x == 0) {
+      const bool last = ptx::atomic_add_acq_rel(a.counters + from, 1) == to - from;
+      if (last) a.counters[from] = 0;
+      sm.joins = last;
+    }
+    ptx::named_bar_sync(1, 32 * kWarps);
+    if (!sm.joins) continue;
+    __threadfence();
+    for (int r = row8; r < rows; r += 32 * kWarps / kQuads) {
+      auto part = [&](int b) { return (2 * b + (b == from)) * kRows + r; };
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+      for (int b = from; b <= to; ++b) top = fmaxf(top, __ldcg(&a.part_stats[part(b)]).x);
+      const float base = top == -INFINITY ? 0.f : top;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int b = from; b <= to; ++b) {
+        const float2 st = __ldcg(&a.part_stats[part(b)]);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.parts + (int64_t)part(b) * D) +
+                                quad);
+        const float f = exp2_approx(st.x - base);
+        sum += st.y * f;
+        acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
+      }
+      store_row<D>(a, s, w.head, r, quad, acc, sum, top);
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap& v,
+                   cudaStream_t st) {
+  static PerDevice<bool> raised;
+  constexpr size_t smem = sizeof(Smem<D>) + 1024;
+  static_assert(smem <= 232448, "a block's shared memory");
+  const cudaError_t e = once_a_device(raised, g.device, [] {
+    return cudaFuncSetAttribute(attention_few_kernel<D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attention_few_kernel<D>, dim3(g.num_sms < kAttnBlocks ? g.num_sms : kAttnBlocks),
+                    dim3(kThreads), smem, st, g.args, k, v);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_few(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap& v,
+                                 cudaStream_t st) {
+  return g.head_dim == 64 ? launch<64>(g, k, v, st) : launch<128>(g, k, v, st);
+}
+
+}  // namespace mxmoe

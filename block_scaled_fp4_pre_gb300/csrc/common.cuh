@@ -404,6 +404,8 @@ cudaError_t launch_kv_append(const RopeArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------------------
 // Attention over a paged cache (attention.cu).
+constexpr int kAttnBlocks = 160;   // most blocks of a kernel
+constexpr int kAttnRows = 256;     // most rows of an item
 struct AttnArgs {
   const uint16_t* q;               // [tokens, q_heads, head_dim], stride ldq
   const uint16_t* k_cache;         // [num_pages, kv_heads, page_size, head_dim]
@@ -415,6 +417,10 @@ struct AttnArgs {
   KvBatch batch;
   int q_heads, kv_heads, group, num_pages, page_shift;
   int32_t* flags;
+  // workspace: parts of cut items, two a block, and a counter a block (zero between calls)
+  float* parts;                    // [blocks][2][rows][head_dim]
+  float2* part_stats;              // [blocks][2][rows]: log2 of the largest term, sum
+  int32_t* counters;
 };
 struct AttnLaunch {
   AttnArgs args;

@@ -80,4 +80,21 @@ inline cudaError_t make_tmap_scales(CUtensorMap* m, const void* base, uint64_t p
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// bf16 rows of D elements (64 or 128) read in boxes of 64 elements x box_rows, 128-byte swizzle;
+// rows past the end read as zeros.
+inline cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows,
+                                  uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {D, rows};
+  const cuuint64_t strides[1] = {2 * D};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace mxmoe

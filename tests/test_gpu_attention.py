@@ -186,11 +186,11 @@ def test_refusals():
     good = dict(seq=seq, cu=cu, pages=pages, batch=2, tokens=4, max_new=2, pages_ld=3, shared=16)
 
     def call(batch=None, q=p.q.data_ptr(), ldq=1024, k=p.k.data_ptr(), v=p.v.data_ptr(), scale=1.0,
-             o=out.data_ptr(), ldo=1024, lse=None):
+             o=out.data_ptr(), ldo=1024, lse=None, append=True):
         b = mx.KvBatch(*(batch or good).values())
         a = f.moe_attention(ctypes.byref(D), ctypes.byref(b), q, ldq, k, v, scale, o, ldo, lse,
                             p.ws.data_ptr(), p.ws.nbytes, None)
-        c = f.moe_kv_append(ctypes.byref(D), ctypes.byref(b), None, None, None, None, 0, None, 0, q,
+        c = append and f.moe_kv_append(ctypes.byref(D), ctypes.byref(b), None, None, None, None, 0, None, 0, q,
                             ldq, o, ldo, k, v, p.ws.data_ptr(), p.ws.nbytes, None)
         return a, c
 
@@ -210,7 +210,7 @@ def test_refusals():
     for change in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                    dict(scale=float("inf")), dict(lse=out.data_ptr() + 2), dict(ldo=1020),
                    dict(ldo=0)):
-        assert call(**change)[0] == bad, change
+        assert call(**change, append=False)[0] == bad, change
     assert call(good | dict(tokens=0, cu=None), q=None, o=None) == (ok, ok)
 
     ref, b, rope = ctypes.byref(D), ctypes.byref(p.batch), mx.make_rope_dims(128)
