@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libmxmoe.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["api.cu", "dispatch.cu", "gemm.cu", "pair.cu", "noalloc.cu", "peak.cu", "mxfp8.cu",
            "ops.cu", "norm.cu", "linear.cu", "few.cu", "rope.cu",
-           "attention.cu", "attn_few.cu", "attn_api.cu"]
+           "attention.cu", "attn_few.cu", "attn_tile.cu", "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
          "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

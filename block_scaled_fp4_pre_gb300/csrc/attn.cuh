@@ -137,9 +137,65 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* 
   }
 }
 
+// What ends a row: its sums, with m the log2 of the term they are relative to, join the shared
+// prefix's (main part) and become the output, or are kept (SHARED).  `index` is the row among
+// its kv head's rows of all tokens.
+struct Finish {
+  float4* keep;
+  const float4* other;
+  float mine, theirs, inv, lse;
+};
+template <int D, bool SHARED>
+__device__ __forceinline__ Finish finish_begin(const AttnArgs& a, int kv_head, int64_t index,
+                                               float m, float l) {
+  Finish f;
+  const int64_t at = (int64_t)kv_head * a.batch.tokens * a.group + index;
+  f.keep = reinterpret_cast<float4*>(a.shared_parts + at * D);
+  f.other = nullptr;
+  if (SHARED) {
+    a.shared_stats[at] = make_float2(m, l);
+    return f;
+  }
+  f.mine = 1.f;
+  f.theirs = 0.f;
+  if (a.kstart > 0) {
+    const float2 st = a.shared_stats[at];
+    const float top = fmaxf(m, st.x), base = top == -INFINITY ? 0.f : top;
+    f.other = f.keep;
+    f.mine = exp2_approx(m - base);
+    f.theirs = exp2_approx(st.x - base);
+    l = l * f.mine + st.y * f.theirs;
+    m = top;
+  }
+  f.inv = l > 0.f ? 1.f / l : 0.f;
+  f.lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  return f;
+}
+// Four elements of the row.
+template <int D, bool SHARED>
+__device__ __forceinline__ void finish_quad(const AttnArgs& a, const Finish& f, int64_t token,
+                                            int head, int quad, float4 v) {
+  if (SHARED) {
+    f.keep[quad] = v;
+    return;
+  }
+  if (f.other) {
+    const float4 y = f.other[quad];
+    v.x = v.x * f.mine + y.x * f.theirs;
+    v.y = v.y * f.mine + y.y * f.theirs;
+    v.z = v.z * f.mine + y.z * f.theirs;
+    v.w = v.w * f.mine + y.w * f.theirs;
+  }
+  *reinterpret_cast<uint2*>(a.out + token * a.ldo + head * D + quad * 4) = make_uint2(
+      pack_bf16(v.x * f.inv, v.y * f.inv), pack_bf16(v.z * f.inv, v.w * f.inv));
+}
+
 // Items of at most 16 rows (attn_few.cu).
 constexpr int kAttnFewRows = 16;
 cudaError_t launch_attention_few(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap& v,
                                  cudaStream_t st);
+// Items of any number of rows (attn_tile.cu); shared: the prefix's part for all rows.
+cudaError_t launch_attention_tile(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap& v,
+                                  bool shared, cudaStream_t st);
 
 }  // namespace mxmoe

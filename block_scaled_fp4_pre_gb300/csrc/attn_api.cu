@@ -99,7 +99,7 @@ void set_rope(RopeArgs& a, const moe_rope_dims& d, const void* table) {
 // ---- workspaces ----
 
 struct AttnWs {
-  size_t flags, counters, stats, parts, total;
+  size_t flags, counters, cuts, stats, parts, shared_stats, shared_parts, total;
 };
 
 AttnWs ws_layout(const moe_attention_dims& d) {
@@ -112,8 +112,12 @@ AttnWs ws_layout(const moe_attention_dims& d) {
   };
   L.flags = take(4);
   L.counters = take(kAttnBlocks * sizeof(int32_t));
+  L.cuts = take(kAttnBlocks * sizeof(AttnCut));
   L.stats = take((size_t)kAttnBlocks * 2 * kAttnRows * sizeof(float2));
   L.parts = take((size_t)kAttnBlocks * 2 * kAttnRows * d.head_dim * sizeof(float));
+  const size_t rows = (size_t)d.max_shared_tokens * d.q_heads;
+  L.shared_stats = take(rows * sizeof(float2));
+  L.shared_parts = take(rows * d.head_dim * sizeof(float));
   L.total = o;
   return L;
 }
@@ -387,7 +391,10 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.flags = reinterpret_cast<int32_t*>(w + L.flags);
   a.counters = reinterpret_cast<int32_t*>(w + L.counters);
+  a.cuts = reinterpret_cast<AttnCut*>(w + L.cuts);
   a.part_stats = reinterpret_cast<float2*>(w + L.stats);
+  a.shared_stats = reinterpret_cast<float2*>(w + L.shared_stats);
+  a.shared_parts = reinterpret_cast<float*>(w + L.shared_parts);
   a.parts = reinterpret_cast<float*>(w + L.parts);
   g.head_dim = d->head_dim;
   g.shared = batch->shared_len > 0 && batch->tokens <= d->max_shared_tokens;

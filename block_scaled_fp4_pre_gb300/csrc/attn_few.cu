@@ -64,10 +64,10 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles of a sequence's items; one, of no keys, where its tokens see none.
-__device__ __forceinline__ int tiles_of(const Sequence& s) {
+// Tiles of a sequence's items; one, of no keys, where its tokens see none from kstart on.
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Sequence& s) {
   if (s.t.taken == 0) return 0;
-  return max(1, (s.kend + kAttnTile - 1) / kAttnTile);
+  return max(1, (s.kend - a.kstart + kAttnTile - 1) / kAttnTile);
 }
 
 // Walks the items of a block's range.
@@ -81,7 +81,7 @@ struct Walk {
     if (left <= 0) return false;
     if (begin) {
       s = sequence(a, seq);
-      tiles = tiles_of(s);
+      tiles = tiles_of(a, s);
     } else {
       at += tiles;
       tile = 0;
@@ -89,7 +89,7 @@ struct Walk {
         head = 0;
         do {
           s = sequence(a, ++seq);
-          tiles = tiles_of(s);
+          tiles = tiles_of(a, s);
         } while (tiles == 0);
       }
     }
@@ -100,18 +100,15 @@ struct Walk {
   }
 };
 
-// Four elements of a finished row: its sums divided by the probabilities' sum.
+// Four elements of a row of an item.
 template <int D>
 __device__ __forceinline__ void store_row(const AttnArgs& a, const Sequence& s, int kv_head, int r,
                                           int quad, float4 acc, float sum, float top) {
   const int64_t t = s.t.first + r / a.group;
   const int head = kv_head * a.group + r % a.group;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  *reinterpret_cast<uint2*>(a.out + t * a.ldo + head * D + quad * 4) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse && quad == 0)
-    a.lse[t * a.q_heads + head] =
-        sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  const Finish f = finish_begin<D, false>(a, kv_head, (int64_t)s.t.first * a.group + r, top, sum);
+  finish_quad<D, false>(a, f, t, head, quad, acc);
+  if (a.lse && quad == 0) a.lse[t * a.q_heads + head] = f.lse;
 }
 
 template <int D>
@@ -141,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (a.batch.batch + kThreads - 1) / kThreads;
   const int b0 = min((int)threadIdx.x * per, a.batch.batch), b1 = min(b0 + per, a.batch.batch);
   int64_t mine = 0, line = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of(sequence(a, b));
+  for (int b = b0; b < b1; ++b) mine += tiles_of(a, sequence(a, b));
   int64_t at = block_exclusive_sum(mine, sm.scan, &line) * a.kv_heads;
   line *= a.kv_heads;
   const int N = (int)min((int64_t)gridDim.x, line);
@@ -151,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (begin >= at && begin < at + mine * a.kv_heads) {
     int b = b0, t = 0;
     for (;; ++b) {
-      t = tiles_of(sequence(a, b));
+      t = tiles_of(a, sequence(a, b));
       if (begin < at + (int64_t)t * a.kv_heads) break;
       at += (int64_t)t * a.kv_heads;
     }
@@ -184,11 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (bool first = true; w.next(a, first); first = false) {
       if (w.seq != seq) pages.start(a, seq = w.seq);
       for (int t = w.first; t < w.last; ++t) {
-        const int keys = min(kAttnTile, w.s.kend - t * kAttnTile);
+        const int k0 = a.kstart + t * kAttnTile, keys = min(kAttnTile, w.s.kend - k0);
         if (keys <= 0) continue;
         for (int v = 0; v < 2; ++v) {
           ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-          load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, t * kAttnTile, keys, sm.ring[stage],
+          load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, sm.ring[stage],
                        &sm.full[stage]);
           advance();
         }
@@ -196,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // After a wait that ran out, copies may still be in flight: the block stays for them.
     if (*abort) {
+      if (lane == 0) atomicOr(a.flags, kErrTimeout);
       int never = 0;
       for (int i = 0; i < STAGES; ++i) {
         ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
@@ -237,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
 
     for (int t = w.first; t < w.last; ++t) {
-      if (t * kAttnTile >= s.kend) continue;
-      const int tok = t * kAttnTile + warp * 16;      // the warp's first key
+      if (a.kstart + t * kAttnTile >= s.kend) continue;
+      const int tok = a.kstart + t * kAttnTile + warp * 16;      // the warp's first key
       const bool some = tok < s.kend;
       float x[2][4] = {};
       ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
@@ -420,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_row<D>(a, s, w.head, r, quad, acc, sum, top);
     }
   }
+  if (*abort && lane == 0) atomicOr(a.flags, kErrTimeout);
 }
 
 template <int D>

@@ -406,6 +406,11 @@ cudaError_t launch_kv_append(const RopeArgs& a, cudaStream_t st);
 // Attention over a paged cache (attention.cu).
 constexpr int kAttnBlocks = 160;   // most blocks of a kernel
 constexpr int kAttnRows = 256;     // most rows of an item
+// The item of a tile kernel that begins in a block's range and goes on behind it: rows from
+// row tile rt of the tokens from `first` on, in the parts of blocks [from, to]; to < 0: none.
+struct AttnCut {
+  int first, rt, rows, head, from, to;
+};
 struct AttnArgs {
   const uint16_t* q;               // [tokens, q_heads, head_dim], stride ldq
   const uint16_t* k_cache;         // [num_pages, kv_heads, page_size, head_dim]
@@ -417,10 +422,15 @@ struct AttnArgs {
   KvBatch batch;
   int q_heads, kv_heads, group, num_pages, page_shift;
   int32_t* flags;
+  int kstart;                      // keys below it are the shared prefix's, computed apart
   // workspace: parts of cut items, two a block, and a counter a block (zero between calls)
   float* parts;                    // [blocks][2][rows][head_dim]
   float2* part_stats;              // [blocks][2][rows]: log2 of the largest term, sum
   int32_t* counters;
+  AttnCut* cuts;                   // [blocks]
+  // the prefix's sums of every row: [kv_heads][tokens * group], as parts
+  float* shared_parts;
+  float2* shared_stats;
 };
 struct AttnLaunch {
   AttnArgs args;
@@ -439,6 +449,19 @@ __device__ __forceinline__ NewTokens new_tokens(const KvBatch& b, int seq) {
   const int first = min(max(b.cu_new[seq], 0), b.tokens);
   const int n = min(max(b.cu_new[seq + 1], first), b.tokens) - first;
   return {first, n, min(n, b.max_new)};
+}
+
+// The sequence that new token t belongs to: the last with first token at most t that is not
+// empty there.  -1 behind the last one's tokens.
+__device__ __forceinline__ int sequence_of(const KvBatch& b, int t) {
+  if (!b.cu_new) return t / b.n_each;
+  int lo = 0, hi = b.batch;            // cu[lo] <= t < cu[hi] where the entries are in order
+  if (t >= b.cu_new[hi] || t < b.cu_new[0]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (b.cu_new[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
 }
 
 }  // namespace mxmoe

@@ -28,19 +28,6 @@ __global__ void rope_prepare_kernel(const __grid_constant__ RopeTable t, int pai
   for (int i = threadIdx.x; i < pairs; i += blockDim.x) out[i] = t.turn[i];
 }
 
-// The sequence that new token t belongs to: the last with first token at most t that is not
-// empty there.  -1 behind the last one's tokens.
-__device__ __forceinline__ int sequence_of(const KvBatch& b, int t) {
-  if (!b.cu_new) return t / b.n_each;
-  int lo = 0, hi = b.batch;            // cu[lo] <= t < cu[hi] where the entries are in order
-  if (t >= b.cu_new[hi] || t < b.cu_new[0]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (b.cu_new[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 template <int VEC>
 struct Piece;
 template <>
