@@ -17,6 +17,7 @@
 namespace mxmoe {
 
 constexpr int kAttnTile = 128;            // keys of a tile
+constexpr int kAttnMostKeys = 1 << 30;    // of a sequence
 constexpr unsigned long long kAttnWaitNs = 2000000000ull;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -30,28 +31,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// A sequence in a call: its new tokens, and the keys [.., kend) that the last of them sees.
+// A sequence in a call: its first new token, how many are computed, the position of the first,
+// and the keys [0, kend) that the last of them sees.
 struct Sequence {
-  NewTokens t;
-  int len, kend;
+  int first, taken, base, kend;
 };
 __device__ __forceinline__ Sequence sequence(const AttnArgs& a, int b) {
-  Sequence s;
-  s.t = new_tokens(a.batch, b);
-  s.len = a.batch.seq_lens[b];
-  const int64_t cap = (int64_t)a.batch.pages_ld << a.page_shift;
-  int64_t end = (int64_t)s.len - s.t.n + s.t.taken;
-  if (end > cap) {
+  const NewTokens t = new_tokens(a.batch, b);
+  Sequence s = {t.first, t.taken, max(a.batch.seq_lens[b], 0) - t.n, 0};
+  const int64_t cap = min((int64_t)a.batch.pages_ld << a.page_shift, (int64_t)kAttnMostKeys);
+  if ((int64_t)s.base + s.taken > cap) {      // behind the end of its row of the page table
     atomicOr(a.flags, kErrPage);
-    end = cap;
+    s.base = (int)cap - s.taken;
   }
-  s.kend = end > 0 && s.t.taken > 0 ? (int)end : 0;
+  s.kend = s.taken > 0 ? max(s.base + s.taken, 0) : 0;
   return s;
 }
 // Keys that new token i sees.
 __device__ __forceinline__ int limit_of(const Sequence& s, int i) {
-  const int64_t l = (int64_t)s.len - s.t.n + i + 1;
-  return l > s.kend ? s.kend : l > 0 ? (int)l : 0;
+  return max(s.base + i + 1, 0);
+}
+// r / group for a row of an item.
+__device__ __forceinline__ int token_of(const AttnArgs& a, int r) {
+  return (int)(((uint32_t)r * (uint32_t)a.group_inv) >> 16);
 }
 
 // Position of a block's range on a line of W tiles, and the block that has position p.
@@ -148,7 +150,7 @@ struct Finish {
 template <int D, bool SHARED>
 __device__ __forceinline__ Finish finish_begin(const AttnArgs& a, int kv_head, int64_t index,
                                                float m, float l) {
-  Finish f;
+  Finish f = {};
   const int64_t at = (int64_t)kv_head * a.batch.tokens * a.group + index;
   f.keep = reinterpret_cast<float4*>(a.shared_parts + at * D);
   f.other = nullptr;

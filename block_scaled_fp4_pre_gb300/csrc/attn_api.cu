@@ -141,6 +141,9 @@ moe_status check_dims(const moe_attention_dims* d) {
       d->q_heads % d->kv_heads)
     return fail(MOE_ERR_INVALID_ARG, "q_heads %d must be a multiple of kv_heads %d, at most 1024",
                 d->q_heads, d->kv_heads);
+  if (d->q_heads / d->kv_heads > kAttnRows)
+    return fail(MOE_ERR_INVALID_ARG, "q_heads %d: more than %d for each of kv_heads %d",
+                d->q_heads, kAttnRows, d->kv_heads);
   if (!power_of_two(d->page_size) || d->page_size < 16 || d->page_size > 256)
     return fail(MOE_ERR_INVALID_ARG, "page_size %d must be a power of two in [16, 256]",
                 d->page_size);
@@ -385,6 +388,7 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
   a.q_heads = d->q_heads;
   a.kv_heads = d->kv_heads;
   a.group = d->q_heads / d->kv_heads;
+  a.group_inv = (65536 + a.group - 1) / a.group;
   a.num_pages = d->num_pages;
   a.page_shift = shift_of(d->page_size);
   const AttnWs L = ws_layout(*d);

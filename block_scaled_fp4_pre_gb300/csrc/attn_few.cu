@@ -7,8 +7,8 @@
 // the tensor cores take, so tiles arrive by TMA into a ring as deep as shared memory holds
 // (six of 32 KiB at D = 128) and eight warps go through each tile together, 16 keys a warp,
 // with mma.sync on registers: M = 16 is the rows there are, where a tcgen05 tile would carry 112
-// rows of padding through tensor memory.  Each warp keeps its own running maximum, sum and output; they
-// meet in shared memory at the end of an item.  The maximum is raised, and the output scaled,
+// rows of padding through tensor memory.  Each warp keeps its own running maximum, sum and
+// output; they meet in shared memory at the end of an item.  The maximum is raised, and the output scaled,
 // only where a logit passes it by 2^8: the sums have room for that in fp32, and so has a
 // probability in bf16, whose rounding is relative.
 //
@@ -66,7 +66,7 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 
 // Tiles of a sequence's items; one, of no keys, where its tokens see none from kstart on.
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, const Sequence& s) {
-  if (s.t.taken == 0) return 0;
+  if (s.taken == 0) return 0;
   return max(1, (s.kend - a.kstart + kAttnTile - 1) / kAttnTile);
 }
 
@@ -104,9 +104,9 @@ struct Walk {
 template <int D>
 __device__ __forceinline__ void store_row(const AttnArgs& a, const Sequence& s, int kv_head, int r,
                                           int quad, float4 acc, float sum, float top) {
-  const int64_t t = s.t.first + r / a.group;
-  const int head = kv_head * a.group + r % a.group;
-  const Finish f = finish_begin<D, false>(a, kv_head, (int64_t)s.t.first * a.group + r, top, sum);
+  const int i = token_of(a, r), head = kv_head * a.group + r - i * a.group;
+  const int64_t t = s.first + i;
+  const Finish f = finish_begin<D, false>(a, kv_head, (int64_t)s.first * a.group + r, top, sum);
   finish_quad<D, false>(a, f, t, head, quad, acc);
   if (a.lse && quad == 0) a.lse[t * a.q_heads + head] = f.lse;
 }
@@ -212,15 +212,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int swizzle = lane & 7;
   for (bool first = true; w.next(a, first); first = false) {
     const Sequence& s = w.s;
-    const int rows = s.t.taken * a.group;
+    const int rows = s.taken * a.group;
     uint32_t q[D / 16][4];
     int limit[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = g + 8 * i;
       const bool live = r < rows;
-      const int token = r / a.group, head = w.head * a.group + r % a.group;
-      const uint16_t* src = a.q + (int64_t)(s.t.first + token) * a.ldq + head * D + 2 * c;
+      const int token = token_of(a, r), head = w.head * a.group + r - token * a.group;
+      const uint16_t* src = a.q + (int64_t)(s.first + token) * a.ldq + head * D + 2 * c;
       limit[i] = live ? limit_of(s, token) : 0;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float from = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float u = exp2_approx(x[n][2 * i] - from), v = exp2_approx(x[n][2 * i + 1] - from);
+            const float u = exp2_approx(x[n][2 * i] - from);
+            const float v = exp2_approx(x[n][2 * i + 1] - from);
             l[i] += u + v;
             p[2 * n + i] = pack_bf16(u, v);
           }
@@ -432,8 +433,8 @@ cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap&
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(attention_few_kernel<D>, dim3(g.num_sms < kAttnBlocks ? g.num_sms : kAttnBlocks),
-                    dim3(kThreads), smem, st, g.args, k, v);
+  const int blocks = g.num_sms < kAttnBlocks ? g.num_sms : kAttnBlocks;
+  return launch_pdl(attention_few_kernel<D>, dim3(blocks), dim3(kThreads), smem, st, g.args, k, v);
 }
 
 }  // namespace

@@ -35,20 +35,22 @@ static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the launch's registers"
 
 template <int D>
 struct Sizes {
-  static constexpr int kTileBytes = kTileRows * D * 2;      // of queries, keys or values
-  static constexpr int kStages = (229376 - 2 * kTileBytes) / kTileBytes;
+  static constexpr int kTileBytes = kTileRows * D * 2;   // of keys or values, half the queries
   static constexpr int kHalf = kTileRows * 128;             // 64 columns of a tile
+  static constexpr int kStage = 8 * 4096;                   // 32 rows of 128 bytes a warp
+  static constexpr int kStages = (229376 - kStage - 2 * kTileBytes) / kTileBytes;
 };
 
 template <int D>
 struct Smem {
-  uint8_t q[2][Sizes<D>::kTileBytes];
+  uint8_t q[2 * Sizes<D>::kTileBytes];          // [D / 64][256 rows][128 bytes]
   uint8_t ring[Sizes<D>::kStages][Sizes<D>::kTileBytes];
+  uint8_t stage[8][4096];
   int64_t scan[kThreads / 32];
   uint64_t full[Sizes<D>::kStages], empty[Sizes<D>::kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
-  int64_t start_left, start_at;
-  int start_seq, start_head, start_rt, start_tile;
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], done;
+  int64_t start_at;
+  int start_left, start_seq, start_head, start_rt, start_tile;
   int kend;                                     // SHARED: keys that some row sees
   uint32_t tmem;
   int abort;
@@ -136,48 +138,68 @@ __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uin
 
 // ---- the line ----
 
-// Row tiles (of 256 rows) of a sequence, and the keys that row tile rt's last row sees.
-__device__ __forceinline__ int row_tiles(const AttnArgs& a, const Sequence& s) {
-  return (int)(((int64_t)s.t.taken * a.group + kAttnRows - 1) / kAttnRows);
+// sum over i in [0, n) of floor((a i + b) / m), by Euclid's steps on (m, a).
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    sum += (int64_t)n * (n - 1) / 2 * (a / m) + (int64_t)n * (b / m);
+    a %= m;
+    b %= m;
+    const uint32_t top = a * n + b;
+    n = top / m;
+    b = top % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
 }
-__device__ __forceinline__ int kend_of(const AttnArgs& a, const Sequence& s, int rt) {
-  const int64_t rows = min((int64_t)(rt + 1) * kAttnRows, (int64_t)s.t.taken * a.group);
-  return limit_of(s, (int)((rows - 1) / a.group));
+
+// An item has whole tokens, `step` of them (256 / group) but for a sequence's last.
+__device__ __forceinline__ int key_tiles(int keys) {
+  return max(1, (keys + kAttnTile - 1) / kAttnTile);
 }
-__device__ __forceinline__ int key_tiles(int kstart, int kend) {
-  return max(1, (kend - kstart + kAttnTile - 1) / kAttnTile);
+// Keys from kstart on that row tile rt's last row sees (below 1: none).
+__device__ __forceinline__ int keys_of(const AttnArgs& a, const Sequence& s, int rt, int step) {
+  return s.base - a.kstart + min((rt + 1) * step, s.taken);
 }
-// Tiles of a sequence's items of one head.
-__device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, const Sequence& s) {
+// Tiles of a sequence's first k row tiles of one head.
+__device__ __forceinline__ int64_t tiles_before(const AttnArgs& a, const Sequence& s, int k,
+                                                int step) {
+  const int rts = (s.taken + step - 1) / step;
   int64_t n = 0;
-  const int rts = row_tiles(a, s);
-  for (int rt = 0; rt < rts; ++rt) n += key_tiles(a.kstart, kend_of(a, s, rt));
+  if (k == rts && k > 0) {                  // the last has its own number of tokens
+    --k;
+    n = key_tiles(keys_of(a, s, k, step));
+  }
+  const int unseen = a.kstart - s.base;     // new tokens that see no key from kstart on
+  const int none = min(k, max(0, unseen / step));
+  n += none;
+  if (k > none)
+    n += floor_sum(k - none, kAttnTile, step,
+                   (uint32_t)((none + 1) * step - unseen + kAttnTile - 1));
   return n;
 }
 
-// An item: rows [row0, row0 + rows) of a kv head, counted from token `token0`'s first, and the
-// keys [k0, kend) of tiles [first, last) out of `tiles`, at position `at` of the line.
+// An item: `rows` rows, of the tokens from `token` on, and of the keys [key0, kend) in `tiles`
+// tiles those of tiles [first, last); it is at position `at` of the line.
 template <bool SHARED>
 struct Walk {
-  int64_t left, at;
-  int seq, head, rt, tile;
+  int64_t at;
+  int left, seq, head, rt, tile;
+  int step, rts;
   Sequence s;
-  int rts, kend, tiles, first, last, rows;
-  __device__ __forceinline__ void measure(const AttnArgs& a) {
-    const int64_t all = SHARED ? (int64_t)a.batch.tokens * a.group : (int64_t)s.t.taken * a.group;
-    rows = (int)min((int64_t)kAttnRows, all - (int64_t)rt * kAttnRows);
+  int token, rows, kend, tiles, first, last;
+  __device__ __forceinline__ void enter(const AttnArgs& a) {     // a sequence
     if (!SHARED) {
-      kend = kend_of(a, s, rt);
-      tiles = key_tiles(a.kstart, kend);
+      s = sequence(a, seq);
+      rts = (s.taken + step - 1) / step;
     }
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, bool begin) {
     if (left <= 0) return false;
     if (begin) {
-      if (!SHARED) {
-        s = sequence(a, seq);
-        rts = row_tiles(a, s);
-      }
+      enter(a);
     } else {
       at += tiles;
       tile = 0;
@@ -186,58 +208,68 @@ struct Walk {
         if (++head == a.kv_heads && !SHARED) {
           head = 0;
           do {
-            s = sequence(a, ++seq);
-            rts = row_tiles(a, s);
+            ++seq;
+            enter(a);
           } while (rts == 0);
         }
       }
     }
-    measure(a);
+    const int tokens = min(step, (SHARED ? a.batch.tokens : s.taken) - rt * step);
+    token = rt * step + (SHARED ? 0 : s.first);
+    rows = tokens * a.group;
+    if (!SHARED) {
+      const int keys = keys_of(a, s, rt, step);
+      kend = a.kstart + keys;
+      tiles = key_tiles(keys);
+    }
     first = tile;
-    last = (int)min((int64_t)tiles, tile + left);
+    last = min(tiles, tile + left);
     left -= last - first;
     return true;
   }
   // Tiles of [first, last) that hold a key; the others are behind the last one.
-  __device__ __forceinline__ int busy(int kstart) const {
-    const int from = SHARED ? 0 : kstart;
-    const int n = kend > from ? (kend - from + kAttnTile - 1) / kAttnTile : 0;
+  __device__ __forceinline__ int busy(int key0) const {
+    const int n = kend > key0 ? (kend - key0 + kAttnTile - 1) / kAttnTile : 0;
     return max(0, min(last, n) - first);
   }
 };
 
-// Where the row r of an item lies: its token (-1: none) and head, and the keys it sees.
-struct Row {
-  int token, head, limit;
-  int64_t index;      // among the kv head's rows of all tokens
-};
+// Keys that row r of an item sees; all of its keys where the row is none.
 template <bool SHARED>
-__device__ __forceinline__ Row row_of(const AttnArgs& a, const Walk<SHARED>& w, int r) {
-  Row x = {-1, 0, w.kend, 0};
-  if (r >= w.rows) return x;
-  const int R = w.rt * kAttnRows + r;                 // (tokens * heads: below 2^30)
-  const int i = R / a.group;
-  x.head = w.head * a.group + R % a.group;
-  if (SHARED) {
-    const int b = sequence_of(a.batch, i);
-    if (b < 0) return x;
-    const Sequence s = sequence(a, b);
-    const int at = i - s.t.first;
-    if (at < 0 || at >= s.t.taken) return x;
-    x.token = i;
-    x.limit = min(limit_of(s, at), w.kend);
-    x.index = R;
-  } else {
-    x.token = w.s.t.first + i;
-    x.limit = limit_of(w.s, i);
-    x.index = (int64_t)w.s.t.first * a.group + R;
+__device__ __forceinline__ int row_limit(const AttnArgs& a, const Walk<SHARED>& w, int r) {
+  if (r >= w.rows) return w.kend;
+  const int i = token_of(a, r);
+  if (!SHARED) return limit_of(w.s, w.rt * w.step + i);
+  const int b = sequence_of(a.batch, w.token + i);
+  if (b < 0) return w.kend;
+  const Sequence s = sequence(a, b);
+  const int at = w.token + i - s.first;
+  return at < 0 || at >= s.taken ? w.kend : min(limit_of(s, at), w.kend);
+}
+
+// Rows of 128 bytes (8 pieces) or 64 (4 pieces) of a warp's 32 rows through its part of shared
+// memory, so that global memory sees whole rows: a lane's own row on one side, neighbouring
+// lanes neighbouring pieces of a row on the other.
+template <int PIECES>
+__device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
+  const int turn = PIECES == 8 ? row & 7 : (row >> 1) & 3;
+  return reinterpret_cast<uint4*>(stage + row * (PIECES * 16) + ((piece ^ turn) << 4));
+}
+template <int PIECES, typename F>
+__device__ __forceinline__ void each_piece(int rows, F f) {
+  constexpr int AT_ONCE = 32 / PIECES;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 32 / AT_ONCE; ++k) {
+    const int row = k * AT_ONCE + lane / PIECES;
+    if (row < rows) f(row, lane % PIECES);
   }
-  return x;
 }
 
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tile_kernel(const __grid_constant__ AttnArgs a,
+                          const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap) {
   constexpr int STAGES = Sizes<D>::kStages;
@@ -250,16 +282,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sm.full[i], 1);
       ptx::mbar_init(&sm.empty[i], 1);
     }
+    ptx::mbar_init(&sm.q_full, 1);
+    ptx::mbar_init(&sm.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(&sm.q_full[t], 4);
       ptx::mbar_init(&sm.s_full[t], 1);
-      ptx::mbar_init(&sm.p_full[t], 4);
+      ptx::mbar_init(&sm.p_full[t][0], 4);
+      ptx::mbar_init(&sm.p_full[t][1], 4);
       ptx::mbar_init(&sm.o_full[t], 1);
     }
     ptx::mbar_init(&sm.done, 1);
     ptx::fence_mbar_init();
     sm.abort = 0;
     sm.kend = 0;
+    sm.start_left = 0;
+    ptx::prefetch_tmap(&qmap);
     ptx::prefetch_tmap(&kmap);
     ptx::prefetch_tmap(&vmap);
   }
@@ -274,12 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::pdl_launch_dependents();
 
   // The block's range of the line.
+  const int step = kAttnRows / a.group;
+  const int shared_rts = (a.batch.tokens + step - 1) / step;
+  const int shared_tiles = (a.kstart + kAttnTile - 1) / kAttnTile;
   int64_t line = 0;
   int N;
   if (SHARED) {
-    const int rts = (int)(((int64_t)a.batch.tokens * a.group + kAttnRows - 1) / kAttnRows);
-    const int tiles = (a.kstart + kAttnTile - 1) / kAttnTile;
-    line = (int64_t)a.kv_heads * rts * tiles;
+    line = (int64_t)a.kv_heads * shared_rts * shared_tiles;
     N = (int)min((int64_t)gridDim.x, line);
     int most = 0;
     for (int b = threadIdx.x; b < a.batch.batch; b += kThreads)
@@ -287,19 +324,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicMax(&sm.kend, min(most, a.kstart));
     if (threadIdx.x == 0 && (int)blockIdx.x < N) {
       const int64_t begin = range_start(line, N, blockIdx.x);
-      const int64_t item = begin / tiles;
-      sm.start_tile = (int)(begin % tiles);
-      sm.start_rt = (int)(item % rts);
-      sm.start_head = (int)(item / rts);
-      sm.start_at = item * tiles;
+      const int item = (int)(begin / shared_tiles);
+      sm.start_at = (int64_t)item * shared_tiles;
+      sm.start_tile = (int)(begin - sm.start_at);
+      sm.start_rt = item % shared_rts;
+      sm.start_head = item / shared_rts;
       sm.start_seq = 0;
-      sm.start_left = range_start(line, N, blockIdx.x + 1) - begin;
+      sm.start_left = (int)(range_start(line, N, blockIdx.x + 1) - begin);
     }
   } else {
     const int per = (a.batch.batch + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, a.batch.batch), b1 = min(b0 + per, a.batch.batch);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a, sequence(a, b));
+    for (int b = b0; b < b1; ++b) {
+      const Sequence s = sequence(a, b);
+      mine += tiles_before(a, s, (s.taken + step - 1) / step, step);
+    }
     int64_t at = block_exclusive_sum(mine, sm.scan, &line) * a.kv_heads;
     line *= a.kv_heads;
     N = (int)min((int64_t)gridDim.x, line);
@@ -308,41 +348,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (begin >= at && begin < at + mine * a.kv_heads) {
         int b = b0;
         int64_t n;
+        Sequence s;
         for (;; ++b) {
-          n = tiles_of(a, sequence(a, b));
+          s = sequence(a, b);
+          n = tiles_before(a, s, (s.taken + step - 1) / step, step);
           if (begin < at + n * a.kv_heads) break;
           at += n * a.kv_heads;
         }
-        const Sequence s = sequence(a, b);
-        int head = (int)((begin - at) / n), rt = 0;
+        const int head = (int)((begin - at) / n);
         at += head * n;
-        for (;; ++rt) {
-          const int t = key_tiles(a.kstart, kend_of(a, s, rt));
-          if (begin < at + t) break;
-          at += t;
+        int lo = 0, hi = (s.taken + step - 1) / step;      // the row tile that holds begin
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (at + tiles_before(a, s, mid, step) <= begin) lo = mid; else hi = mid;
         }
+        at += tiles_before(a, s, lo, step);
         sm.start_seq = b;
         sm.start_head = head;
-        sm.start_rt = rt;
+        sm.start_rt = lo;
         sm.start_tile = (int)(begin - at);
         sm.start_at = at;
-        sm.start_left = range_start(line, N, blockIdx.x + 1) - begin;
+        sm.start_left = (int)(range_start(line, N, blockIdx.x + 1) - begin);
       }
     }
   }
   if (threadIdx.x == 0) a.cuts[blockIdx.x].to = -1;      // no item begins here and goes on
   __syncthreads();
-  const bool working = (int)blockIdx.x < N;
   Walk<SHARED> w = {};
-  w.left = working ? sm.start_left : 0;
+  w.left = sm.start_left;
   w.at = sm.start_at;
   w.seq = sm.start_seq;
   w.head = sm.start_head;
   w.rt = sm.start_rt;
   w.tile = sm.start_tile;
+  w.step = step;
   if (SHARED) {
-    w.rts = (int)(((int64_t)a.batch.tokens * a.group + kAttnRows - 1) / kAttnRows);
-    w.tiles = (a.kstart + kAttnTile - 1) / kAttnTile;
+    w.rts = shared_rts;
+    w.tiles = shared_tiles;
     w.kend = sm.kend;
   }
   const int key0 = SHARED ? 0 : a.kstart;
@@ -351,21 +393,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kLoader) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    int stage = 0;
+    uint32_t phase = 0, q_phase = 0;
+    auto advance = [&] {
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    };
     if (warp == kLoader) {
-      // ---- loads: keys and values of a tile, one stage each ----
-      int stage = 0;
-      uint32_t phase = 0;
-      auto advance = [&] {
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-      };
+      // ---- loads: an item's queries; keys and values of a tile, one stage each ----
       Pages pages;
       int seq = -1;
       for (bool first = true; w.next(a, first); first = false) {
+        const int n = w.busy(key0);
+        if (n == 0) continue;
         if (w.seq != seq) pages.start(a, seq = w.seq);
-        const int n = w.busy(a.kstart);
+        ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs);
+        q_phase ^= 1;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&sm.q_full, step * a.group * 2 * D);
+          for (int h = 0; h < D / 64; ++h)
+            ptx::tma_load_3d(sm.q + h * 2 * Sizes<D>::kHalf, &qmap, h * 64, w.head * a.group,
+                             w.token, &sm.q_full, ptx::policy_evict_first());
+        }
+        __syncwarp();
         for (int t = w.first; t < w.first + n; ++t) {
           const int k0 = key0 + t * kAttnTile;
           const int keys = min(kAttnTile, w.kend - k0);
@@ -380,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // After a wait that ran out, copies may still be in flight: the block stays for them.
       if (*abort) {
         int never = 0;
+        ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
         for (int i = 0; i < STAGES; ++i) {
           ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
           advance();
@@ -387,42 +440,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kIssuer) {
       // ---- products ----
-      int stage = 0;
-      uint32_t phase = 0, q_phase = 0, q1_phase = 0, p_phase[2] = {0, 0};
-      auto advance = [&] {
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-      };
+      uint32_t p_phase[2] = {0, 0};
       const uint32_t q_addr = ptx::smem_addr(sm.q), ring = ptx::smem_addr(sm.ring);
       const uint32_t id_s = idesc_bf16(kAttnTile, false), id_o = idesc_bf16(D, true);
       auto scores = [&](int t, uint32_t k_addr) {
         if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32;
-            mma_ss(tmem + kColS + t * 128, ptx::desc_sw128(q_addr + t * Sizes<D>::kTileBytes + off),
-                   ptx::desc_sw128(k_addr + off), id_s, k > 0);
+            const uint32_t q_off = (k >> 2) * 2 * Sizes<D>::kHalf + t * Sizes<D>::kHalf;
+            mma_ss(tmem + kColS + t * 128, ptx::desc_sw128(q_addr + q_off + (k & 3) * 32),
+                   ptx::desc_sw128(k_addr + (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32), id_s,
+                   k > 0);
           }
           ptx::tc_commit(&sm.s_full[t]);
         }
         __syncwarp();
       };
       for (bool first = true; w.next(a, first); first = false) {
-        const int n = w.busy(a.kstart);
+        const int n = w.busy(key0);
         if (n == 0) continue;
         const int active = w.rows > kTileRows ? 2 : 1;
-        ptx::mbar_wait(&sm.q_full[0], q_phase, abort, kAttnWaitNs);
+        ptx::mbar_wait(&sm.q_full, q_phase, abort, kAttnWaitNs);
         q_phase ^= 1;
-        if (active == 2) {
-          ptx::mbar_wait(&sm.q_full[1], q1_phase, abort, kAttnWaitNs);
-          q1_phase ^= 1;
-        }
         ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
         ptx::tc_fence_after();
         for (int t = 0; t < active; ++t) scores(t, ring + stage * Sizes<D>::kTileBytes);
-        if (ptx::elect_one()) ptx::tc_commit(&sm.empty[stage]);
+        if (ptx::elect_one()) {
+          ptx::tc_commit(&sm.empty[stage]);
+          if (n == 1) ptx::tc_commit(&sm.q_empty);
+        }
         __syncwarp();
         advance();
         for (int i = 0; i < n; ++i) {
@@ -433,16 +479,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int steps = (keys + 15) / 16;
           const uint32_t v_addr = ring + v_stage * Sizes<D>::kTileBytes;
           for (int t = 0; t < active; ++t) {
-            ptx::mbar_wait(&sm.p_full[t], p_phase[t], abort, kAttnWaitNs);
-            p_phase[t] ^= 1;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              for (int k = 0; k < steps; ++k)
-                mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + k * 8,
-                       desc_rows(v_addr + k * 2048, Sizes<D>::kHalf), id_o, i > 0 || k > 0);
-              if (i + 1 == n) ptx::tc_commit(&sm.o_full[t]);
+            // P comes in halves: the first one's products run while the second is made
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ptx::mbar_wait(&sm.p_full[t][h], p_phase[t], abort, kAttnWaitNs);
+              ptx::tc_fence_after();
+              if (ptx::elect_one()) {
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                  if (k < steps)
+                    mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + k * 8,
+                           desc_rows(v_addr + k * 2048, Sizes<D>::kHalf), id_o, i > 0 || k > 0);
+                if (h == 1 && i + 1 == n) ptx::tc_commit(&sm.o_full[t]);
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            p_phase[t] ^= 1;
             if (i + 1 < n) {
               if (t == 0) {
                 ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
@@ -454,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ptx::elect_one()) {
             ptx::tc_commit(&sm.empty[v_stage]);
             if (i + 1 < n) ptx::tc_commit(&sm.empty[stage]);
+            if (i + 2 == n) ptx::tc_commit(&sm.q_empty);
           }
           __syncwarp();
           if (i + 1 < n) advance();
@@ -474,33 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_phase = 0, o_phase = 0;
     int loads = 0;                                         // stages that earlier items took
     for (bool first = true; w.next(a, first); first = false) {
-      const int n = w.busy(a.kstart);
+      const int n = w.busy(key0);
       const int v0 = loads;
       loads += 2 * n;
       if (t == 1 && w.rows <= kTileRows) continue;
-      const Row row = row_of<SHARED>(a, w, r);
-      if (n > 0) {
-        // queries: 16-byte pieces, neighbouring lanes neighbouring pieces of a row
-        constexpr int PIECES = D / 8;
-        const int in = threadIdx.x & 127;
-#pragma unroll 4
-        for (int i = in; i < kTileRows * PIECES; i += 128) {
-          const int qr = i / PIECES, piece = i % PIECES;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          const int rr = t * kTileRows + qr;
-          if (rr < w.rows) {
-            const int R = w.rt * kAttnRows + rr;
-            const int64_t token = R / a.group + (SHARED ? 0 : w.s.t.first);
-            const int head = w.head * a.group + R % a.group;
-            v = *reinterpret_cast<const uint4*>(a.q + token * a.ldq + head * D + piece * 8);
-          }
-          *reinterpret_cast<uint4*>(sm.q[t] + (piece >> 3) * Sizes<D>::kHalf + qr * 128 +
-                                    (((piece & 7) ^ (qr & 7)) << 4)) = v;
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.q_full[t]);
-      }
+      const int limit = row_limit(a, w, r);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
         const int k0 = key0 + (w.first + i) * kAttnTile;
@@ -512,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j) tmem_ld32_issue(s_col + j * 32, x + j * 32);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_wait_ld32(x + j * 32);
-        if (__any_sync(0xFFFFFFFFu, k0 + kAttnTile > row.limit)) {
-          const int seen = row.limit - k0;
+        if (__any_sync(0xFFFFFFFFu, k0 + kAttnTile > limit)) {
+          const int seen = limit - k0;
 #pragma unroll
           for (int j = 0; j < 128; ++j)
             if (j >= seen) x[j] = 0xFF800000u;
@@ -540,6 +571,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (t == 0 && w.kend - k0 < kAttnTile && (w.kend - k0) % 16 != 0) {
+          // values behind the last key may be anything, and 0 times them must be 0: the rows
+          // that share the last key's sixteen are cleared
+          const int at = v0 + 2 * i + 1, stage = at % STAGES;
+          ptx::mbar_wait(&sm.full[stage], (at / STAGES) & 1, abort, kAttnWaitNs);
+          const int from_row = w.kend - k0, to_row = (from_row + 15) / 16 * 16;
+          for (int e = threadIdx.x; e < (to_row - from_row) * (D / 8); e += 128) {
+            const int vr = from_row + e / (D / 8), piece = e % (D / 8);
+            *reinterpret_cast<uint4*>(sm.ring[stage] + (piece >> 3) * Sizes<D>::kHalf + vr * 128 +
+                                      ((piece & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+        }
         const float from = m == -INFINITY ? 0.f : m;
         const uint64_t scale2 = pair(a.scale_log2, a.scale_log2), from2 = pair(-from, -from);
         uint64_t sum[2] = {0, 0};
@@ -557,48 +601,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[e] = pack_bf16(u, v);
           }
           ptx::tmem_st16(s_col + j * 16, p);
+          if (j & 1) {
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][j >> 1]);
+          }
         }
         sum[0] = add2(sum[0], sum[1]);
         l += lo_of(sum[0]) + hi_of(sum[0]);
-        if (t == 0 && (w.kend - k0) % 16 != 0 && w.kend - k0 < kAttnTile) {
-          // values behind the last key may be anything, and 0 times them must be 0: the rows
-          // that share the last key's sixteen are cleared
-          const int at = v0 + 2 * i + 1, stage = at % STAGES;
-          ptx::mbar_wait(&sm.full[stage], (at / STAGES) & 1, abort, kAttnWaitNs);
-          const int from_row = w.kend - k0, to_row = (from_row + 15) / 16 * 16;
-          for (int e = threadIdx.x; e < (to_row - from_row) * (D / 8); e += 128) {
-            const int vr = from_row + e / (D / 8), piece = e % (D / 8);
-            *reinterpret_cast<uint4*>(sm.ring[stage] + (piece >> 3) * Sizes<D>::kHalf + vr * 128 +
-                                      ((piece & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          ptx::fence_proxy_async_smem();
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.p_full[t]);
       }
 
       // ---- the item's end ----
-      if (n > 0) {
-        ptx::mbar_wait(&sm.o_full[t], o_phase, abort, kAttnWaitNs);
-        o_phase ^= 1;
-        ptx::tc_fence_after();
-      }
       const bool whole = w.first == 0 && w.last == w.tiles;
       const int slot = 2 * blockIdx.x + (w.first == 0);
       if (w.first == 0 && !whole && r == 0) {
         AttnCut cut;
-        cut.first = SHARED ? 0 : w.s.t.first;
-        cut.rt = w.rt;
+        cut.first = w.token;
         cut.rows = w.rows;
         cut.head = w.head;
         cut.from = blockIdx.x;
         cut.to = block_of(line, N, w.at + w.tiles - 1);
         a.cuts[blockIdx.x] = cut;
       }
-      Finish fin;
-      if (whole && row.token >= 0) fin = finish_begin<D, SHARED>(a, w.head, row.index, m, l);
+      const int row0 = warp * 32, live = w.rows - row0;     // the warp's rows of the item
+      const int64_t index = (int64_t)w.token * a.group + r;
+      Finish fin = {};
+      if (whole && r < w.rows) fin = finish_begin<D, SHARED>(a, w.head, index, m, l);
+      float* keep = SHARED && whole
+                        ? a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
+                                            (int64_t)w.token * a.group + row0) * D
+                        : a.parts + ((int64_t)slot * kAttnRows + row0) * D;
+      const float* other = a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
+                                             (int64_t)w.token * a.group + row0) * D;
+      uint8_t* stage = sm.stage[warp];
+      if (n > 0) {
+        ptx::mbar_wait(&sm.o_full[t], o_phase, abort, kAttnWaitNs);
+        o_phase ^= 1;
+        ptx::tc_fence_after();
+      }
 #pragma unroll 1
       for (int j = 0; j < D; j += 32) {
         uint32_t o[32];
@@ -609,26 +650,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (r < w.rows && !whole) {
-          float4* dst =
-              reinterpret_cast<float4*>(a.parts + ((int64_t)slot * kAttnRows + r) * D + j);
+        if (SHARED || !whole) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-        } else if (whole && row.token >= 0) {
+            *staged<8>(stage, lane, e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                                                    o[4 * e + 3]);
+          __syncwarp();
+          each_piece<8>(live, [&](int row, int piece) {
+            *reinterpret_cast<uint4*>(keep + (int64_t)row * D + j + piece * 4) =
+                *staged<8>(stage, row, piece);
+          });
+        } else {
+          if (a.kstart > 0) {
+            each_piece<8>(live, [&](int row, int piece) {
+              *staged<8>(stage, row, piece) =
+                  *reinterpret_cast<const uint4*>(other + (int64_t)row * D + j + piece * 4);
+            });
+            __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            finish_quad<D, SHARED>(a, fin, row.token, row.head, j / 4 + e,
-                                   make_float4(__uint_as_float(o[4 * e]),
-                                               __uint_as_float(o[4 * e + 1]),
-                                               __uint_as_float(o[4 * e + 2]),
-                                               __uint_as_float(o[4 * e + 3])));
+            for (int e = 0; e < 8; ++e) {
+              const uint4 y = *staged<8>(stage, lane, e);
+              const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                o[4 * e + c] = __float_as_uint(__uint_as_float(o[4 * e + c]) * fin.mine +
+                                               __uint_as_float(z[c]) * fin.theirs);
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t z[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              z[c] = pack_bf16(__uint_as_float(o[8 * e + 2 * c]) * fin.inv,
+                               __uint_as_float(o[8 * e + 2 * c + 1]) * fin.inv);
+            *staged<4>(stage, lane, e) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+          __syncwarp();
+          each_piece<4>(live, [&](int row, int piece) {
+            const int i = token_of(a, row0 + row);
+            const int head = w.head * a.group + row0 + row - i * a.group;
+            *reinterpret_cast<uint4*>(a.out + (int64_t)(w.token + i) * a.ldo + head * D + j +
+                                      piece * 8) = *staged<4>(stage, row, piece);
+          });
         }
+        __syncwarp();
       }
       if (r < w.rows && !whole) a.part_stats[slot * kAttnRows + r] = make_float2(m, l);
-      if (whole && row.token >= 0 && !SHARED && a.lse)
-        a.lse[(int64_t)row.token * a.q_heads + row.head] = fin.lse;
+      if (r < w.rows && whole && !SHARED && a.lse) {
+        const int i = token_of(a, r);
+        a.lse[(int64_t)(w.token + i) * a.q_heads + w.head * a.group + r - i * a.group] = fin.lse;
+      }
       ptx::tc_fence_before();
     }
   }
@@ -649,8 +722,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   const int quad = threadIdx.x % (D / 4);
   const int r = blockIdx.y * kJoinRows + threadIdx.x / (D / 4);
   if (cut.to < 0 || r >= cut.rows) return;
-  const int64_t R = (int64_t)cut.rt * kAttnRows + r;
-  const int token = cut.first + (int)(R / a.group);
+  const int i = token_of(a, r), head = cut.head * a.group + r - i * a.group;
+  const int64_t token = cut.first + i;
   auto part = [&](int b) { return (int64_t)(2 * b + (b == cut.from)) * kAttnRows + r; };
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 8
@@ -665,11 +738,10 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
     sum += st.y * f;
     acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
   }
-  const int head = cut.head * a.group + (int)(R % a.group);
   const Finish fin =
-      finish_begin<D, SHARED>(a, cut.head, (int64_t)cut.first * a.group + R, top, sum);
+      finish_begin<D, SHARED>(a, cut.head, (int64_t)cut.first * a.group + r, top, sum);
   finish_quad<D, SHARED>(a, fin, token, head, quad, acc);
-  if (!SHARED && a.lse && quad == 0) a.lse[(int64_t)token * a.q_heads + head] = fin.lse;
+  if (!SHARED && a.lse && quad == 0) a.lse[token * a.q_heads + head] = fin.lse;
 }
 
 template <int D, bool SHARED>
@@ -683,16 +755,19 @@ cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap&
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
+  const AttnArgs& a = g.args;
+  CUtensorMap q;
+  e = make_tmap_heads(&q, a.q, D, a.q_heads, a.batch.tokens, a.ldq, a.group, kAttnRows / a.group);
+  if (e != cudaSuccess) return e;
   const int blocks = g.num_sms < kAttnBlocks ? g.num_sms : kAttnBlocks;
-  e = launch_pdl(attention_tile_kernel<D, SHARED>, dim3(blocks), dim3(kThreads), smem, st, g.args,
+  e = launch_pdl(attention_tile_kernel<D, SHARED>, dim3(blocks), dim3(kThreads), smem, st, a, q,
                  k, v);
   if (e != cudaSuccess) return e;
-  const int64_t rows =
-      (int64_t)(SHARED ? g.args.batch.tokens : g.args.batch.max_new) * g.args.group;
+  const int64_t rows = (int64_t)(SHARED ? a.batch.tokens : a.batch.max_new) * a.group;
   const int most = (int)(rows < kAttnRows ? rows : kAttnRows);
   return launch_pdl(attention_join_kernel<D, SHARED>,
                     dim3(blocks, (most + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * D / 4), 0,
-                    st, g.args);
+                    st, a);
 }
 
 }  // namespace

@@ -406,10 +406,10 @@ cudaError_t launch_kv_append(const RopeArgs& a, cudaStream_t st);
 // Attention over a paged cache (attention.cu).
 constexpr int kAttnBlocks = 160;   // most blocks of a kernel
 constexpr int kAttnRows = 256;     // most rows of an item
-// The item of a tile kernel that begins in a block's range and goes on behind it: rows from
-// row tile rt of the tokens from `first` on, in the parts of blocks [from, to]; to < 0: none.
+// The item of a tile kernel that begins in a block's range and goes on behind it: rows of the
+// tokens from `first` on, in the parts of blocks [from, to]; to < 0: none.
 struct AttnCut {
-  int first, rt, rows, head, from, to;
+  int first, rows, head, from, to;
 };
 struct AttnArgs {
   const uint16_t* q;               // [tokens, q_heads, head_dim], stride ldq
@@ -421,6 +421,7 @@ struct AttnArgs {
   float scale_log2;                // scale * log2(e)
   KvBatch batch;
   int q_heads, kv_heads, group, num_pages, page_shift;
+  int group_inv;                   // ceil(2^16 / group)
   int32_t* flags;
   int kstart;                      // keys below it are the shared prefix's, computed apart
   // workspace: parts of cut items, two a block, and a counter a block (zero between calls)

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       if (seq < 0) continue;
       const NewTokens nt = new_tokens(a.batch, seq);
       const int at = (int)t - nt.first;
-      pos = a.batch.seq_lens[seq] - nt.n + at;
+      pos = max(a.batch.seq_lens[seq], 0) - nt.n + at;
       if (at < 0 || at >= nt.taken || pos < 0) continue;
       if (!is_q) {
         const int slot = pos >> a.page_shift;

@@ -97,4 +97,22 @@ inline cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t D, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// bf16 heads [tokens, heads, D] with `ld` elements from token to token, read in boxes of 64
+// elements x box_heads x box_tokens that land as rows of 128 bytes, 128-byte swizzle.
+inline cudaError_t make_tmap_heads(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads,
+                                   uint64_t tokens, uint64_t ld, uint32_t box_heads,
+                                   uint32_t box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {D, heads, tokens};
+  const cuuint64_t strides[2] = {2 * D, 2 * ld};
+  const cuuint32_t box[3] = {64, box_heads, box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace mxmoe

@@ -483,8 +483,8 @@ MXMOE_API moe_status moe_rope(const moe_rope_dims *dims, const void *table_dev, 
  * The cache is two bf16 arrays [num_pages, kv_heads, page_size, head_dim], contiguous and
  * 128-byte aligned: the rows of one page and head lie together.  A sequence's token p is row
  * p % page_size of the page that entry p / page_size of its page table row names.
- * Ranges: head_dim 64 or 128; q_heads a multiple of kv_heads, at most 1024; page_size a power of
- * two in [16, 256]; num_pages >= 1 with num_pages * kv_heads * page_size < 2^31; max_tokens (of
+ * Ranges: head_dim 64 or 128; q_heads a multiple of kv_heads, at most 1024 and 256 times it;
+ * page_size a power of two in [16, 256]; num_pages >= 1 with num_pages * kv_heads * page_size < 2^31; max_tokens (of
  * one call) in [1, 2^20]; 0 <= max_shared_tokens <= max_tokens. */
 typedef struct moe_attention_dims {
     int32_t q_heads;
@@ -498,7 +498,8 @@ typedef struct moe_attention_dims {
 
 /* One step's batch: `batch` sequences (1 .. 4096) with `tokens` new tokens (0 .. max_tokens),
  * packed sequence after sequence.
- *   seq_lens_dev  int32 [batch]      tokens of each sequence, the new ones among them
+ *   seq_lens_dev  int32 [batch]      tokens of each sequence, the new ones among them; at most
+ *                 2^30
  *   cu_new_dev    int32 [batch + 1]  first new token of each sequence and, last, their number;
  *                                    NULL: tokens / batch each (a whole number)
  *   pages_dev     int32 [batch, pages_ld]  page tables, at least 1 entry a row
@@ -509,8 +510,8 @@ typedef struct moe_attention_dims {
  *                 must name them; other rows' entries for them are not read.
  * New token i of a sequence of length L with n new ones is at position p = L - n + i: it sees
  * the keys 0 .. p.  Positions below 0 (a padded batch: length 0, one token) see nothing: zeros,
- * lse minus infinity.  Rows of q, k, v and the outputs behind cu_new_dev's last entry are
- * neither read nor written.  Values outside their ranges in these arrays are cut to them or
+ * lse minus infinity.  Rows of q, k and v behind cu_new_dev's last entry do not matter,
+ * and the outputs' are not written.  Values outside their ranges in these arrays are cut to them or
  * raise MOE_ERR_PAGE at the next moe_attention_check; nothing outside the given buffers is
  * accessed. */
 typedef struct moe_kv_batch {
