@@ -26,7 +26,8 @@ namespace mxmoe {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kLoader = 8, kIssuer = 9;         // warps; eight before them hold a row a thread
+// Warps: eight with a row a thread, one that loads, one a row tile that issues its products.
+constexpr int kLoader = 8, kIssuer = 9;
 constexpr int kThreads = 384;                   // whole warpgroups, as register shares go by
 // 384 threads start with 168 registers: the softmax's two warpgroups take 208, the third 88
 // (2 x 208 + 88 = 3 x 168).
@@ -135,6 +136,25 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// 64 scores to terms exp2(x scale - from), packed, and their sums.
+__device__ __forceinline__ void terms(uint32_t (&p)[32], const uint32_t* x, uint64_t scale2,
+                                      float from, uint64_t (&sum)[2]) {
+  const uint64_t from2 = pair(-from, -from);
+  sum[0] = sum[1] = 0;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const uint64_t z =
+        fma2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, from2);
+    const float u = exp2_approx(lo_of(z)), v = exp2_approx(hi_of(z));
+    sum[e & 1] = add2(sum[e & 1], pair(u, v));
+    p[e] = pack_bf16(u, v);
+  }
+}
 
 // ---- the line ----
 
@@ -247,23 +267,39 @@ __device__ __forceinline__ int row_limit(const AttnArgs& a, const Walk<SHARED>& 
   return at < 0 || at >= s.taken ? w.kend : min(limit_of(s, at), w.kend);
 }
 
-// Rows of 128 bytes (8 pieces) or 64 (4 pieces) of a warp's 32 rows through its part of shared
-// memory, so that global memory sees whole rows: a lane's own row on one side, neighbouring
-// lanes neighbouring pieces of a row on the other.
-template <int PIECES>
+// A warp's 32 rows of 128 bytes (8 pieces) go through its part of shared memory, so that global
+// memory sees whole rows: a lane's own row on one side, neighbouring lanes neighbouring pieces of
+// a row on the other.
 __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
-  const int turn = PIECES == 8 ? row & 7 : (row >> 1) & 3;
-  return reinterpret_cast<uint4*>(stage + row * (PIECES * 16) + ((piece ^ turn) << 4));
+  return reinterpret_cast<uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
 }
-template <int PIECES, typename F>
+__device__ __forceinline__ void write_row(uint8_t* stage, int row, const uint32_t* v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    *staged(stage, row, e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+  __syncwarp();
+}
+template <typename F>
 __device__ __forceinline__ void each_piece(int rows, F f) {
-  constexpr int AT_ONCE = 32 / PIECES;
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < 32 / AT_ONCE; ++k) {
-    const int row = k * AT_ONCE + lane / PIECES;
-    if (row < rows) f(row, lane % PIECES);
+  for (int k = 0; k < 8; ++k) {
+    const int row = 4 * k + (lane >> 3);
+    if (row < rows) f(row, lane & 7);
   }
+}
+// 32 columns of a row's output; zeros where nothing was computed.
+__device__ __forceinline__ void load_output(uint32_t (&o)[32], uint32_t col, bool any) {
+  if (any) {
+    tmem_ld32_issue(col, o);
+    tmem_wait_ld32(o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0u;
+  }
+}
+__device__ __forceinline__ uint32_t add_scaled(uint32_t x, float f, uint32_t y, float g) {
+  return __float_as_uint(__uint_as_float(x) * f + __uint_as_float(y) * g);
 }
 
 template <int D, bool SHARED>
@@ -280,17 +316,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       ptx::mbar_init(&sm.full[i], 1);
-      ptx::mbar_init(&sm.empty[i], 1);
+      ptx::mbar_init(&sm.empty[i], 2);
     }
     ptx::mbar_init(&sm.q_full, 1);
-    ptx::mbar_init(&sm.q_empty, 1);
+    ptx::mbar_init(&sm.q_empty, 2);
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&sm.s_full[t], 1);
       ptx::mbar_init(&sm.p_full[t][0], 4);
       ptx::mbar_init(&sm.p_full[t][1], 4);
       ptx::mbar_init(&sm.o_full[t], 1);
     }
-    ptx::mbar_init(&sm.done, 1);
+    ptx::mbar_init(&sm.done, 2);
     ptx::fence_mbar_init();
     sm.abort = 0;
     sm.kend = 0;
@@ -340,35 +376,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Sequence s = sequence(a, b);
       mine += tiles_before(a, s, (s.taken + step - 1) / step, step);
     }
-    int64_t at = block_exclusive_sum(mine, sm.scan, &line) * a.kv_heads;
+    const int64_t before = block_exclusive_sum(mine, sm.scan, &line) * a.kv_heads;
     line *= a.kv_heads;
     N = (int)min((int64_t)gridDim.x, line);
     if ((int)blockIdx.x < N) {
       const int64_t begin = range_start(line, N, blockIdx.x);
-      if (begin >= at && begin < at + mine * a.kv_heads) {
+      if (begin >= before && begin < before + mine * a.kv_heads) {
+        int64_t at = before, n;
         int b = b0;
-        int64_t n;
-        Sequence s;
         for (;; ++b) {
-          s = sequence(a, b);
+          const Sequence s = sequence(a, b);
           n = tiles_before(a, s, (s.taken + step - 1) / step, step);
           if (begin < at + n * a.kv_heads) break;
           at += n * a.kv_heads;
         }
-        const int head = (int)((begin - at) / n);
-        at += head * n;
-        int lo = 0, hi = (s.taken + step - 1) / step;      // the row tile that holds begin
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (at + tiles_before(a, s, mid, step) <= begin) lo = mid; else hi = mid;
-        }
-        at += tiles_before(a, s, lo, step);
+        sm.start_head = (int)((begin - at) / n);
+        sm.start_at = at + sm.start_head * n;
         sm.start_seq = b;
-        sm.start_head = head;
-        sm.start_rt = lo;
-        sm.start_tile = (int)(begin - at);
-        sm.start_at = at;
         sm.start_left = (int)(range_start(line, N, blockIdx.x + 1) - begin);
+      }
+      __syncthreads();
+      if (warp == 0) {                                     // the row tile that holds begin
+        const Sequence s = sequence(a, sm.start_seq);
+        const int64_t rest = begin - sm.start_at;
+        int lo = 0, hi = (s.taken + step - 1) / step;
+        while (hi - lo > 1) {
+          const int every = (hi - lo + 31) / 32;
+          const int mine = lo + lane * every;
+          const bool before = mine < hi && tiles_before(a, s, mine, step) <= rest;
+          lo += (__popc(__ballot_sync(0xFFFFFFFFu, before)) - 1) * every;
+          hi = min(hi, lo + every);
+        }
+        if (lane == 0) {
+          const int64_t n = tiles_before(a, s, lo, step);
+          sm.start_rt = lo;
+          sm.start_tile = (int)(rest - n);
+          sm.start_at += n;
+        }
       }
     }
   }
@@ -438,78 +482,75 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance();
         }
       }
-    } else if (warp == kIssuer) {
-      // ---- products ----
-      uint32_t p_phase[2] = {0, 0};
-      const uint32_t q_addr = ptx::smem_addr(sm.q), ring = ptx::smem_addr(sm.ring);
+    } else if (warp < kIssuer + 2) {
+      // ---- products: a warp a row tile, so that neither waits for the other's softmax ----
+      const int t = warp - kIssuer;
+      uint32_t p_phase = 0;
+      const uint32_t q_addr = ptx::smem_addr(sm.q) + t * Sizes<D>::kHalf;
+      const uint32_t ring = ptx::smem_addr(sm.ring);
+      const uint32_t s_col = tmem + kColS + t * 128, o_col = tmem + kColO + t * 128;
       const uint32_t id_s = idesc_bf16(kAttnTile, false), id_o = idesc_bf16(D, true);
-      auto scores = [&](int t, uint32_t k_addr) {
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t q_off = (k >> 2) * 2 * Sizes<D>::kHalf + t * Sizes<D>::kHalf;
-            mma_ss(tmem + kColS + t * 128, ptx::desc_sw128(q_addr + q_off + (k & 3) * 32),
-                   ptx::desc_sw128(k_addr + (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32), id_s,
-                   k > 0);
-          }
-          ptx::tc_commit(&sm.s_full[t]);
-        }
-        __syncwarp();
-      };
       for (bool first = true; w.next(a, first); first = false) {
         const int n = w.busy(key0);
         if (n == 0) continue;
-        const int active = w.rows > kTileRows ? 2 : 1;
         ptx::mbar_wait(&sm.q_full, q_phase, abort, kAttnWaitNs);
         q_phase ^= 1;
-        ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
-        ptx::tc_fence_after();
-        for (int t = 0; t < active; ++t) scores(t, ring + stage * Sizes<D>::kTileBytes);
-        if (ptx::elect_one()) {
-          ptx::tc_commit(&sm.empty[stage]);
-          if (n == 1) ptx::tc_commit(&sm.q_empty);
+        if (t == 1 && w.rows <= kTileRows) {     // no rows: the operands pass by
+          if (lane == 0) ptx::mbar_arrive(&sm.q_empty);
+          for (int i = 0; i < 2 * n; ++i) {
+            ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+            if (lane == 0) ptx::mbar_arrive(&sm.empty[stage]);
+            __syncwarp();
+            advance();
+          }
+          continue;
         }
-        __syncwarp();
-        advance();
-        for (int i = 0; i < n; ++i) {
-          const int v_stage = stage;
-          ptx::mbar_wait(&sm.full[v_stage], phase, abort, kAttnWaitNs);
-          advance();
-          const int keys = min(kAttnTile, w.kend - (key0 + (w.first + i) * kAttnTile));
-          const int steps = (keys + 15) / 16;
-          const uint32_t v_addr = ring + v_stage * Sizes<D>::kTileBytes;
-          for (int t = 0; t < active; ++t) {
+        for (int i = 0; i <= n; ++i) {
+          // P V of tile i - 1, then the scores of tile i
+          if (i > 0) {
+            const int keys = min(kAttnTile, w.kend - (key0 + (w.first + i - 1) * kAttnTile));
+            const int steps = (keys + 15) / 16;
+            const uint32_t v_addr = ring + stage * Sizes<D>::kTileBytes;
+            ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
             // P comes in halves: the first one's products run while the second is made
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              ptx::mbar_wait(&sm.p_full[t][h], p_phase[t], abort, kAttnWaitNs);
+              ptx::mbar_wait(&sm.p_full[t][h], p_phase, abort, kAttnWaitNs);
               ptx::tc_fence_after();
               if (ptx::elect_one()) {
 #pragma unroll
                 for (int k = 4 * h; k < 4 * h + 4; ++k)
                   if (k < steps)
-                    mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + k * 8,
-                           desc_rows(v_addr + k * 2048, Sizes<D>::kHalf), id_o, i > 0 || k > 0);
-                if (h == 1 && i + 1 == n) ptx::tc_commit(&sm.o_full[t]);
+                    mma_ts(o_col, s_col + k * 8, desc_rows(v_addr + k * 2048, Sizes<D>::kHalf),
+                           id_o, i > 1 || k > 0);
+                if (h == 1) {
+                  ptx::tc_commit(&sm.empty[stage]);
+                  if (i == n) ptx::tc_commit(&sm.o_full[t]);
+                }
               }
               __syncwarp();
             }
-            p_phase[t] ^= 1;
-            if (i + 1 < n) {
-              if (t == 0) {
-                ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
-                ptx::tc_fence_after();
-              }
-              scores(t, ring + stage * Sizes<D>::kTileBytes);
+            p_phase ^= 1;
+            advance();
+          }
+          if (i < n) {
+            const uint32_t k_addr = ring + stage * Sizes<D>::kTileBytes;
+            ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(s_col,
+                       ptx::desc_sw128(q_addr + (k >> 2) * 2 * Sizes<D>::kHalf + (k & 3) * 32),
+                       ptx::desc_sw128(k_addr + (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32), id_s,
+                       k > 0);
+              ptx::tc_commit(&sm.s_full[t]);
+              ptx::tc_commit(&sm.empty[stage]);
+              if (i + 1 == n) ptx::tc_commit(&sm.q_empty);
             }
+            __syncwarp();
+            advance();
           }
-          if (ptx::elect_one()) {
-            ptx::tc_commit(&sm.empty[v_stage]);
-            if (i + 1 < n) ptx::tc_commit(&sm.empty[stage]);
-            if (i + 2 == n) ptx::tc_commit(&sm.q_empty);
-          }
-          __syncwarp();
-          if (i + 1 < n) advance();
         }
       }
       // no product may be in flight when tensor memory is given back
@@ -525,6 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // 32 lanes a warp
     const uint32_t s_col = lanes + kColS + t * 128, o_col = lanes + kColO + t * 128;
     uint32_t s_phase = 0, o_phase = 0;
+    // The two warpgroups take turns at the arithmetic: while one has its scores, the other's
+    // products run.  (Side by side they would end together and wait for the tensor cores
+    // together: 1840 us instead of 1647 for a prompt of 16384 tokens, 32 heads.)
+    if (t == 1) named_bar_arrive(2, 256);
     int loads = 0;                                         // stages that earlier items took
     for (bool first = true; w.next(a, first); first = false) {
       const int n = w.busy(key0);
@@ -532,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       loads += 2 * n;
       if (t == 1 && w.rows <= kTileRows) continue;
       const int limit = row_limit(a, w, r);
+      const bool both = w.rows > kTileRows;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
         const int k0 = key0 + (w.first + i) * kAttnTile;
@@ -543,12 +589,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j) tmem_ld32_issue(s_col + j * 32, x + j * 32);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_wait_ld32(x + j * 32);
+        if (both) ptx::named_bar_sync(2 + t, 256);
         if (__any_sync(0xFFFFFFFFu, k0 + kAttnTile > limit)) {
           const int seen = limit - k0;
 #pragma unroll
           for (int j = 0; j < 128; ++j)
             if (j >= seen) x[j] = 0xFF800000u;
         }
+        // The first half's terms against the maximum so far, while the tile's own maximum is
+        // found: it passes by 2^8 in few tiles but an item's first, and then they are made
+        // again.
+        const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
+        uint64_t sum[2];
+        uint32_t p[32];
+        float from = m == -INFINITY ? 0.f : m;
+        terms(p, x, scale2, from, sum);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j]));
@@ -570,46 +625,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tmem_st16(o_col + j + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
             }
           }
+          from = m == -INFINITY ? 0.f : m;
+          terms(p, x, scale2, from, sum);
         }
-        if (t == 0 && w.kend - k0 < kAttnTile && (w.kend - k0) % 16 != 0) {
+        if (w.kend - k0 < kAttnTile && (w.kend - k0) % 16 != 0) {
           // values behind the last key may be anything, and 0 times them must be 0: the rows
-          // that share the last key's sixteen are cleared
+          // that share the last key's sixteen are cleared, by each row tile before its own
+          // products (the second to come writes zeros over zeros)
           const int at = v0 + 2 * i + 1, stage = at % STAGES;
           ptx::mbar_wait(&sm.full[stage], (at / STAGES) & 1, abort, kAttnWaitNs);
           const int from_row = w.kend - k0, to_row = (from_row + 15) / 16 * 16;
-          for (int e = threadIdx.x; e < (to_row - from_row) * (D / 8); e += 128) {
+          for (int e = threadIdx.x & 127; e < (to_row - from_row) * (D / 8); e += 128) {
             const int vr = from_row + e / (D / 8), piece = e % (D / 8);
             *reinterpret_cast<uint4*>(sm.ring[stage] + (piece >> 3) * Sizes<D>::kHalf + vr * 128 +
                                       ((piece & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
           ptx::fence_proxy_async_smem();
         }
-        const float from = m == -INFINITY ? 0.f : m;
-        const uint64_t scale2 = pair(a.scale_log2, a.scale_log2), from2 = pair(-from, -from);
-        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t z =
-                fma2(pair(__uint_as_float(x[32 * j + 2 * e]),
-                          __uint_as_float(x[32 * j + 2 * e + 1])),
-                     scale2, from2);
-            const float u = exp2_approx(lo_of(z)), v = exp2_approx(hi_of(z));
-            sum[e & 1] = add2(sum[e & 1], pair(u, v));
-            p[e] = pack_bf16(u, v);
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            l += lo_of(sum[0]) + hi_of(sum[0]) + (lo_of(sum[1]) + hi_of(sum[1]));
+            terms(p, x + 64, scale2, from, sum);
+            if (both) named_bar_arrive(3 - t, 256);
           }
-          ptx::tmem_st16(s_col + j * 16, p);
-          if (j & 1) {
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][j >> 1]);
-          }
+          ptx::tmem_st16(s_col + h * 32, *reinterpret_cast<uint32_t(*)[16]>(p));
+          ptx::tmem_st16(s_col + h * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(p + 16));
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][h]);
         }
-        sum[0] = add2(sum[0], sum[1]);
-        l += lo_of(sum[0]) + hi_of(sum[0]);
+        l += lo_of(sum[0]) + hi_of(sum[0]) + (lo_of(sum[1]) + hi_of(sum[1]));
       }
 
       // ---- the item's end ----
@@ -634,68 +681,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                         : a.parts + ((int64_t)slot * kAttnRows + row0) * D;
       const float* other = a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
                                              (int64_t)w.token * a.group + row0) * D;
+      // this lane's eighth of every fourth row of the output
+      uint16_t* dst[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = row0 + 4 * k + (lane >> 3), i = token_of(a, at);
+        dst[k] = a.out + (int64_t)(w.token + i) * a.ldo +
+                 (w.head * a.group + at - i * a.group) * D + (lane & 7) * 8;
+      }
       uint8_t* stage = sm.stage[warp];
       if (n > 0) {
         ptx::mbar_wait(&sm.o_full[t], o_phase, abort, kAttnWaitNs);
         o_phase ^= 1;
         ptx::tc_fence_after();
       }
+      if (SHARED || !whole) {
 #pragma unroll 1
-      for (int j = 0; j < D; j += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32_issue(o_col + j, o);
-          tmem_wait_ld32(o);
-        } else {
+        for (int j = 0; j < D; j += 32) {
+          uint32_t o[32];
+          load_output(o, o_col + j, n > 0);
+          write_row(stage, lane, o);
+          uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (SHARED || !whole) {
+          for (int k = 0; k < 8; ++k) v[k] = *staged(stage, 4 * k + (lane >> 3), lane & 7);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *staged<8>(stage, lane, e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
-                                                    o[4 * e + 3]);
+          for (int k = 0; k < 8; ++k) {
+            const int row = 4 * k + (lane >> 3);
+            if (row < live) *reinterpret_cast<uint4*>(keep + row * D + j + (lane & 7) * 4) = v[k];
+          }
           __syncwarp();
-          each_piece<8>(live, [&](int row, int piece) {
-            *reinterpret_cast<uint4*>(keep + (int64_t)row * D + j + piece * 4) =
-                *staged<8>(stage, row, piece);
-          });
-        } else {
-          if (a.kstart > 0) {
-            each_piece<8>(live, [&](int row, int piece) {
-              *staged<8>(stage, row, piece) =
-                  *reinterpret_cast<const uint4*>(other + (int64_t)row * D + j + piece * 4);
-            });
-            __syncwarp();
+        }
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < D; j += 64) {
+          uint32_t z[32];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 y = *staged<8>(stage, lane, e);
-              const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            load_output(o, o_col + j + 32 * half, n > 0);
+            if (a.kstart > 0) {
+              each_piece(live, [&](int row, int piece) {
+                *staged(stage, row, piece) = *reinterpret_cast<const uint4*>(
+                    other + row * D + j + 32 * half + piece * 4);
+              });
+              __syncwarp();
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                o[4 * e + c] = __float_as_uint(__uint_as_float(o[4 * e + c]) * fin.mine +
-                                               __uint_as_float(z[c]) * fin.theirs);
+              for (int e = 0; e < 8; ++e) {
+                const uint4 y = *staged(stage, lane, e);
+                o[4 * e] = add_scaled(o[4 * e], fin.mine, y.x, fin.theirs);
+                o[4 * e + 1] = add_scaled(o[4 * e + 1], fin.mine, y.y, fin.theirs);
+                o[4 * e + 2] = add_scaled(o[4 * e + 2], fin.mine, y.z, fin.theirs);
+                o[4 * e + 3] = add_scaled(o[4 * e + 3], fin.mine, y.w, fin.theirs);
+              }
+              __syncwarp();
             }
-            __syncwarp();
-          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t z[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              z[c] = pack_bf16(__uint_as_float(o[8 * e + 2 * c]) * fin.inv,
-                               __uint_as_float(o[8 * e + 2 * c + 1]) * fin.inv);
-            *staged<4>(stage, lane, e) = make_uint4(z[0], z[1], z[2], z[3]);
+            for (int e = 0; e < 16; ++e)
+              z[16 * half + e] = pack_bf16(__uint_as_float(o[2 * e]) * fin.inv,
+                                           __uint_as_float(o[2 * e + 1]) * fin.inv);
           }
+          write_row(stage, lane, z);
+          uint4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = *staged(stage, 4 * k + (lane >> 3), lane & 7);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (4 * k + (lane >> 3) < live) *reinterpret_cast<uint4*>(dst[k] + j) = v[k];
           __syncwarp();
-          each_piece<4>(live, [&](int row, int piece) {
-            const int i = token_of(a, row0 + row);
-            const int head = w.head * a.group + row0 + row - i * a.group;
-            *reinterpret_cast<uint4*>(a.out + (int64_t)(w.token + i) * a.ldo + head * D + j +
-                                      piece * 8) = *staged<4>(stage, row, piece);
-          });
         }
-        __syncwarp();
       }
       if (r < w.rows && !whole) a.part_stats[slot * kAttnRows + r] = make_float2(m, l);
       if (r < w.rows && whole && !SHARED && a.lse) {
@@ -712,36 +765,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the items that the blocks of a tile kernel cut: block (c, y) the rows
 // [y kJoinRows, ..) of the item that begins in block c's range and goes on behind it.
-constexpr int kJoinRows = 8;
+constexpr int kJoinRows = 32;
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(kJoinRows * D / 4)
+__global__ void __launch_bounds__(256)
     attention_join_kernel(const __grid_constant__ AttnArgs a) {
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
   const AttnCut cut = a.cuts[blockIdx.x];
-  const int quad = threadIdx.x % (D / 4);
-  const int r = blockIdx.y * kJoinRows + threadIdx.x / (D / 4);
-  if (cut.to < 0 || r >= cut.rows) return;
-  const int i = token_of(a, r), head = cut.head * a.group + r - i * a.group;
-  const int64_t token = cut.first + i;
-  auto part = [&](int b) { return (int64_t)(2 * b + (b == cut.from)) * kAttnRows + r; };
-  float top = -INFINITY, sum = 0.f;
+  if (cut.to < 0) return;
+  constexpr int kQuads = D / 4;
+  const int quad = threadIdx.x % kQuads;
+  const int end = min(cut.rows, ((int)blockIdx.y + 1) * kJoinRows);
+  for (int r = blockIdx.y * kJoinRows + threadIdx.x / kQuads; r < end; r += 256 / kQuads) {
+    const int i = token_of(a, r), head = cut.head * a.group + r - i * a.group;
+    const int64_t token = cut.first + i;
+    auto part = [&](int b) { return (int64_t)(2 * b + (b == cut.from)) * kAttnRows + r; };
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll 8
-  for (int b = cut.from; b <= cut.to; ++b) top = fmaxf(top, a.part_stats[part(b)].x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = cut.from; b <= cut.to; ++b) top = fmaxf(top, a.part_stats[part(b)].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int b = cut.from; b <= cut.to; ++b) {
-    const float2 st = a.part_stats[part(b)];
-    const float4 y = *(reinterpret_cast<const float4*>(a.parts + part(b) * D) + quad);
-    const float f = exp2_approx(st.x - base);
-    sum += st.y * f;
-    acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
+    for (int b = cut.from; b <= cut.to; ++b) {
+      const float2 st = a.part_stats[part(b)];
+      const float4 y = *(reinterpret_cast<const float4*>(a.parts + part(b) * D) + quad);
+      const float f = exp2_approx(st.x - base);
+      sum += st.y * f;
+      acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
+    }
+    const Finish fin =
+        finish_begin<D, SHARED>(a, cut.head, (int64_t)cut.first * a.group + r, top, sum);
+    finish_quad<D, SHARED>(a, fin, token, head, quad, acc);
+    if (!SHARED && a.lse && quad == 0) a.lse[token * a.q_heads + head] = fin.lse;
   }
-  const Finish fin =
-      finish_begin<D, SHARED>(a, cut.head, (int64_t)cut.first * a.group + r, top, sum);
-  finish_quad<D, SHARED>(a, fin, token, head, quad, acc);
-  if (!SHARED && a.lse && quad == 0) a.lse[token * a.q_heads + head] = fin.lse;
 }
 
 template <int D, bool SHARED>
@@ -766,7 +822,7 @@ cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap&
   const int64_t rows = (int64_t)(SHARED ? a.batch.tokens : a.batch.max_new) * a.group;
   const int most = (int)(rows < kAttnRows ? rows : kAttnRows);
   return launch_pdl(attention_join_kernel<D, SHARED>,
-                    dim3(blocks, (most + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * D / 4), 0,
+                    dim3(blocks, (most + kJoinRows - 1) / kJoinRows), dim3(256), 0,
                     st, a);
 }
 
