@@ -95,15 +95,17 @@ struct Pages {
     shared_pages = a.batch.shared_len >> a.page_shift;
     base = -64;
   }
-  // Entry first + i, i in [0, n), n at most 32, each lane its own i (converged warp).
-  __device__ __forceinline__ int get(const AttnArgs& a, int first, int n, int i) {
+  // Makes the entries [first, first + n), n at most 32, ready for at (converged warp).
+  __device__ __forceinline__ void fetch(const AttnArgs& a, int first, int n) {
     if (first < base || first + n > base + 32) {
       base = first;
       const int at = first + (int)(threadIdx.x & 31);
       mine = -1;
       if (at < a.batch.pages_ld) mine = at < shared_pages ? shared[at] : row[at];
     }
-    return __shfl_sync(0xFFFFFFFFu, mine, first - base + i);
+  }
+  __device__ __forceinline__ int at(int i) const {
+    return __shfl_sync(0xFFFFFFFFu, mine, i - base);
   }
 };
 
@@ -118,24 +120,30 @@ __device__ __forceinline__ int cache_row(const AttnArgs& a, int page, int head, 
 }
 
 // Loads the boxes of one tile of keys (or values) from key k0 of a sequence, `keys` of them
-// (1 .. kAttnTile), into dst: [D / 64][kAttnTile rows][128 bytes], swizzled.  A converged
-// warp; what no box covers keeps its old contents.
+// (1 .. kAttnTile), into dst: [D / 64][kAttnTile rows][128 bytes], swizzled.  A converged warp,
+// box after box: with a lane a box the copies' operands go to uniform registers lane by lane,
+// which took 140 cycles a box.  What no box covers keeps its old contents.
 template <int D>
 __device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* map, Pages& pages,
                                           int head, int k0, int keys, uint8_t* dst,
                                           uint64_t* bar) {
   constexpr int HALVES = D / 64;
-  const int lane = threadIdx.x & 31;
   const int box = min(1 << a.page_shift, kAttnTile);
   const int boxes = (keys + box - 1) / box;
-  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, boxes * HALVES * box * 128);
+  const int first = k0 >> a.page_shift, r = k0 & ((1 << a.page_shift) - 1);
+  pages.fetch(a, first, boxes);
+  if (ptx::elect_one()) ptx::mbar_arrive_expect_tx(bar, boxes * HALVES * box * 128);
   __syncwarp();
-  const int i = min(lane / HALVES, boxes - 1), half = lane % HALVES;
-  const int page = pages.get(a, k0 >> a.page_shift, boxes, i);
-  if (lane < boxes * HALVES) {
-    const int y = cache_row(a, page, head, k0 & ((1 << a.page_shift) - 1));
-    ptx::tma_load_2d(dst + (half * kAttnTile + i * box) * 128, map, half * 64, y, bar,
-                     ptx::policy_evict_normal());
+  const uint64_t policy = ptx::policy_evict_normal();
+#pragma unroll 2
+  for (int i = 0; i < boxes; ++i) {
+    const int y = cache_row(a, pages.at(first + i), head, r);
+    if (ptx::elect_one()) {
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+        ptx::tma_load_2d(dst + (h * kAttnTile + i * box) * 128, map, h * 64, y, bar, policy);
+    }
+    __syncwarp();
   }
 }
 
@@ -190,6 +198,46 @@ __device__ __forceinline__ void finish_quad(const AttnArgs& a, const Finish& f, 
   }
   *reinterpret_cast<uint2*>(a.out + token * a.ldo + head * D + quad * 4) = make_uint2(
       pack_bf16(v.x * f.inv, v.y * f.inv), pack_bf16(v.z * f.inv, v.w * f.inv));
+}
+
+// Row r's four elements `quad` of a cut item, over its parts of blocks [from, to] in their
+// order: the sum of its terms, relative to 2^top, and of their products.  A block's parts lie at
+// [2 block + whether the item begins there], `rows` rows each.  Eight parts' loads at a time.
+struct Joined {
+  float4 acc;
+  float sum, top;
+};
+template <int D>
+__device__ __forceinline__ Joined join_parts(const AttnArgs& a, int from, int to, int rows, int r,
+                                             int quad) {
+  constexpr int kAtOnce = 8;
+  Joined j = {make_float4(0.f, 0.f, 0.f, 0.f), 0.f, -INFINITY};
+  for (int b0 = from; b0 <= to; b0 += kAtOnce) {
+    float2 st[kAtOnce];
+    float4 y[kAtOnce];
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int b = min(b0 + e, to);
+      const int64_t at = (int64_t)(2 * b + (b == from)) * rows + r;
+      st[e] = __ldcg(&a.part_stats[at]);
+      y[e] = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + quad);
+    }
+    float up = j.top;
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) up = fmaxf(up, st[e].x);
+    const float base = up == -INFINITY ? 0.f : up, f = exp2_approx(j.top - base);
+    j.top = up;
+    j.sum *= f;
+    j.acc.x *= f; j.acc.y *= f; j.acc.z *= f; j.acc.w *= f;
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const float g = b0 + e <= to ? exp2_approx(st[e].x - base) : 0.f;
+      j.sum += st[e].y * g;
+      j.acc.x += y[e].x * g; j.acc.y += y[e].y * g;
+      j.acc.z += y[e].z * g; j.acc.w += y[e].w * g;
+    }
+  }
+  return j;
 }
 
 // Items of at most 16 rows (attn_few.cu).

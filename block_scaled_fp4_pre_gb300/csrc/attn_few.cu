@@ -21,14 +21,15 @@ namespace mxmoe {
 namespace {
 
 constexpr int kRows = 16;
-constexpr int kWarps = 8;                       // of consumers; one more loads
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 8;                       // of consumers; two more load keys and values
+constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kGroup = 8;                       // rows that the warps add up at a time
 
 template <int D>
 struct Ring {
   static constexpr int kBytes = kAttnTile * D * 2;
-  static constexpr int kStages = 196608 / kBytes;
+  static constexpr int kStages = 196608 / kBytes;   // keys and values in turn
+  static_assert(kStages % 2 == 0, "keys keep to the even stages");
 };
 
 template <int D>
@@ -174,8 +175,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  if (warp == kWarps) {
-    // ---- loads: keys and values of a tile, one stage each ----
+  if (warp >= kWarps) {
+    // ---- loads: keys by one warp into the even stages, values by the other into the odd ----
+    const int v = warp - kWarps;
+    stage = v;
+    auto advance2 = [&] {
+      if ((stage += 2) >= STAGES) {
+        stage -= STAGES;
+        phase ^= 1;
+      }
+    };
     Pages pages;
     int seq = -1;
     for (bool first = true; w.next(a, first); first = false) {
@@ -183,21 +192,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = w.first; t < w.last; ++t) {
         const int k0 = a.kstart + t * kAttnTile, keys = min(kAttnTile, w.s.kend - k0);
         if (keys <= 0) continue;
-        for (int v = 0; v < 2; ++v) {
-          ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-          load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, sm.ring[stage],
-                       &sm.full[stage]);
-          advance();
-        }
+        ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
+        load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, sm.ring[stage],
+                     &sm.full[stage]);
+        advance2();
       }
     }
     // After a wait that ran out, copies may still be in flight: the block stays for them.
     if (*abort) {
       if (lane == 0) atomicOr(a.flags, kErrTimeout);
       int never = 0;
-      for (int i = 0; i < STAGES; ++i) {
+      for (int i = 0; i < STAGES; i += 2) {
         ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
-        advance();
+        advance2();
       }
     }
     return;
@@ -390,7 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- a cut item: the block that comes last joins its parts ----
     const int from = block_of(line, N, w.at), to = block_of(line, N, w.at + w.tiles - 1);
-    __threadfence();
     ptx::named_bar_sync(1, 32 * kWarps);
     if (threadIdx.x == 0) {
       const bool last = ptx::atomic_add_acq_rel(a.counters + from, 1) == to - from;
@@ -399,24 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::named_bar_sync(1, 32 * kWarps);
     if (!sm.joins) continue;
-    __threadfence();
     for (int r = row8; r < rows; r += 32 * kWarps / kQuads) {
-      auto part = [&](int b) { return (2 * b + (b == from)) * kRows + r; };
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll 8
-      for (int b = from; b <= to; ++b) top = fmaxf(top, __ldcg(&a.part_stats[part(b)]).x);
-      const float base = top == -INFINITY ? 0.f : top;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int b = from; b <= to; ++b) {
-        const float2 st = __ldcg(&a.part_stats[part(b)]);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.parts + (int64_t)part(b) * D) +
-                                quad);
-        const float f = exp2_approx(st.x - base);
-        sum += st.y * f;
-        acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
-      }
-      store_row<D>(a, s, w.head, r, quad, acc, sum, top);
+      const Joined j = join_parts<D>(a, from, to, kRows, r, quad);
+      store_row<D>(a, s, w.head, r, quad, j.acc, j.sum, j.top);
     }
   }
   if (*abort && lane == 0) atomicOr(a.flags, kErrTimeout);

@@ -18,6 +18,8 @@
 // before it hands over the next P, when no product on it is in flight.
 //
 // Bound by the tensor cores: 4 x 128 x 128 x D operations a tile pair at the dense bf16 rate.
+#include <algorithm>
+
 #include "attn.cuh"
 #include "per_device.h"
 #include "tmap.cuh"
@@ -26,8 +28,9 @@ namespace mxmoe {
 namespace {
 
 constexpr int kTileRows = 128;
-// Warps: eight with a row a thread, one that loads, one a row tile that issues its products.
-constexpr int kLoader = 8, kIssuer = 9;
+// Warps: eight with a row a thread, one that loads queries and keys and one for values, one a row
+// tile that issues its products.
+constexpr int kLoader = 8, kIssuer = 10;
 constexpr int kThreads = 384;                   // whole warpgroups, as register shares go by
 // 384 threads start with 168 registers: the softmax's two warpgroups take 208, the third 88
 // (2 x 208 + 88 = 3 x 168).
@@ -40,6 +43,7 @@ struct Sizes {
   static constexpr int kHalf = kTileRows * 128;             // 64 columns of a tile
   static constexpr int kStage = 8 * 4096;                   // 32 rows of 128 bytes a warp
   static constexpr int kStages = (229376 - kStage - 2 * kTileBytes) / kTileBytes;
+  static_assert(kStages % 2 == 0, "keys keep to the even stages");
 };
 
 template <int D>
@@ -416,7 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (threadIdx.x == 0) a.cuts[blockIdx.x].to = -1;      // no item begins here and goes on
+  // Entries of the cuts: an item's where the prefix's are fewer than the blocks, else the
+  // block's that the item begins in.
+  const bool by_item = SHARED && a.kv_heads * shared_rts <= (int)gridDim.x;
+  if (threadIdx.x == 0 && !by_item) a.cuts[blockIdx.x].to = -1;
   __syncthreads();
   Walk<SHARED> w = {};
   w.left = sm.start_left;
@@ -445,44 +452,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
     };
-    if (warp == kLoader) {
-      // ---- loads: an item's queries; keys and values of a tile, one stage each ----
+    if (warp < kIssuer) {
+      // ---- loads: an item's queries; keys into the even stages, values into the odd ----
+      const int v = warp - kLoader;
+      stage = v;
+      auto advance2 = [&] {
+        if ((stage += 2) >= STAGES) {
+          stage -= STAGES;
+          phase ^= 1;
+        }
+      };
       Pages pages;
       int seq = -1;
       for (bool first = true; w.next(a, first); first = false) {
         const int n = w.busy(key0);
         if (n == 0) continue;
         if (w.seq != seq) pages.start(a, seq = w.seq);
-        ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs);
-        q_phase ^= 1;
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&sm.q_full, step * a.group * 2 * D);
-          for (int h = 0; h < D / 64; ++h)
-            ptx::tma_load_3d(sm.q + h * 2 * Sizes<D>::kHalf, &qmap, h * 64, w.head * a.group,
-                             w.token, &sm.q_full, ptx::policy_evict_first());
+        if (v == 0) {
+          ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs);
+          q_phase ^= 1;
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(&sm.q_full, step * a.group * 2 * D);
+            for (int h = 0; h < D / 64; ++h)
+              ptx::tma_load_3d(sm.q + h * 2 * Sizes<D>::kHalf, &qmap, h * 64, w.head * a.group,
+                               w.token, &sm.q_full, ptx::policy_evict_first());
+          }
+          __syncwarp();
         }
-        __syncwarp();
         for (int t = w.first; t < w.first + n; ++t) {
           const int k0 = key0 + t * kAttnTile;
-          const int keys = min(kAttnTile, w.kend - k0);
-          for (int v = 0; v < 2; ++v) {
-            ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-            load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, sm.ring[stage],
-                         &sm.full[stage]);
-            advance();
-          }
+          ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
+          load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kAttnTile, w.kend - k0),
+                       sm.ring[stage], &sm.full[stage]);
+          advance2();
         }
       }
       // After a wait that ran out, copies may still be in flight: the block stays for them.
       if (*abort) {
         int never = 0;
-        ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
-        for (int i = 0; i < STAGES; ++i) {
+        if (v == 0) ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
+        for (int i = 0; i < STAGES; i += 2) {
           ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
-          advance();
+          advance2();
         }
       }
-    } else if (warp < kIssuer + 2) {
+    } else {
       // ---- products: a warp a row tile, so that neither waits for the other's softmax ----
       const int t = warp - kIssuer;
       uint32_t p_phase = 0;
@@ -662,14 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the item's end ----
       const bool whole = w.first == 0 && w.last == w.tiles;
       const int slot = 2 * blockIdx.x + (w.first == 0);
-      if (w.first == 0 && !whole && r == 0) {
+      if (w.first == 0 && (!whole || by_item) && r == 0) {
         AttnCut cut;
         cut.first = w.token;
         cut.rows = w.rows;
         cut.head = w.head;
         cut.from = blockIdx.x;
-        cut.to = block_of(line, N, w.at + w.tiles - 1);
-        a.cuts[blockIdx.x] = cut;
+        cut.to = whole ? -1 : block_of(line, N, w.at + w.tiles - 1);
+        a.cuts[by_item ? w.head * shared_rts + w.rt : blockIdx.x] = cut;
       }
       const int row0 = warp * 32, live = w.rows - row0;     // the warp's rows of the item
       const int64_t index = (int64_t)w.token * a.group + r;
@@ -764,38 +778,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the items that the blocks of a tile kernel cut: block (c, y) the rows
-// [y kJoinRows, ..) of the item that begins in block c's range and goes on behind it.
-constexpr int kJoinRows = 32;
+// [y rows_a_block, ..) of entry c of the cuts.
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(256)
-    attention_join_kernel(const __grid_constant__ AttnArgs a) {
+    attention_join_kernel(const __grid_constant__ AttnArgs a, int rows_a_block) {
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
   const AttnCut cut = a.cuts[blockIdx.x];
   if (cut.to < 0) return;
   constexpr int kQuads = D / 4;
   const int quad = threadIdx.x % kQuads;
-  const int end = min(cut.rows, ((int)blockIdx.y + 1) * kJoinRows);
-  for (int r = blockIdx.y * kJoinRows + threadIdx.x / kQuads; r < end; r += 256 / kQuads) {
+  const int end = min(cut.rows, ((int)blockIdx.y + 1) * rows_a_block);
+  for (int r = blockIdx.y * rows_a_block + threadIdx.x / kQuads; r < end; r += 256 / kQuads) {
     const int i = token_of(a, r), head = cut.head * a.group + r - i * a.group;
     const int64_t token = cut.first + i;
-    auto part = [&](int b) { return (int64_t)(2 * b + (b == cut.from)) * kAttnRows + r; };
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll 8
-    for (int b = cut.from; b <= cut.to; ++b) top = fmaxf(top, a.part_stats[part(b)].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int b = cut.from; b <= cut.to; ++b) {
-      const float2 st = a.part_stats[part(b)];
-      const float4 y = *(reinterpret_cast<const float4*>(a.parts + part(b) * D) + quad);
-      const float f = exp2_approx(st.x - base);
-      sum += st.y * f;
-      acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
-    }
+    const Joined j = join_parts<D>(a, cut.from, cut.to, kAttnRows, r, quad);
     const Finish fin =
-        finish_begin<D, SHARED>(a, cut.head, (int64_t)cut.first * a.group + r, top, sum);
-    finish_quad<D, SHARED>(a, fin, token, head, quad, acc);
+        finish_begin<D, SHARED>(a, cut.head, (int64_t)cut.first * a.group + r, j.top, j.sum);
+    finish_quad<D, SHARED>(a, fin, token, head, quad, j.acc);
     if (!SHARED && a.lse && quad == 0) a.lse[token * a.q_heads + head] = fin.lse;
   }
 }
@@ -821,9 +821,13 @@ cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap&
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)(SHARED ? a.batch.tokens : a.batch.max_new) * a.group;
   const int most = (int)(rows < kAttnRows ? rows : kAttnRows);
-  return launch_pdl(attention_join_kernel<D, SHARED>,
-                    dim3(blocks, (most + kJoinRows - 1) / kJoinRows), dim3(256), 0,
-                    st, a);
+  // 8 rows a block, or more where that would be more blocks than are resident together
+  const int step = kAttnRows / a.group, eights = (most + 7) / 8;
+  const int64_t items = (int64_t)a.kv_heads * ((a.batch.tokens + step - 1) / step);
+  const int cuts = SHARED && items <= blocks ? (int)items : blocks;
+  const int y = std::min(eights, std::max(1, 8 * g.num_sms / cuts));
+  return launch_pdl(attention_join_kernel<D, SHARED>, dim3(cuts, y), dim3(256), 0, st, a,
+                    (eights + y - 1) / y * 8);
 }
 
 }  // namespace
