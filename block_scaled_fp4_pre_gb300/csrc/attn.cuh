@@ -119,32 +119,31 @@ __device__ __forceinline__ int cache_row(const AttnArgs& a, int page, int head, 
   return ((page * a.kv_heads + head) << a.page_shift) + r;
 }
 
-// Loads the boxes of one tile of keys (or values) from key k0 of a sequence, `keys` of them
-// (1 .. kAttnTile), into dst: [D / 64][kAttnTile rows][128 bytes], swizzled.  A converged warp,
-// box after box: with a lane a box the copies' operands go to uniform registers lane by lane,
-// which took 140 cycles a box.  What no box covers keeps its old contents.
-template <int D>
+// Loads one tile of keys (or values) from key k0 of a sequence, `keys` of them (1 ..
+// kAttnTile), into dst: [D / 64][kAttnTile rows][128 bytes], swizzled; what no box covers keeps
+// its old contents.  PARTS converged warps share the boxes, each its own with an arrival of its
+// own on bar.  A box takes its warp 130 cycles to issue from a lane each (260 one after another
+// by an elected lane), so pages of 16 keys need the warps; copies themselves overlap.
+template <int D, int PARTS>
 __device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* map, Pages& pages,
-                                          int head, int k0, int keys, uint8_t* dst,
+                                          int head, int k0, int keys, int part, uint8_t* dst,
                                           uint64_t* bar) {
   constexpr int HALVES = D / 64;
   const int box = min(1 << a.page_shift, kAttnTile);
-  const int boxes = (keys + box - 1) / box;
+  const int boxes = (keys + box - 1) / box, mine = (boxes * HALVES - part + PARTS - 1) / PARTS;
   const int first = k0 >> a.page_shift, r = k0 & ((1 << a.page_shift) - 1);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, mine * box * 128);
   pages.fetch(a, first, boxes);
-  if (ptx::elect_one()) ptx::mbar_arrive_expect_tx(bar, boxes * HALVES * box * 128);
+  const int which = min(lane, mine - 1) * PARTS + part, i = max(which, 0) / HALVES;
+  const int page = pages.at(first + i);
   __syncwarp();
-  const uint64_t policy = ptx::policy_evict_normal();
-#pragma unroll 2
-  for (int i = 0; i < boxes; ++i) {
-    const int y = cache_row(a, pages.at(first + i), head, r);
-    if (ptx::elect_one()) {
-#pragma unroll
-      for (int h = 0; h < HALVES; ++h)
-        ptx::tma_load_2d(dst + (h * kAttnTile + i * box) * 128, map, h * 64, y, bar, policy);
-    }
-    __syncwarp();
+  if (lane < mine) {
+    const int y = cache_row(a, page, head, r), h = which % HALVES;
+    ptx::tma_load_2d(dst + (h * kAttnTile + i * box) * 128, map, h * 64, y, bar,
+                     ptx::policy_evict_normal());
   }
+  __syncwarp();
 }
 
 // What ends a row: its sums, with m the log2 of the term they are relative to, join the shared

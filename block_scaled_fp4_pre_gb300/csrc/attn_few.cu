@@ -21,8 +21,9 @@ namespace mxmoe {
 namespace {
 
 constexpr int kRows = 16;
-constexpr int kWarps = 8;                       // of consumers; two more load keys and values
-constexpr int kThreads = 32 * (kWarps + 2);
+constexpr int kWarps = 8;                       // of consumers
+constexpr int kLoaders = 2;                     // warps that load keys, and values
+constexpr int kThreads = 32 * (kWarps + 2 * kLoaders);
 constexpr int kGroup = 8;                       // rows that the warps add up at a time
 
 template <int D>
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      ptx::mbar_init(&sm.full[i], 1);
+      ptx::mbar_init(&sm.full[i], kLoaders);
       ptx::mbar_init(&sm.empty[i], kWarps);
     }
     ptx::fence_mbar_init();
@@ -176,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= kWarps) {
-    // ---- loads: keys by one warp into the even stages, values by the other into the odd ----
-    const int v = warp - kWarps;
+    // ---- loads: keys into the even stages, values into the odd ----
+    const int v = (warp - kWarps) & 1, part = (warp - kWarps) >> 1;
     stage = v;
     auto advance2 = [&] {
       if ((stage += 2) >= STAGES) {
@@ -193,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k0 = a.kstart + t * kAttnTile, keys = min(kAttnTile, w.s.kend - k0);
         if (keys <= 0) continue;
         ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-        load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, sm.ring[stage],
-                     &sm.full[stage]);
+        load_tile<D, kLoaders>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, part,
+                               sm.ring[stage], &sm.full[stage]);
         advance2();
       }
     }

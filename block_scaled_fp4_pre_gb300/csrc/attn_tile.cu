@@ -482,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = w.first; t < w.first + n; ++t) {
           const int k0 = key0 + t * kAttnTile;
           ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-          load_tile<D>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kAttnTile, w.kend - k0),
-                       sm.ring[stage], &sm.full[stage]);
+          load_tile<D, 1>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kAttnTile, w.kend - k0), 0,
+                          sm.ring[stage], &sm.full[stage]);
           advance2();
         }
       }
