@@ -102,8 +102,10 @@ class AttentionDims(ctypes.Structure):
 def make_attention_dims(q_heads: int, kv_heads: int, head_dim: int, num_pages: int,
                         page_size: int, max_tokens: int, max_shared_tokens: int = 0
                         ) -> AttentionDims:
-    return AttentionDims(q_heads, kv_heads, head_dim, num_pages, page_size, max_tokens,
-                         max_shared_tokens)
+    d = AttentionDims(q_heads, kv_heads, head_dim, num_pages, page_size, max_tokens,
+                      max_shared_tokens)
+    d.cache_shape = (num_pages, kv_heads, page_size, head_dim)   # of each cache
+    return d
 
 
 class KvBatch(ctypes.Structure):
@@ -569,47 +571,58 @@ def moe_rope_prepare(dims: RopeDims, table, stream=None) -> None:
                                   _stream(stream)))
 
 
-def _here(t, name: str) -> int:
+def _here(t, name: str, device: int | None = None) -> int:
     """Address of a tensor on the current device."""
-    if t.get_device() == _current_device():
+    if device is None:
+        device = _current_device()
+    if t.get_device() == device:
         return t.data_ptr()
     raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: need a tensor on the current CUDA device "
-                                        f"{_current_device()}, got one on {t.device}")
+                                        f"{device}, got one on {t.device}")
 
 
 def _heads(t, tokens: int, heads: int, D: int, name: str) -> int:
     """Token stride of bf16 [tokens, heads, D] or [tokens, heads * D], a token's row contiguous."""
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
     if t.dtype is torch.bfloat16:
+        row = heads * D
         if shape == (tokens, heads, D):
+            if t.is_contiguous():
+                return row
+            strides = t.stride()
             if (strides[2] == 1 or D == 1) and (strides[1] == D or heads == 1):
-                return strides[0] if tokens > 1 else heads * D
-        elif shape == (tokens, heads * D) and (strides[1] == 1 or heads * D == 1):
-            return strides[0] if tokens > 1 else heads * D
+                return strides[0] if tokens > 1 else row
+        elif shape == (tokens, row):
+            strides = t.stride()
+            if strides[1] == 1 or row == 1:
+                return strides[0] if tokens > 1 else row
     raise ValueError(f"{name}: need bf16 [{tokens}, {heads}, {D}] with contiguous tokens, got "
-                     f"{t.dtype} {list(shape)}, strides {strides}")
+                     f"{t.dtype} {list(shape)}, strides {t.stride()}")
 
 
-def _ints(t, n: int, name: str) -> int:
+def _ints(t, n: int, name: str, device: int | None = None) -> int:
     if t.dtype is torch.int32 and t.numel() == n and t.is_contiguous():
-        return _here(t, name)
+        return _here(t, name, device)
     raise ValueError(f"{name}: need {n} contiguous int32, got {t.dtype} {list(t.shape)}")
 
 
 def moe_rope(dims: RopeDims, table, x, positions, out=None, stream=None) -> None:
     """Rotates x, bf16 [tokens, heads, head_dim] with contiguous tokens, by each token's int32
     position, into out or in place."""
-    out = x if out is None else out
     if x.dim() != 3:
         raise ValueError(f"x: need [tokens, heads, head_dim], got {list(x.shape)}")
     T, heads, D = x.shape
     if D != dims.head_dim:
         raise ValueError(f"x: heads of {D} elements, the rotation's of {dims.head_dim}")
-    ldx, ldo = _heads(x, T, heads, D, "x"), _heads(out, T, heads, D, "out")
+    device = _current_device()
+    px, ldx = _here(x, "x", device), _heads(x, T, heads, D, "x")
+    po, ldo = px, ldx
+    if out is not None and out is not x:
+        po, ldo = _here(out, "out", device), _heads(out, T, heads, D, "out")
     status = (_lib or lib()).moe_rope(
-        ctypes.byref(dims), _bytes(table, 4 * dims.rotary_dim, "table"), _here(x, "x"), ldx,
-        _ints(positions, T, "positions"), T, heads, _here(out, "out"), ldo,
-        _raw_stream(_current_device()) if stream is None else _stream(stream))
+        ctypes.byref(dims), _bytes(table, 4 * dims.rotary_dim, "table"), px, ldx,
+        _ints(positions, T, "positions", device), T, heads, po, ldo,
+        _raw_stream(device) if stream is None else _stream(stream))
     if status:
         _check(status)
 
@@ -640,43 +653,49 @@ def moe_attention_workspace_init(dims: AttentionDims, ws, stream=None) -> None:
                                               _nbytes(ws), _stream(stream)))
 
 
-def _cache(t, dims: AttentionDims, name: str) -> int:
-    shape = (dims.num_pages, dims.kv_heads, dims.page_size, dims.head_dim)
-    if t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous():
-        return _here(t, name)
-    raise ValueError(f"{name}: need contiguous bf16 {list(shape)}, got {t.dtype} {list(t.shape)}")
+def _cache(t, dims: AttentionDims, name: str, device: int) -> int:
+    if t.dtype is torch.bfloat16 and t.shape == dims.cache_shape and t.is_contiguous():
+        return _here(t, name, device)
+    raise ValueError(f"{name}: need contiguous bf16 {list(dims.cache_shape)}, got {t.dtype} "
+                     f"{list(t.shape)}")
 
 
-def _on_device(batch: KvBatch) -> None:
-    if batch.device != _current_device():
+def _batch_device(batch: KvBatch) -> int:
+    device = _current_device()
+    if batch.device != device:
         raise MoeError(MOE_ERR_INVALID_ARG, f"batch: its tensors lie on device {batch.device}, "
-                                            f"current is {_current_device()}")
+                                            f"current is {device}")
+    return device
 
 
 def moe_kv_append(dims: AttentionDims, batch: KvBatch, k, v, k_cache, v_cache, ws, *, rope=None,
                   table=None, positions=None, q=None, q_out=None, stream=None) -> None:
     """Appends keys (rotated, given rope and its table) and values to the paged cache, and
     rotates q into q_out (or in place).  q, k and v are bf16 [tokens, heads, head_dim]."""
-    T, D, hk, hq = batch.tokens, dims.head_dim, dims.kv_heads, dims.q_heads
-    _on_device(batch)
+    device = _batch_device(batch)
+    T, (_, hk, _, D) = batch.tokens, dims.cache_shape
     pq = pqo = pt = None
     ldq = ldqo = 0
     if q is not None:
-        q_out = q if q_out is None else q_out
-        ldq, ldqo = _heads(q, T, hq, D, "q"), _heads(q_out, T, hq, D, "q_out")
-        pq, pqo = _here(q, "q"), _here(q_out, "q_out")
+        hq = dims.q_heads
+        pq, ldq = _here(q, "q", device), _heads(q, T, hq, D, "q")
+        pqo, ldqo = pq, ldq
+        if q_out is not None and q_out is not q:
+            pqo, ldqo = _here(q_out, "q_out", device), _heads(q_out, T, hq, D, "q_out")
     elif q_out is not None:
         raise ValueError("q_out: given without q")
     if rope is not None:
         pt = _bytes(table, 4 * rope.rotary_dim, "table")
         rope = ctypes.byref(rope)
-    ldk, ldv = _heads(k, T, hk, D, "k"), _heads(v, T, hk, D, "v")
+    elif table is not None:
+        raise ValueError("table: given without rope")
     status = (_lib or lib()).moe_kv_append(
         ctypes.byref(dims), ctypes.byref(batch), rope, pt,
-        None if positions is None else _ints(positions, T, "positions"), pq, ldq, pqo, ldqo,
-        _here(k, "k"), ldk, _here(v, "v"), ldv, _cache(k_cache, dims, "k_cache"),
-        _cache(v_cache, dims, "v_cache"), _here(ws, "workspace"), ws.nbytes,
-        _raw_stream(_current_device()) if stream is None else _stream(stream))
+        None if positions is None else _ints(positions, T, "positions", device), pq, ldq, pqo,
+        ldqo, _here(k, "k", device), _heads(k, T, hk, D, "k"), _here(v, "v", device),
+        _heads(v, T, hk, D, "v"), _cache(k_cache, dims, "k_cache", device),
+        _cache(v_cache, dims, "v_cache", device), _here(ws, "workspace", device), ws.nbytes,
+        _raw_stream(device) if stream is None else _stream(stream))
     if status:
         _check(status)
 
@@ -687,20 +706,20 @@ def moe_attention(dims: AttentionDims, batch: KvBatch, q, k_cache, v_cache, out,
 
     q and out are bf16 [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads] or None; scale is
     head_dim ** -0.5 unless given."""
-    T, D, hq = batch.tokens, dims.head_dim, dims.q_heads
-    _on_device(batch)
-    ldq, ldo = _heads(q, T, hq, D, "q"), _heads(out, T, hq, D, "out")
+    device = _batch_device(batch)
+    T, D, hq = batch.tokens, dims.cache_shape[3], dims.q_heads
     pl = None
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.shape != (T, hq) or not lse.is_contiguous():
             raise ValueError(f"lse: need contiguous fp32 [{T}, {hq}]")
-        pl = _here(lse, "lse")
+        pl = _here(lse, "lse", device)
     status = (_lib or lib()).moe_attention(
-        ctypes.byref(dims), ctypes.byref(batch), _here(q, "q"), ldq,
-        _cache(k_cache, dims, "k_cache"), _cache(v_cache, dims, "v_cache"),
-        D ** -0.5 if scale is None else scale, _here(out, "out"), ldo, pl,
-        _here(ws, "workspace"), ws.nbytes,
-        _raw_stream(_current_device()) if stream is None else _stream(stream))
+        ctypes.byref(dims), ctypes.byref(batch), _here(q, "q", device),
+        _heads(q, T, hq, D, "q"), _cache(k_cache, dims, "k_cache", device),
+        _cache(v_cache, dims, "v_cache", device), D ** -0.5 if scale is None else scale,
+        _here(out, "out", device), _heads(out, T, hq, D, "out"), pl,
+        _here(ws, "workspace", device), ws.nbytes,
+        _raw_stream(device) if stream is None else _stream(stream))
     if status:
         _check(status)
 
