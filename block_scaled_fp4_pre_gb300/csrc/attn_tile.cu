@@ -53,7 +53,7 @@ struct Smem {
   uint8_t stage[8][4096];
   int64_t scan[kThreads / 32];
   uint64_t full[Sizes<D>::kStages], empty[Sizes<D>::kStages];
-  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], done;
+  uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2], done;
   int64_t start_at;
   int start_left, start_seq, start_head, start_rt, start_tile;
   int kend;                                     // SHARED: keys that some row sees
@@ -61,7 +61,9 @@ struct Smem {
   int abort;
 };
 
-// tensor memory: scores (and P) of both tiles, then the outputs
+// Keys of a step: a row tile has two steps' scores (and, in their place, P) in tensor memory.
+constexpr int kStep = 64;
+// tensor memory: scores of both tiles, then the outputs
 constexpr uint32_t kColS = 0, kColO = 256;
 
 // D[tmem] (+)= A[smem] B[smem]^T and A[tmem] B[smem], bf16.
@@ -140,10 +142,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-
-__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
 
 // 64 scores to terms exp2(x scale - from), packed, and their sums.
 __device__ __forceinline__ void terms(uint32_t (&p)[32], const uint32_t* x, uint64_t scale2,
@@ -325,10 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&sm.q_full, 1);
     ptx::mbar_init(&sm.q_empty, 2);
     for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(&sm.s_full[t], 1);
-      ptx::mbar_init(&sm.p_full[t][0], 4);
-      ptx::mbar_init(&sm.p_full[t][1], 4);
-      ptx::mbar_init(&sm.o_full[t], 1);
+      for (int u = 0; u < 2; ++u) {
+        ptx::mbar_init(&sm.s_full[t][u], 1);
+        ptx::mbar_init(&sm.p_full[t][u], 4);
+      }
+      ptx::mbar_init(&sm.o_done[t], 1);
     }
     ptx::mbar_init(&sm.done, 2);
     ptx::fence_mbar_init();
@@ -444,24 +443,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kLoader) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    int stage = 0;
-    uint32_t phase = 0, q_phase = 0;
-    auto advance = [&] {
-      if (++stage == STAGES) {
-        stage = 0;
+    uint32_t q_phase = 0;
+    auto advance2 = [](int& stage, uint32_t& phase) {     // keys and values have every other stage
+      if ((stage += 2) >= STAGES) {
+        stage -= STAGES;
         phase ^= 1;
       }
     };
     if (warp < kIssuer) {
       // ---- loads: an item's queries; keys into the even stages, values into the odd ----
       const int v = warp - kLoader;
-      stage = v;
-      auto advance2 = [&] {
-        if ((stage += 2) >= STAGES) {
-          stage -= STAGES;
-          phase ^= 1;
-        }
-      };
+      int stage = v;
+      uint32_t phase = 0;
       Pages pages;
       int seq = -1;
       for (bool first = true; w.next(a, first); first = false) {
@@ -484,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
           load_tile<D, 1>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kAttnTile, w.kend - k0), 0,
                           sm.ring[stage], &sm.full[stage]);
-          advance2();
+          advance2(stage, phase);
         }
       }
       // After a wait that ran out, copies may still be in flight: the block stays for them.
@@ -493,17 +486,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (v == 0) ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
         for (int i = 0; i < STAGES; i += 2) {
           ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
-          advance2();
+          advance2(stage, phase);
         }
       }
     } else {
       // ---- products: a warp a row tile, so that neither waits for the other's softmax ----
       const int t = warp - kIssuer;
-      uint32_t p_phase = 0;
+      int k_stage = 0, v_stage = 1;
+      uint32_t k_phase = 0, v_phase = 0, p_phase = 0;
       const uint32_t q_addr = ptx::smem_addr(sm.q) + t * Sizes<D>::kHalf;
       const uint32_t ring = ptx::smem_addr(sm.ring);
       const uint32_t s_col = tmem + kColS + t * 128, o_col = tmem + kColO + t * 128;
-      const uint32_t id_s = idesc_bf16(kAttnTile, false), id_o = idesc_bf16(D, true);
+      const uint32_t id_s = idesc_bf16(kStep, false), id_o = idesc_bf16(D, true);
       for (bool first = true; w.next(a, first); first = false) {
         const int n = w.busy(key0);
         if (n == 0) continue;
@@ -511,60 +505,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_phase ^= 1;
         if (t == 1 && w.rows <= kTileRows) {     // no rows: the operands pass by
           if (lane == 0) ptx::mbar_arrive(&sm.q_empty);
-          for (int i = 0; i < 2 * n; ++i) {
-            ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
-            if (lane == 0) ptx::mbar_arrive(&sm.empty[stage]);
+          for (int i = 0; i < n; ++i) {
+            ptx::mbar_wait(&sm.full[k_stage], k_phase, abort, kAttnWaitNs);
+            if (lane == 0) ptx::mbar_arrive(&sm.empty[k_stage]);
+            advance2(k_stage, k_phase);
+            ptx::mbar_wait(&sm.full[v_stage], v_phase, abort, kAttnWaitNs);
+            if (lane == 0) ptx::mbar_arrive(&sm.empty[v_stage]);
+            advance2(v_stage, v_phase);
             __syncwarp();
-            advance();
           }
           continue;
         }
-        for (int i = 0; i <= n; ++i) {
-          // P V of tile i - 1, then the scores of tile i
-          if (i > 0) {
-            const int keys = min(kAttnTile, w.kend - (key0 + (w.first + i - 1) * kAttnTile));
-            const int steps = (keys + 15) / 16;
-            const uint32_t v_addr = ring + stage * Sizes<D>::kTileBytes;
-            ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
-            // P comes in halves: the first one's products run while the second is made
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              ptx::mbar_wait(&sm.p_full[t][h], p_phase, abort, kAttnWaitNs);
-              ptx::tc_fence_after();
-              if (ptx::elect_one()) {
-#pragma unroll
-                for (int k = 4 * h; k < 4 * h + 4; ++k)
-                  if (k < steps)
-                    mma_ts(o_col, s_col + k * 8, desc_rows(v_addr + k * 2048, Sizes<D>::kHalf),
-                           id_o, i > 1 || k > 0);
-                if (h == 1) {
-                  ptx::tc_commit(&sm.empty[stage]);
-                  if (i == n) ptx::tc_commit(&sm.o_full[t]);
-                }
-              }
-              __syncwarp();
-            }
-            p_phase ^= 1;
-            advance();
-          }
-          if (i < n) {
-            const uint32_t k_addr = ring + stage * Sizes<D>::kTileBytes;
-            ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+        const int keys = min(w.kend - key0 - w.first * kAttnTile, n * kAttnTile);
+        const int steps = (keys + kStep - 1) / kStep;
+        // Scores of step j into its half of the tile's columns; a step of the two that share a
+        // tile of keys waits for it, the last of them hands it back.
+        auto scores = [&](int j) {
+          if ((j & 1) == 0) {
+            ptx::mbar_wait(&sm.full[k_stage], k_phase, abort, kAttnWaitNs);
             ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_ss(s_col,
-                       ptx::desc_sw128(q_addr + (k >> 2) * 2 * Sizes<D>::kHalf + (k & 3) * 32),
-                       ptx::desc_sw128(k_addr + (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32), id_s,
-                       k > 0);
-              ptx::tc_commit(&sm.s_full[t]);
-              ptx::tc_commit(&sm.empty[stage]);
-              if (i + 1 == n) ptx::tc_commit(&sm.q_empty);
-            }
-            __syncwarp();
-            advance();
           }
+          const bool last = (j & 1) != 0 || j + 1 == steps;
+          if (ptx::elect_one()) {
+            const uint32_t k_addr =
+                ring + k_stage * Sizes<D>::kTileBytes + (j & 1) * (kStep * 128);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(s_col + (j & 1) * kStep,
+                     ptx::desc_sw128(q_addr + (k >> 2) * 2 * Sizes<D>::kHalf + (k & 3) * 32),
+                     ptx::desc_sw128(k_addr + (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32), id_s,
+                     k > 0);
+            ptx::tc_commit(&sm.s_full[t][j & 1]);
+            if (last) ptx::tc_commit(&sm.empty[k_stage]);
+            if (j + 1 == steps) ptx::tc_commit(&sm.q_empty);
+          }
+          __syncwarp();
+          if (last) advance2(k_stage, k_phase);
+        };
+        scores(0);
+        if (steps > 1) scores(1);
+        for (int j = 0; j < steps; ++j) {
+          if ((j & 1) == 0) ptx::mbar_wait(&sm.full[v_stage], v_phase, abort, kAttnWaitNs);
+          ptx::mbar_wait(&sm.p_full[t][j & 1], (p_phase >> (j & 1)) & 1, abort, kAttnWaitNs);
+          p_phase ^= 1u << (j & 1);
+          ptx::tc_fence_after();
+          const bool last = (j & 1) != 0 || j + 1 == steps;
+          const int parts = (min(kStep, keys - j * kStep) + 15) / 16;
+          if (ptx::elect_one()) {
+            const uint32_t v_addr =
+                ring + v_stage * Sizes<D>::kTileBytes + (j & 1) * (kStep * 128);
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k)
+              if (k < parts)
+                mma_ts(o_col, s_col + (j & 1) * kStep + k * 8,
+                       desc_rows(v_addr + k * 2048, Sizes<D>::kHalf), id_o, j > 0 || k > 0);
+            ptx::tc_commit(&sm.o_done[t]);
+            if (last) ptx::tc_commit(&sm.empty[v_stage]);
+          }
+          __syncwarp();
+          if (last) advance2(v_stage, v_phase);
+          if (j + 2 < steps) scores(j + 2);
         }
       }
       // no product may be in flight when tensor memory is given back
@@ -579,97 +579,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = threadIdx.x;             // row of the item
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // 32 lanes a warp
     const uint32_t s_col = lanes + kColS + t * 128, o_col = lanes + kColO + t * 128;
-    uint32_t s_phase = 0, o_phase = 0;
-    // The two warpgroups take turns at the arithmetic: while one has its scores, the other's
-    // products run.  (Side by side they would end together and wait for the tensor cores
-    // together: 1840 us instead of 1647 for a prompt of 16384 tokens, 32 heads.)
-    if (t == 1) named_bar_arrive(2, 256);
-    int loads = 0;                                         // stages that earlier items took
+    const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
+    uint32_t s_phase = 0, o_phase = 0;                    // o_phase: of the last product's end
+    int loads = 0;                                        // tiles of values that earlier items took
     for (bool first = true; w.next(a, first); first = false) {
       const int n = w.busy(key0);
       const int v0 = loads;
-      loads += 2 * n;
+      loads += n;
       if (t == 1 && w.rows <= kTileRows) continue;
       const int limit = row_limit(a, w, r);
-      const bool both = w.rows > kTileRows;
+      const int base = key0 + w.first * kAttnTile;
+      const int keys = min(w.kend - base, n * kAttnTile);
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < n; ++i) {
-        const int k0 = key0 + (w.first + i) * kAttnTile;
-        ptx::mbar_wait(&sm.s_full[t], s_phase, abort, kAttnWaitNs);
-        s_phase ^= 1;
+      for (int j = 0; j * kStep < keys; ++j) {
+        const uint32_t x_col = s_col + (j & 1) * kStep;
+        ptx::mbar_wait(&sm.s_full[t][j & 1], (s_phase >> (j & 1)) & 1, abort, kAttnWaitNs);
+        s_phase ^= 1u << (j & 1);
         ptx::tc_fence_after();
-        uint32_t x[128];
+        uint32_t x[kStep];
+        tmem_ld32_issue(x_col, x);
+        tmem_ld32_issue(x_col + 32, x + 32);
+        tmem_wait_ld32(x);
+        tmem_wait_ld32(x + 32);
+        const int seen = limit - base - j * kStep;
+        if (__any_sync(0xFFFFFFFFu, seen < kStep)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32_issue(s_col + j * 32, x + j * 32);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_wait_ld32(x + j * 32);
-        if (both) ptx::named_bar_sync(2 + t, 256);
-        if (__any_sync(0xFFFFFFFFu, k0 + kAttnTile > limit)) {
-          const int seen = limit - k0;
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (j >= seen) x[j] = 0xFF800000u;
+          for (int e = 0; e < kStep; ++e)
+            if (e >= seen) x[e] = 0xFF800000u;
         }
-        // The first half's terms against the maximum so far, while the tile's own maximum is
-        // found: it passes by 2^8 in few tiles but an item's first, and then they are made
-        // again.
-        const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-        uint64_t sum[2];
-        uint32_t p[32];
-        float from = m == -INFINITY ? 0.f : m;
-        terms(p, x, scale2, from, sum);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j]));
+        for (int e = 0; e < kStep; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
         const float up = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
         if (__any_sync(0xFFFFFFFFu, up > m + 8.f)) {
           const float to = fmaxf(m, up);
           const float f = to == m ? 1.f : exp2_approx(m - to);
           m = to;
           l *= f;
-          if (i > 0) {
+          if (j > 0) {
+            ptx::mbar_wait(&sm.o_done[t], o_phase ^ 1, abort, kAttnWaitNs);
+            ptx::tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
+            for (int e0 = 0; e0 < D; e0 += 32) {
               uint32_t o[32];
-              tmem_ld32_issue(o_col + j, o);
+              tmem_ld32_issue(o_col + e0, o);
               tmem_wait_ld32(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              ptx::tmem_st16(o_col + j, *reinterpret_cast<uint32_t(*)[16]>(o));
-              ptx::tmem_st16(o_col + j + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+              ptx::tmem_st16(o_col + e0, *reinterpret_cast<uint32_t(*)[16]>(o));
+              ptx::tmem_st16(o_col + e0 + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
             }
           }
-          from = m == -INFINITY ? 0.f : m;
-          terms(p, x, scale2, from, sum);
         }
-        if (w.kend - k0 < kAttnTile && (w.kend - k0) % 16 != 0) {
+        if (keys - j * kStep < kStep && keys % 16 != 0) {
           // values behind the last key may be anything, and 0 times them must be 0: the rows
           // that share the last key's sixteen are cleared, by each row tile before its own
           // products (the second to come writes zeros over zeros)
-          const int at = v0 + 2 * i + 1, stage = at % STAGES;
-          ptx::mbar_wait(&sm.full[stage], (at / STAGES) & 1, abort, kAttnWaitNs);
-          const int from_row = w.kend - k0, to_row = (from_row + 15) / 16 * 16;
+          const int at = v0 + j / 2, v = 2 * (at % (STAGES / 2)) + 1;
+          ptx::mbar_wait(&sm.full[v], (at / (STAGES / 2)) & 1, abort, kAttnWaitNs);
+          const int from_row = keys % kAttnTile, to_row = (from_row + 15) / 16 * 16;
           for (int e = threadIdx.x & 127; e < (to_row - from_row) * (D / 8); e += 128) {
             const int vr = from_row + e / (D / 8), piece = e % (D / 8);
-            *reinterpret_cast<uint4*>(sm.ring[stage] + (piece >> 3) * Sizes<D>::kHalf + vr * 128 +
+            *reinterpret_cast<uint4*>(sm.ring[v] + (piece >> 3) * Sizes<D>::kHalf + vr * 128 +
                                       ((piece & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
           ptx::fence_proxy_async_smem();
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            l += lo_of(sum[0]) + hi_of(sum[0]) + (lo_of(sum[1]) + hi_of(sum[1]));
-            terms(p, x + 64, scale2, from, sum);
-            if (both) named_bar_arrive(3 - t, 256);
-          }
-          ptx::tmem_st16(s_col + h * 32, *reinterpret_cast<uint32_t(*)[16]>(p));
-          ptx::tmem_st16(s_col + h * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(p + 16));
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][h]);
-        }
+        const float from = m == -INFINITY ? 0.f : m;
+        uint64_t sum[2] = {0, 0};
+        uint32_t p[32];
+        terms(p, x, scale2, from, sum);
+        ptx::tmem_st16(x_col, *reinterpret_cast<uint32_t(*)[16]>(p));
+        ptx::tmem_st16(x_col + 16, *reinterpret_cast<uint32_t(*)[16]>(p + 16));
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][j & 1]);
+        o_phase ^= 1;
         l += lo_of(sum[0]) + hi_of(sum[0]) + (lo_of(sum[1]) + hi_of(sum[1]));
       }
 
@@ -705,8 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint8_t* stage = sm.stage[warp];
       if (n > 0) {
-        ptx::mbar_wait(&sm.o_full[t], o_phase, abort, kAttnWaitNs);
-        o_phase ^= 1;
+        ptx::mbar_wait(&sm.o_done[t], o_phase ^ 1, abort, kAttnWaitNs);
         ptx::tc_fence_after();
       }
       if (SHARED || !whole) {
