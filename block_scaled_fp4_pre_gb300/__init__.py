@@ -182,6 +182,7 @@ def lib() -> ctypes.CDLL:
             "moe_rope": ([RD, vp, vp, i64, vp, i64, i32, vp, i64, vp], i32),
             "moe_attention_workspace_size": ([AD], sz),
             "moe_attention_workspace_init": ([AD, vp, sz, vp], i32),
+            "moe_attention_set_shared": ([vp, i32], i32),
             "moe_kv_append": ([AD, KB, RD, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
                                vp, sz, vp], i32),
             "moe_attention": ([AD, KB, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, sz, vp],
@@ -651,6 +652,16 @@ def moe_attention_workspace_size(dims: AttentionDims) -> int:
 def moe_attention_workspace_init(dims: AttentionDims, ws, stream=None) -> None:
     _check(lib().moe_attention_workspace_init(ctypes.byref(dims), _bytes(ws, 0, "workspace"),
                                               _nbytes(ws), _stream(stream)))
+
+
+MOE_SHARED_AUTO = 0
+MOE_SHARED_ALWAYS = 1
+MOE_SHARED_NEVER = 2
+
+
+def moe_attention_set_shared(ws, mode: int) -> None:
+    """A shared prefix in one pass for the batch, for each sequence, or what pays (auto)."""
+    _check(lib().moe_attention_set_shared(_ptr(ws), int(mode)))
 
 
 def _cache(t, dims: AttentionDims, name: str, device: int) -> int:

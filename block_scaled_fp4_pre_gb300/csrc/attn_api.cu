@@ -123,7 +123,11 @@ AttnWs ws_layout(const moe_attention_dims& d) {
 }
 
 std::mutex g_mu;
-std::map<const void*, moe_attention_dims> g_attention;
+struct AttnState {
+  moe_attention_dims dims;
+  int32_t shared;   // moe_attention_set_shared
+};
+std::map<const void*, AttnState> g_attention;
 
 bool power_of_two(int v) { return v > 0 && (v & (v - 1)) == 0; }
 int shift_of(int v) {
@@ -165,7 +169,8 @@ bool same(const moe_attention_dims& a, const moe_attention_dims& b) {
          a.max_tokens == b.max_tokens && a.max_shared_tokens == b.max_shared_tokens;
 }
 
-moe_status check_ws(const moe_attention_dims* d, const void* ws, size_t ws_bytes) {
+moe_status check_ws(const moe_attention_dims* d, const void* ws, size_t ws_bytes,
+                    int32_t* shared) {
   if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
   const size_t need = ws_layout(*d).total;
@@ -176,8 +181,9 @@ moe_status check_ws(const moe_attention_dims* d, const void* ws, size_t ws_bytes
   if (it == g_attention.end())
     return fail(MOE_ERR_WORKSPACE_MISMATCH,
                 "workspace %p was not initialised by moe_attention_workspace_init", ws);
-  if (!same(it->second, *d))
+  if (!same(it->second.dims, *d))
     return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was initialised for other dims", ws);
+  *shared = it->second.shared;
   return MOE_OK;
 }
 
@@ -294,10 +300,22 @@ moe_status moe_attention_workspace_init(const moe_attention_dims* d, void* ws, s
   if (e != cudaSuccess) return cuda_fail(e, "workspace clear");
   try {
     std::lock_guard<std::mutex> lk(g_mu);
-    g_attention[ws] = *d;
+    g_attention[ws] = AttnState{*d, MOE_SHARED_AUTO};
   } catch (...) {
     return fail(MOE_ERR_CUDA, "out of host memory for the workspace registry");
   }
+  return MOE_OK;
+}
+
+moe_status moe_attention_set_shared(void* ws, int32_t mode) {
+  if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if (mode < MOE_SHARED_AUTO || mode > MOE_SHARED_NEVER)
+    return fail(MOE_ERR_INVALID_ARG, "unknown mode %d", mode);
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_attention.find(ws);
+  if (it == g_attention.end())
+    return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was not initialised", ws);
+  it->second.shared = mode;
   return MOE_OK;
 }
 
@@ -308,7 +326,8 @@ moe_status moe_kv_append(const moe_attention_dims* d, const moe_kv_batch* batch,
                          void* ws, size_t ws_bytes, void* stream) {
   moe_status s = check_dims(d);
   if (s) return s;
-  if ((s = check_ws(d, ws, ws_bytes))) return s;
+  int32_t shared;
+  if ((s = check_ws(d, ws, ws_bytes, &shared))) return s;
   RopeArgs a = {};
   if ((s = check_batch(d, batch, &a.batch))) return s;
   if ((rope == nullptr) != (table == nullptr))
@@ -363,7 +382,8 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
                          void* stream) {
   moe_status s = check_dims(d);
   if (s) return s;
-  if ((s = check_ws(d, ws, ws_bytes))) return s;
+  int32_t shared = 0;
+  if ((s = check_ws(d, ws, ws_bytes, &shared))) return s;
   AttnLaunch g = {};
   if ((s = check_batch(d, batch, &g.args.batch))) return s;
   if (!(scale > 0.f) || std::isinf(scale))
@@ -401,7 +421,8 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
   a.shared_parts = reinterpret_cast<float*>(w + L.shared_parts);
   a.parts = reinterpret_cast<float*>(w + L.parts);
   g.head_dim = d->head_dim;
-  g.shared = batch->shared_len > 0 && batch->tokens <= d->max_shared_tokens;
+  g.shared = batch->shared_len > 0 && batch->tokens <= d->max_shared_tokens ? shared
+                                                                            : MOE_SHARED_NEVER;
   g.num_sms = moe_device_sm_count();
   if (g.num_sms <= 0 || cudaGetDevice(&g.device) != cudaSuccess)
     return fail(MOE_ERR_CUDA, "no CUDA device");

@@ -53,7 +53,7 @@ struct Smem {
   uint8_t stage[8][4096];
   int64_t scan[kThreads / 32];
   uint64_t full[Sizes<D>::kStages], empty[Sizes<D>::kStages];
-  uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2], done;
+  uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_prev[2], o_full[2], done;
   int64_t start_at;
   int start_left, start_seq, start_head, start_rt, start_tile;
   int kend;                                     // SHARED: keys that some row sees
@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&sm.s_full[t][u], 1);
         ptx::mbar_init(&sm.p_full[t][u], 4);
       }
-      ptx::mbar_init(&sm.o_done[t], 1);
+      ptx::mbar_init(&sm.o_prev[t], 1);
+      ptx::mbar_init(&sm.o_full[t], 1);
     }
     ptx::mbar_init(&sm.done, 2);
     ptx::fence_mbar_init();
@@ -571,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (k < parts)
                 mma_ts(o_col, s_col + (j & 1) * kStep + k * 8,
                        desc_rows(v_addr + k * 2048, Sizes<D>::kHalf), id_o, j > 0 || k > 0);
-            ptx::tc_commit(&sm.o_done[t]);
+            if (j + 2 == steps) ptx::tc_commit(&sm.o_prev[t]);
+            if (j + 1 == steps) ptx::tc_commit(&sm.o_full[t]);
             if (last) ptx::tc_commit(&sm.empty[v_stage]);
           }
           __syncwarp();
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // 32 lanes a warp
     const uint32_t s_col = lanes + kColS + t * 128, o_col = lanes + kColO + t * 128;
     const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-    uint32_t s_phase = 0, o_phase = 0;                    // o_phase: of the last product's end
+    uint32_t s_phase = 0, prev_phase = 0, o_phase = 0;
     int loads = 0;                                        // tiles of values that earlier items took
     for (bool first = true; w.next(a, first); first = false) {
       const int n = w.busy(key0);
@@ -629,7 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = to;
           l *= f;
           if (j > 0) {
-            ptx::mbar_wait(&sm.o_done[t], o_phase ^ 1, abort, kAttnWaitNs);
+            // No product may be in flight on the output: step j - 1's end comes before the scores
+            // of step j + 1, or has a barrier of its own before the item's last step.
+            if ((j + 1) * kStep < keys)
+              ptx::mbar_wait(&sm.s_full[t][(j + 1) & 1], (s_phase >> ((j + 1) & 1)) & 1, abort,
+                             kAttnWaitNs);
+            else
+              ptx::mbar_wait(&sm.o_prev[t], prev_phase, abort, kAttnWaitNs);
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int e0 = 0; e0 < D; e0 += 32) {
@@ -667,7 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][j & 1]);
-        o_phase ^= 1;
         l += lo_of(sum[0]) + hi_of(sum[0]) + (lo_of(sum[1]) + hi_of(sum[1]));
       }
 
@@ -703,7 +710,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint8_t* stage = sm.stage[warp];
       if (n > 0) {
-        ptx::mbar_wait(&sm.o_done[t], o_phase ^ 1, abort, kAttnWaitNs);
+        if (keys > kStep) {
+          ptx::mbar_wait(&sm.o_prev[t], prev_phase, abort, kAttnWaitNs);
+          prev_phase ^= 1;
+        }
+        ptx::mbar_wait(&sm.o_full[t], o_phase, abort, kAttnWaitNs);
+        o_phase ^= 1;
         ptx::tc_fence_after();
       }
       if (SHARED || !whole) {

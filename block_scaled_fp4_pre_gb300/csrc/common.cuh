@@ -436,7 +436,7 @@ struct AttnArgs {
 struct AttnLaunch {
   AttnArgs args;
   int head_dim;
-  bool shared;                     // the shared prefix is computed once for the batch
+  int shared;                      // MOE_SHARED_*
   int device, num_sms;             // the current device
 };
 cudaError_t launch_attention(const AttnLaunch& g, cudaStream_t st);

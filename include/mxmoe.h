@@ -526,13 +526,21 @@ typedef struct moe_kv_batch {
 } moe_kv_batch;
 
 /* Bytes of the workspace; 0 for bad dims.  Host only.  max_shared_tokens sizes the part that
- * calls with a shared prefix use; calls of more tokens read the prefix once for each sequence
- * instead, with the same results up to fp32 summation order. */
+ * calls with a shared prefix use; calls of more tokens read the prefix for each sequence. */
 MXMOE_API size_t moe_attention_workspace_size(const moe_attention_dims *dims);
 /* Clears and registers a workspace (256-byte aligned), as moe_workspace_init does for the
  * layer's.  One call at a time may use a workspace. */
 MXMOE_API moe_status moe_attention_workspace_init(const moe_attention_dims *dims, void *ws_dev,
                                                   size_t ws_bytes, void *stream);
+
+/* How calls on this workspace compute a shared prefix:
+ *   MOE_SHARED_AUTO (default after moe_attention_workspace_init)  in one pass for the batch
+ *                     where an estimate of both says that it pays, else for each sequence;
+ *   MOE_SHARED_ALWAYS, MOE_SHARED_NEVER  the one or the other (ALWAYS up to max_shared_tokens).
+ * The results are the same up to fp32 summation order.  Host only.  MOE_ERR_INVALID_ARG for an
+ * unknown mode, MOE_ERR_WORKSPACE_MISMATCH for a workspace that was not initialised. */
+enum { MOE_SHARED_AUTO = 0, MOE_SHARED_ALWAYS = 1, MOE_SHARED_NEVER = 2 };
+MXMOE_API moe_status moe_attention_set_shared(void *ws_dev, int32_t mode);
 
 /* Writes the new tokens' keys and values into the cache, the keys rotated on the way, and
  * rotates the queries:

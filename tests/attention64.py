@@ -47,7 +47,8 @@ class Paged:
     that no sequence reaches hold NaN."""
 
     def __init__(self, new, old, q_heads=8, kv_heads=2, D=128, page=16, shared=0, seed=0,
-                 uniform=False, spare=0, max_shared=None, tail=0, wide=0, q_size=2.0):
+                 uniform=False, spare=0, max_shared=None, tail=0, wide=0, q_size=2.0,
+                 share=mx.MOE_SHARED_ALWAYS):
         rng, g = random.Random(seed), torch.Generator(device="cuda").manual_seed(seed)
         self.new, self.shared, self.D, self.page = new, shared, D, page
         self.hq, self.hk = q_heads, kv_heads
@@ -69,12 +70,12 @@ class Paged:
         self.k, self.v = (torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
                           for _ in range(2))
         for b in range(len(new)):
-            for j in range(self.lens[b]):
-                if b and j < shared:
-                    continue
-                p, r = self.slot(b, j)
-                self.k[p, :, r] = torch.randn(kv_heads, D, generator=g, device="cuda").bfloat16()
-                self.v[p, :, r] = torch.randn(kv_heads, D, generator=g, device="cuda").bfloat16()
+            at = [self.slot(b, j) for j in range(shared if b else 0, self.lens[b])]
+            if at:
+                p, r = (torch.tensor(x, device="cuda") for x in zip(*at))
+                for cache in (self.k, self.v):
+                    cache[p, :, r] = torch.randn(len(at), kv_heads, D, generator=g,
+                                                 device="cuda").bfloat16()
         self.q = (torch.randn(self.T, q_heads, D, generator=g, device="cuda") * q_size).bfloat16()
         cu = [0]
         for n in new:
@@ -90,6 +91,7 @@ class Paged:
         self.ws = torch.empty(mx.moe_attention_workspace_size(self.dims), dtype=torch.uint8,
                               device="cuda").fill_(255)
         mx.moe_attention_workspace_init(self.dims, self.ws)
+        mx.moe_attention_set_shared(self.ws, share)
 
     def slot(self, b, j):
         return int(self.table[0 if j < self.shared else b, j // self.page]), j % self.page
@@ -147,3 +149,25 @@ class Paged:
         assert torch.all(out[self.cu[-1]:] == 77.0)
         if lse is not None:
             assert torch.all(lse[self.cu[-1]:] == 77.0)
+
+    def check_rows(self, out, lse):
+        """As check, sequence by sequence and head by head."""
+        G, scale = self.hq // self.hk, self.D ** -0.5
+        for b, n in enumerate(self.new):
+            K, V = self.rows(self.k, b), self.rows(self.v, b)
+            L, t = self.lens[b], slice(self.cu[b], self.cu[b + 1])
+            hidden = torch.arange(L, device="cuda") > torch.arange(L - n, L, device="cuda").view(n, 1)
+            ends = torch.arange(L - n + 1, L + 1, device="cuda").double().view(n, 1)
+            for h in range(self.hq):
+                q, k, v = self.q[t, h].double(), K[:, h // G], V[:, h // G]
+                s = (q @ k.T * scale).masked_fill_(hidden, -math.inf)
+                e = ((q.abs() @ k.abs().T).masked_fill_(hidden, 0).amax(-1, True) * scale
+                     * (self.D + 4) * 2.0 ** -23)
+                top = torch.logsumexp(s, -1, keepdim=True)
+                p = torch.exp(s - top)
+                want, size = p @ v, p @ v.abs()
+                tol = size * (2.0 ** -8 + 2 * torch.expm1(e) + ends * 2.0 ** -23 + 2.0 ** -20)
+                tol = tol + (want.abs() + tol) * 2.0 ** -8
+                assert torch.all((out[t, h].double() - want).abs() <= tol), (b, h)
+                tol = e + ends * 2.0 ** -23 + (top.abs() + 1) * 2.0 ** -21
+                assert torch.all((lse[t, h].double().view(n, 1) - top).abs() <= tol), (b, h)

@@ -87,6 +87,7 @@ def test_rope_of_no_tokens_is_a_no_op(mx):
 @pytest.mark.parametrize("change,status", [
     (dict(head_dim=96), 2), (dict(head_dim=0), 2), (dict(head_dim=256), 2), (dict(kv_heads=0), 1),
     (dict(kv_heads=3), 1), (dict(q_heads=0), 1), (dict(q_heads=1026), 1),
+    (dict(q_heads=514, kv_heads=2), 1),
     (dict(q_heads=1, kv_heads=2), 1), (dict(page_size=8), 1), (dict(page_size=48), 1),
     (dict(page_size=512), 1), (dict(page_size=-16), 1), (dict(num_pages=0), 1),
     (dict(num_pages=1 << 26), 1), (dict(num_pages=(1 << 31) - 1), 1), (dict(max_tokens=0), 1),
@@ -112,6 +113,9 @@ def test_workspaces(mx):
     assert f.moe_attention_workspace_init(ref, 1040, 1 << 40, None) == mx.MOE_ERR_INVALID_ARG
     assert f.moe_attention_workspace_init(ref, 1024, 16, None) == mx.MOE_ERR_WORKSPACE_TOO_SMALL
     assert f.moe_attention_workspace_init(None, 1024, 16, None) == mx.MOE_ERR_INVALID_ARG
+    assert f.moe_attention_set_shared(None, 0) == mx.MOE_ERR_INVALID_ARG
+    assert f.moe_attention_set_shared(1024, 3) == mx.MOE_ERR_INVALID_ARG
+    assert f.moe_attention_set_shared(1024, 0) == mx.MOE_ERR_WORKSPACE_MISMATCH
     assert f.moe_attention_check(None, None) == mx.MOE_ERR_INVALID_ARG
     assert f.moe_attention_check(1024, None) == mx.MOE_ERR_WORKSPACE_MISMATCH
     b = mx.KvBatch(1024, None, 1024, 1, 1, 1, 4, 0)

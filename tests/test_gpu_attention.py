@@ -44,6 +44,19 @@ def test_prompts(n, D):
     both(new=[n, n], old=[3, 200], D=D, uniform=True)
 
 
+@pytest.mark.parametrize("D,q_heads,kv_heads,new,old,shared", [
+    (128, 32, 8, [3000], [0], 0), (64, 13, 13, [124, 90, 78] * 6, [0] * 18, 768),
+    (128, 39, 13, [157, 142, 150] * 4, [88, 474, 200] * 4, 0), (64, 2, 2, [1000] * 30, [0] * 30, 0),
+    (128, 8, 8, [2100, 1], [1000, 5000], 0)])
+def test_many_tiles(D, q_heads, kv_heads, new, old, shared):
+    # long enough lines for every block to have several items and products queued behind them
+    p = Paged(new=new, old=old, q_heads=q_heads, kv_heads=kv_heads, D=D, page=128, shared=shared)
+    for mode in ((mx.MOE_SHARED_ALWAYS, mx.MOE_SHARED_NEVER) if shared else (0,)):
+        mx.moe_attention_set_shared(p.ws, mode)
+        for _ in range(3):
+            p.check_rows(*p.run())
+
+
 def test_ragged_batch():
     both(new=[1, 0, 17, 200, 0, 2, 1, 64, 0], old=[40, 30, 0, 129, 0, 1000, 0, 64, 5], page=32)
 
@@ -71,10 +84,38 @@ def test_sequences_without_a_token_give_zeros():
 def test_shared_prefix(new, uniform, shared, D):
     old = [(37 * i) % 150 for i in range(len(new))]
     p, out, lse = both(new=new, old=old, uniform=uniform, shared=shared, D=D)
-    # the same with the prefix computed for each sequence
+    # the same with the prefix computed for each sequence: by choice, or for want of workspace
+    mx.moe_attention_set_shared(p.ws, mx.MOE_SHARED_NEVER)
+    o2, l2 = p.run()
+    p.check(o2, l2)
     q = Paged(new=new, old=old, uniform=uniform, shared=shared, D=D, max_shared=0)
-    o2, l2 = q.run()
-    q.check(o2, l2)
+    o3, l3 = q.run()
+    assert torch.equal(o2, o3) and torch.equal(l2, l3)
+
+
+def test_one_sequence_with_a_shared_prefix():
+    both(new=[1], old=[40], shared=64, uniform=True)
+    both(new=[300], old=[40], shared=64, uniform=True)
+
+
+def test_a_prefix_that_pays_is_shared_by_itself():
+    # 16 MB of keys and values, 40 times: one pass by the estimate, as when it is asked for
+    p = Paged(new=[1] * 40, old=[3 * i for i in range(40)], shared=16384, q_heads=8, page=64,
+              share=mx.MOE_SHARED_AUTO, uniform=True)
+    a, l = p.run()
+    mx.moe_attention_set_shared(p.ws, mx.MOE_SHARED_ALWAYS)
+    b, m = p.run()
+    assert torch.equal(a, b) and torch.equal(l, m)
+    mx.moe_attention_set_shared(p.ws, mx.MOE_SHARED_NEVER)
+    c, _ = p.run()
+    assert not torch.equal(a, c)
+    p.check(a, l)
+
+
+def test_more_rows_than_the_blocks_take_together():
+    # the prefix's items outnumber the blocks: some whole, some cut
+    both(new=[40] * 20, old=[i for i in range(20)], shared=48, q_heads=128, kv_heads=16, D=64,
+         uniform=True)
 
 
 def test_shared_prefix_of_sequences_that_end_inside_it():
