@@ -156,8 +156,8 @@ class Paged:
         for b, n in enumerate(self.new):
             K, V = self.rows(self.k, b), self.rows(self.v, b)
             L, t = self.lens[b], slice(self.cu[b], self.cu[b + 1])
-            hidden = torch.arange(L, device="cuda") > torch.arange(L - n, L, device="cuda").view(n, 1)
-            ends = torch.arange(L - n + 1, L + 1, device="cuda").double().view(n, 1)
+            ends = torch.arange(L - n + 1, L + 1, device="cuda").view(n, 1)
+            hidden = torch.arange(L, device="cuda") >= ends
             for h in range(self.hq):
                 q, k, v = self.q[t, h].double(), K[:, h // G], V[:, h // G]
                 s = (q @ k.T * scale).masked_fill_(hidden, -math.inf)

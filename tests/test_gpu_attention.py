@@ -231,8 +231,9 @@ def test_refusals():
         b = mx.KvBatch(*(batch or good).values())
         a = f.moe_attention(ctypes.byref(D), ctypes.byref(b), q, ldq, k, v, scale, o, ldo, lse,
                             p.ws.data_ptr(), p.ws.nbytes, None)
-        c = append and f.moe_kv_append(ctypes.byref(D), ctypes.byref(b), None, None, None, None, 0, None, 0, q,
-                            ldq, o, ldo, k, v, p.ws.data_ptr(), p.ws.nbytes, None)
+        c = append and f.moe_kv_append(ctypes.byref(D), ctypes.byref(b), None, None, None, None, 0,
+                                       None, 0, q, ldq, o, ldo, k, v, p.ws.data_ptr(),
+                                       p.ws.nbytes, None)
         return a, c
 
     bad, ok = mx.MOE_ERR_INVALID_ARG, mx.MOE_OK
