@@ -38,7 +38,7 @@ cudaError_t launch_attention(const AttnLaunch& call, cudaStream_t st) {
   AttnLaunch g = call;
   AttnArgs& a = g.args;
   const uint64_t rows = ((uint64_t)a.num_pages * a.kv_heads) << a.page_shift;
-  const uint32_t box = a.page_shift < 7 ? 1u << a.page_shift : kAttnTile;
+  const uint32_t box = 1u << a.page_shift < kAttnBox ? 1u << a.page_shift : kAttnBox;
   CUtensorMap k, v;
   cudaError_t e = make_tmap_bf16(&k, a.k_cache, g.head_dim, rows, box);
   if (e == cudaSuccess) e = make_tmap_bf16(&v, a.v_cache, g.head_dim, rows, box);

@@ -1,7 +1,7 @@
 // What the attention kernels share: the line of work that they cut into equal ranges, and the
 // loads of keys and values by page.
 //
-// The work of a call is a line of tiles (128 keys of one item), item after item; block c of N
+// The work of a call is a line of tiles (128 or 64 keys of one item), item after item; block c of N
 // takes the tiles [c W / N, (c + 1) W / N).  So every block streams the same number of keys,
 // whatever the sequences' lengths, and an item is cut only where a block's range ends: a block
 // has at most two parts of items, its first and its last.  Parts go to the workspace, and the
@@ -16,7 +16,8 @@
 
 namespace mxmoe {
 
-constexpr int kAttnTile = 128;            // keys of a tile
+constexpr int kAttnTile = 128;            // keys of a tile of the few-row kernel
+constexpr int kAttnBox = 64;              // most keys of a box that is loaded
 constexpr int kAttnMostKeys = 1 << 30;    // of a sequence
 constexpr unsigned long long kAttnWaitNs = 2000000000ull;
 
@@ -119,28 +120,28 @@ __device__ __forceinline__ int cache_row(const AttnArgs& a, int page, int head, 
   return ((page * a.kv_heads + head) << a.page_shift) + r;
 }
 
-// Loads one tile of keys (or values) from key k0 of a sequence, `keys` of them (1 ..
-// kAttnTile), into dst: [D / 64][kAttnTile rows][128 bytes], swizzled; what no box covers keeps
-// its old contents.  PARTS converged warps share the boxes, each its own with an arrival of its
+// Loads one tile of keys (or values) from key k0 of a sequence, `keys` of them (1 .. TILE), into
+// dst: [D / 64][TILE rows][128 bytes], swizzled; what no box covers keeps its old contents.  PARTS converged warps share the boxes, each its own with an arrival of its
 // own on bar.  A box takes its warp 130 cycles to issue from a lane each (260 one after another
 // by an elected lane), so pages of 16 keys need the warps; copies themselves overlap.
-template <int D, int PARTS>
+template <int D, int TILE, int PARTS>
 __device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* map, Pages& pages,
                                           int head, int k0, int keys, int part, uint8_t* dst,
                                           uint64_t* bar) {
   constexpr int HALVES = D / 64;
-  const int box = min(1 << a.page_shift, kAttnTile);
+  const int box = min(1 << a.page_shift, kAttnBox);
   const int boxes = (keys + box - 1) / box, mine = (boxes * HALVES - part + PARTS - 1) / PARTS;
   const int first = k0 >> a.page_shift, r = k0 & ((1 << a.page_shift) - 1);
   const int lane = threadIdx.x & 31;
   if (lane == 0) ptx::mbar_arrive_expect_tx(bar, mine * box * 128);
-  pages.fetch(a, first, boxes);
-  const int which = min(lane, mine - 1) * PARTS + part, i = max(which, 0) / HALVES;
-  const int page = pages.at(first + i);
+  pages.fetch(a, first, ((r + (boxes - 1) * box) >> a.page_shift) + 1);
+  const int which = max(min(lane, mine - 1) * PARTS + part, 0), i = which / HALVES;
+  const int at = r + i * box;                      // (a page may hold several boxes)
+  const int page = pages.at(first + (at >> a.page_shift));
   __syncwarp();
   if (lane < mine) {
-    const int y = cache_row(a, page, head, r), h = which % HALVES;
-    ptx::tma_load_2d(dst + (h * kAttnTile + i * box) * 128, map, h * 64, y, bar,
+    const int y = cache_row(a, page, head, at & ((1 << a.page_shift) - 1)), h = which % HALVES;
+    ptx::tma_load_2d(dst + (h * TILE + i * box) * 128, map, h * 64, y, bar,
                      ptx::policy_evict_normal());
   }
   __syncwarp();

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k0 = a.kstart + t * kAttnTile, keys = min(kAttnTile, w.s.kend - k0);
         if (keys <= 0) continue;
         ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-        load_tile<D, kLoaders>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, part,
+        load_tile<D, kAttnTile, kLoaders>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, part,
                                sm.ring[stage], &sm.full[stage]);
         advance2();
       }

@@ -27,6 +27,7 @@
 namespace mxmoe {
 namespace {
 
+constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kTileRows = 128;
 // Warps: eight with a row a thread, one that loads queries and keys and one for values, one a row
 // tile that issues its products.
@@ -37,20 +38,25 @@ constexpr int kThreads = 384;                   // whole warpgroups, as register
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the launch's registers");
 
+constexpr int kTile = 64;                       // keys of a tile
+
 template <int D>
 struct Sizes {
-  static constexpr int kTileBytes = kTileRows * D * 2;   // of keys or values, half the queries
-  static constexpr int kHalf = kTileRows * 128;             // 64 columns of a tile
+  static constexpr int kBytes = kTile * D * 2;              // a tile of keys or values
+  static constexpr int kHalf = kTile * 128;                 // 64 columns of it
+  static constexpr int kQueries = kAttnRows * D * 2;
+  static constexpr int kQueryHalf = kAttnRows * 128;
   static constexpr int kStage = 8 * 4096;                   // 32 rows of 128 bytes a warp
-  static constexpr int kStages = (229376 - kStage - 2 * kTileBytes) / kTileBytes;
+  static constexpr int kStages = (229376 - kStage - kQueries) / kBytes;
   static_assert(kStages % 2 == 0, "keys keep to the even stages");
 };
 
 template <int D>
 struct Smem {
-  uint8_t q[2 * Sizes<D>::kTileBytes];          // [D / 64][256 rows][128 bytes]
-  uint8_t ring[Sizes<D>::kStages][Sizes<D>::kTileBytes];
+  uint8_t q[Sizes<D>::kQueries];                // [D / 64][256 rows][128 bytes]
+  uint8_t ring[Sizes<D>::kStages][Sizes<D>::kBytes];
   uint8_t stage[8][4096];
+  float2 split[kTileRows];                      // a split item's second share: maximum, sum
   int64_t scan[kThreads / 32];
   uint64_t full[Sizes<D>::kStages], empty[Sizes<D>::kStages];
   uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_prev[2], o_full[2], done;
@@ -61,9 +67,8 @@ struct Smem {
   int abort;
 };
 
-// Keys of a step: a row tile has two steps' scores (and, in their place, P) in tensor memory.
-constexpr int kStep = 64;
-// tensor memory: scores of both tiles, then the outputs
+// Tensor memory: scores of both row tiles (each of two tiles of keys, and, in their place, P),
+// then the outputs.
 constexpr uint32_t kColS = 0, kColO = 256;
 
 // D[tmem] (+)= A[smem] B[smem]^T and A[tmem] B[smem], bf16.
@@ -181,11 +186,11 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 // before its first.  An item's end takes 5 to 8 thousand cycles, a tile 3.1; without it the
 // blocks at the short items of a prompt's beginning were last (16384 tokens: 1614 us; with 2, 3,
 // 5: 1560, 1567, 1584).
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 4;
 
 // An item has whole tokens, `step` of them (256 / group) but for a sequence's last.
 __device__ __forceinline__ int key_tiles(int keys) {
-  return max(1, (keys + kAttnTile - 1) / kAttnTile);
+  return max(1, (keys + kTile - 1) / kTile);
 }
 // Keys from kstart on that row tile rt's last row sees (below 1: none).
 __device__ __forceinline__ int keys_of(const AttnArgs& a, const Sequence& s, int rt, int step) {
@@ -204,8 +209,8 @@ __device__ __forceinline__ int64_t line_before(const AttnArgs& a, const Sequence
   const int none = min(k, max(0, unseen / step));
   n += none;
   if (k > none)
-    n += floor_sum(k - none, kAttnTile, step,
-                   (uint32_t)((none + 1) * step - unseen + kAttnTile - 1));
+    n += floor_sum(k - none, kTile, step,
+                   (uint32_t)((none + 1) * step - unseen + kTile - 1));
   return n;
 }
 
@@ -262,10 +267,29 @@ struct Walk {
   }
   // Tiles of [first, last) that hold a key; the others are behind the last one.
   __device__ __forceinline__ int busy(int key0) const {
-    const int n = kend > key0 ? (kend - key0 + kAttnTile - 1) / kAttnTile : 0;
+    const int n = kend > key0 ? (kend - key0 + kTile - 1) / kTile : 0;
     return max(0, min(last, n) - first);
   }
 };
+
+// What row tile t does of an item: with rows for both, all of its `n` tiles of keys; where the
+// rows fill one at most, every other tile (t 0 the first), the sums joined at the end.
+struct Share {
+  bool split;
+  int tiles, base, t;
+  // The share's tile j among the item's, counted from the block's first, and its first key.
+  __device__ __forceinline__ int tile(int j) const { return split ? 2 * j + t : j; }
+  __device__ __forceinline__ int key_of(int j) const { return base + tile(j) * kTile; }
+};
+template <bool SHARED>
+__device__ __forceinline__ Share share_of(const Walk<SHARED>& w, int key0, int n, int t) {
+  Share s;
+  s.split = w.rows <= kTileRows;
+  s.t = t;
+  s.base = key0 + w.first * kTile;
+  s.tiles = s.split ? (n + 1 - t) >> 1 : n;
+  return s;
+}
 
 // Keys that row r of an item sees; all of its keys where the row is none.
 template <bool SHARED>
@@ -325,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
       raw + ((1024 - (ptx::smem_addr(raw) & 1023)) & 1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       ptx::mbar_init(&sm.full[i], 1);
@@ -363,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The block's range of the line.
   const int step = kAttnRows / a.group;
   const int shared_rts = (a.batch.tokens + step - 1) / step;
-  const int shared_tiles = (a.kstart + kAttnTile - 1) / kAttnTile;
+  const int shared_tiles = (a.kstart + kTile - 1) / kTile;
   int64_t line = 0;
   int N;
   if (SHARED) {
@@ -480,16 +504,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(&sm.q_full, step * a.group * 2 * D);
             for (int h = 0; h < D / 64; ++h)
-              ptx::tma_load_3d(sm.q + h * 2 * Sizes<D>::kHalf, &qmap, h * 64, w.head * a.group,
+              ptx::tma_load_3d(sm.q + h * Sizes<D>::kQueryHalf, &qmap, h * 64, w.head * a.group,
                                w.token, &sm.q_full, ptx::policy_evict_first());
           }
           __syncwarp();
         }
         for (int t = w.first; t < w.first + n; ++t) {
-          const int k0 = key0 + t * kAttnTile;
+          const int k0 = key0 + t * kTile;
           ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-          load_tile<D, 1>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kAttnTile, w.kend - k0), 0,
-                          sm.ring[stage], &sm.full[stage]);
+          load_tile<D, kTile, 1>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kTile, w.kend - k0),
+                                 0, sm.ring[stage], &sm.full[stage]);
           advance2(stage, phase);
         }
       }
@@ -504,81 +528,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---- products: a warp a row tile, so that neither waits for the other's softmax ----
+      // What steers the loops comes from votes and shuffles, and descriptors grow by sums, so
+      // that the compiler keeps them in uniform registers: each of a product's operands would
+      // be moved there first otherwise (100 cycles a product, where the tensor cores take 32
+      // to 64).
       const int t = warp - kIssuer;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(kAll, ptx::mbar_wait(bar, parity, abort, kAttnWaitNs));
+      };
       int k_stage = 0, v_stage = 1;
       uint32_t k_phase = 0, v_phase = 0, p_phase = 0;
-      const uint32_t q_addr = ptx::smem_addr(sm.q) + t * Sizes<D>::kHalf;
-      const uint32_t ring = ptx::smem_addr(sm.ring);
       const uint32_t s_col = tmem + kColS + t * 128, o_col = tmem + kColO + t * 128;
-      const uint32_t id_s = idesc_bf16(kStep, false), id_o = idesc_bf16(D, true);
-      for (bool first = true; w.next(a, first); first = false) {
-        const int n = w.busy(key0);
+      const uint32_t id_s = idesc_bf16(kTile, false), id_o = idesc_bf16(D, true);
+      const uint64_t q_desc = ptx::desc_sw128(ptx::smem_addr(sm.q));
+      const uint64_t k_desc = ptx::desc_sw128(ptx::smem_addr(sm.ring));
+      const uint64_t v_desc = desc_rows(ptx::smem_addr(sm.ring), Sizes<D>::kHalf);
+      auto pass = [&](int& stage, uint32_t& phase) {       // a tile of the other row tile's share
+        wait(&sm.full[stage], phase);
+        if (ptx::elect_one()) ptx::mbar_arrive(&sm.empty[stage]);
+        __syncwarp();
+        advance2(stage, phase);
+      };
+      for (bool first = true; __any_sync(kAll, w.next(a, first)); first = false) {
+        const int n = __shfl_sync(kAll, w.busy(key0), 0);
         if (n == 0) continue;
-        ptx::mbar_wait(&sm.q_full, q_phase, abort, kAttnWaitNs);
+        const bool split = __any_sync(kAll, w.rows <= kTileRows);
+        const int tiles = split ? (n + 1 - t) >> 1 : n;
+        // keys from the block's first tile on
+        const int keys = __shfl_sync(kAll, w.kend - key0 - w.first * kTile, 0);
+        const uint64_t q_tile = q_desc + (split ? 0 : t * ((kTileRows * 128) >> 4));
+        wait(&sm.q_full, q_phase);
         q_phase ^= 1;
-        if (t == 1 && w.rows <= kTileRows) {     // no rows: the operands pass by
-          if (lane == 0) ptx::mbar_arrive(&sm.q_empty);
-          for (int i = 0; i < n; ++i) {
-            ptx::mbar_wait(&sm.full[k_stage], k_phase, abort, kAttnWaitNs);
-            if (lane == 0) ptx::mbar_arrive(&sm.empty[k_stage]);
-            advance2(k_stage, k_phase);
-            ptx::mbar_wait(&sm.full[v_stage], v_phase, abort, kAttnWaitNs);
-            if (lane == 0) ptx::mbar_arrive(&sm.empty[v_stage]);
-            advance2(v_stage, v_phase);
-            __syncwarp();
-          }
-          continue;
-        }
-        const int keys = min(w.kend - key0 - w.first * kAttnTile, n * kAttnTile);
-        const int steps = (keys + kStep - 1) / kStep;
-        // Scores of step j into its half of the tile's columns; a step of the two that share a
-        // tile of keys waits for it, the last of them hands it back.
-        auto scores = [&](int j) {
-          if ((j & 1) == 0) {
-            ptx::mbar_wait(&sm.full[k_stage], k_phase, abort, kAttnWaitNs);
-            ptx::tc_fence_after();
-          }
-          const bool last = (j & 1) != 0 || j + 1 == steps;
+        auto scores = [&](int j) {                         // into their half of the columns
+          if (split && j + t > 0) pass(k_stage, k_phase);
+          wait(&sm.full[k_stage], k_phase);
+          ptx::tc_fence_after();
+          const uint64_t kd = k_desc + (uint64_t)(k_stage * (Sizes<D>::kBytes >> 4));
+          const uint32_t col = s_col + (j & 1) * kTile;
           if (ptx::elect_one()) {
-            const uint32_t k_addr =
-                ring + k_stage * Sizes<D>::kTileBytes + (j & 1) * (kStep * 128);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ss(s_col + (j & 1) * kStep,
-                     ptx::desc_sw128(q_addr + (k >> 2) * 2 * Sizes<D>::kHalf + (k & 3) * 32),
-                     ptx::desc_sw128(k_addr + (k >> 2) * Sizes<D>::kHalf + (k & 3) * 32), id_s,
-                     k > 0);
+              mma_ss(col, q_tile + (k >> 2) * (Sizes<D>::kQueryHalf >> 4) + (k & 3) * 2,
+                     kd + (k >> 2) * (Sizes<D>::kHalf >> 4) + (k & 3) * 2, id_s, k > 0);
             ptx::tc_commit(&sm.s_full[t][j & 1]);
-            if (last) ptx::tc_commit(&sm.empty[k_stage]);
-            if (j + 1 == steps) ptx::tc_commit(&sm.q_empty);
+            ptx::tc_commit(&sm.empty[k_stage]);
+            if (j + 1 == tiles) ptx::tc_commit(&sm.q_empty);
           }
           __syncwarp();
-          if (last) advance2(k_stage, k_phase);
+          advance2(k_stage, k_phase);
         };
-        scores(0);
-        if (steps > 1) scores(1);
-        for (int j = 0; j < steps; ++j) {
-          if ((j & 1) == 0) ptx::mbar_wait(&sm.full[v_stage], v_phase, abort, kAttnWaitNs);
-          ptx::mbar_wait(&sm.p_full[t][j & 1], (p_phase >> (j & 1)) & 1, abort, kAttnWaitNs);
+        if (tiles > 0) scores(0);
+        if (tiles > 1) scores(1);
+        for (int j = 0; j < tiles; ++j) {
+          if (split && j + t > 0) pass(v_stage, v_phase);
+          wait(&sm.full[v_stage], v_phase);
+          wait(&sm.p_full[t][j & 1], (p_phase >> (j & 1)) & 1);
           p_phase ^= 1u << (j & 1);
           ptx::tc_fence_after();
-          const bool last = (j & 1) != 0 || j + 1 == steps;
-          const int parts = (min(kStep, keys - j * kStep) + 15) / 16;
+          const uint64_t vd = v_desc + (uint64_t)(v_stage * (Sizes<D>::kBytes >> 4));
+          const uint32_t col = s_col + (j & 1) * kTile;
+          const int left = keys - (split ? 2 * j + t : j) * kTile;
+          const uint32_t more = j > 0;
           if (ptx::elect_one()) {
-            const uint32_t v_addr =
-                ring + v_stage * Sizes<D>::kTileBytes + (j & 1) * (kStep * 128);
+            mma_ts(o_col, col, vd, id_o, more);
 #pragma unroll
-            for (int k = 0; k < kStep / 16; ++k)
-              if (k < parts)
-                mma_ts(o_col, s_col + (j & 1) * kStep + k * 8,
-                       desc_rows(v_addr + k * 2048, Sizes<D>::kHalf), id_o, j > 0 || k > 0);
-            if (j + 2 == steps) ptx::tc_commit(&sm.o_prev[t]);
-            if (j + 1 == steps) ptx::tc_commit(&sm.o_full[t]);
-            if (last) ptx::tc_commit(&sm.empty[v_stage]);
+            for (int k = 1; k < kTile / 16; ++k)
+              if (k * 16 < left) mma_ts(o_col, col + k * 8, vd + k * (2048 >> 4), id_o, 1u);
+            if (j + 2 == tiles) ptx::tc_commit(&sm.o_prev[t]);
+            if (j + 1 == tiles) ptx::tc_commit(&sm.o_full[t]);
+            ptx::tc_commit(&sm.empty[v_stage]);
           }
           __syncwarp();
-          if (last) advance2(v_stage, v_phase);
-          if (j + 2 < steps) scores(j + 2);
+          advance2(v_stage, v_phase);
+          if (j + 2 < tiles) scores(j + 2);
+        }
+        if (tiles == 0 && ptx::elect_one()) ptx::mbar_arrive(&sm.q_empty);
+        __syncwarp();
+        if (split && n > 2 * tiles - 1 + t) {              // one behind the share's last
+          pass(k_stage, k_phase);
+          pass(v_stage, v_phase);
         }
       }
       // no product may be in flight when tensor memory is given back
@@ -590,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax: a thread a row ----
-    const int t = warp >> 2, r = threadIdx.x;             // row of the item
+    const int t = warp >> 2, peers = 1 + (warp & 3);      // barrier of the two warps of 32 rows
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // 32 lanes a warp
     const uint32_t s_col = lanes + kColS + t * 128, o_col = lanes + kColO + t * 128;
     const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
@@ -600,30 +628,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = w.busy(key0);
       const int v0 = loads;
       loads += n;
-      if (t == 1 && w.rows <= kTileRows) continue;
+      const Share share = share_of(w, key0, n, t);
+      const int tiles = share.tiles;
+      if (share.split && t == 1 && tiles == 0) continue;
+      const int r = share.split ? threadIdx.x & 127 : threadIdx.x;     // row of the item
       const int limit = row_limit(a, w, r);
-      const int base = key0 + w.first * kAttnTile;
-      const int keys = min(w.kend - base, n * kAttnTile);
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j * kStep < keys; ++j) {
-        const uint32_t x_col = s_col + (j & 1) * kStep;
+      int k0 = share.key_of(0);
+      for (int j = 0; j < tiles; ++j, k0 += share.split ? 2 * kTile : kTile) {
+        const uint32_t x_col = s_col + (j & 1) * kTile;
         ptx::mbar_wait(&sm.s_full[t][j & 1], (s_phase >> (j & 1)) & 1, abort, kAttnWaitNs);
         s_phase ^= 1u << (j & 1);
         ptx::tc_fence_after();
-        uint32_t x[kStep];
+        uint32_t x[kTile];
         tmem_ld32_issue(x_col, x);
         tmem_ld32_issue(x_col + 32, x + 32);
         tmem_wait_ld32(x);
         tmem_wait_ld32(x + 32);
-        const int seen = limit - base - j * kStep;
-        if (__any_sync(0xFFFFFFFFu, seen < kStep)) {
+        const int seen = limit - k0;
+        if (__any_sync(0xFFFFFFFFu, seen < kTile)) {
 #pragma unroll
-          for (int e = 0; e < kStep; ++e)
+          for (int e = 0; e < kTile; ++e)
             if (e >= seen) x[e] = 0xFF800000u;
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < kStep; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
+        for (int e = 0; e < kTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
         const float up = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
         if (__any_sync(0xFFFFFFFFu, up > m + 8.f)) {
           const float to = fmaxf(m, up);
@@ -631,9 +661,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = to;
           l *= f;
           if (j > 0) {
-            // No product may be in flight on the output: step j - 1's end comes before the scores
-            // of step j + 1, or has a barrier of its own before the item's last step.
-            if ((j + 1) * kStep < keys)
+            // No product may be in flight on the output: tile j - 1's end comes before the scores
+            // of tile j + 1, or has a barrier of its own before the item's last.
+            if (j + 1 < tiles)
               ptx::mbar_wait(&sm.s_full[t][(j + 1) & 1], (s_phase >> ((j + 1) & 1)) & 1, abort,
                              kAttnWaitNs);
             else
@@ -651,13 +681,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (keys - j * kStep < kStep && keys % 16 != 0) {
+        if (w.kend - k0 < kTile && (w.kend - k0) % 16 != 0) {
           // values behind the last key may be anything, and 0 times them must be 0: the rows
           // that share the last key's sixteen are cleared, by each row tile before its own
           // products (the second to come writes zeros over zeros)
-          const int at = v0 + j / 2, v = 2 * (at % (STAGES / 2)) + 1;
+          const int at = v0 + share.tile(j), v = 2 * (at % (STAGES / 2)) + 1;
           ptx::mbar_wait(&sm.full[v], (at / (STAGES / 2)) & 1, abort, kAttnWaitNs);
-          const int from_row = keys % kAttnTile, to_row = (from_row + 15) / 16 * 16;
+          const int from_row = w.kend - k0, to_row = (from_row + 15) / 16 * 16;
           for (int e = threadIdx.x & 127; e < (to_row - from_row) * (D / 8); e += 128) {
             const int vr = from_row + e / (D / 8), piece = e % (D / 8);
             *reinterpret_cast<uint4*>(sm.ring[v] + (piece >> 3) * Sizes<D>::kHalf + vr * 128 +
@@ -679,9 +709,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the item's end ----
+      float f0 = 1.f, f1 = 0.f;
+      const bool joined = share.split && n > 1;              // a second share
+      if (joined) {
+        if (t == 1) sm.split[r] = make_float2(m, l);
+        ptx::named_bar_sync(peers, 64);
+        if (t == 0) {
+          const float2 other = sm.split[r];
+          const float up = fmaxf(m, other.x), base = up == -INFINITY ? 0.f : up;
+          f0 = exp2_approx(m - base);
+          f1 = exp2_approx(other.x - base);
+          m = up;
+          l = l * f0 + other.y * f1;
+        }
+      }
       const bool whole = w.first == 0 && w.last == w.tiles;
       const int slot = 2 * blockIdx.x + (w.first == 0);
-      if (w.first == 0 && (!whole || by_item) && r == 0) {
+      if (w.first == 0 && (!whole || by_item) && threadIdx.x == 0) {
         AttnCut cut;
         cut.first = w.token;
         cut.rows = w.rows;
@@ -690,10 +734,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         cut.to = whole ? -1 : block_of(line, N, w.at + w.tiles - 1);
         a.cuts[by_item ? w.head * shared_rts + w.rt : blockIdx.x] = cut;
       }
-      const int row0 = warp * 32, live = w.rows - row0;     // the warp's rows of the item
+      const int row0 = r - lane, live = w.rows - row0;      // the warp's rows of the item
       const int64_t index = (int64_t)w.token * a.group + r;
       Finish fin = {};
-      if (whole && r < w.rows) fin = finish_begin<D, SHARED>(a, w.head, index, m, l);
+      if (whole && r < w.rows && !(share.split && t == 1))
+        fin = finish_begin<D, SHARED>(a, w.head, index, m, l);
       float* keep = SHARED && whole
                         ? a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
                                             (int64_t)w.token * a.group + row0) * D
@@ -710,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint8_t* stage = sm.stage[warp];
       if (n > 0) {
-        if (keys > kStep) {
+        if (tiles > 1) {
           ptx::mbar_wait(&sm.o_prev[t], prev_phase, abort, kAttnWaitNs);
           prev_phase ^= 1;
         }
@@ -718,11 +763,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         o_phase ^= 1;
         ptx::tc_fence_after();
       }
-      if (SHARED || !whole) {
+      // 32 columns of the row's output, of both shares
+      auto output = [&](uint32_t (&o)[32], int j) {
+        load_output(o, o_col + j, n > 0);
+        if (joined) {
+          ptx::named_bar_sync(peers, 64);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 y = *staged(sm.stage[warp + 4], lane, e);
+            o[4 * e] = add_scaled(o[4 * e], f0, y.x, f1);
+            o[4 * e + 1] = add_scaled(o[4 * e + 1], f0, y.y, f1);
+            o[4 * e + 2] = add_scaled(o[4 * e + 2], f0, y.z, f1);
+            o[4 * e + 3] = add_scaled(o[4 * e + 3], f0, y.w, f1);
+          }
+          ptx::named_bar_sync(peers, 64);
+        }
+      };
+      if (share.split && t == 1) {               // to the other warpgroup
 #pragma unroll 1
         for (int j = 0; j < D; j += 32) {
           uint32_t o[32];
-          load_output(o, o_col + j, n > 0);
+          load_output(o, o_col + j, true);
+          write_row(stage, lane, o);
+          ptx::named_bar_sync(peers, 64);
+          ptx::named_bar_sync(peers, 64);
+        }
+      } else if (SHARED || !whole) {
+#pragma unroll 1
+        for (int j = 0; j < D; j += 32) {
+          uint32_t o[32];
+          output(o, j);
           write_row(stage, lane, o);
           uint4 v[8];
 #pragma unroll
@@ -741,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t o[32];
-            load_output(o, o_col + j + 32 * half, n > 0);
+            output(o, j + 32 * half);
             if (a.kstart > 0) {
               each_piece(live, [&](int row, int piece) {
                 *staged(stage, row, piece) = *reinterpret_cast<const uint4*>(
@@ -773,8 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-      if (r < w.rows && !whole) a.part_stats[slot * kAttnRows + r] = make_float2(m, l);
-      if (r < w.rows && whole && !SHARED && a.lse) {
+      const bool keeper = !share.split || t == 0;
+      if (keeper && r < w.rows && !whole) a.part_stats[slot * kAttnRows + r] = make_float2(m, l);
+      if (keeper && r < w.rows && whole && !SHARED && a.lse) {
         const int i = token_of(a, r);
         a.lse[(int64_t)(w.token + i) * a.q_heads + w.head * a.group + r - i * a.group] = fin.lse;
       }
