@@ -121,28 +121,38 @@ __device__ __forceinline__ int cache_row(const AttnArgs& a, int page, int head, 
 }
 
 // Loads one tile of keys (or values) from key k0 of a sequence, `keys` of them (1 .. TILE), into
-// dst: [D / 64][TILE rows][128 bytes], swizzled; what no box covers keeps its old contents.  PARTS converged warps share the boxes, each its own with an arrival of its
-// own on bar.  A box takes its warp 130 cycles to issue from a lane each (260 one after another
-// by an elected lane), so pages of 16 keys need the warps; copies themselves overlap.
+// dst: [D / 64][TILE rows][128 bytes], swizzled; what no box covers keeps its old contents.
+// PARTS converged warps share the boxes, each its own with an arrival of its own on bar.  The
+// boxes' places come from shuffles and the loop's bounds from values that the caller made uniform,
+// so that a copy's operands stay in uniform registers (see attn_tile.cu).
 template <int D, int TILE, int PARTS>
 __device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* map, Pages& pages,
                                           int head, int k0, int keys, int part, uint8_t* dst,
                                           uint64_t* bar) {
   constexpr int HALVES = D / 64;
+  constexpr int MOST = TILE / 16 * HALVES / PARTS;        // boxes of a part, pages of 16 keys
   const int box = min(1 << a.page_shift, kAttnBox);
   const int boxes = (keys + box - 1) / box, mine = (boxes * HALVES - part + PARTS - 1) / PARTS;
   const int first = k0 >> a.page_shift, r = k0 & ((1 << a.page_shift) - 1);
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, mine * box * 128);
   pages.fetch(a, first, ((r + (boxes - 1) * box) >> a.page_shift) + 1);
+  // each lane the row of one box
+  const int lane = threadIdx.x & 31;
   const int which = max(min(lane, mine - 1) * PARTS + part, 0), i = which / HALVES;
-  const int at = r + i * box;                      // (a page may hold several boxes)
+  const int at = r + i * box;                             // (a page may hold several boxes)
   const int page = pages.at(first + (at >> a.page_shift));
+  const int y = cache_row(a, page, head, at & ((1 << a.page_shift) - 1));
   __syncwarp();
-  if (lane < mine) {
-    const int y = cache_row(a, page, head, at & ((1 << a.page_shift) - 1)), h = which % HALVES;
-    ptx::tma_load_2d(dst + (h * TILE + i * box) * 128, map, h * 64, y, bar,
-                     ptx::policy_evict_normal());
+  if (ptx::elect_one()) ptx::mbar_arrive_expect_tx(bar, mine * box * 128);
+  __syncwarp();
+  const uint64_t policy = ptx::policy_evict_normal();
+#pragma unroll
+  for (int e = 0; e < MOST; ++e) {
+    const int row = __shfl_sync(0xFFFFFFFFu, y, e);
+    if (e < mine) {
+      const int w = e * PARTS + part, h = w % HALVES;
+      if (ptx::elect_one())
+        ptx::tma_load_2d(dst + (h * TILE + w / HALVES * box) * 128, map, h * 64, row, bar, policy);
+    }
   }
   __syncwarp();
 }

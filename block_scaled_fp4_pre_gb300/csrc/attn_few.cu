@@ -20,6 +20,7 @@
 namespace mxmoe {
 namespace {
 
+constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kRows = 16;
 constexpr int kWarps = 8;                       // of consumers
 constexpr int kLoaders = 2;                     // warps that load keys, and values
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(
       raw + ((1024 - (ptx::smem_addr(raw) & 1023)) & 1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       ptx::mbar_init(&sm.full[i], kLoaders);
@@ -198,14 +199,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Pages pages;
     int seq = -1;
-    for (bool first = true; w.next(a, first); first = false) {
-      if (w.seq != seq) pages.start(a, seq = w.seq);
-      for (int t = w.first; t < w.last; ++t) {
-        const int k0 = a.kstart + t * kAttnTile, keys = min(kAttnTile, w.s.kend - k0);
-        if (keys <= 0) continue;
-        ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-        load_tile<D, kAttnTile, kLoaders>(a, v ? &vmap : &kmap, pages, w.head, k0, keys, part,
-                               sm.ring[stage], &sm.full[stage]);
+    for (bool first = true; __any_sync(kAll, w.next(a, first)); first = false) {
+      if (__any_sync(kAll, w.seq != seq)) pages.start(a, seq = w.seq);
+      const int head = __shfl_sync(kAll, w.head, 0), kend = __shfl_sync(kAll, w.s.kend, 0);
+      int k0 = __shfl_sync(kAll, a.kstart + w.first * kAttnTile, 0);
+      const int n = __shfl_sync(kAll, w.last - w.first, 0);
+      for (int i = 0; i < n && k0 < kend; ++i, k0 += kAttnTile) {
+        __all_sync(kAll, ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs));
+        load_tile<D, kAttnTile, kLoaders>(a, v ? &vmap : &kmap, pages, head, k0,
+                                          min(kAttnTile, kend - k0), part, sm.ring[stage],
+                                          &sm.full[stage]);
         advance2();
       }
     }

@@ -494,26 +494,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       Pages pages;
       int seq = -1;
-      for (bool first = true; w.next(a, first); first = false) {
-        const int n = w.busy(key0);
+      for (bool first = true; __any_sync(kAll, w.next(a, first)); first = false) {
+        const int n = __shfl_sync(kAll, w.busy(key0), 0);
         if (n == 0) continue;
-        if (w.seq != seq) pages.start(a, seq = w.seq);
+        if (__any_sync(kAll, w.seq != seq)) pages.start(a, seq = w.seq);
+        const int head = __shfl_sync(kAll, w.head, 0);
+        int k0 = __shfl_sync(kAll, key0 + w.first * kTile, 0);
+        const int kend = __shfl_sync(kAll, w.kend, 0);
         if (v == 0) {
-          ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs);
+          const int token = __shfl_sync(kAll, w.token, 0);
+          __all_sync(kAll, ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs));
           q_phase ^= 1;
           if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(&sm.q_full, step * a.group * 2 * D);
             for (int h = 0; h < D / 64; ++h)
-              ptx::tma_load_3d(sm.q + h * Sizes<D>::kQueryHalf, &qmap, h * 64, w.head * a.group,
-                               w.token, &sm.q_full, ptx::policy_evict_first());
+              ptx::tma_load_3d(sm.q + h * Sizes<D>::kQueryHalf, &qmap, h * 64, head * a.group,
+                               token, &sm.q_full, ptx::policy_evict_first());
           }
           __syncwarp();
         }
-        for (int t = w.first; t < w.first + n; ++t) {
-          const int k0 = key0 + t * kTile;
-          ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs);
-          load_tile<D, kTile, 1>(a, v ? &vmap : &kmap, pages, w.head, k0, min(kTile, w.kend - k0),
-                                 0, sm.ring[stage], &sm.full[stage]);
+        for (int i = 0; i < n; ++i, k0 += kTile) {
+          __all_sync(kAll, ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs));
+          load_tile<D, kTile, 1>(a, v ? &vmap : &kmap, pages, head, k0, min(kTile, kend - k0), 0,
+                                 sm.ring[stage], &sm.full[stage]);
           advance2(stage, phase);
         }
       }
