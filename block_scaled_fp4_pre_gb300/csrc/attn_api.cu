@@ -111,7 +111,7 @@ AttnWs ws_layout(const moe_attention_dims& d) {
     return at;
   };
   L.flags = take(4);
-  L.counters = take(kAttnBlocks * sizeof(int32_t));
+  L.counters = take(2 * kAttnBlocks * sizeof(int32_t));
   L.cuts = take(kAttnBlocks * sizeof(AttnCut));
   L.stats = take((size_t)kAttnBlocks * 2 * kAttnRows * sizeof(float2));
   L.parts = take((size_t)kAttnBlocks * 2 * kAttnRows * d.head_dim * sizeof(float));

@@ -64,7 +64,7 @@ struct Smem {
   int start_left, start_seq, start_head, start_rt, start_tile;
   int kend;                                     // SHARED: keys that some row sees
   uint32_t tmem;
-  int abort;
+  int abort, joins[2];
 };
 
 // Tensor memory: scores of both row tiles (each of two tiles of keys, and, in their place, P),
@@ -339,6 +339,56 @@ __device__ __forceinline__ uint32_t add_scaled(uint32_t x, float f, uint32_t y, 
   return __float_as_uint(__uint_as_float(x) * f + __uint_as_float(y) * g);
 }
 
+// A warp joins the parts of its rows [row0, row0 + rows) of an item, eight passes' loads at a
+// time, in the order of the line.
+template <int D>
+__device__ __forceinline__ void join_rows(const AttnArgs& a, int kv_head, int token, int from,
+                                          int to, int row0, int rows) {
+  constexpr int QUADS = D / 4, PASS = 32 / QUADS, U = 8;     // rows a pass, passes at a time
+  const int lane = threadIdx.x & 31, quad = lane % QUADS;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += U * PASS) {
+    float top[U], sum[U];
+    float4 acc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      top[u] = -INFINITY;
+      sum[u] = 0.f;
+      acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int b = from; b <= to; ++b) {
+      const int64_t base = (int64_t)(2 * b + (b == from)) * kAttnRows + row0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = base + min(r0 + u * PASS + lane / QUADS, rows - 1);
+        const float2 st = __ldcg(&a.part_stats[at]);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + quad);
+        const float up = fmaxf(top[u], st.x), from_ = up == -INFINITY ? 0.f : up;
+        const float f = exp2_approx(top[u] - from_), g = exp2_approx(st.x - from_);
+        top[u] = up;
+        sum[u] = sum[u] * f + st.y * g;
+        acc[u].x = acc[u].x * f + y.x * g;
+        acc[u].y = acc[u].y * f + y.y * g;
+        acc[u].z = acc[u].z * f + y.z * g;
+        acc[u].w = acc[u].w * f + y.w * g;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * PASS + lane / QUADS;
+      if (r < rows) {
+        const int i = token_of(a, row0 + r), head = kv_head * a.group + row0 + r - i * a.group;
+        const int64_t t = token + i;
+        const Finish fin = finish_begin<D, false>(
+            a, kv_head, (int64_t)token * a.group + row0 + r, top[u], sum[u]);
+        finish_quad<D, false>(a, fin, t, head, quad, acc[u]);
+        if (a.lse && quad == 0) a.lse[t * a.q_heads + head] = fin.lse;
+      }
+    }
+  }
+}
+
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tile_kernel(const __grid_constant__ AttnArgs a,
@@ -459,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Entries of the cuts: an item's where the prefix's are fewer than the blocks, else the
   // block's that the item begins in.
   const bool by_item = SHARED && a.kv_heads * shared_rts <= (int)gridDim.x;
-  if (threadIdx.x == 0 && !by_item) a.cuts[blockIdx.x].to = -1;
+  if (threadIdx.x == 0 && !by_item && !a.join_here) a.cuts[blockIdx.x].to = -1;
   __syncthreads();
   Walk<SHARED> w = {};
   w.left = sm.start_left;
@@ -728,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool whole = w.first == 0 && w.last == w.tiles;
       const int slot = 2 * blockIdx.x + (w.first == 0);
-      if (w.first == 0 && (!whole || by_item) && threadIdx.x == 0) {
+      if (w.first == 0 && (by_item || (!whole && !a.join_here)) && threadIdx.x == 0) {
         AttnCut cut;
         cut.first = w.token;
         cut.rows = w.rows;
@@ -853,6 +903,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.lse[(int64_t)(w.token + i) * a.q_heads + w.head * a.group + r - i * a.group] = fin.lse;
       }
       ptx::tc_fence_before();
+      if (!SHARED && !whole && a.join_here && keeper) {
+        // The rows' parts are joined by the block that comes last.
+        const int from = block_of(line, N, w.at), to = block_of(line, N, w.at + w.tiles - 1);
+        ptx::named_bar_sync(5 + t, 128);
+        if ((threadIdx.x & 127) == 0) {
+          int32_t* counter = a.counters + 2 * from + t;
+          const bool last = ptx::atomic_add_acq_rel(counter, 1) == to - from;
+          if (last) *counter = 0;
+          sm.joins[t] = last;
+        }
+        ptx::named_bar_sync(5 + t, 128);
+        if (sm.joins[t])
+          join_rows<D>(a, w.head, w.token, from, to, row0, min(live, 32));
+      }
     }
   }
   __syncthreads();
@@ -894,18 +958,24 @@ cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap&
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
-  const AttnArgs& a = g.args;
+  AttnArgs a = g.args;
+  const int step = kAttnRows / a.group;
+  // An item's parts are joined within the kernel where they are few: with more items than SMs
+  // a block's range is longer than most, and a short row of the page table bounds the rest.
+  // Elsewhere (one launch more, 4 to 10 us) many blocks join an item's many parts together.
+  a.join_here = !SHARED && ((int64_t)a.kv_heads * (a.batch.tokens / step) >= g.num_sms ||
+                            ((int64_t)a.batch.pages_ld << a.page_shift) <= 8 * kTile);
   CUtensorMap q;
   e = make_tmap_heads(&q, a.q, D, a.q_heads, a.batch.tokens, a.ldq, a.group, kAttnRows / a.group);
   if (e != cudaSuccess) return e;
   const int blocks = g.num_sms < kAttnBlocks ? g.num_sms : kAttnBlocks;
   e = launch_pdl(attention_tile_kernel<D, SHARED>, dim3(blocks), dim3(kThreads), smem, st, a, q,
                  k, v);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.join_here) return e;
   const int64_t rows = (int64_t)(SHARED ? a.batch.tokens : a.batch.max_new) * a.group;
   const int most = (int)(rows < kAttnRows ? rows : kAttnRows);
   // 8 rows a block, or more where that would be more blocks than are resident together
-  const int step = kAttnRows / a.group, eights = (most + 7) / 8;
+  const int eights = (most + 7) / 8;
   const int64_t items = (int64_t)a.kv_heads * ((a.batch.tokens + step - 1) / step);
   const int cuts = SHARED && items <= blocks ? (int)items : blocks;
   const int y = std::min(eights, std::max(1, 8 * g.num_sms / cuts));

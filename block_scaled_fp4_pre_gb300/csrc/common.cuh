@@ -424,7 +424,8 @@ struct AttnArgs {
   int group_inv;                   // ceil(2^16 / group)
   int32_t* flags;
   int kstart;                      // keys below it are the shared prefix's, computed apart
-  // workspace: parts of cut items, two a block, and a counter a block (zero between calls)
+  int join_here;                   // tile kernel: the last block joins an item's parts
+  // workspace: parts of cut items, two a block, and two counters a block (zero between calls)
   float* parts;                    // [blocks][2][rows][head_dim]
   float2* part_stats;              // [blocks][2][rows]: log2 of the largest term, sum
   int32_t* counters;
