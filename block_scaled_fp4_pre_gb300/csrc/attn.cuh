@@ -165,6 +165,15 @@ struct Finish {
   const float4* other;
   float mine, theirs, inv, lse;
 };
+// The row's factors where its sums are joined with another part's (maximum, sum).
+__device__ __forceinline__ void finish_sums(Finish& f, float m, float l, float2 part) {
+  const float top = fmaxf(m, part.x), base = top == -INFINITY ? 0.f : top;
+  f.mine = exp2_approx(m - base);
+  f.theirs = exp2_approx(part.x - base);
+  l = l * f.mine + part.y * f.theirs;
+  f.inv = l > 0.f ? 1.f / l : 0.f;
+  f.lse = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
 template <int D, bool SHARED>
 __device__ __forceinline__ Finish finish_begin(const AttnArgs& a, int kv_head, int64_t index,
                                                float m, float l) {
@@ -176,19 +185,12 @@ __device__ __forceinline__ Finish finish_begin(const AttnArgs& a, int kv_head, i
     a.shared_stats[at] = make_float2(m, l);
     return f;
   }
-  f.mine = 1.f;
-  f.theirs = 0.f;
   if (a.kstart > 0) {
-    const float2 st = a.shared_stats[at];
-    const float top = fmaxf(m, st.x), base = top == -INFINITY ? 0.f : top;
     f.other = f.keep;
-    f.mine = exp2_approx(m - base);
-    f.theirs = exp2_approx(st.x - base);
-    l = l * f.mine + st.y * f.theirs;
-    m = top;
+    finish_sums(f, m, l, a.shared_stats[at]);
+  } else {
+    finish_sums(f, m, l, make_float2(-INFINITY, 0.f));
   }
-  f.inv = l > 0.f ? 1.f / l : 0.f;
-  f.lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
   return f;
 }
 // Four elements of the row.

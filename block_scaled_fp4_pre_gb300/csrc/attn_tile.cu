@@ -29,7 +29,7 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kTileRows = 128;
-// Warps: eight with a row a thread, one that loads queries and keys and one for values, one a row
+// Warps: eight with a row a thread, one that loads keys and one for values and queries, one a row
 // tile that issues its products.
 constexpr int kLoader = 8, kIssuer = 10;
 constexpr int kThreads = 384;                   // whole warpgroups, as register shares go by
@@ -188,6 +188,10 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 // 5: 1560, 1567, 1584).
 constexpr int kItemCost = 4;
 
+// Items of up to this many tiles are not cut: a block takes all of one whose first tile is in its
+// range.
+constexpr int kShortItem = 6;
+
 // An item has whole tokens, `step` of them (256 / group) but for a sequence's last.
 __device__ __forceinline__ int key_tiles(int keys) {
   return max(1, (keys + kTile - 1) / kTile);
@@ -230,40 +234,44 @@ struct Walk {
     }
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, bool begin) {
-    if (left <= 0) return false;
-    if (begin) {
-      enter(a);
-    } else {
-      at += tiles + kItemCost;
-      tile = -kItemCost;
-      if (++rt == rts) {
-        rt = 0;
-        if (++head == a.kv_heads && !SHARED) {
-          head = 0;
-          do {
-            ++seq;
-            enter(a);
-          } while (rts == 0);
+    for (;; begin = false) {
+      if (left <= 0) return false;
+      if (begin) {
+        enter(a);
+      } else {
+        at += tiles + kItemCost;
+        tile = -kItemCost;
+        if (++rt == rts) {
+          rt = 0;
+          if (++head == a.kv_heads && !SHARED) {
+            head = 0;
+            do {
+              ++seq;
+              enter(a);
+            } while (rts == 0);
+          }
         }
       }
+      if (tile < 0) {                        // the positions before its first tile
+        left += tile;
+        if (left <= 0) return false;
+        tile = 0;
+      }
+      const int tokens = min(step, (SHARED ? a.batch.tokens : s.taken) - rt * step);
+      token = rt * step + (SHARED ? 0 : s.first);
+      rows = tokens * a.group;
+      if (!SHARED) {
+        const int keys = keys_of(a, s, rt, step);
+        kend = a.kstart + keys;
+        tiles = key_tiles(keys);
+      }
+      first = tile;
+      last = min(tiles, tile + left);
+      left -= last - first;
+      if (SHARED || tiles > kShortItem) return true;
+      last = tiles;                          // whole, the block's that its first tile is in
+      if (first == 0) return true;
     }
-    if (tile < 0) {                          // the positions before its first tile
-      left += tile;
-      if (left <= 0) return false;
-      tile = 0;
-    }
-    const int tokens = min(step, (SHARED ? a.batch.tokens : s.taken) - rt * step);
-    token = rt * step + (SHARED ? 0 : s.first);
-    rows = tokens * a.group;
-    if (!SHARED) {
-      const int keys = keys_of(a, s, rt, step);
-      kend = a.kstart + keys;
-      tiles = key_tiles(keys);
-    }
-    first = tile;
-    last = min(tiles, tile + left);
-    left -= last - first;
-    return true;
   }
   // Tiles of [first, last) that hold a key; the others are behind the last one.
   __device__ __forceinline__ int busy(int key0) const {
@@ -339,53 +347,22 @@ __device__ __forceinline__ uint32_t add_scaled(uint32_t x, float f, uint32_t y, 
   return __float_as_uint(__uint_as_float(x) * f + __uint_as_float(y) * g);
 }
 
-// A warp joins the parts of its rows [row0, row0 + rows) of an item, eight passes' loads at a
-// time, in the order of the line.
+// A warp joins the parts of its rows [row0, row0 + rows) of an item, in the order of the line.
+// Seldom needed, and short: code that runs once a block is read from L2 as it goes (unrolled for
+// eight rows at a time this took 33 thousand cycles).
 template <int D>
-__device__ __forceinline__ void join_rows(const AttnArgs& a, int kv_head, int token, int from,
-                                          int to, int row0, int rows) {
-  constexpr int QUADS = D / 4, PASS = 32 / QUADS, U = 8;     // rows a pass, passes at a time
+__device__ __noinline__ void join_rows(const AttnArgs& a, int kv_head, int token, int from, int to,
+                                       int row0, int rows) {
+  constexpr int QUADS = D / 4, PASS = 32 / QUADS;
   const int lane = threadIdx.x & 31, quad = lane % QUADS;
 #pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += U * PASS) {
-    float top[U], sum[U];
-    float4 acc[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      top[u] = -INFINITY;
-      sum[u] = 0.f;
-      acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll 2
-    for (int b = from; b <= to; ++b) {
-      const int64_t base = (int64_t)(2 * b + (b == from)) * kAttnRows + row0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = base + min(r0 + u * PASS + lane / QUADS, rows - 1);
-        const float2 st = __ldcg(&a.part_stats[at]);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + quad);
-        const float up = fmaxf(top[u], st.x), from_ = up == -INFINITY ? 0.f : up;
-        const float f = exp2_approx(top[u] - from_), g = exp2_approx(st.x - from_);
-        top[u] = up;
-        sum[u] = sum[u] * f + st.y * g;
-        acc[u].x = acc[u].x * f + y.x * g;
-        acc[u].y = acc[u].y * f + y.y * g;
-        acc[u].z = acc[u].z * f + y.z * g;
-        acc[u].w = acc[u].w * f + y.w * g;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * PASS + lane / QUADS;
-      if (r < rows) {
-        const int i = token_of(a, row0 + r), head = kv_head * a.group + row0 + r - i * a.group;
-        const int64_t t = token + i;
-        const Finish fin = finish_begin<D, false>(
-            a, kv_head, (int64_t)token * a.group + row0 + r, top[u], sum[u]);
-        finish_quad<D, false>(a, fin, t, head, quad, acc[u]);
-        if (a.lse && quad == 0) a.lse[t * a.q_heads + head] = fin.lse;
-      }
-    }
+  for (int r = row0 + lane / QUADS; r < row0 + rows; r += PASS) {
+    const Joined j = join_parts<D>(a, from, to, kAttnRows, r, quad);
+    const int i = token_of(a, r), head = kv_head * a.group + r - i * a.group;
+    const Finish fin =
+        finish_begin<D, false>(a, kv_head, (int64_t)token * a.group + r, j.top, j.sum);
+    finish_quad<D, false>(a, fin, token + i, head, quad, j.acc);
+    if (a.lse && quad == 0) a.lse[(int64_t)(token + i) * a.q_heads + head] = fin.lse;
   }
 }
 
@@ -538,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     if (warp < kIssuer) {
-      // ---- loads: an item's queries; keys into the even stages, values into the odd ----
+      // ---- loads: keys into the even stages; values into the odd, and an item's queries, which
+      // wait for the last item's scores: the next keys do not wait with them ----
       const int v = warp - kLoader;
       int stage = v;
       uint32_t phase = 0;
@@ -551,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int head = __shfl_sync(kAll, w.head, 0);
         int k0 = __shfl_sync(kAll, key0 + w.first * kTile, 0);
         const int kend = __shfl_sync(kAll, w.kend, 0);
-        if (v == 0) {
+        if (v == 1) {
           const int token = __shfl_sync(kAll, w.token, 0);
           __all_sync(kAll, ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs));
           q_phase ^= 1;
@@ -573,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // After a wait that ran out, copies may still be in flight: the block stays for them.
       if (*abort) {
         int never = 0;
-        if (v == 0) ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
+        if (v == 1) ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
         for (int i = 0; i < STAGES; i += 2) {
           ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
           advance2(stage, phase);
@@ -776,28 +754,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = l * f0 + other.y * f1;
         }
       }
-      const bool whole = w.first == 0 && w.last == w.tiles;
+      const bool keeper = !share.split || t == 0;            // has the rows' end
+      bool whole = w.first == 0 && w.last == w.tiles;
       const int slot = 2 * blockIdx.x + (w.first == 0);
+      int from = 0, to = 0;                                  // blocks of a cut item
+      if (!whole) {
+        from = w.first == 0 ? blockIdx.x : block_of(line, N, w.at);
+        to = block_of(line, N, w.at + w.tiles - 1);
+      }
       if (w.first == 0 && (by_item || (!whole && !a.join_here)) && threadIdx.x == 0) {
         AttnCut cut;
         cut.first = w.token;
         cut.rows = w.rows;
         cut.head = w.head;
         cut.from = blockIdx.x;
-        cut.to = whole ? -1 : block_of(line, N, w.at + w.tiles - 1);
+        cut.to = whole ? -1 : to;
         a.cuts[by_item ? w.head * shared_rts + w.rt : blockIdx.x] = cut;
       }
       const int row0 = r - lane, live = w.rows - row0;      // the warp's rows of the item
       const int64_t index = (int64_t)w.token * a.group + r;
+      const float* other = a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
+                                             (int64_t)w.token * a.group + row0) * D;
+      bool merge = a.kstart > 0;                             // with what `other` points to
       Finish fin = {};
-      if (whole && r < w.rows && !(share.split && t == 1))
+      if (!SHARED && !whole && a.join_here && keeper && to == from + 1 && !merge) {
+        // An item of two parts whose other one is there: joined on the way out.
+        if ((threadIdx.x & 127) == 0) {
+          int32_t* counter = a.counters + 2 * from + t;
+          sm.joins[t] = ptx::ld_acquire(counter) == 1;
+          if (sm.joins[t]) *counter = 0;
+        }
+        ptx::named_bar_sync(5 + t, 128);
+        if (sm.joins[t]) {
+          const int64_t at = (int64_t)(w.first == 0 ? 2 * to : 2 * from + 1) * kAttnRows;
+          if (r < w.rows) finish_sums(fin, m, l, __ldcg(&a.part_stats[at + r]));
+          other = a.parts + (at + row0) * D;
+          whole = merge = true;
+        }
+        ptx::named_bar_sync(5 + t, 128);
+      } else if (whole && r < w.rows && keeper) {
         fin = finish_begin<D, SHARED>(a, w.head, index, m, l);
+      }
       float* keep = SHARED && whole
                         ? a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
                                             (int64_t)w.token * a.group + row0) * D
                         : a.parts + ((int64_t)slot * kAttnRows + row0) * D;
-      const float* other = a.shared_parts + ((int64_t)w.head * a.batch.tokens * a.group +
-                                             (int64_t)w.token * a.group + row0) * D;
       // this lane's eighth of every fourth row of the output
       uint16_t* dst[8];
 #pragma unroll
@@ -865,10 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int half = 0; half < 2; ++half) {
             uint32_t o[32];
             output(o, j + 32 * half);
-            if (a.kstart > 0) {
+            if (merge) {
               each_piece(live, [&](int row, int piece) {
-                *staged(stage, row, piece) = *reinterpret_cast<const uint4*>(
-                    other + row * D + j + 32 * half + piece * 4);
+                *staged(stage, row, piece) = __ldcg(reinterpret_cast<const uint4*>(
+                    other + row * D + j + 32 * half + piece * 4));
               });
               __syncwarp();
 #pragma unroll
@@ -896,7 +897,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-      const bool keeper = !share.split || t == 0;
       if (keeper && r < w.rows && !whole) a.part_stats[slot * kAttnRows + r] = make_float2(m, l);
       if (keeper && r < w.rows && whole && !SHARED && a.lse) {
         const int i = token_of(a, r);
@@ -904,8 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::tc_fence_before();
       if (!SHARED && !whole && a.join_here && keeper) {
-        // The rows' parts are joined by the block that comes last.
-        const int from = block_of(line, N, w.at), to = block_of(line, N, w.at + w.tiles - 1);
+        // Else the rows' parts are joined by the block that comes last.
         ptx::named_bar_sync(5 + t, 128);
         if ((threadIdx.x & 127) == 0) {
           int32_t* counter = a.counters + 2 * from + t;
@@ -960,11 +959,12 @@ cudaError_t launch(const AttnLaunch& g, const CUtensorMap& k, const CUtensorMap&
   if (e != cudaSuccess) return e;
   AttnArgs a = g.args;
   const int step = kAttnRows / a.group;
-  // An item's parts are joined within the kernel where they are few: with more items than SMs
-  // a block's range is longer than most, and a short row of the page table bounds the rest.
-  // Elsewhere (one launch more, 4 to 10 us) many blocks join an item's many parts together.
-  a.join_here = !SHARED && ((int64_t)a.kv_heads * (a.batch.tokens / step) >= g.num_sms ||
-                            ((int64_t)a.batch.pages_ld << a.page_shift) <= 8 * kTile);
+  // An item's parts are joined within the kernel where they are few: with twice as many items as
+  // SMs a block's range is longer than most.  Elsewhere (a launch more, 4 to 10 us) many
+  // blocks join an item's many parts together.  A short row of the page table leaves no item
+  // that is cut.
+  a.join_here = !SHARED && ((int64_t)a.kv_heads * (a.batch.tokens / step) >= 2 * g.num_sms ||
+                            ((int64_t)a.batch.pages_ld << a.page_shift) <= kShortItem * kTile);
   CUtensorMap q;
   e = make_tmap_heads(&q, a.q, D, a.q_heads, a.batch.tokens, a.ldq, a.group, kAttnRows / a.group);
   if (e != cudaSuccess) return e;
