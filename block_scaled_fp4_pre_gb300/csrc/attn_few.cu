@@ -71,6 +71,10 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // 17.4; 64 sequences behind 8192 common tokens, with the prefix's part, 103, 92, 88, 87.
 constexpr int kItemCost = 3;
 
+// Items of up to this many tiles are not cut: a block takes all of one whose first tile is in its
+// range.
+constexpr int kShortItem = 4;
+
 // Length on the line of a sequence's items: their tiles, one, of no keys, where the tokens see
 // none from kstart on.
 __device__ __forceinline__ int length_of(const AttnArgs& a, const Sequence& s) {
@@ -86,30 +90,34 @@ struct Walk {
   Sequence s;
   int tiles, first, last;   // the current item's tiles, and those of them in the range
   __device__ __forceinline__ bool next(const AttnArgs& a, bool begin) {
-    if (left <= 0) return false;
-    if (begin) {
-      s = sequence(a, seq);
-      tiles = length_of(a, s) - kItemCost;
-    } else {
-      at += tiles + kItemCost;
-      tile = -kItemCost;
-      if (++head == a.kv_heads) {
-        head = 0;
-        do {
-          s = sequence(a, ++seq);
-          tiles = length_of(a, s) - kItemCost;
-        } while (tiles < 0);
-      }
-    }
-    if (tile < 0) {                          // the positions before its first tile
-      left += tile;
+    for (;; begin = false) {
       if (left <= 0) return false;
-      tile = 0;
+      if (begin) {
+        s = sequence(a, seq);
+        tiles = length_of(a, s) - kItemCost;
+      } else {
+        at += tiles + kItemCost;
+        tile = -kItemCost;
+        if (++head == a.kv_heads) {
+          head = 0;
+          do {
+            s = sequence(a, ++seq);
+            tiles = length_of(a, s) - kItemCost;
+          } while (tiles < 0);
+        }
+      }
+      if (tile < 0) {                        // the positions before its first tile
+        left += tile;
+        if (left <= 0) return false;
+        tile = 0;
+      }
+      first = tile;
+      last = min(tiles, tile + left);
+      left -= last - first;
+      if (tiles > kShortItem) return true;
+      last = tiles;                          // whole, the block's that its first tile is in
+      if (first == 0) return true;
     }
-    first = tile;
-    last = min(tiles, tile + left);
-    left -= last - first;
-    return true;
   }
 };
 
