@@ -131,6 +131,19 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
 // Two fp32 at a time.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
@@ -664,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (share.split && t == 1 && tiles == 0) continue;
       const int r = share.split ? threadIdx.x & 127 : threadIdx.x;     // row of the item
       const int limit = row_limit(a, w, r);
+      const int all_see = __reduce_min_sync(kAll, limit);    // keys that every row of the warp sees
       float m = -INFINITY, l = 0.f;
       int k0 = share.key_of(0);
       for (int j = 0; j < tiles; ++j, k0 += share.split ? 2 * kTile : kTile) {
@@ -676,8 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32_issue(x_col + 32, x + 32);
         tmem_wait_ld32(x);
         tmem_wait_ld32(x + 32);
-        const int seen = limit - k0;
-        if (__any_sync(0xFFFFFFFFu, seen < kTile)) {
+        if (all_see - k0 < kTile) {
+          const int seen = limit - k0;
 #pragma unroll
           for (int e = 0; e < kTile; ++e)
             if (e >= seen) x[e] = 0xFF800000u;
@@ -707,12 +721,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld32(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              ptx::tmem_st16(o_col + e0, *reinterpret_cast<uint32_t(*)[16]>(o));
-              ptx::tmem_st16(o_col + e0 + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+              tmem_st32(o_col + e0, o);
             }
           }
         }
-        if (w.kend - k0 < kTile && (w.kend - k0) % 16 != 0) {
+        if (j + 1 == tiles && w.kend - k0 < kTile && (w.kend - k0) % 16 != 0) {
           // values behind the last key may be anything, and 0 times them must be 0: the rows
           // that share the last key's sixteen are cleared, by each row tile before its own
           // products (the second to come writes zeros over zeros)
@@ -730,8 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum[2] = {0, 0};
         uint32_t p[32];
         terms(p, x, scale2, from, sum);
-        ptx::tmem_st16(x_col, *reinterpret_cast<uint32_t(*)[16]>(p));
-        ptx::tmem_st16(x_col + 16, *reinterpret_cast<uint32_t(*)[16]>(p + 16));
+        tmem_st32(x_col, p);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
