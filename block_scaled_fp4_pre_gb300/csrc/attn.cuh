@@ -157,6 +157,12 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, const CUtensorMap* 
   __syncwarp();
 }
 
+// x f + y g, each product rounded: the same from either side, so that an item of two parts has the
+// same bits whichever of its blocks joins them, and by whichever way.
+__device__ __forceinline__ float add_scaled(float x, float f, float y, float g) {
+  return __fadd_rn(__fmul_rn(x, f), __fmul_rn(y, g));
+}
+
 // What ends a row: its sums, with m the log2 of the term they are relative to, join the shared
 // prefix's (main part) and become the output, or are kept (SHARED).  `index` is the row among
 // its kv head's rows of all tokens.
@@ -170,7 +176,7 @@ __device__ __forceinline__ void finish_sums(Finish& f, float m, float l, float2 
   const float top = fmaxf(m, part.x), base = top == -INFINITY ? 0.f : top;
   f.mine = exp2_approx(m - base);
   f.theirs = exp2_approx(part.x - base);
-  l = l * f.mine + part.y * f.theirs;
+  l = add_scaled(l, f.mine, part.y, f.theirs);
   f.inv = l > 0.f ? 1.f / l : 0.f;
   f.lse = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -203,10 +209,10 @@ __device__ __forceinline__ void finish_quad(const AttnArgs& a, const Finish& f, 
   }
   if (f.other) {
     const float4 y = f.other[quad];
-    v.x = v.x * f.mine + y.x * f.theirs;
-    v.y = v.y * f.mine + y.y * f.theirs;
-    v.z = v.z * f.mine + y.z * f.theirs;
-    v.w = v.w * f.mine + y.w * f.theirs;
+    v.x = add_scaled(v.x, f.mine, y.x, f.theirs);
+    v.y = add_scaled(v.y, f.mine, y.y, f.theirs);
+    v.z = add_scaled(v.z, f.mine, y.z, f.theirs);
+    v.w = add_scaled(v.w, f.mine, y.w, f.theirs);
   }
   *reinterpret_cast<uint2*>(a.out + token * a.ldo + head * D + quad * 4) = make_uint2(
       pack_bf16(v.x * f.inv, v.y * f.inv), pack_bf16(v.z * f.inv, v.w * f.inv));
@@ -239,14 +245,17 @@ __device__ __forceinline__ Joined join_parts(const AttnArgs& a, int from, int to
     for (int e = 0; e < kAtOnce; ++e) up = fmaxf(up, st[e].x);
     const float base = up == -INFINITY ? 0.f : up, f = exp2_approx(j.top - base);
     j.top = up;
-    j.sum *= f;
-    j.acc.x *= f; j.acc.y *= f; j.acc.z *= f; j.acc.w *= f;
+    j.sum = __fmul_rn(j.sum, f);
+    j.acc.x = __fmul_rn(j.acc.x, f); j.acc.y = __fmul_rn(j.acc.y, f);
+    j.acc.z = __fmul_rn(j.acc.z, f); j.acc.w = __fmul_rn(j.acc.w, f);
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) {
       const float g = b0 + e <= to ? exp2_approx(st[e].x - base) : 0.f;
-      j.sum += st[e].y * g;
-      j.acc.x += y[e].x * g; j.acc.y += y[e].y * g;
-      j.acc.z += y[e].z * g; j.acc.w += y[e].w * g;
+      j.sum = add_scaled(j.sum, 1.f, st[e].y, g);
+      j.acc.x = add_scaled(j.acc.x, 1.f, y[e].x, g);
+      j.acc.y = add_scaled(j.acc.y, 1.f, y[e].y, g);
+      j.acc.z = add_scaled(j.acc.z, 1.f, y[e].z, g);
+      j.acc.w = add_scaled(j.acc.w, 1.f, y[e].w, g);
     }
   }
   return j;

@@ -356,8 +356,8 @@ __device__ __forceinline__ void load_output(uint32_t (&o)[32], uint32_t col, boo
     for (int e = 0; e < 32; ++e) o[e] = 0u;
   }
 }
-__device__ __forceinline__ uint32_t add_scaled(uint32_t x, float f, uint32_t y, float g) {
-  return __float_as_uint(__uint_as_float(x) * f + __uint_as_float(y) * g);
+__device__ __forceinline__ uint32_t add_bits(uint32_t x, float f, uint32_t y, float g) {
+  return __float_as_uint(add_scaled(__uint_as_float(x), f, __uint_as_float(y), g));
 }
 
 // A warp joins the parts of its rows [row0, row0 + rows) of an item, in the order of the line.
@@ -837,10 +837,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint4 y = *staged(sm.stage[warp + 4], lane, e);
-            o[4 * e] = add_scaled(o[4 * e], f0, y.x, f1);
-            o[4 * e + 1] = add_scaled(o[4 * e + 1], f0, y.y, f1);
-            o[4 * e + 2] = add_scaled(o[4 * e + 2], f0, y.z, f1);
-            o[4 * e + 3] = add_scaled(o[4 * e + 3], f0, y.w, f1);
+            o[4 * e] = add_bits(o[4 * e], f0, y.x, f1);
+            o[4 * e + 1] = add_bits(o[4 * e + 1], f0, y.y, f1);
+            o[4 * e + 2] = add_bits(o[4 * e + 2], f0, y.z, f1);
+            o[4 * e + 3] = add_bits(o[4 * e + 3], f0, y.w, f1);
           }
           ptx::named_bar_sync(peers, 64);
         }
@@ -887,10 +887,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const uint4 y = *staged(stage, lane, e);
-                o[4 * e] = add_scaled(o[4 * e], fin.mine, y.x, fin.theirs);
-                o[4 * e + 1] = add_scaled(o[4 * e + 1], fin.mine, y.y, fin.theirs);
-                o[4 * e + 2] = add_scaled(o[4 * e + 2], fin.mine, y.z, fin.theirs);
-                o[4 * e + 3] = add_scaled(o[4 * e + 3], fin.mine, y.w, fin.theirs);
+                o[4 * e] = add_bits(o[4 * e], fin.mine, y.x, fin.theirs);
+                o[4 * e + 1] = add_bits(o[4 * e + 1], fin.mine, y.y, fin.theirs);
+                o[4 * e + 2] = add_bits(o[4 * e + 2], fin.mine, y.z, fin.theirs);
+                o[4 * e + 3] = add_bits(o[4 * e + 3], fin.mine, y.w, fin.theirs);
               }
               __syncwarp();
             }
