@@ -433,17 +433,22 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
 
 moe_status moe_attention_check(void* ws, void* stream) {
   if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  moe_attention_dims dims;
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    if (g_attention.find(ws) == g_attention.end())
+    const auto it = g_attention.find(ws);
+    if (it == g_attention.end())
       return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was not initialised", ws);
+    dims = it->second.dims;
   }
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
   int32_t flag = 0;
   if ((e = cudaMemcpy(&flag, ws, sizeof(flag), cudaMemcpyDeviceToHost)))
     return cuda_fail(e, "flag read");
-  if ((e = cudaMemset(ws, 0, sizeof(flag)))) return cuda_fail(e, "flag clear");
+  // a call that gave up may have left its counters of parts behind
+  const size_t clear = flag & kErrTimeout ? ws_layout(dims).cuts : sizeof(flag);
+  if ((e = cudaMemset(ws, 0, clear))) return cuda_fail(e, "flag clear");
   if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a device wait ran past its limit");
   if (flag & kErrPage)
     return fail(MOE_ERR_PAGE, "a token's page is outside its table or the cache");

@@ -484,8 +484,8 @@ MXMOE_API moe_status moe_rope(const moe_rope_dims *dims, const void *table_dev, 
  * 128-byte aligned: the rows of one page and head lie together.  A sequence's token p is row
  * p % page_size of the page that entry p / page_size of its page table row names.
  * Ranges: head_dim 64 or 128; q_heads a multiple of kv_heads, at most 1024 and 256 times it;
- * page_size a power of two in [16, 256]; num_pages >= 1 with num_pages * kv_heads * page_size < 2^31; max_tokens (of
- * one call) in [1, 2^20]; 0 <= max_shared_tokens <= max_tokens. */
+ * page_size a power of two in [16, 256]; num_pages >= 1 with num_pages * kv_heads * page_size <
+ * 2^31; max_tokens (of one call) in [1, 2^20]; 0 <= max_shared_tokens <= max_tokens. */
 typedef struct moe_attention_dims {
     int32_t q_heads;
     int32_t kv_heads;
@@ -567,11 +567,11 @@ MXMOE_API moe_status moe_kv_append(const moe_attention_dims *dims, const moe_kv_
  *   out_dev  bf16, the same with ldo; shares no memory with q or the caches
  *   lse_dev  fp32 [tokens, q_heads], ln of the sum of exp(scale * q . k), or NULL
  *   scale    finite and positive
- * Strides are multiples of 8 and at least a row, pointers 16-byte aligned.  The caches hold the new tokens' keys and
- * values already (moe_kv_append).  Rows of the cache that no token of the call sees may hold
- * anything, those that one sees finite values; q is finite.  Products of bf16 values
- * are summed in fp32, the probabilities rounded to bf16 for theirs with the values, their sum
- * taken in fp32.  Results do not depend on timing. */
+ * Strides are multiples of 8 and at least a row, pointers 16-byte aligned.  The caches hold the
+ * new tokens' keys and values already (moe_kv_append).  Rows of the cache that no token of the
+ * call sees may hold anything, those that one sees finite values; q is finite.  Products of bf16
+ * values are summed in fp32, the probabilities rounded to bf16 for theirs with the values, their
+ * sum taken in fp32.  Results do not depend on timing. */
 MXMOE_API moe_status moe_attention(const moe_attention_dims *dims, const moe_kv_batch *batch,
                                    const void *q_dev, int64_t ldq, const void *k_cache_dev,
                                    const void *v_cache_dev, float scale, void *out_dev,
@@ -579,7 +579,8 @@ MXMOE_API moe_status moe_attention(const moe_attention_dims *dims, const moe_kv_
                                    void *stream);
 
 /* Synchronises `stream`, then reads and clears the workspace's error flags: MOE_ERR_PAGE,
- * MOE_ERR_TIMEOUT or MOE_OK. */
+ * MOE_ERR_TIMEOUT (outputs of the calls since the last check are undefined, the workspace is ready
+ * for the next) or MOE_OK. */
 MXMOE_API moe_status moe_attention_check(void *ws_dev, void *stream);
 
 /* FP4 tensor-core throughput probe (measurement only; the denominator of the

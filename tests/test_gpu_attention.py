@@ -216,6 +216,21 @@ def test_same_bits_whatever_the_blocks_order(D):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("new", [1, 300])
+def test_a_workspace_after_a_timeout(new):
+    # as a call that gave up leaves it: the flag set and counters of parts begun
+    p = Paged(new=[new], old=[9000], q_heads=32, kv_heads=8, uniform=True)
+    a, l = p.run()
+    words = p.ws.view(torch.int32)
+    words[0] = 2
+    words[256:512] = 1
+    with pytest.raises(mx.MoeError) as e:
+        mx.moe_attention_check(p.ws)
+    assert e.value.status == mx.MOE_ERR_TIMEOUT
+    b, m = p.run()
+    assert torch.equal(a, b) and torch.equal(l, m)
+
+
 @pytest.mark.parametrize("new", [1, 50])
 def test_bad_pages_are_reported(new):
     p = Paged(new=[new, new], old=[200, 200])
