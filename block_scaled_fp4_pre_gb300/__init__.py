@@ -94,6 +94,11 @@ class AttentionDims(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
                 ("max_shared_tokens", ctypes.c_int32)]
 
+    @property
+    def cache_shape(self) -> tuple[int, int, int, int]:
+        """Of each cache."""
+        return self.num_pages, self.kv_heads, self.page_size, self.head_dim
+
     def __repr__(self):
         return ("AttentionDims("
                 + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")")
@@ -102,10 +107,8 @@ class AttentionDims(ctypes.Structure):
 def make_attention_dims(q_heads: int, kv_heads: int, head_dim: int, num_pages: int,
                         page_size: int, max_tokens: int, max_shared_tokens: int = 0
                         ) -> AttentionDims:
-    d = AttentionDims(q_heads, kv_heads, head_dim, num_pages, page_size, max_tokens,
-                      max_shared_tokens)
-    d.cache_shape = (num_pages, kv_heads, page_size, head_dim)   # of each cache
-    return d
+    return AttentionDims(q_heads, kv_heads, head_dim, num_pages, page_size, max_tokens,
+                         max_shared_tokens)
 
 
 class KvBatch(ctypes.Structure):
@@ -607,6 +610,13 @@ def _ints(t, n: int, name: str, device: int | None = None) -> int:
     raise ValueError(f"{name}: need {n} contiguous int32, got {t.dtype} {list(t.shape)}")
 
 
+def _table(table, rope: RopeDims, device: int) -> int:
+    """Address of the rotation's table; raw addresses pass."""
+    if isinstance(table, torch.Tensor):
+        _here(table, "table", device)
+    return _bytes(table, 4 * rope.rotary_dim, "table")
+
+
 def moe_rope(dims: RopeDims, table, x, positions, out=None, stream=None) -> None:
     """Rotates x, bf16 [tokens, heads, head_dim] with contiguous tokens, by each token's int32
     position, into out or in place."""
@@ -621,7 +631,7 @@ def moe_rope(dims: RopeDims, table, x, positions, out=None, stream=None) -> None
     if out is not None and out is not x:
         po, ldo = _here(out, "out", device), _heads(out, T, heads, D, "out")
     status = (_lib or lib()).moe_rope(
-        ctypes.byref(dims), _bytes(table, 4 * dims.rotary_dim, "table"), px, ldx,
+        ctypes.byref(dims), _table(table, dims, device), px, ldx,
         _ints(positions, T, "positions", device), T, heads, po, ldo,
         _raw_stream(device) if stream is None else _stream(stream))
     if status:
@@ -664,10 +674,10 @@ def moe_attention_set_shared(ws, mode: int) -> None:
     _check(lib().moe_attention_set_shared(_ptr(ws), int(mode)))
 
 
-def _cache(t, dims: AttentionDims, name: str, device: int) -> int:
-    if t.dtype is torch.bfloat16 and t.shape == dims.cache_shape and t.is_contiguous():
+def _cache(t, shape: tuple, name: str, device: int) -> int:
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous():
         return _here(t, name, device)
-    raise ValueError(f"{name}: need contiguous bf16 {list(dims.cache_shape)}, got {t.dtype} "
+    raise ValueError(f"{name}: need contiguous bf16 {list(shape)}, got {t.dtype} "
                      f"{list(t.shape)}")
 
 
@@ -684,7 +694,8 @@ def moe_kv_append(dims: AttentionDims, batch: KvBatch, k, v, k_cache, v_cache, w
     """Appends keys (rotated, given rope and its table) and values to the paged cache, and
     rotates q into q_out (or in place).  q, k and v are bf16 [tokens, heads, head_dim]."""
     device = _batch_device(batch)
-    T, (_, hk, _, D) = batch.tokens, dims.cache_shape
+    T, shape = batch.tokens, dims.cache_shape
+    _, hk, _, D = shape
     pq = pqo = pt = None
     ldq = ldqo = 0
     if q is not None:
@@ -696,7 +707,7 @@ def moe_kv_append(dims: AttentionDims, batch: KvBatch, k, v, k_cache, v_cache, w
     elif q_out is not None:
         raise ValueError("q_out: given without q")
     if rope is not None:
-        pt = _bytes(table, 4 * rope.rotary_dim, "table")
+        pt = _table(table, rope, device)
         rope = ctypes.byref(rope)
     elif table is not None:
         raise ValueError("table: given without rope")
@@ -704,8 +715,8 @@ def moe_kv_append(dims: AttentionDims, batch: KvBatch, k, v, k_cache, v_cache, w
         ctypes.byref(dims), ctypes.byref(batch), rope, pt,
         None if positions is None else _ints(positions, T, "positions", device), pq, ldq, pqo,
         ldqo, _here(k, "k", device), _heads(k, T, hk, D, "k"), _here(v, "v", device),
-        _heads(v, T, hk, D, "v"), _cache(k_cache, dims, "k_cache", device),
-        _cache(v_cache, dims, "v_cache", device), _here(ws, "workspace", device), ws.nbytes,
+        _heads(v, T, hk, D, "v"), _cache(k_cache, shape, "k_cache", device),
+        _cache(v_cache, shape, "v_cache", device), _here(ws, "workspace", device), ws.nbytes,
         _raw_stream(device) if stream is None else _stream(stream))
     if status:
         _check(status)
@@ -718,7 +729,8 @@ def moe_attention(dims: AttentionDims, batch: KvBatch, q, k_cache, v_cache, out,
     q and out are bf16 [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads] or None; scale is
     head_dim ** -0.5 unless given."""
     device = _batch_device(batch)
-    T, D, hq = batch.tokens, dims.cache_shape[3], dims.q_heads
+    T, shape, hq = batch.tokens, dims.cache_shape, dims.q_heads
+    D = shape[3]
     pl = None
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.shape != (T, hq) or not lse.is_contiguous():
@@ -726,8 +738,8 @@ def moe_attention(dims: AttentionDims, batch: KvBatch, q, k_cache, v_cache, out,
         pl = _here(lse, "lse", device)
     status = (_lib or lib()).moe_attention(
         ctypes.byref(dims), ctypes.byref(batch), _here(q, "q", device),
-        _heads(q, T, hq, D, "q"), _cache(k_cache, dims, "k_cache", device),
-        _cache(v_cache, dims, "v_cache", device), D ** -0.5 if scale is None else scale,
+        _heads(q, T, hq, D, "q"), _cache(k_cache, shape, "k_cache", device),
+        _cache(v_cache, shape, "v_cache", device), D ** -0.5 if scale is None else scale,
         _here(out, "out", device), _heads(out, T, hq, D, "out"), pl,
         _here(ws, "workspace", device), ws.nbytes,
         _raw_stream(device) if stream is None else _stream(stream))

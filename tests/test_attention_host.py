@@ -25,6 +25,13 @@ def attn(mx, **change):
     return mx.make_attention_dims(**d)
 
 
+def test_the_cache_has_the_shape_of_the_dims(mx):
+    d = mx.AttentionDims(8, 2, 128, 10, 16, 64, 0)
+    assert d.cache_shape == (10, 2, 16, 128)
+    d.num_pages = 100
+    assert d.cache_shape == (100, 2, 16, 128)
+
+
 def test_table_sizes(mx):
     for D, r in ((8, 2), (128, 128), (128, 30), (512, 512)):
         assert mx.moe_rope_table_size(mx.make_rope_dims(D, r)) == r // 2 * 8
