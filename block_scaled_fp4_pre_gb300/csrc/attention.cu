@@ -9,13 +9,14 @@ namespace {
 // what it takes and what it saves, in us.
 //
 // Apart, each sequence streams the prefix: in the few-row kernel at 11 TB/s, mostly from L2; in
-// the tile kernel as tiles of its own items, 1.55 us a tile and SM (1.1 at 64 elements a head), the
-// last item of a sequence as long as a whole one.  Together it is the tiles of the whole batch's
-// rows, two launches, and the hand-over of each row's sums.  Measured, apart / shared, 32 heads of
-// 128 on 8 kv heads: 32 sequences of one token behind 1024 common ones 27.3 / 29.7 us, behind
-// 4096 59.3 / 38.3; 4 behind 16384 30.4 / 32.8, 8 52.4 / 35.1; 16 of 5 tokens behind 1024 29.0 /
-// 35.6, behind 4096 56.0 / 43.3; 32 of 30 tokens behind 4096 96.7 / 102.5, behind 16384 321 / 250;
-// 8 of 400 tokens behind 16384 704 / 715.
+// the tile kernel as tiles of its own items, 1.55 us for 128 keys and 256 rows on an SM (1.1 at 64
+// elements a head), the last item of a sequence as long as a whole one.  Together it is the tiles of
+// the whole batch's rows, two launches, and the hand-over of each row's sums.  Measured, apart /
+// shared, 32 heads of 128 on 8 kv heads: 32 sequences of one token behind 1024 common ones 29.7 /
+// 33.4 us, behind 4096 63.8 / 37.4; 4 behind 16384 33.4 / 31.6, 8 56.8 / 34.2; 16 of 5 tokens
+// behind 1024 26.3 / 35.0, behind 4096 46.3 / 42.0; 32 of 30 tokens behind 4096 81.0 / 97.2, behind
+// 16384 252 / 223; 8 of 400 tokens behind 16384 625 / 679; 4 of 130 155 / 138, where the estimate
+// takes the slower way, as with 16 of 5 at 64 elements a head on 2 kv heads (35.5 / 32.1).
 bool worth_sharing(const AttnLaunch& g, bool few) {
   const AttnArgs& a = g.args;
   const double batch = a.batch.batch, prefix = a.batch.shared_len, D = g.head_dim;

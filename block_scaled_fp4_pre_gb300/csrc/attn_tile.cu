@@ -7,17 +7,26 @@
 //   SHARED   rows of all sequences, the common prefix's keys [0, kstart): one pass over the
 //            prefix serves the whole batch; its unfinished sums go to the workspace, where
 //            the main part's rows pick them up
-// A tile of keys (128) goes through S = Q K^T (both operands in shared memory, 128 x 128 fp32 in
+// A tile of 64 keys goes through S = Q K^T (both operands in shared memory, 128 x 64 fp32 in
 // tensor memory), a thread a row for the softmax, and O += P V with P as bf16 in tensor memory,
 // in the columns of S that it came from, and V as the transposed operand.
 //
-// The tensor cores alternate between the two row tiles: while one tile's scores are in the hands
-// of its warpgroup, the other's products run.  The loader keeps a ring of key and value tiles
-// full.  The running maximum is raised only where a logit passes it by 2^8 (the sums and the
-// rounding of P allow it), so the output in tensor memory is rarely scaled; its warpgroup does that
-// before it hands over the next P, when no product on it is in flight.
+// A row tile has a warp that issues its products, a warpgroup for its softmax and two buffers of
+// scores: the next tile's scores are made during this one's softmax, and the tensor cores alternate
+// between the row tiles.  Where an item's rows fill one row tile at most, the two take every other
+// tile of its keys instead and add up at its end.  The loaders keep a ring of key and value
+// tiles full.  The running maximum is raised only where a logit passes it by 2^8 (the sums
+// and the rounding of P allow it), so the output in tensor memory is rarely scaled; its warpgroup
+// does that before it hands over the next P, when no product on it is in flight.
 //
-// Bound by the tensor cores: 4 x 128 x 128 x D operations a tile pair at the dense bf16 rate.
+// Bound by the tensor cores: 4 x 128 x 64 x D operations a row tile and tile of keys at the dense
+// bf16 rate.  1415 us for a prompt of 16384 tokens, 32 heads of 128 on 8 (1554 TFLOP/s, 0.82 of the
+// measured rate of a library's product; 1483 us once the board's power limit sets in); the scores'
+// products, 64 columns wide, read more of shared memory than they compute, and tiles of 128 columns
+// would leave no room for two buffers a row tile beside the outputs.  At 64 elements a head the
+// softmax's instructions take longer than the products: 4 prompts of 2048 103 us.  With one row
+// tile an item it is bound by HBM: 19 drafts of 8 tokens over 8192 keys 103 us (0.93 of the measured
+// copy bandwidth).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -196,13 +205,14 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 }
 
 // What an item costs beside its tiles (its queries, its end), in tiles: positions of the line
-// before its first.  An item's end takes 5 to 8 thousand cycles, a tile 3.1; without it the
-// blocks at the short items of a prompt's beginning were last (16384 tokens: 1614 us; with 2, 3,
-// 5: 1560, 1567, 1584).
+// before its first.  us with 2, 3, 4, 5, 6: a prompt of 16384 tokens 1462, 1428, 1415, 1416, 1422;
+// of 4096 129, 120, 116, 117, 118; 4 of 2048 at 64 elements a head 108, 104, 103, 105, 106.
 constexpr int kItemCost = 4;
 
 // Items of up to this many tiles are not cut: a block takes all of one whose first tile is in its
-// range.
+// range.  us with 0, 3, 6, 12: 54 prompts of 110 tokens 71.3, 59.8, 59.4, 59.4; 106 of 12 tokens
+// 16.7, 11.8, 11.7, 11.9; 117 drafts of 8 over 300 tokens 50.8, 51.6, 50.6, 46.2; 8 drafts of 5
+// behind 16384 common tokens 59.3, 59.8, 59.8, 66.0.
 constexpr int kShortItem = 6;
 
 // An item has whole tokens, `step` of them (256 / group) but for a sequence's last.

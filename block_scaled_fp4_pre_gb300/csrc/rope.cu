@@ -14,10 +14,10 @@
 // with few tokens latency counts, and a thread takes one head.  Queries, keys and values of an
 // append are one launch: thread groups of the three tensors side by side.
 //
-// Bound by HBM at large token counts: 8191 tokens of 40 heads of 128, half of them rotated, 27.1
-// us (168 MB, 0.93 of the measured copy bandwidth); an append of 15.3 k tokens of 32 query and
-// 8 + 8 key and value heads 60.7 us (382 MB, 0.94).  By latency at few: one token 2.0 us, its
-// append with queries 3.0 us (its page is looked up in three dependent loads).
+// Bound by HBM at large token counts: 8191 tokens of 40 heads of 128, half of them rotated, 27.7
+// us (168 MB, 0.91 of the measured copy bandwidth); an append of 15.3 k tokens of 32 query and
+// 8 + 8 key and value heads 61.5 us (382 MB, 0.93).  By latency at few: one token 2.6 us, its
+// append with queries 3.2 us (its page is looked up in three dependent loads).
 #include <cuda_runtime.h>
 
 #include "common.cuh"

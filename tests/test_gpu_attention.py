@@ -216,6 +216,51 @@ def test_same_bits_whatever_the_blocks_order(D):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("new", [[1, 2], [90, 1, 300]])
+def test_offsets_past_32_bits(new):
+    # the same pages at the end of caches of more than 2^32 elements, appended there and read
+    p = Paged(new=new, old=[700] * len(new), page=256, q_heads=16, kv_heads=8)
+    a, l = p.run()
+    pages, more = p.k.shape[0], 16384
+    dims = mx.make_attention_dims(p.hq, p.hk, p.D, pages + more, p.page, p.T)
+    batch = mx.make_kv_batch(p.batch.tensors[0], p.batch.tensors[2] + more, p.T,
+                             cu_new=p.batch.tensors[1], max_new=max(new))
+    ws = torch.empty(mx.moe_attention_workspace_size(dims), dtype=torch.uint8, device="cuda")
+    mx.moe_attention_workspace_init(dims, ws)
+    k, v = (torch.empty(dims.cache_shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[more:], v[more:] = p.k, p.v
+    rows = [torch.empty(p.T, p.hk, p.D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for b, n in enumerate(new):
+        for i in range(n):
+            page, r = p.slot(b, p.lens[b] - n + i)
+            for cache, far, row in zip((p.k, p.v), (k, v), rows):
+                row[p.cu[b] + i] = cache[page, :, r]
+                far[more + page, :, r] = 5.0
+    mx.moe_kv_append(dims, batch, *rows, k, v, ws)
+    out, lse = torch.empty_like(a), torch.empty_like(l)
+    mx.moe_attention(dims, batch, p.q, k, v, out, ws, lse=lse)
+    mx.moe_attention_check(ws)
+    assert torch.equal(out, a) and torch.equal(lse, l)
+
+
+def test_calls_on_two_streams():
+    calls = [Paged(new=[1] * 40, old=[997] * 40, uniform=True, seed=1),
+             Paged(new=[300, 70], old=[500, 900], shared=64, seed=2)]
+    want = [p.run() for p in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[(torch.full_like(a, 77.0), torch.full_like(l, 77.0)) for _ in range(20)]
+           for a, l in want]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for p, outs, stream in zip(calls, got, streams):
+            mx.moe_attention(p.dims, p.batch, p.q, p.k, p.v, outs[i][0], p.ws, lse=outs[i][1],
+                             stream=stream)
+    for p, stream in zip(calls, streams):
+        mx.moe_attention_check(p.ws, stream)
+    for (a, l), outs in zip(want, got):
+        assert all(torch.equal(a, b) and torch.equal(l, m) for b, m in outs)
+
+
 @pytest.mark.parametrize("new", [1, 300])
 def test_a_workspace_after_a_timeout(new):
     # as a call that gave up leaves it: the flag set and counters of parts begun
