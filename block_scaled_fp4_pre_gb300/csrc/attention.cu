@@ -10,8 +10,8 @@ namespace {
 //
 // Apart, each sequence streams the prefix: in the few-row kernel at 11 TB/s, mostly from L2; in
 // the tile kernel as tiles of its own items, 1.55 us for 128 keys and 256 rows on an SM (1.1 at 64
-// elements a head), the last item of a sequence as long as a whole one.  Together it is the tiles of
-// the whole batch's rows, two launches, and the hand-over of each row's sums.  Measured, apart /
+// elements a head), the last item of a sequence as long as a whole one.  Together it is the tiles
+// of the whole batch's rows, two launches, and the hand-over of each row's sums.  Measured, apart /
 // shared, 32 heads of 128 on 8 kv heads: 32 sequences of one token behind 1024 common ones 29.7 /
 // 33.4 us, behind 4096 63.8 / 37.4; 4 behind 16384 33.4 / 31.6, 8 56.8 / 34.2; 16 of 5 tokens
 // behind 1024 26.3 / 35.0, behind 4096 46.3 / 42.0; 32 of 30 tokens behind 4096 81.0 / 97.2, behind

@@ -71,9 +71,9 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 
 // What an item costs beside its tiles (its queries, its end), in tiles: positions of the line
-// before its first.  us with 1, 2, 3, 4: 48 ragged sequences of 64 elements a head 19.1, 17.4, 17.1,
-// 17.3; 64 sequences behind common tokens, with the prefix's part, 93.7, 86.2, 85.0, 84.6; 7 drafts
-// of 4 over 9 k tokens 16.4, 15.8, 15.4, 15.8.
+// before its first.  us with 1, 2, 3, 4: 48 ragged sequences of 64 elements a head 19.1, 17.4,
+// 17.1, 17.3; 64 sequences behind common tokens, with the prefix's part, 93.7, 86.2, 85.0, 84.6; 7
+// drafts of 4 over 9 k tokens 16.4, 15.8, 15.4, 15.8.
 constexpr int kItemCost = 3;
 
 // Items of up to this many tiles are not cut: a block takes all of one whose first tile is in its

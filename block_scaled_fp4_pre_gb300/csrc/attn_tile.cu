@@ -25,8 +25,8 @@
 // products, 64 columns wide, read more of shared memory than they compute, and tiles of 128 columns
 // would leave no room for two buffers a row tile beside the outputs.  At 64 elements a head the
 // softmax's instructions take longer than the products: 4 prompts of 2048 103 us.  With one row
-// tile an item it is bound by HBM: 19 drafts of 8 tokens over 8192 keys 103 us (0.93 of the measured
-// copy bandwidth).
+// tile an item it is bound by HBM: 19 drafts of 8 tokens over 8192 keys 103 us (0.93 of the
+// measured copy bandwidth).
 #include <algorithm>
 
 #include "attn.cuh"
