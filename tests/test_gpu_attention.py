@@ -32,6 +32,11 @@ def test_head_groups(q_heads, kv_heads, D):
     both(new=[1, 1, 1], old=[70, 0, 401], q_heads=q_heads, kv_heads=kv_heads, D=D, uniform=True)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads", [(100, 1), (255, 1), (256, 1), (1024, 4)])
+def test_large_head_groups(q_heads, kv_heads):
+    both(new=[1, 3, 2], old=[70, 0, 401], q_heads=q_heads, kv_heads=kv_heads, D=64, shared=16)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 def test_page_sizes(page):
     both(new=[1, 3, 70], old=[300, 513, 0], page=page, spare=5)
@@ -67,6 +72,20 @@ def test_many_sequences():
     both(new=[1] * 300, old=old, q_heads=4, uniform=True)
     new = torch.randint(0, 4, (300,), generator=g).tolist()
     both(new=new, old=old, q_heads=4)
+
+
+@pytest.mark.parametrize("q_heads", [2, 40])
+def test_most_sequences(q_heads):
+    g = torch.Generator().manual_seed(6)
+    p = Paged(new=[1] * 4096, old=torch.randint(0, 40, (4096,), generator=g).tolist(),
+              q_heads=q_heads, kv_heads=1, D=64, uniform=True)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("shared", [0, 32])
+@pytest.mark.parametrize("q_heads", [8, 80])
+def test_no_sequence_has_a_token(q_heads, shared):
+    both(new=[0, 0, 0], old=[5, 0, 700], q_heads=q_heads, shared=shared, tail=3)
 
 
 def test_sequences_without_a_token_give_zeros():
