@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t begin = range_start(line, N, blockIdx.x);
   const int64_t end = range_start(line, N, blockIdx.x + 1);
   if (begin >= at && begin < at + mine * a.kv_heads) {
-    int b = b0, t = 0;
-    for (;; ++b) {
+    int b = b0, t = (int)mine;
+    for (; per > 1; ++b) {
       t = length_of(a, sequence(a, b));
       if (begin < at + (int64_t)t * a.kv_heads) break;
       at += (int64_t)t * a.kv_heads;
