@@ -46,6 +46,7 @@ struct Smem {
   int64_t scan[kThreads / 32];
   uint64_t full[Ring<D>::kStages], empty[Ring<D>::kStages];
   int start_left, start_seq, start_head, start_tile;
+  int issued[2][kLoaders];                      // tiles of keys, and of values, by each loader
   int abort, joins;
 };
 
@@ -191,7 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.head = sm.start_head;
   w.tile = sm.start_tile;
   w.at = begin - w.tile;
+  // A warp whose wait has run out, or that finds that another's has, loads, reads and releases
+  // nothing more.
   volatile int* abort = &sm.abort;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(kAll, ptx::mbar_wait(bar, parity, abort, kAttnWaitNs));
+  };
   int stage = 0;
   uint32_t phase = 0;
   auto advance = [&] {
@@ -212,29 +219,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     Pages pages;
-    int seq = -1;
-    for (bool first = true; __any_sync(kAll, w.next(a, first)); first = false) {
+    int seq = -1, issued = 0;
+    for (bool first = true; ok && __any_sync(kAll, w.next(a, first)); first = false) {
       if (__any_sync(kAll, w.seq != seq)) pages.start(a, seq = w.seq);
       const int head = __shfl_sync(kAll, w.head, 0), kend = __shfl_sync(kAll, w.s.kend, 0);
       int k0 = __shfl_sync(kAll, a.kstart + w.first * kAttnTile, 0);
       const int n = __shfl_sync(kAll, w.last - w.first, 0);
       for (int i = 0; i < n && k0 < kend; ++i, k0 += kAttnTile) {
-        __all_sync(kAll, ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs));
+        ok = wait(&sm.empty[stage], phase ^ 1);
+        if (!ok) break;
         load_tile<D, kAttnTile, kLoaders>(a, v ? &vmap : &kmap, pages, head, k0,
                                           min(kAttnTile, kend - k0), part, sm.ring[stage],
                                           &sm.full[stage]);
         advance2();
+        ++issued;
       }
     }
-    // After a wait that ran out, copies may still be in flight: the block stays for them.
-    if (*abort) {
-      if (lane == 0) atomicOr(a.flags, kErrTimeout);
-      int never = 0;
-      for (int i = 0; i < STAGES; i += 2) {
-        ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
-        advance2();
-      }
-    }
+    if (!ok && lane == 0) atomicOr(a.flags, kErrTimeout);
+    // Every copy issued here must have landed before the block exits.  A stage's phase takes an
+    // arrival of each loader: after a wait that ran out, the one that stopped first makes up for
+    // the tiles that the other has gone on with (at most a ring's, as no stage is released
+    // before all have arrived for it).
+    static_assert(kLoaders == 2, "a loader and the other");
+    constexpr int kMine = STAGES / 2;
+    if (lane == 0) sm.issued[v][part] = issued;
+    ptx::named_bar_sync(2 + v, 32 * kLoaders);
+    const int other = sm.issued[v][part ^ 1], all = max(issued, other);
+    if (lane == 0)
+      for (int i = issued; i < other; ++i) ptx::mbar_arrive(&sm.full[2 * (i % kMine) + v]);
+    int never = 0;
+    for (int i = max(all - kMine, 0); i < all; ++i)
+      ptx::mbar_wait(&sm.full[2 * (i % kMine) + v], (i / kMine) & 1, &never, kAttnWaitNs);
     return;
   }
 
@@ -245,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
   const uint32_t k_base = (warp * 16 + k_row) * 128, v_base = (warp * 16 + v_row) * 128;
   const int swizzle = lane & 7;
-  for (bool first = true; w.next(a, first); first = false) {
+  for (bool first = true; ok && w.next(a, first); first = false) {
     const Sequence& s = w.s;
     const int rows = s.taken * a.group;
     uint32_t q[D / 16][4];
@@ -274,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = a.kstart + t * kAttnTile + warp * 16;      // the warp's first key
       const bool some = tok < s.kend;
       float x[2][4] = {};
-      ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+      ok = wait(&sm.full[stage], phase);
+      if (!ok) break;
       if (some) {
         float y[2][4] = {};                            // two chains a key group
         const uint32_t base = ring + stage * Ring<D>::kBytes + k_base;
@@ -340,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      ptx::mbar_wait(&sm.full[stage], phase, abort, kAttnWaitNs);
+      ok = wait(&sm.full[stage], phase);
+      if (!ok) break;
       if (some) {
         const uint32_t base = ring + stage * Ring<D>::kBytes + v_base;
         // values behind the last key may be anything: 0 times them must be 0
@@ -376,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
       if (c == 0) sm.stats[warp][g + 8 * i] = make_float2(m[i], l[i]);
     }
-    ptx::named_bar_sync(1, 32 * kWarps);
+    ok = ptx::named_bar_and(1, 32 * kWarps, ok);
+    if (!ok) break;
     const bool whole = w.first == 0 && w.last == w.tiles;
     // parts: a block's second is one that begins an item, its first one that does not
     const int slot = 2 * blockIdx.x + (w.first == 0);
@@ -438,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_row<D>(a, s, w.head, r, quad, j.acc, j.sum, j.top);
     }
   }
-  if (*abort && lane == 0) atomicOr(a.flags, kErrTimeout);
+  if (!ok && lane == 0) atomicOr(a.flags, kErrTimeout);
 }
 
 template <int D>
