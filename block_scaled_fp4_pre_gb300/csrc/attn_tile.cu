@@ -526,7 +526,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int key0 = SHARED ? 0 : a.kstart;
   const uint32_t tmem = sm.tmem;
+  // Once a wait has run out every other one gives up too.  The loaders stop there, and the issuers
+  // issue and release nothing more, so that no load meets a copy in flight.  The softmax's warps
+  // hand over no more terms and go through their items: those that meet at barriers have the same
+  // ones.  What they read and store then is undefined, within the call's tensors.
   volatile int* abort = &sm.abort;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(kAll, ptx::mbar_wait(bar, parity, abort, kAttnWaitNs));
+  };
 
   if (warp >= kLoader) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       Pages pages;
       int seq = -1;
-      for (bool first = true; __any_sync(kAll, w.next(a, first)); first = false) {
+      for (bool first = true; ok && __any_sync(kAll, w.next(a, first)); first = false) {
         const int n = __shfl_sync(kAll, w.busy(key0), 0);
         if (n == 0) continue;
         if (__any_sync(kAll, w.seq != seq)) pages.start(a, seq = w.seq);
@@ -554,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kend = __shfl_sync(kAll, w.kend, 0);
         if (v == 1) {
           const int token = __shfl_sync(kAll, w.token, 0);
-          __all_sync(kAll, ptx::mbar_wait(&sm.q_empty, q_phase ^ 1, abort, kAttnWaitNs));
+          ok = wait(&sm.q_empty, q_phase ^ 1);
+          if (!ok) break;
           q_phase ^= 1;
           if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(&sm.q_full, step * a.group * 2 * D);
@@ -565,31 +574,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         for (int i = 0; i < n; ++i, k0 += kTile) {
-          __all_sync(kAll, ptx::mbar_wait(&sm.empty[stage], phase ^ 1, abort, kAttnWaitNs));
+          ok = wait(&sm.empty[stage], phase ^ 1);
+          if (!ok) break;
           load_tile<D, kTile, 1>(a, v ? &vmap : &kmap, pages, head, k0, min(kTile, kend - k0), 0,
                                  sm.ring[stage], &sm.full[stage]);
           advance2(stage, phase);
         }
       }
-      // After a wait that ran out, copies may still be in flight: the block stays for them.
-      if (*abort) {
-        int never = 0;
-        if (v == 1) ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
-        for (int i = 0; i < STAGES; i += 2) {
-          ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
-          advance2(stage, phase);
-        }
+      // Every copy issued here must have landed before the block exits.
+      int never = 0;
+      if (v == 1) ptx::mbar_wait(&sm.q_full, q_phase ^ 1, &never, kAttnWaitNs);
+#pragma unroll 1
+      for (int i = 0; i < STAGES; i += 2) {
+        ptx::mbar_wait(&sm.full[stage], phase ^ 1, &never, kAttnWaitNs);
+        advance2(stage, phase);
       }
     } else {
       // ---- products: a warp a row tile, so that neither waits for the other's softmax ----
       // What steers the loops comes from votes and shuffles, and descriptors grow by sums, so
       // that the compiler keeps them in uniform registers: each of a product's operands would
       // be moved there first otherwise (100 cycles a product, where the tensor cores take 32
-      // to 64).
+      // to 64).  For the same reason a wait that gave up leaves no loop before its item's end (a
+      // prompt of 16384 tokens 1421 us, with a way out behind each wait 1450).
       const int t = warp - kIssuer;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(kAll, ptx::mbar_wait(bar, parity, abort, kAttnWaitNs));
-      };
       int k_stage = 0, v_stage = 1;
       uint32_t k_phase = 0, v_phase = 0, p_phase = 0;
       const uint32_t s_col = tmem + kColS + t * 128, o_col = tmem + kColO + t * 128;
@@ -598,12 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = ptx::desc_sw128(ptx::smem_addr(sm.ring));
       const uint64_t v_desc = desc_rows(ptx::smem_addr(sm.ring), Sizes<D>::kHalf);
       auto pass = [&](int& stage, uint32_t& phase) {       // a tile of the other row tile's share
-        wait(&sm.full[stage], phase);
-        if (ptx::elect_one()) ptx::mbar_arrive(&sm.empty[stage]);
+        ok &= wait(&sm.full[stage], phase);
+        if (ptx::elect_one() && ok) ptx::mbar_arrive(&sm.empty[stage]);
         __syncwarp();
         advance2(stage, phase);
       };
-      for (bool first = true; __any_sync(kAll, w.next(a, first)); first = false) {
+      for (bool first = true; ok && __any_sync(kAll, w.next(a, first)); first = false) {
         const int n = __shfl_sync(kAll, w.busy(key0), 0);
         if (n == 0) continue;
         const bool split = __any_sync(kAll, w.rows <= kTileRows);
@@ -611,15 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys from the block's first tile on
         const int keys = __shfl_sync(kAll, w.kend - key0 - w.first * kTile, 0);
         const uint64_t q_tile = q_desc + (split ? 0 : t * ((kTileRows * 128) >> 4));
-        wait(&sm.q_full, q_phase);
+        ok &= wait(&sm.q_full, q_phase);
         q_phase ^= 1;
         auto scores = [&](int j) {                         // into their half of the columns
           if (split && j + t > 0) pass(k_stage, k_phase);
-          wait(&sm.full[k_stage], k_phase);
+          ok &= wait(&sm.full[k_stage], k_phase);
           ptx::tc_fence_after();
           const uint64_t kd = k_desc + (uint64_t)(k_stage * (Sizes<D>::kBytes >> 4));
           const uint32_t col = s_col + (j & 1) * kTile;
-          if (ptx::elect_one()) {
+          if (ptx::elect_one() && ok) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_ss(col, q_tile + (k >> 2) * (Sizes<D>::kQueryHalf >> 4) + (k & 3) * 2,
@@ -635,15 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tiles > 1) scores(1);
         for (int j = 0; j < tiles; ++j) {
           if (split && j + t > 0) pass(v_stage, v_phase);
-          wait(&sm.full[v_stage], v_phase);
-          wait(&sm.p_full[t][j & 1], (p_phase >> (j & 1)) & 1);
+          ok &= wait(&sm.full[v_stage], v_phase);
+          ok &= wait(&sm.p_full[t][j & 1], (p_phase >> (j & 1)) & 1);
           p_phase ^= 1u << (j & 1);
           ptx::tc_fence_after();
           const uint64_t vd = v_desc + (uint64_t)(v_stage * (Sizes<D>::kBytes >> 4));
           const uint32_t col = s_col + (j & 1) * kTile;
           const int left = keys - (split ? 2 * j + t : j) * kTile;
           const uint32_t more = j > 0;
-          if (ptx::elect_one()) {
+          if (ptx::elect_one() && ok) {
             mma_ts(o_col, col, vd, id_o, more);
 #pragma unroll
             for (int k = 1; k < kTile / 16; ++k)
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance2(v_stage, v_phase);
           if (j + 2 < tiles) scores(j + 2);
         }
-        if (tiles == 0 && ptx::elect_one()) ptx::mbar_arrive(&sm.q_empty);
+        if (tiles == 0 && ptx::elect_one() && ok) ptx::mbar_arrive(&sm.q_empty);
         __syncwarp();
         if (split && n > 2 * tiles - 1 + t) {              // one behind the share's last
           pass(k_stage, k_phase);
@@ -693,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < tiles; ++j, k0 += share.split ? 2 * kTile : kTile) {
         const uint32_t x_col = s_col + (j & 1) * kTile;
         ptx::mbar_wait(&sm.s_full[t][j & 1], (s_phase >> (j & 1)) & 1, abort, kAttnWaitNs);
+        bool gave_up = *abort;            // (what the wait returns costs 1% more)
         s_phase ^= 1u << (j & 1);
         ptx::tc_fence_after();
         uint32_t x[kTile];
@@ -719,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // No product may be in flight on the output: tile j - 1's end comes before the scores
             // of tile j + 1, or has a barrier of its own before the item's last.
             if (j + 1 < tiles)
-              ptx::mbar_wait(&sm.s_full[t][(j + 1) & 1], (s_phase >> ((j + 1) & 1)) & 1, abort,
-                             kAttnWaitNs);
+              gave_up |= !wait(&sm.s_full[t][(j + 1) & 1], (s_phase >> ((j + 1) & 1)) & 1);
             else
-              ptx::mbar_wait(&sm.o_prev[t], prev_phase, abort, kAttnWaitNs);
+              gave_up |= !wait(&sm.o_prev[t], prev_phase);
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int e0 = 0; e0 < D; e0 += 32) {
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // that share the last key's sixteen are cleared, by each row tile before its own
           // products (the second to come writes zeros over zeros)
           const int at = v0 + share.tile(j), v = 2 * (at % (STAGES / 2)) + 1;
-          ptx::mbar_wait(&sm.full[v], (at / (STAGES / 2)) & 1, abort, kAttnWaitNs);
+          if (!wait(&sm.full[v], (at / (STAGES / 2)) & 1)) break;
           const int from_row = w.kend - k0, to_row = (from_row + 15) / 16 * 16;
           for (int e = threadIdx.x & 127; e < (to_row - from_row) * (D / 8); e += 128) {
             const int vr = from_row + e / (D / 8), piece = e % (D / 8);
@@ -757,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.p_full[t][j & 1]);
+        if (lane == 0 && !gave_up) ptx::mbar_arrive(&sm.p_full[t][j & 1]);
         l += lo_of(sum[0]) + hi_of(sum[0]) + (lo_of(sum[1]) + hi_of(sum[1]));
       }
 

@@ -8,7 +8,7 @@ import pytest
 
 from tests.test_kernel_rules_host import kernels
 
-FILES = [("attn_few.cu", "attention_few_kernel")]
+FILES = [("attn_few.cu", "attention_few_kernel"), ("attn_tile.cu", "attention_tile_kernel")]
 
 
 def statement(body: str, at: int) -> str:
@@ -45,14 +45,24 @@ def test_every_wait_is_heeded(name, kernel):
     body = kernels(name)[kernel]
     assert len(waits(body)) >= 3
     for at in waits(body):
-        s = statement(body, at)
-        assert re.match(r"ok = |return ", s), s
-    # and nothing is loaded, released or stored on where one has run out
-    for m in re.finditer(r"\bok = (?:ok && )?wait\(", body):
-        end = body.index(";", m.end()) + 1
-        while re.match(r"\s*ok = ok && wait\(", body[end:]):
-            end = body.index(";", end) + 1
-        assert re.match(r"\s*if \(!ok\) (?:break|return);|\s*\}", body[end:]), body[end:end + 80]
+        s, after = statement(body, at), body[body.index(";", at) + 1:]
+        if re.match(r"ok = wait\(", s):                # on the spot
+            assert re.match(r"\s*if \(!ok\) break;", after), s
+        elif re.match(r"ptx::mbar_wait\(&sm\.s_full", s):
+            assert re.match(r"\s*bool gave_up = \*abort;", after), s
+        elif not re.match(r"ptx::mbar_wait\(&sm\.o_", s):   # (what follows is only read)
+            assert re.match(r"ok &= wait\(|(?:if \(.*\)|else)\s+gave_up \|= !wait\(|if \(!wait\(.*break;",
+                            s), s
+
+
+def test_nothing_is_issued_or_released_after_a_wait_that_ran_out():
+    body = kernels("attn_tile.cu")["attention_tile_kernel"]
+    found = [m.start() for m in re.finditer(r"\bmma_[st]s\(|tc_commit\(&sm\.(?!done)|mbar_arrive\(&sm\.",
+                                            body)]
+    assert len(found) >= 10
+    for at in found:
+        heads = conditions(body, at)
+        assert any(re.search(r"\bif \([^;]*&& (?:ok|!gave_up)\)", h) for h in heads), heads[-1]
 
 
 @pytest.mark.parametrize("name,kernel", FILES)
