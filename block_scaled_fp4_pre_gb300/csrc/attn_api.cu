@@ -441,14 +441,13 @@ moe_status moe_attention_check(void* ws, void* stream) {
       return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was not initialised", ws);
     dims = it->second.dims;
   }
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t flag = 0;
-  if ((e = cudaMemcpy(&flag, ws, sizeof(flag), cudaMemcpyDeviceToHost)))
-    return cuda_fail(e, "flag read");
+  cudaError_t e = read_flags(&flag, ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, "flag read");
   // a call that gave up may have left its counters of parts behind
   const size_t clear = flag & kErrTimeout ? ws_layout(dims).cuts : sizeof(flag);
-  if ((e = cudaMemset(ws, 0, clear))) return cuda_fail(e, "flag clear");
+  if (flag && (e = clear_flags(ws, clear, st))) return cuda_fail(e, "flag clear");
   if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a device wait ran past its limit");
   if (flag & kErrPage)
     return fail(MOE_ERR_PAGE, "a token's page is outside its table or the cache");

@@ -55,6 +55,19 @@ constexpr int kErrRouting = 1;
 constexpr int kErrTimeout = 2;
 constexpr int kErrPage = 4;
 
+// A check's read of the error bits and its clear of them.  Both on its own stream and done when
+// they return: a clear on the default stream could still run, or fall between two kernels, when
+// the next call's kernels set the bits again on a stream that does not wait for that one.
+inline cudaError_t read_flags(int32_t* flag, const void* dev, cudaStream_t st) {
+  const cudaError_t e = cudaMemcpyAsync(flag, dev, sizeof(*flag), cudaMemcpyDeviceToHost, st);
+  const cudaError_t waited = cudaStreamSynchronize(st);
+  return e != cudaSuccess ? e : waited;
+}
+inline cudaError_t clear_flags(void* dev, size_t bytes, cudaStream_t st) {
+  const cudaError_t e = cudaMemsetAsync(dev, 0, bytes, st);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(st);
+}
+
 // Other words of ws.flags: [1] number of token tiles, [2] valid assignments,
 // [3] next work item of the layer kernel, [4] blocks of the layer kernel done.
 constexpr int kFlagTiles = 1;
