@@ -706,13 +706,11 @@ moe_status moe_check(void* ws, void* stream) {
   }
   const WsLayout L = ws_layout(d);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaStreamSynchronize(st);
-  if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
   int32_t flag = 0;
-  int32_t* dflag = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + L.off_flags);
-  if ((e = cudaMemcpy(&flag, dflag, sizeof(flag), cudaMemcpyDeviceToHost)))
-    return cuda_fail(e, "flag read");
-  if ((e = cudaMemset(dflag, 0, sizeof(int32_t)))) return cuda_fail(e, "flag clear");
+  uint8_t* dflag = static_cast<uint8_t*>(ws) + L.off_flags;
+  cudaError_t e = read_flags(&flag, dflag, st);
+  if (e != cudaSuccess) return cuda_fail(e, "flag read");
+  if (flag && (e = clear_flags(dflag, sizeof(flag), st))) return cuda_fail(e, "flag clear");
   if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a device wait ran past its limit");
   if (flag & kErrRouting)
     return fail(MOE_ERR_ROUTING, "topk ids outside [0, num_experts) were skipped");

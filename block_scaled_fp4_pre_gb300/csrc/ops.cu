@@ -304,12 +304,11 @@ moe_status moe_linear_check(void* ws, void* stream) {
     if (g_linear.find(ws) == g_linear.end())
       return fail(MOE_ERR_WORKSPACE_MISMATCH, "workspace %p was not initialised", ws);
   }
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t flag = 0;
-  if ((e = cudaMemcpy(&flag, ws, sizeof(flag), cudaMemcpyDeviceToHost)))
-    return cuda_fail(e, "flag read");
-  if ((e = cudaMemset(ws, 0, sizeof(flag)))) return cuda_fail(e, "flag clear");
+  cudaError_t e = read_flags(&flag, ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, "flag read");
+  if (flag && (e = clear_flags(ws, sizeof(flag), st))) return cuda_fail(e, "flag clear");
   if (flag & kErrTimeout) return fail(MOE_ERR_TIMEOUT, "a device wait ran past its limit");
   return MOE_OK;
 }

@@ -17,7 +17,9 @@ def function(name: str, file: str) -> str:
     return text[start:text.index("\n}\n", start)]
 
 
-@pytest.mark.parametrize("name,file", [("moe_attention_check", "attn_api.cu")])
+@pytest.mark.parametrize("name,file", [("moe_attention_check", "attn_api.cu"),
+                                       ("moe_check", "api.cu"),
+                                       ("moe_linear_check", "ops.cu")])
 def test_a_check_uses_no_other_stream(name, file):
     # cudaMemset on the default stream is not ordered with what another stream runs next
     body = function(name, file)
