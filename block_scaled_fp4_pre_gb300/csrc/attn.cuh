@@ -177,8 +177,9 @@ __device__ __forceinline__ void finish_sums(Finish& f, float m, float l, float2 
   f.mine = exp2_approx(m - base);
   f.theirs = exp2_approx(part.x - base);
   l = add_scaled(l, f.mine, part.y, f.theirs);
-  f.inv = l > 0.f ? 1.f / l : 0.f;
-  f.lse = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  // 0: no key; NaN where a key's logit is, for both outputs
+  f.inv = l == 0.f ? 0.f : 1.f / l;
+  f.lse = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
 }
 template <int D, bool SHARED>
 __device__ __forceinline__ Finish finish_begin(const AttnArgs& a, int kv_head, int64_t index,

@@ -569,9 +569,10 @@ MXMOE_API moe_status moe_kv_append(const moe_attention_dims *dims, const moe_kv_
  *   scale    finite and positive
  * Strides are multiples of 8 and at least a row, pointers 16-byte aligned.  The caches hold the
  * new tokens' keys and values already (moe_kv_append).  Rows of the cache that no token of the
- * call sees may hold anything, those that one sees finite values; q is finite.  Products of bf16
- * values are summed in fp32, the probabilities rounded to bf16 for theirs with the values, their
- * sum taken in fp32.  Results do not depend on timing. */
+ * call sees may hold anything, those that one sees finite values; q is finite.  (A key with a NaN
+ * that a token sees makes that token's outputs and lse NaN.)  Products of bf16 values are summed
+ * in fp32, the probabilities rounded to bf16 for theirs with the values, their sum taken in fp32.
+ * Results do not depend on timing. */
 MXMOE_API moe_status moe_attention(const moe_attention_dims *dims, const moe_kv_batch *batch,
                                    const void *q_dev, int64_t ldq, const void *k_cache_dev,
                                    const void *v_cache_dev, float scale, void *out_dev,
