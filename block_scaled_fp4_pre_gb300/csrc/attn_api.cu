@@ -386,8 +386,9 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
   if ((s = check_ws(d, ws, ws_bytes, &shared))) return s;
   AttnLaunch g = {};
   if ((s = check_batch(d, batch, &g.args.batch))) return s;
-  if (!(scale > 0.f) || std::isinf(scale))
-    return fail(MOE_ERR_INVALID_ARG, "scale must be finite and above 0");
+  const float scale_log2 = (float)(scale * 1.4426950408889634);
+  if (!(scale > 0.f) || std::isinf(scale_log2))    // (a logit of 0 would become NaN)
+    return fail(MOE_ERR_INVALID_ARG, "scale and scale * log2(e) must be finite and above 0");
   if (batch->tokens == 0) return MOE_OK;
   if (!given(q) || !given(out) || !aligned(lse, 4))
     return fail(MOE_ERR_INVALID_ARG, "q and out must be given and every tensor 16-byte aligned");
@@ -404,7 +405,7 @@ moe_status moe_attention(const moe_attention_dims* d, const moe_kv_batch* batch,
   a.lse = lse;
   a.ldq = ldq;
   a.ldo = ldo;
-  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.q_heads = d->q_heads;
   a.kv_heads = d->kv_heads;
   a.group = d->q_heads / d->kv_heads;

@@ -566,7 +566,7 @@ MXMOE_API moe_status moe_kv_append(const moe_attention_dims *dims, const moe_kv_
  *   q_dev    bf16 [tokens, q_heads, head_dim], token stride ldq
  *   out_dev  bf16, the same with ldo; shares no memory with q or the caches
  *   lse_dev  fp32 [tokens, q_heads], ln of the sum of exp(scale * q . k), or NULL
- *   scale    finite and positive
+ *   scale    finite and positive, as is its product with log2 e in fp32
  * Strides are multiples of 8 and at least a row, pointers 16-byte aligned.  The caches hold the
  * new tokens' keys and values already (moe_kv_append).  Rows of the cache that no token of the
  * call sees may hold anything, those that one sees finite values; q is finite.  (A key with a NaN
