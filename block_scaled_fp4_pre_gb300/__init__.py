@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import numpy as np
@@ -182,6 +183,7 @@ def lib() -> ctypes.CDLL:
             "moe_debug_linear_give_up": ([vp, i32], i32),
             "moe_rope_table_size": ([RD], sz),
             "moe_rope_prepare": ([RD, vp, sz, vp], i32),
+            "moe_rope_prepare_frequencies": ([RD, vp, vp, sz, vp], i32),
             "moe_rope": ([RD, vp, vp, i64, vp, i64, i32, vp, i64, vp], i32),
             "moe_attention_workspace_size": ([AD], sz),
             "moe_attention_workspace_init": ([AD, vp, sz, vp], i32),
@@ -573,6 +575,41 @@ def moe_rope_prepare(dims: RopeDims, table, stream=None) -> None:
     """Writes the rotation's table, once for the calls that take it with these dims."""
     _check(lib().moe_rope_prepare(ctypes.byref(dims), _bytes(table, 0, "table"), _nbytes(table),
                                   _stream(stream)))
+
+
+def moe_rope_prepare_frequencies(dims: RopeDims, frequencies, table, stream=None) -> None:
+    """The same with the caller's own frequencies, radians from one position to the next for each
+    of the rotary_dim / 2 pairs."""
+    w = [float(f) for f in frequencies]
+    if len(w) != dims.rotary_dim // 2:
+        raise ValueError(f"frequencies: need {dims.rotary_dim // 2}, got {len(w)}")
+    _check(lib().moe_rope_prepare_frequencies(
+        ctypes.byref(dims), (ctypes.c_double * len(w))(*w), _bytes(table, 0, "table"),
+        _nbytes(table), _stream(stream)))
+
+
+def yarn_frequencies(rotary_dim: int, base: float, factor: float, original_length: float,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, whole: bool = True
+                     ) -> list[float]:
+    """YaRN's frequencies with a ramp over the pairs' indices, as many models are trained with it
+    (MOE_ROPE_YARN's is one over their turns): from base^(-2i / rotary_dim) up to the index at
+    which a pair makes beta_fast turns over the trained length, to that over factor from the one
+    with beta_slow turns on.  The two indices are rounded outwards to whole ones unless told not to."""
+    d = rotary_dim
+
+    def index(turns):                    # original_length base^(-2 index / d) = 2 pi turns
+        return d * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    low, high = index(beta_fast), index(beta_slow)
+    if whole:
+        low, high = math.floor(low), math.ceil(high)
+    low, high = max(low, 0), min(high, d - 1)
+    frequencies = []
+    for i in range(d // 2):
+        w = base ** (-2 * i / d)
+        g = 1 - min(1.0, max(0.0, (i - low) / max(high - low, 1e-3)))
+        frequencies.append(w * g + w / factor * (1 - g))
+    return frequencies
 
 
 def _here(t, name: str, device: int | None = None) -> int:

@@ -21,13 +21,18 @@ from block_scaled_fp4_pre_gb300 import block as blk
 
 
 class Attention:
-    """A layer's paged cache, rotation and buffers, for up to dims.max_tokens tokens a step."""
+    """A layer's paged cache, rotation (of the caller's frequencies, if given) and buffers, for up
+    to dims.max_tokens tokens a step."""
 
-    def __init__(self, dims: mx.AttentionDims, rope: mx.RopeDims, device="cuda"):
+    def __init__(self, dims: mx.AttentionDims, rope: mx.RopeDims, device="cuda",
+                 frequencies=None):
         u8, bf = torch.uint8, torch.bfloat16
         self.dims, self.rope = dims, rope
         self.table = torch.empty(mx.moe_rope_table_size(rope), dtype=u8, device=device)
-        mx.moe_rope_prepare(rope, self.table)
+        if frequencies is None:
+            mx.moe_rope_prepare(rope, self.table)
+        else:
+            mx.moe_rope_prepare_frequencies(rope, frequencies, self.table)
         self.k_cache, self.v_cache = (torch.zeros(dims.cache_shape, dtype=bf, device=device)
                                       for _ in range(2))
         self.ws = torch.empty(mx.moe_attention_workspace_size(dims), dtype=u8, device=device)

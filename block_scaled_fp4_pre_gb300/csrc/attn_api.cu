@@ -71,9 +71,10 @@ float magnitude_of(const moe_rope_dims& d) {
   return d.scaling == MOE_ROPE_YARN ? (float)(0.1 * std::log(d.factor) + 1.0) : 1.f;
 }
 
-// 2^64 times the part of a turn that pair i rotates by from one position to the next.
-uint64_t turn_of(const moe_rope_dims& d, int i) {
-  constexpr double kTurn = 6.283185307179586476925;
+constexpr double kTurn = 6.283185307179586476925;
+
+// Radians that pair i rotates by from one position to the next.
+double frequency_of(const moe_rope_dims& d, int i) {
   const double n = d.rotary_dim;
   double base = d.base;
   if (d.scaling == MOE_ROPE_NTK) base *= std::pow(d.factor, n / (n - 2.0));
@@ -85,7 +86,7 @@ uint64_t turn_of(const moe_rope_dims& d, int i) {
         std::fmin(1.0, std::fmax(0.0, (turns - d.beta_slow) / (d.beta_fast - d.beta_slow)));
     w = w * g + w / d.factor * (1.0 - g);
   }
-  return (uint64_t)std::ldexp(w / kTurn, 64);   // w <= 1
+  return w;   // at most 1
 }
 
 void set_rope(RopeArgs& a, const moe_rope_dims& d, const void* table) {
@@ -94,6 +95,28 @@ void set_rope(RopeArgs& a, const moe_rope_dims& d, const void* table) {
   a.head_dim = d.head_dim;
   a.rotary_dim = d.rotary_dim;
   a.layout = d.layout;
+}
+
+// The table, of w (radians a position) or, where that is null, of the dims' frequencies.
+moe_status prepare_rope(const moe_rope_dims* d, const double* w, void* table, size_t table_bytes,
+                        void* stream) {
+  const moe_status s = check_rope(d);
+  if (s) return s;
+  if (!given(table)) return fail(MOE_ERR_INVALID_ARG, "table NULL or not 16-byte aligned");
+  const int pairs = d->rotary_dim / 2;
+  if (table_bytes < pairs * sizeof(uint64_t))
+    return fail(MOE_ERR_INVALID_ARG, "table has %zu bytes, needs %zu", table_bytes,
+                pairs * sizeof(uint64_t));
+  RopeTable t = {};   // parts of a turn, times 2^64
+  for (int i = 0; i < pairs; ++i) {
+    const double part = (w ? w[i] : frequency_of(*d, i)) / kTurn;
+    if (!(part >= 0.0 && part < 1.0))
+      return fail(MOE_ERR_INVALID_ARG, "frequency %d must be in [0, 2 pi)", i);
+    t.turn[i] = (uint64_t)std::ldexp(part, 64);
+  }
+  const cudaError_t e = launch_rope_prepare(t, pairs, table, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope prepare");
+  return MOE_OK;
 }
 
 // ---- workspaces ----
@@ -238,18 +261,13 @@ size_t moe_rope_table_size(const moe_rope_dims* d) {
 
 moe_status moe_rope_prepare(const moe_rope_dims* d, void* table, size_t table_bytes,
                             void* stream) {
-  const moe_status s = check_rope(d);
-  if (s) return s;
-  if (!given(table)) return fail(MOE_ERR_INVALID_ARG, "table NULL or not 16-byte aligned");
-  const int pairs = d->rotary_dim / 2;
-  if (table_bytes < pairs * sizeof(uint64_t))
-    return fail(MOE_ERR_INVALID_ARG, "table has %zu bytes, needs %zu", table_bytes,
-                pairs * sizeof(uint64_t));
-  RopeTable t = {};
-  for (int i = 0; i < pairs; ++i) t.turn[i] = turn_of(*d, i);
-  const cudaError_t e = launch_rope_prepare(t, pairs, table, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "rope prepare");
-  return MOE_OK;
+  return prepare_rope(d, nullptr, table, table_bytes, stream);
+}
+
+moe_status moe_rope_prepare_frequencies(const moe_rope_dims* d, const double* w, void* table,
+                                        size_t table_bytes, void* stream) {
+  if (!w) return fail(MOE_ERR_INVALID_ARG, "w is NULL");
+  return prepare_rope(d, w, table, table_bytes, stream);
 }
 
 moe_status moe_rope(const moe_rope_dims* d, const void* table, const void* x, int64_t ldx,

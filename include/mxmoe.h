@@ -442,7 +442,11 @@ MXMOE_API moe_status moe_debug_linear_give_up(void *ws_dev, int32_t on);
  *                      (rotary_dim > 2)
  *   MOE_ROPE_YARN      w * g + w / factor * (1 - g), g = clamp((t - beta_slow) / (beta_fast -
  *                      beta_slow), 0, 1) with t = original_length * w / (2 pi), the turns over
- *                      the trained length (Peng et al. 2023, "YaRN")
+ *                      the trained length (Peng et al. 2023, "YaRN").  g follows the number of
+ *                      turns, as in the paper's equation.  Many models are trained with a g that
+ *                      follows the pair's index i between those at which t is beta_fast and
+ *                      beta_slow: a frequency may differ by several times.  Theirs go to
+ *                      moe_rope_prepare_frequencies, with this scaling for the magnitude.
  * magnitude m: 0 means 1, for MOE_ROPE_YARN 0.1 ln(factor) + 1.  Angles are exact to 2^-52 of
  * a turn times the position: they are whole products modulo one turn in 64-bit fixed point, w in
  * double.  Cosines, sines and the rotation are fp32, rounded once to bf16.
@@ -469,6 +473,12 @@ typedef struct moe_rope_dims {
 MXMOE_API size_t moe_rope_table_size(const moe_rope_dims *dims);
 MXMOE_API moe_status moe_rope_prepare(const moe_rope_dims *dims, void *table_dev,
                                       size_t table_bytes, void *stream);
+/* The same with w of the caller's own: w_host double [rotary_dim / 2], read before the call
+ * returns, radians from one position to the next, each in [0, 2 pi).  Of dims, base and what
+ * scales it then count for the magnitude alone. */
+MXMOE_API moe_status moe_rope_prepare_frequencies(const moe_rope_dims *dims, const double *w_host,
+                                                  void *table_dev, size_t table_bytes,
+                                                  void *stream);
 
 /* Rotates x_dev, bf16 [tokens, heads, head_dim] with ldx elements from token to token, into
  * out_dev (ldo; out may be x itself with the same stride, and shares no memory with it
