@@ -22,10 +22,13 @@ from block_scaled_fp4_pre_gb300 import block as blk
 
 class Attention:
     """A layer's paged cache, rotation (of the caller's frequencies, if given) and buffers, for up
-    to dims.max_tokens tokens a step."""
+    to dims.max_tokens tokens a step.
+
+    The workspace (42 MB and more at 128 elements a head) holds nothing between calls: layers whose
+    calls follow one another on one stream can share that of the first, `ws`."""
 
     def __init__(self, dims: mx.AttentionDims, rope: mx.RopeDims, device="cuda",
-                 frequencies=None):
+                 frequencies=None, ws=None):
         u8, bf = torch.uint8, torch.bfloat16
         self.dims, self.rope = dims, rope
         self.table = torch.empty(mx.moe_rope_table_size(rope), dtype=u8, device=device)
@@ -35,8 +38,10 @@ class Attention:
             mx.moe_rope_prepare_frequencies(rope, frequencies, self.table)
         self.k_cache, self.v_cache = (torch.zeros(dims.cache_shape, dtype=bf, device=device)
                                       for _ in range(2))
-        self.ws = torch.empty(mx.moe_attention_workspace_size(dims), dtype=u8, device=device)
-        mx.moe_attention_workspace_init(dims, self.ws)
+        self.ws = ws
+        if ws is None:
+            self.ws = torch.empty(mx.moe_attention_workspace_size(dims), dtype=u8, device=device)
+            mx.moe_attention_workspace_init(dims, self.ws)
         self.q, self.attn = (torch.empty(dims.max_tokens, dims.q_heads, dims.head_dim, dtype=bf,
                                          device=device) for _ in range(2))
 
