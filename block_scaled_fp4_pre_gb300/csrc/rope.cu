@@ -81,8 +81,6 @@ __device__ __forceinline__ void rotate_adjacent(uint4& a, const float (&c)[8],
     if (i < pairs) x[i] = r;
   }
 }
-__device__ __forceinline__ void rotate_adjacent(uint16_t&, const float (&)[1], const float (&)[1],
-                                                int) {}
 
 struct Threads {
   int chunks;          // pieces (or pairs of pieces) of a head that threads hold
@@ -187,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     for (int j = 0; j < U; ++j) {
       if (h0 + j < sec.heads) {
         if (pairs > 0) {
-          if (HALF) rotate(x[j], y[j], cs, sn);
+          if constexpr (HALF) rotate(x[j], y[j], cs, sn);
           else rotate_adjacent(x[j], cs, sn, pairs);
         }
         uint16_t* d = dst + (h0 + j) * head_step;
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       }
     }
   }
-  }
+}
 
 template <int VEC, bool HALF, bool APPEND, int HP>
 cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
