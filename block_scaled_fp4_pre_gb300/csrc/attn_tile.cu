@@ -20,12 +20,12 @@
 // does that before it hands over the next P, when no product on it is in flight.
 //
 // Bound by the tensor cores: 4 x 128 x 64 x D operations a row tile and tile of keys at the dense
-// bf16 rate.  1415 us for a prompt of 16384 tokens, 32 heads of 128 on 8 (1554 TFLOP/s, 0.82 of the
-// measured rate of a library's product; 1483 us once the board's power limit sets in); the scores'
+// bf16 rate.  1424 us for a prompt of 16384 tokens, 32 heads of 128 on 8 (1544 TFLOP/s, 0.82 of the
+// measured rate of a library's product; 1532 us once the board's power limit sets in); the scores'
 // products, 64 columns wide, read more of shared memory than they compute, and tiles of 128 columns
 // would leave no room for two buffers a row tile beside the outputs.  At 64 elements a head the
-// softmax's instructions take longer than the products: 4 prompts of 2048 103 us.  With one row
-// tile an item it is bound by HBM: 19 drafts of 8 tokens over 8192 keys 103 us (0.93 of the
+// softmax's instructions take longer than the products: 4 prompts of 2048 105 us.  With one row
+// tile an item it is bound by HBM: 19 drafts of 8 tokens over 8192 keys 103 us (0.92 of the
 // measured copy bandwidth).
 #include <algorithm>
 
@@ -210,9 +210,9 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 constexpr int kItemCost = 4;
 
 // Items of up to this many tiles are not cut: a block takes all of one whose first tile is in its
-// range.  us with 0, 3, 6, 12: 54 prompts of 110 tokens 71.3, 59.8, 59.4, 59.4; 106 of 12 tokens
-// 16.7, 11.8, 11.7, 11.9; 117 drafts of 8 over 300 tokens 50.8, 51.6, 50.6, 46.2; 8 drafts of 5
-// behind 16384 common tokens 59.3, 59.8, 59.8, 66.0.
+// range.  us with 0, 3, 6, 12, 32 heads of 128 on 8: 54 prompts of 110 tokens 44.8, 43.0, 43.0,
+// 43.0; 106 of 12 tokens 32.7, 31.3, 31.3, 31.3; 117 drafts of 8 over 300 tokens 57.0, 57.4, 51.8,
+// 51.6; 8 drafts of 5 behind 16384 common tokens 58.7, 59.0, 59.1, 64.4.
 constexpr int kShortItem = 6;
 
 // An item has whole tokens, `step` of them (256 / group) but for a sequence's last.

@@ -17,7 +17,9 @@
 // Bound by HBM at large token counts: 8191 tokens of 40 heads of 128, half of them rotated, 27.7
 // us (168 MB, 0.91 of the measured copy bandwidth); an append of 15.3 k tokens of 32 query and
 // 8 + 8 key and value heads 61.5 us (382 MB, 0.93).  By latency at few: one token 2.6 us, its
-// append with queries 3.2 us (its page is looked up in three dependent loads).
+// append with queries 3.2 us (its page is looked up in three dependent loads).  Halves that are not
+// whole 16-byte pieces are bound by their 2-byte loads and stores: 8191 tokens of 32 heads of 80
+// with 20 rotated 34.9 us (84 MB, 0.36), adjacent pairs of the same 15.4.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
